@@ -19,7 +19,8 @@ from ._lib import GqaError, check, load  # noqa: F401
 
 HEAD_DIM = 256
 
-__all__ = ["prefill", "prefill_pair", "masked", "decode", "verify_tree", "kv_append", "kv_keep", "decode_plan", "decode_split", "lse_merge",
+__all__ = ["prefill", "prefill_pair", "masked", "decode", "verify_tree", "kv_append", "kv_keep", "block_plan",
+           "kv8_append", "kv8_keep", "kv8_decode", "kv8_workspace_size", "decode_plan", "decode_split", "lse_merge",
            "decode_workspace_size", "last_device_status", "set_wait_timeout_ns",
            "selftest_wait_timeout", "decode_noalloc", "launch_log", "GqaError",
            "load"]
@@ -308,6 +309,177 @@ def kv_keep(k_cache, v_cache, kv_lens, cu_rows, keep_idx, cu_keep, kv_lens_out=N
     check(load().gqa_kv_keep(_ptr(k_cache), _ptr(v_cache), _ptr(kv_lens), _ptr(cu_rows),
                              _ptr(keep_idx), _ptr(cu_keep), _ptr(kv_lens_out), B, Hkv, Lcap,
                              _stream()), "gqa_kv_keep")
+
+
+def _i32(t, numel, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {numel} entries")
+
+
+def _tables(block_tables, B):
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise ValueError("block_tables must be an int32 CUDA tensor [B, max_blocks]")
+    _i32(block_tables, B * block_tables.shape[1], "block_tables")
+    return block_tables.shape[1]
+
+
+def _kv8_pools(k_pool, v_pool, k_scale, v_scale):
+    """(num_blocks, Hkv, block_size) of checked pools and scales."""
+    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        _need(t, torch.float8_e4m3fn, 4, name)
+    N, Hkv, bs, _ = k_pool.shape
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+            raise TypeError(f"{name} must be a float32 tensor")
+        if tuple(t.shape) != (N, Hkv) or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [num_blocks, Hkv]")
+    return N, Hkv, bs
+
+
+def _one_device(*tensors):
+    """The tensors' common device, made current for the call."""
+    d = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != d:
+            raise ValueError("the tensors of a call must be on one device")
+    return torch.cuda.device(d)
+
+
+def block_plan(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, block_size, T,
+               slots=None, kv_lens_out=None):
+    """Block tables and slot maps of a paged cache from request lengths, on the GPU.
+
+    Sequence b holds kv_lens[b] keys and gets cu_rows[b+1] - cu_rows[b] new rows; after the
+    call it owns exactly the blocks that they need.  int32 CUDA tensors, updated in place:
+    block_tables [B, max_blocks], n_blocks [B], free_list [num_blocks] and free_count [1] (a
+    stack).  Surplus blocks go back first (length 0 and no rows: a finished request), then
+    growing sequences take theirs in order.  T: rows in the batch, cu_rows[B] or more.
+    Returns (slots int32 [T], kv_lens_out int32 [B]): the place of each new row (block *
+    block_size + row; -1 without one) for kv8_append, and the lengths with the new rows for
+    kv8_decode.  A sequence that the pool has no blocks for keeps its length, its slots are
+    -1, and last_device_status() gives GQA_ERR_NO_BLOCKS (7)."""
+    B = kv_lens.numel()
+    _i32(kv_lens, B, "kv_lens")
+    _i32(cu_rows, B + 1, "cu_rows")
+    max_blocks = _tables(block_tables, B)
+    _i32(n_blocks, B, "n_blocks")
+    _i32(free_list, free_list.numel(), "free_list")
+    _i32(free_count, 1, "free_count")
+    T = int(T)
+    if slots is None:
+        slots = torch.empty(max(T, 0), dtype=torch.int32, device=kv_lens.device)
+    if kv_lens_out is None:
+        kv_lens_out = torch.empty_like(kv_lens)
+    _i32(slots, T, "slots")
+    _i32(kv_lens_out, B, "kv_lens_out")
+    with _one_device(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, slots,
+                     kv_lens_out):
+        check(load().gqa_block_plan(_ptr(kv_lens), _ptr(cu_rows), _ptr(block_tables),
+                                    _ptr(n_blocks), _ptr(free_list), _ptr(free_count),
+                                    _ptr(slots), _ptr(kv_lens_out), B, T, max_blocks,
+                                    free_list.numel(), int(block_size), _stream()),
+              "gqa_block_plan")
+    return slots, kv_lens_out
+
+
+def kv8_append(k_new, v_new, slots, k_pool, v_pool, k_scale, v_scale):
+    """Quantises new rows ([T,Hkv,256] bf16 or fp16) into the paged 8-bit cache at their slots
+    (int32 [T], from block_plan; -1 skips a row).  k_pool, v_pool: float8_e4m3fn [num_blocks,
+    Hkv, block_size, 256]; k_scale, v_scale: float32 [num_blocks, Hkv], one power of two per
+    block and head, kept as large as the block's rows ask (rows that a block holds already
+    are rounded again when its scale grows)."""
+    sfx = _elem(k_new, "k_new")
+    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+        _need(t, k_new.dtype, 3, n)
+    N, Hkv, bs = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    T = k_new.shape[0]
+    if k_new.shape[1] != Hkv or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [T, Hkv, 256] with the pools' Hkv")
+    _i32(slots, T, "slots")
+    with _one_device(k_new, v_new, slots, k_pool, v_pool, k_scale, v_scale):
+        fn = getattr(load(), "gqa_kv8_append" + sfx)
+        check(fn(_ptr(k_new), _ptr(v_new), _ptr(slots), _ptr(k_pool), _ptr(v_pool),
+                 _ptr(k_scale), _ptr(v_scale), T, Hkv, N, bs, _stream()), "gqa_kv8_append" + sfx)
+
+
+def kv8_keep(k_pool, v_pool, k_scale, v_scale, block_tables, kv_lens, cu_rows, keep_idx, cu_keep,
+             kv_lens_out=None):
+    """kv_keep() for the paged 8-bit cache: the accepted draft rows (at most 64 per sequence)
+    move to the front of each sequence's draft region, as if their values had been appended
+    there; writes the new lengths into kv_lens_out when given."""
+    N, Hkv, bs = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    B = kv_lens.numel()
+    _i32(kv_lens, B, "kv_lens")
+    max_blocks = _tables(block_tables, B)
+    _i32(cu_rows, B + 1, "cu_rows")
+    _i32(keep_idx, keep_idx.numel(), "keep_idx")
+    _i32(cu_keep, B + 1, "cu_keep")
+    if kv_lens_out is not None:
+        _i32(kv_lens_out, B, "kv_lens_out")
+    with _one_device(k_pool, v_pool, k_scale, v_scale, block_tables, kv_lens, cu_rows, keep_idx,
+                     cu_keep, kv_lens_out):
+        check(load().gqa_kv8_keep(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                                  _ptr(block_tables), _ptr(kv_lens), _ptr(cu_rows),
+                                  _ptr(keep_idx), _ptr(cu_keep), _ptr(kv_lens_out),
+                                  keep_idx.numel(), B, Hkv, N, bs, max_blocks, _stream()), "gqa_kv8_keep")
+
+
+def kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len):
+    return int(load().gqa_kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len))
+
+
+def kv8_decode(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu_rows=None,
+               tree_mask=None, max_rows=None, max_kv_len=None, workspace=None, out=None,
+               return_lse=False):
+    """Decode, chain-verify and (with tree_mask, int64 [T]) tree-verify rows over the paged
+    8-bit cache.  q, g: [T,Hq,256] bf16 or fp16; pools and scales as kv8_append writes them;
+    block_tables int32 [B, max_blocks]; kv_lens int32 [B] counts the new rows; cu_rows int32
+    [B+1] or None (one row per sequence).  Returns out [T,Hq,256]; rows behind cu_rows[B] (a
+    padded batch) are left as they were in a given out."""
+    sfx = _elem(q, "q")
+    _need(q, q.dtype, 3, "q")
+    N, Hkv, bs = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    if g is not None:
+        _need(g, q.dtype, 3, "g")
+        if g.shape != q.shape:
+            raise ValueError("g must have q's shape")
+    T, Hq, _ = q.shape
+    B = kv_lens.numel()
+    _i32(kv_lens, B, "kv_lens")
+    max_blocks = _tables(block_tables, B)
+    if cu_rows is not None:
+        _i32(cu_rows, B + 1, "cu_rows")
+    if tree_mask is not None and (tree_mask.dtype != torch.int64 or not tree_mask.is_cuda
+                                  or not tree_mask.is_contiguous() or tree_mask.numel() != T):
+        raise ValueError("tree_mask must be a contiguous int64 CUDA tensor of T entries")
+    if max_kv_len is None:           # synchronises; pass it to avoid the copy
+        max_kv_len = max(1, int(kv_lens.max().item()))
+    if max_rows is None:
+        max_rows = 1 if cu_rows is None else max(1, int((cu_rows[1:] - cu_rows[:-1]).max().item()))
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, q.dtype, 3, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:    # (a given workspace is checked by the library itself)
+        need = kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    with _one_device(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu_rows,
+                     tree_mask, workspace, out):
+        fn = getattr(load(), "gqa_kv8_decode" + sfx)
+        code = fn(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(g),
+                  _ptr(block_tables), _ptr(kv_lens), _ptr(cu_rows), _ptr(tree_mask), _ptr(out),
+                  _ptr(lse), B, T, Hq, Hkv, N, bs, max_blocks, int(max_rows), int(max_kv_len),
+                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream())
+    check(code, "gqa_kv8_decode" + sfx)
+    return (out, lse) if return_lse else out
 
 
 def decode_split(q, k_cache, v_cache, kv_lens, cu_rows=None, max_rows=None, max_kv_len=None,

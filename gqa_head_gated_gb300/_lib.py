@@ -19,6 +19,7 @@ STATUS = {
     4: "GQA_ERR_TIMEOUT",
     5: "GQA_ERR_WORKSPACE",
     6: "GQA_ERR_DEVICE_RANGE",
+    7: "GQA_ERR_NO_BLOCKS",
 }
 
 
@@ -60,9 +61,15 @@ SIGNATURES = {
     "gqa_attn_mask_check": (_I, [_I, _I, _I, _I, _I, _I, _P, _P, _I]),
     "gqa_attn_masked": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
                              _I, _P]),
+    "gqa_block_plan": (_I, [_P] * 8 + [_I] * 5 + [_P]),
+    "gqa_kv8_append": (_I, [_P] * 7 + [_I] * 4 + [_P]),
+    "gqa_kv8_keep": (_I, [_P] * 10 + [_I] * 6 + [_P]),
+    "gqa_kv8_workspace_size": (ctypes.c_size_t, [_I] * 6),
+    "gqa_kv8_decode": (_I, [_P] * 12 + [_I] * 9 + [_P, ctypes.c_size_t, _P]),
 }
-for _name in ("gqa_attn_masked", "gqa_attn_prefill", "gqa_attn_decode", "gqa_attn_verify_tree",
-              "gqa_attn_decode_split", "attn_lse_merge"):
+for _name in ("gqa_kv8_append", "gqa_kv8_decode", "gqa_attn_masked", "gqa_attn_prefill",
+              "gqa_attn_decode", "gqa_attn_verify_tree", "gqa_attn_decode_split",
+              "attn_lse_merge"):
     SIGNATURES[_name + "_f16"] = SIGNATURES[_name]   # fp16 twins, same arguments
 
 _lib = None

@@ -456,6 +456,7 @@ const char* gqa_status_string(int status) {
     case GQA_ERR_TIMEOUT: return "device wait timed out";
     case GQA_ERR_WORKSPACE: return "workspace too small";
     case GQA_ERR_DEVICE_RANGE: return "device-side range error (kv_lens / cu_rows)";
+    case GQA_ERR_NO_BLOCKS: return "no free cache blocks left";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,406 @@
+// Writing the paged 8-bit KV cache: kv8_append quantises new rows behind the keys that
+// their blocks hold; kv8_keep moves the accepted draft rows of a sequence to the front
+// of its draft region.
+//
+// The rule, per (block, KV head), K and V apart, for the run of rows written to a block:
+//   a    = largest finite |x| of the run, E(a) = least e >= -126 with a <= 448 * 2^e
+//   e    = E(a) when the run starts at the block's first row, else max(e_old, E(a))
+//   rows before the run are rounded again by 2^(e_old - e) where the scale grew
+//   q    = e4m3(x * 2^-e), nearest even; NaN and +-Inf are stored as NaN (e4m3 has no
+//          infinity, and a saturated one would pass for a number)
+// keep is the same rule applied to the kept rows' values, as if they had been appended
+// behind the first len - r keys.
+//
+// Both are memory-bound at prompt sizes and latency-bound for a decode step.
+#include <cuda_runtime.h>
+
+#include "kv8_common.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kWindow = 64;               // tokens whose runs a CTA writes
+constexpr int kSpan = kWindow + 128;      // the last of them may reach a block further
+constexpr int kRowsPerWarp = kWindow / kWarps;
+
+template <bool kF16>
+__device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack_elem2<kF16>(w[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+struct AppendParams {
+  const uint4* x[2];        // K, V new rows: 16-bit [T, Hkv, 256]
+  uint2* pool[2];           // e4m3 [num_blocks, Hkv, bs, 256]
+  float* scale[2];          // [num_blocks, Hkv]
+  const int* slots;
+  int T, Hkv, num_blocks, bs_log2;
+  LaunchCtl ctl;
+};
+
+// Rounds a block's first n rows again, from scale `s_old` to 2^e (one warp a row).
+__device__ __forceinline__ void rescale_rows(uint2* block, int n, float s_old, int e) {
+  const float inv = pow2f(-e);
+  for (int r = threadIdx.x >> 5; r < n; r += kWarps) {
+    uint2* const a = block + r * 32 + (threadIdx.x & 31);
+    float f[8];
+    from_e4m3x8(*a, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * s_old * inv;
+    *a = to_e4m3x8(f);
+  }
+}
+
+// One CTA: the runs that start in its window of 64 tokens, for one KV head of K or V.
+// A token's run is the tokens before it in the same block; a run is at most one block.
+// Every warp keeps its 8 window rows in registers between the maximum and the rounding;
+// rows of the last run past the window are read twice.
+template <bool kF16>
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams p) {
+  __shared__ int s_slot[kSpan + 1];          // slot of token w0 - 1 + i
+  __shared__ uint32_t s_start[kSpan / 32];   // bit i: token w0 + i starts a run
+  __shared__ uint32_t s_break[kSpan / 32];   // bit i: token w0 + i starts a run or is in none
+  __shared__ uint32_t s_max[kWindow];        // by run (its first token): largest |x|, then
+  __shared__ int s_exp[kWindow];             // the exponent of its scale
+  __shared__ float s_old[kWindow];           // the scale that the rows before it have
+  __shared__ int s_grown[kWindow];
+  __shared__ int s_n_grown;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int w0 = blockIdx.x * kWindow, g = blockIdx.y, kv = blockIdx.z;
+  const int bs = 1 << p.bs_log2;
+  const int n_span = min(kWindow + bs, p.T - w0);   // tokens from w0 on that matter here
+  const uint4* const x = p.x[kv];
+  uint2* const pool = p.pool[kv];
+
+  // The window's rows are on their way while the runs are worked out.
+  uint4 u[kRowsPerWarp];
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    const int t = w0 + warp + k * kWarps;
+    if (t < p.T) u[k] = __ldg(x + (size_t(t) * p.Hkv + g) * 32 + lane);
+  }
+  for (int i = tid; i < kSpan + 1; i += kThreads) {
+    const int t = w0 - 1 + i;
+    s_slot[i] = t >= 0 && i <= n_span ? __ldg(p.slots + t) : -1;
+  }
+  if (tid < kWindow) s_max[tid] = 0u;
+  if (tid == 0) s_n_grown = 0;
+  __syncthreads();
+  const long long n_slots = (long long)p.num_blocks << p.bs_log2;
+  if (tid < kSpan) {   // kSpan / 32 whole warps
+    const int before = s_slot[tid], s = s_slot[tid + 1];
+    bool in = s >= 0 && s < n_slots;
+    bool start = in && (before < 0 || before >= n_slots || s != before + 1 || (s & (bs - 1)) == 0);
+    // a token in the block of the one before it but not behind it has no place
+    const bool bad = (s < -1 || s >= n_slots) ||
+                     (start && before >= 0 && (s >> p.bs_log2) == (before >> p.bs_log2));
+    if (bad) {
+      in = start = false;
+      if (tid < kWindow && g == 0 && kv == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+    }
+    const uint32_t st = __ballot_sync(0xffffffffu, start);
+    const uint32_t br = __ballot_sync(0xffffffffu, start || !in);
+    if (lane == 0) {
+      s_start[warp] = st;
+      s_break[warp] = br;
+    }
+  }
+  __syncthreads();
+  // First token of token w0 + i's run, -1 when it is in no run that starts in the window.
+  const auto run_of = [&](int i) -> int {
+    if (i >= n_span) return -1;
+    int w = i >> 5;
+    uint32_t m = s_break[w] & (0xffffffffu >> (31 - (i & 31)));
+    while (m == 0u && w > 0) m = s_break[--w];
+    if (m == 0u) return -1;
+    const int f = w * 32 + 31 - __clz(m);
+    return f < kWindow && ((s_start[f >> 5] >> (f & 31)) & 1u) ? f : -1;
+  };
+  int run[kRowsPerWarp];
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    const int i = warp + k * kWarps;
+    run[k] = run_of(i);
+    if (run[k] < 0) continue;
+    float f[8];
+    unpack8<kF16>(u[k], f);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, finite_amax_bits(f));
+    if (lane == 0) atomicMax(&s_max[run[k]], m);
+  }
+  for (int i = kWindow + warp; i < n_span; i += kWarps) {
+    const int r = run_of(i);
+    if (r < 0) break;   // past the last run
+    float f[8];
+    unpack8<kF16>(__ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), f);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, finite_amax_bits(f));
+    if (lane == 0) atomicMax(&s_max[r], m);
+  }
+  __syncthreads();
+  if (tid < kWindow && ((s_start[tid >> 5] >> (tid & 31)) & 1u)) {
+    const int s = s_slot[tid + 1];
+    float* const sp = p.scale[kv] + size_t(s >> p.bs_log2) * p.Hkv + g;
+    int e = scale_exp(s_max[tid]);
+    if ((s & (bs - 1)) != 0) {
+      const float old = *sp;
+      e = max(e, stored_exp(old));
+      if (pow2f(e) != old) {
+        s_old[tid] = old;
+        s_grown[atomicAdd(&s_n_grown, 1)] = tid;
+      }
+    }
+    s_exp[tid] = e;
+    *sp = pow2f(e);
+  }
+  __syncthreads();
+  const auto put = [&](int i, int r, uint4 v) {
+    float f[8];
+    unpack8<kF16>(v, f);
+    const float inv = pow2f(-s_exp[r]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] *= inv;
+    const int s = s_slot[i + 1];
+    pool[((size_t(s >> p.bs_log2) * p.Hkv + g) * bs + (s & (bs - 1))) * 32 + lane] = to_e4m3x8(f);
+  };
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k)
+    if (run[k] >= 0) put(warp + k * kWarps, run[k], u[k]);
+  for (int i = kWindow + warp; i < n_span; i += kWarps) {
+    const int r = run_of(i);
+    if (r < 0) break;
+    put(i, r, __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane));
+  }
+  for (int j = 0; j < s_n_grown; ++j) {
+    const int r = s_grown[j], s = s_slot[r + 1];
+    rescale_rows(pool + (size_t(s >> p.bs_log2) * p.Hkv + g) * bs * 32, s & (bs - 1), s_old[r],
+                 s_exp[r]);
+  }
+}
+
+// ---------------------------------------------------------------- keep
+constexpr int kMaxKeep = 64;                              // as many as a tree has rows
+constexpr int kKeepPerWarp = kMaxKeep / kWarps;
+constexpr int kMaxRuns = kMaxKeep / 16 + 1;               // blocks that they can touch
+
+struct KeepParams {
+  uint2* pool[2];
+  float* scale[2];
+  const int* tables;
+  const int* kv_lens;
+  const int* cu_rows;
+  const int* keep_idx;
+  const int* cu_keep;
+  int* lens_out;
+  int n_keep, B, Hkv, num_blocks, max_blocks, bs_log2;
+  LaunchCtl ctl;
+};
+
+// One CTA: one sequence and KV head of K or V.  All kept rows are in registers before
+// the first is written (a block's scale may change while later rows of it are due).
+__global__ void __launch_bounds__(kThreads) kv8_keep_kernel(const KeepParams p) {
+  __shared__ int s_idx[kMaxKeep];
+  __shared__ int s_bad;
+  __shared__ uint32_t s_max[kMaxRuns];
+  __shared__ int s_exp[kMaxRuns];
+  __shared__ float s_old;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x, g = blockIdx.y, kv = blockIdx.z;
+  const int bs = 1 << p.bs_log2;
+  const int r = p.cu_rows[b + 1] - p.cu_rows[b];
+  const int L = p.kv_lens[b];
+  const int k0 = p.cu_keep[b], nk = p.cu_keep[b + 1] - k0;
+  const int base = L - r;
+  const int* const table = p.tables + (long long)b * p.max_blocks;
+  const bool ok = r >= 0 && L >= r && nk >= 0 && nk <= r && nk <= kMaxKeep && k0 >= 0 &&
+                  (long long)k0 + nk <= p.n_keep &&
+                  (long long)L <= ((long long)p.max_blocks << p.bs_log2);
+  if (tid == 0) s_bad = ok ? 0 : 1;
+  if (tid < kMaxRuns) s_max[tid] = 0u;
+  __syncthreads();
+  if (ok && tid < nk) {
+    const int i = p.keep_idx[k0 + tid];
+    s_idx[tid] = i;
+    const int before = tid == 0 ? -1 : p.keep_idx[k0 + tid - 1];
+    const bool fine = i >= 0 && i < r && i > before;
+    const int src = fine ? table[(base + i) >> p.bs_log2] : -1;
+    const int dst = fine ? table[(base + tid) >> p.bs_log2] : -1;
+    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) s_bad = 1;
+  }
+  __syncthreads();
+  if (s_bad) {
+    if (tid == 0 && g == 0 && kv == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+    return;
+  }
+  if (tid == 0 && g == 0 && kv == 0 && p.lens_out != nullptr) p.lens_out[b] = base + nk;
+  uint2* const pool = p.pool[kv];
+  float* const scale = p.scale[kv];
+  const auto block_at = [&](int pos) { return size_t(table[pos >> p.bs_log2]) * p.Hkv + g; };
+  const int run0 = base >> p.bs_log2;
+  uint2 q[kKeepPerWarp];
+  float sc[kKeepPerWarp];
+#pragma unroll
+  for (int k = 0; k < kKeepPerWarp; ++k) {
+    const int i = warp + k * kWarps;
+    if (i >= nk) continue;
+    const int pos = base + s_idx[i];
+    const size_t blk = block_at(pos);
+    q[k] = pool[(blk * bs + (pos & (bs - 1))) * 32 + lane];
+    sc[k] = scale[blk];
+  }
+#pragma unroll
+  for (int k = 0; k < kKeepPerWarp; ++k) {
+    const int i = warp + k * kWarps;
+    if (i >= nk) continue;
+    float f[8];
+    from_e4m3x8(q[k], f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] *= sc[k];
+    const uint32_t m = __reduce_max_sync(0xffffffffu, finite_amax_bits(f));
+    if (lane == 0) atomicMax(&s_max[((base + i) >> p.bs_log2) - run0], m);
+  }
+  __syncthreads();   // every kept row and its scale are read
+  const int n_runs = nk == 0 ? 0 : ((base + nk - 1) >> p.bs_log2) - run0 + 1;
+  if (tid < n_runs) {
+    float* const sp = scale + block_at((run0 + tid) << p.bs_log2);
+    int e = scale_exp(s_max[tid]);
+    if (tid == 0 && (base & (bs - 1)) != 0) {
+      s_old = *sp;
+      e = max(e, stored_exp(s_old));
+    }
+    s_exp[tid] = e;
+    *sp = pow2f(e);
+  }
+  __syncthreads();
+  if (nk == 0) return;
+#pragma unroll
+  for (int k = 0; k < kKeepPerWarp; ++k) {
+    const int i = warp + k * kWarps;
+    if (i >= nk) continue;
+    const int pos = base + i;
+    const float inv = pow2f(-s_exp[(pos >> p.bs_log2) - run0]);
+    float f[8];
+    from_e4m3x8(q[k], f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] = f[c] * sc[k] * inv;
+    pool[(block_at(pos) * bs + (pos & (bs - 1))) * 32 + lane] = to_e4m3x8(f);
+  }
+  const int off0 = base & (bs - 1);
+  if (off0 != 0 && pow2f(s_exp[0]) != s_old)
+    rescale_rows(pool + block_at(base) * bs * 32, off0, s_old, s_exp[0]);
+}
+
+int log2_of(int block_size) {
+  int n = 0;
+  while ((1 << n) < block_size) ++n;
+  return n;
+}
+
+int append_impl(bool f16, const void* Knew, const void* Vnew, const int* slots, void* k_pool,
+                void* v_pool, float* k_scale, float* v_scale, int T, int Hkv, int num_blocks,
+                int block_size, gqa_stream_t stream) {
+  if (T < 0) return GQA_ERR_INVALID_ARG;
+  const int st = check_kv8_pool(num_blocks, Hkv, block_size);
+  if (st != GQA_OK) return st;
+  if (Hkv > 65535 || (long long)T * Hkv >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  if (T == 0) return GQA_OK;
+  if (Knew == nullptr || Vnew == nullptr || slots == nullptr || k_pool == nullptr ||
+      v_pool == nullptr || k_scale == nullptr || v_scale == nullptr)
+    return GQA_ERR_INVALID_ARG;
+  if (!aligned_to(Knew, 16) || !aligned_to(Vnew, 16) || !aligned_to(k_pool, 16) ||
+      !aligned_to(v_pool, 16) || !aligned_to(slots, 4) || !aligned_to(k_scale, 4) ||
+      !aligned_to(v_scale, 4))
+    return GQA_ERR_INVALID_ARG;
+  AppendParams p;
+  p.x[0] = static_cast<const uint4*>(Knew);
+  p.x[1] = static_cast<const uint4*>(Vnew);
+  p.pool[0] = static_cast<uint2*>(k_pool);
+  p.pool[1] = static_cast<uint2*>(v_pool);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.slots = slots;
+  p.T = T;
+  p.Hkv = Hkv;
+  p.num_blocks = num_blocks;
+  p.bs_log2 = log2_of(block_size);
+  if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
+  const dim3 grid((T + kWindow - 1) / kWindow, Hkv, 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (f16)
+    kv8_append_kernel<true><<<grid, kThreads, 0, s>>>(p);
+  else
+    kv8_append_kernel<false><<<grid, kThreads, 0, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
+  note_launch(f16 ? "kv8_append_kernel<fp16>" : "kv8_append_kernel<bf16>",
+              (long long)grid.x * grid.y * grid.z, kThreads, 0);
+  return GQA_OK;
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" {
+
+int gqa_kv8_append(const void* Knew, const void* Vnew, const int* slots, void* k_pool, void* v_pool,
+                   float* k_scale, float* v_scale, int T, int Hkv, int num_blocks, int block_size,
+                   gqa_stream_t stream) {
+  return append_impl(false, Knew, Vnew, slots, k_pool, v_pool, k_scale, v_scale, T, Hkv,
+                     num_blocks, block_size, stream);
+}
+int gqa_kv8_append_f16(const void* Knew, const void* Vnew, const int* slots, void* k_pool,
+                       void* v_pool, float* k_scale, float* v_scale, int T, int Hkv,
+                       int num_blocks, int block_size, gqa_stream_t stream) {
+  return append_impl(true, Knew, Vnew, slots, k_pool, v_pool, k_scale, v_scale, T, Hkv, num_blocks,
+                     block_size, stream);
+}
+
+int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                 const int* block_tables, const int* kv_lens, const int* cu_rows,
+                 const int* keep_idx, const int* cu_keep, int* kv_lens_out, int n_keep, int B,
+                 int Hkv, int num_blocks, int block_size, int max_blocks, gqa_stream_t stream) {
+  if (B < 1 || max_blocks < 1 || n_keep < 0) return GQA_ERR_INVALID_ARG;
+  const int st = check_kv8_pool(num_blocks, Hkv, block_size);
+  if (st != GQA_OK) return st;
+  if (Hkv > 65535 || (long long)max_blocks * block_size >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  if (k_pool == nullptr || v_pool == nullptr || k_scale == nullptr || v_scale == nullptr ||
+      block_tables == nullptr || kv_lens == nullptr || cu_rows == nullptr ||
+      (keep_idx == nullptr && n_keep > 0) || cu_keep == nullptr || kv_lens_out == kv_lens)
+    return GQA_ERR_INVALID_ARG;
+  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return GQA_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)k_scale, (const void*)v_scale, (const void*)block_tables,
+                        (const void*)kv_lens, (const void*)cu_rows, (const void*)keep_idx,
+                        (const void*)cu_keep, (const void*)kv_lens_out})
+    if (!aligned_to(q, 4)) return GQA_ERR_INVALID_ARG;
+  KeepParams p;
+  p.pool[0] = static_cast<uint2*>(k_pool);
+  p.pool[1] = static_cast<uint2*>(v_pool);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.tables = block_tables;
+  p.kv_lens = kv_lens;
+  p.cu_rows = cu_rows;
+  p.keep_idx = keep_idx;
+  p.cu_keep = cu_keep;
+  p.lens_out = kv_lens_out;
+  p.n_keep = n_keep;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks;
+  p.bs_log2 = log2_of(block_size);
+  if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
+  const dim3 grid(B, Hkv, 2);
+  kv8_keep_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
+  note_launch("kv8_keep_kernel", (long long)B * Hkv * 2, kThreads, 0);
+  return GQA_OK;
+}
+
+}  // extern "C"

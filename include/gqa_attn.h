@@ -85,7 +85,8 @@ typedef enum {
   GQA_ERR_CUDA = 3,        /* a CUDA call or launch failed                         */
   GQA_ERR_TIMEOUT = 4,     /* device: a bounded wait ran out (kernel returned)     */
   GQA_ERR_WORKSPACE = 5,   /* decode workspace too small                           */
-  GQA_ERR_DEVICE_RANGE = 6 /* device: kv_lens / cu_rows out of range (work skipped) */
+  GQA_ERR_DEVICE_RANGE = 6, /* device: kv_lens / cu_rows out of range (work skipped) */
+  GQA_ERR_NO_BLOCKS = 7    /* device: a sequence's new blocks did not fit the pool    */
 } gqa_status;
 
 /* Static, NUL-terminated description of a status code. */
@@ -413,6 +414,108 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
                         const long long* mask_strides, void* out, float* lse_out, int B, int Hq,
                         int Hkv, int Lq, int Lkv, int causal, int kv_offset, int head_chunking,
                         gqa_stream_t stream);
+
+/*
+ * The paged 8-bit KV cache: half the bytes of a 16-bit cache in blocks that are handed
+ * out as sequences grow, for decode and draft verification.  A step is
+ *   gqa_block_plan -> gqa_kv8_append -> gqa_kv8_decode (-> gqa_kv8_keep after a verify).
+ *
+ * k_pool, v_pool: e4m3 [num_blocks, Hkv, block_size, 256]; block_size 16, 32, 64 or 128.
+ * k_scale, v_scale: fp32 [num_blocks, Hkv]: a row's values are e4m3 * scale.  The writing
+ *   calls store powers of two; gqa_kv8_decode takes any finite scales >= 0.
+ * block_tables: int32 [B, max_blocks]: entry i of sequence b is the pool block that holds
+ *   its keys i*block_size .. (i+1)*block_size - 1.  No block belongs to two sequences that
+ *   one call writes: its contents are unspecified after such a call (no access is out of
+ *   range).  A block that is only read may be shared.
+ * num_blocks * Hkv * block_size < 2^31 and max_blocks * block_size < 2^31
+ * (GQA_ERR_UNSUPPORTED above); the pools themselves may pass 2^32 bytes.
+ *
+ * gqa_block_plan: block tables and slot maps from request lengths, on the device.  After it
+ * sequence b owns exactly ceil((kv_lens[b] + r_b) / block_size) blocks, r_b = cu_rows[b+1] -
+ * cu_rows[b] new rows: a finished request is one with length 0 and no rows, refused drafts
+ * are given back by the next call with the shorter length.
+ *   n_blocks: int32 [B], blocks that b owns (block_tables[b, 0 .. n_blocks[b])); updated.
+ *   free_list: int32 [num_blocks], free_count: int32 [1]: a stack of free blocks, its top
+ *     at free_list[free_count - 1]; updated.
+ *   First the surplus entries are released: the k-th of R in (b, i) order goes to
+ *   free_list[free_count + R - 1 - k], and its table entry becomes -1.  Then the growing
+ *   sequences take theirs from the top, in order of b.  A sequence whose blocks (with those
+ *   of every sequence before it) do not fit takes none, and GQA_ERR_NO_BLOCKS is recorded.
+ *   slots: int32 [T]: block * block_size + row in the block of new row t (T >= cu_rows[B]);
+ *     -1 for the rows of a sequence that was not served, and behind the last sequence.
+ *     May be NULL when T == 0.
+ *   kv_lens_out: int32 [B]: kv_lens[b] + r_b, what gqa_kv8_decode takes after the append
+ *     (kv_lens[b] when b was not served).  May be kv_lens itself.
+ * A sequence that breaks the bounds (a negative length or count, more than max_blocks
+ * blocks, cu_rows that fall or pass T) is not served and keeps its blocks, and
+ * GQA_ERR_DEVICE_RANGE is recorded.  B <= 8192 (GQA_ERR_UNSUPPORTED above).
+ */
+int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block_tables, int* n_blocks,
+                   int* free_list, int* free_count, int* slots, int* kv_lens_out, int B, int T,
+                   int max_blocks, int num_blocks, int block_size, gqa_stream_t stream);
+
+/*
+ * Quantising append.  Knew, Vnew: bf16 (fp16: _f16) [T, Hkv, 256]; slots: int32 [T] as
+ * gqa_block_plan writes them (a row whose slot is -1 is skipped).  Consecutive tokens with
+ * consecutive slots in one block are a run; per run and KV head, K and V apart:
+ *   E    = least e >= -126 with (largest finite |x| of the run) <= 448 * 2^e
+ *   e    = E when the run starts at the block's first row, else max(the stored scale's, E)
+ *   the block's rows before the run are rounded again when its scale grew
+ *   q    = x * 2^-e rounded to e4m3, nearest even; NaN and +-Inf are stored as NaN.
+ * A slot outside the pool, or in the block of the token before it but not right behind it,
+ * is skipped with the run that it starts, and GQA_ERR_DEVICE_RANGE is recorded.
+ */
+int gqa_kv8_append(const void* Knew, const void* Vnew, const int* slots, void* k_pool, void* v_pool,
+                   float* k_scale, float* v_scale, int T, int Hkv, int num_blocks, int block_size,
+                   gqa_stream_t stream);
+int gqa_kv8_append_f16(const void* Knew, const void* Vnew, const int* slots, void* k_pool,
+                       void* v_pool, float* k_scale, float* v_scale, int T, int Hkv,
+                       int num_blocks, int block_size, gqa_stream_t stream);
+
+/*
+ * gqa_kv_keep for the 8-bit cache: the accepted draft rows of each sequence (keep_idx via
+ * cu_keep, strictly increasing draft-row indices, at most 64 per sequence) move to positions
+ * kv_lens[b] - r_b + k.  The result is that of appending the values which the kept rows
+ * stand for behind the first kv_lens[b] - r_b keys, by gqa_kv8_append's rule; rows behind
+ * the last kept one hold no key any more.  n_keep: entries of keep_idx.  kv_lens_out: NULL or int32 [B] (not kv_lens),
+ * receiving kv_lens[b] - r_b + (number kept).  A sequence with an invalid list or table
+ * entry is left untouched and GQA_ERR_DEVICE_RANGE is recorded.
+ */
+int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                 const int* block_tables, const int* kv_lens, const int* cu_rows,
+                 const int* keep_idx, const int* cu_keep, int* kv_lens_out, int n_keep, int B,
+                 int Hkv, int num_blocks, int block_size, int max_blocks, gqa_stream_t stream);
+
+/*
+ * Decode, chain verify (tree_mask NULL) and tree verify over the paged 8-bit cache: as
+ * gqa_attn_decode / gqa_attn_verify_tree with K_j = k_pool row * k_scale and V_j likewise.
+ * Q, G, out: bf16 (fp16: _f16) [T, Hq, 256]; G may be NULL.  kv_lens counts the new rows,
+ * cu_rows may be NULL for one row per sequence (T == B, max_rows == 1; no tree_mask).
+ * max_rows (at most 64 with tree_mask) and max_kv_len bound r_b and kv_lens[b].
+ * T may exceed cu_rows[B] (a padded batch): rows behind the last sequence, and those of a
+ * sequence that breaks the bounds (skipped, GQA_ERR_DEVICE_RANGE recorded), are left as
+ * they were in out and lse_out.  A row that sees no key gives zeros, lse -inf.
+ * A table entry outside the pool reads as keys and values of zero, and
+ * GQA_ERR_DEVICE_RANGE is recorded.  A NaN in the row of a key that a row does not see
+ * (a stale row of a block included) never changes its output; a NaN that it sees
+ * propagates.  A Q row that holds NaN or +-Inf gives NaN.
+ * workspace: gqa_kv8_workspace_size() bytes, 16-byte aligned; calls that may overlap on the
+ * GPU need one each.
+ */
+size_t gqa_kv8_workspace_size(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len);
+int gqa_kv8_decode(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
+                   const float* v_scale, const void* G, const int* block_tables,
+                   const int* kv_lens, const int* cu_rows, const unsigned long long* tree_mask,
+                   void* out, float* lse_out, int B, int T, int Hq, int Hkv, int num_blocks,
+                   int block_size, int max_blocks, int max_rows, int max_kv_len, void* workspace,
+                   size_t workspace_bytes, gqa_stream_t stream);
+int gqa_kv8_decode_f16(const void* Q, const void* k_pool, const void* v_pool,
+                       const float* k_scale, const float* v_scale, const void* G,
+                       const int* block_tables, const int* kv_lens, const int* cu_rows,
+                       const unsigned long long* tree_mask, void* out, float* lse_out, int B,
+                       int T, int Hq, int Hkv, int num_blocks, int block_size, int max_blocks,
+                       int max_rows, int max_kv_len, void* workspace, size_t workspace_bytes,
+                       gqa_stream_t stream);
 
 #ifdef __cplusplus
 }

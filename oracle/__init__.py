@@ -12,3 +12,7 @@ from .attention import (  # noqa: F401
     attend_rows, prefill, decode, lse_merge, head_chunk_plan, decode_head_chunked,
     tree_visible_keys, decode_tree, chain_masks, kv_append, kv_keep, masked_rows, sdpa_masked,
 )
+from .kv8 import (  # noqa: F401
+    E4M3, E4M3_MAX, e4m3_encode, scale_exponent, block_plan, kv8_append, kv8_keep,
+    kv8_contiguous,
+)
