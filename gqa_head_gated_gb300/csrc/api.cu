@@ -174,6 +174,7 @@ int decode_check_args(int B, int T, int Hq, int Hkv, int Lcap, int max_rows, int
   return check_decode_args(B, T, Hq, Hkv, Lcap, max_rows, max_kv_len, has_cu_rows);
 }
 bool make_launch_ctl(LaunchCtl* ctl) { return make_ctl(ctl); }
+int device_sm_count() { return sm_count(); }
 
 namespace {
 

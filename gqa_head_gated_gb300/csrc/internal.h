@@ -102,6 +102,8 @@ int decode_check_args(int B, int T, int Hq, int Hkv, int Lcap, int max_rows, int
                       bool has_cu_rows);
 // The launch control block (status word, wait bound) for the current device.
 bool make_launch_ctl(LaunchCtl* ctl);
+// SMs of the current device (152 where there is none).
+int device_sm_count();
 int decode_bf16_with_workspace(const void* Q, const void* Kcache, const void* Vcache,
                                const void* G, const int* kv_lens, const int* cu_rows, void* out,
                                float* lse_out, int B, int T, int Hq, int Hkv, int Lcap,

@@ -1,0 +1,822 @@
+// The attention of decode / verify rows over the paged 8-bit cache, written as partial
+// results (O / l, m + ln l) for the merge in kv8_decode.cu.
+//
+//   s_rj = (q_r . k_j) * ks_j / 16     p_rj = exp(s_rj - m_r)     l_r = sum_j p_rj
+//   O_r  = sum_j p_rj * vs_j * v_j     (ks_j, vs_j: the scales of key j's block and head)
+//
+// What bounds it: HBM.  A key costs 512 bytes per KV head; the rows of a decode or draft
+// step that share it are few.  So the cache's bytes go from TMA straight into the tensor
+// core, never through registers: both products run as tcgen05 kind::f8f6f4 with the
+// cache as operand A and the rows, few, along N:
+//   S^T [128 keys, rows]   = K [128 keys, 256] . Q^T      A K-major as it lies in the block
+//   O^T [2 x 128 dims, rows] += V^T [dims, 128 keys] . P^T    A MN-major, the same bytes
+// With N this small a product costs reading A (32 KB at 128 bytes a clock per operand),
+// whatever N is, and that pays for exactness: Q and P, which have more bits than e4m3,
+// enter as sums of e4m3 terms in columns of their own:
+//   q = 2^e (t0 + t1 / 16 (+ t2 / 256)): 2 terms hold a bf16's 8 bits, 3 an fp16's 11
+//     (each step of 16 is the 4 bits that e4m3 rounds to; elements below 2^-18 of the
+//     row's largest lose bits, an absolute error of 2^-23 of that, 2^-27 in fp16);
+//   p = t0 + t1 / 32 + t2 / 1024, p <= 256: relative error 2^-12, and what is dropped is
+//     below 2^-20, 2^-25 of the row's largest p.
+//
+// The softmax thread of key j holds S^T's lane j: its block's scales are two scalars of
+// the thread, the visible-key test is one comparison per row, and block sizes cost
+// nothing.  Two references per row, the same in all threads: p uses ref_r, for s + log2 vs
+// (the probabilities as the product sees them, so a block of tiny values next to one of
+// large ones loses no bits), l uses ml_r, for s.  They move only when a key passes them
+// by more than 2^8 (2^64), which one barrier per tile detects; then the warps exchange
+// maxima and O is rescaled in tensor memory.
+//
+// Roles (192 threads): warp 0 copies (TMA, a block per box; scales by cp.async), warp 1
+// issues the products, warps 2..5 are the softmax and epilogue.  One CTA per SM; the key
+// tiles of all (sequence, KV head, row block) segments are laid end to end and cut into
+// equal contiguous shares, so ragged lengths cost no tail; the copies run ahead across
+// segments.  A share that crosses segments writes one part per piece.
+//
+// A key that a row does not see has p = 0 by selection.  V rows past the last visible key
+// of a tile are zeroed in shared memory, and NaN codes of keys that only some rows see are
+// taken out before the product and put back for the rows that see them.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdio>
+
+#include "kv8_attn.h"
+#include "kv8_common.cuh"
+#include "ptx_sm100.cuh"
+#include "tc_common.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kTile = 128;                       // keys per tile
+constexpr int kHalfBytes = kTile * 128;          // 128 keys x 128 dims of K or V
+constexpr int kSlotBytes = 2 * kHalfBytes;
+constexpr int kAttnThreads = 192;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kPTerms = 3;
+constexpr int kScaleRing = 8;      // tiles whose scales are held: see the producer
+constexpr int kMaxTileBlocks = kTile / 16;
+constexpr float kSlack = 8.f;      // p <= 2^8
+constexpr float kTop = 5.f;        // a moved reference leaves the row's largest p at 2^5
+constexpr float kLSlack = 64.f;    // l's terms stay below 2^64
+constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
+
+template <int MB, bool kF16>
+struct Cfg {
+  static constexpr int kQTerms = kF16 ? 3 : 2;
+  static constexpr int kNS = MB * kQTerms;       // columns of S^T
+  static constexpr int kNO = MB * kPTerms;       // columns of each half of O^T
+  static constexpr int kKS = 3;                  // K slots
+  static constexpr int kVS = MB == 16 ? 3 : 2;   // V slots
+  static constexpr uint32_t kStep = MB * 4;      // tensor-memory columns of each of
+  static constexpr uint32_t kTmS = 0;            // the two S buffers
+  static constexpr uint32_t kTmO = 2 * kStep;    // and the two halves of O
+  static constexpr uint32_t kCols = 4 * kStep;
+  static_assert(kNS <= int(kStep) && kNO <= int(kStep), "S and O fit their columns");
+  static constexpr uint32_t kIdescS = ptx::idesc_f32acc(128, kNS, 0, 0, 0);
+  static constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, kNO, 1, 1, 0);
+};
+
+template <int MB, bool kF16>
+struct __align__(1024) AttnSmem {
+  using C = Cfg<MB, kF16>;
+  uint8_t q[2][C::kNS * 128];              // [half of D][column][128 bytes, swizzled]
+  uint8_t p[2][C::kNO * kTile];            // [buffer][16 columns][key][16 bytes]
+  uint8_t k[C::kKS][kSlotBytes];
+  uint8_t v[C::kVS][kSlotBytes];
+  float scale[kScaleRing][2][kMaxTileBlocks];
+  uint64_t k_full[C::kKS], k_empty[C::kKS], v_full[C::kVS], v_empty[C::kVS];
+  uint64_t sc_full[kScaleRing];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, o_full, drain;
+  unsigned long long hit;                  // NaN V rows taken out: bit of key pr_lo + i
+  unsigned long long mask[MB];
+  long long base[kKv8Seqs + 1];            // first tile of each sequence's segments
+  int lim[MB];
+  float fac[MB];
+  alignas(16) float red[2][MB][4];         // read as float4
+  uint32_t tmem_base;
+  int abort, zero;
+};
+
+struct Piece {
+  int b, g, rb, s;        // sequence, KV head, row block, part
+  int rows, t0, kv_len;   // of the sequence
+  int k_lo, k_hi;         // keys of the piece that some row of the block sees
+  int n_tiles;
+  long long next;         // position after the piece
+  bool last;              // ends its segment
+};
+
+__device__ __forceinline__ bool seq_of(const Kv8AttnArgs& p, int b, int& t0, int& rows, int& kv) {
+  kv = p.kv_lens[b];
+  t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
+  rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
+  return rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
+         kv <= p.max_kv_len;
+}
+
+// The piece of this CTA's share that starts at `pos` (the share ends at `end`).
+template <int MB>
+__device__ __forceinline__ Piece piece_at(const Kv8AttnArgs& p, const long long* base, long long pos,
+                                          long long end, long long W, long long n_cta) {
+  Piece x;
+  int lo = 0, hi = p.B - 1;   // last sequence that starts at or before pos
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (base[mid] <= pos) lo = mid; else hi = mid - 1;
+  }
+  x.b = lo;
+  seq_of(p, lo, x.t0, x.rows, x.kv_len);
+  const int n_rb = (x.rows * p.gqa + MB - 1) / MB;
+  const long long len = (x.kv_len + kTile - 1) / kTile;
+  const long long seg = (pos - base[lo]) / len;
+  x.g = int(seg / n_rb);
+  x.rb = int(seg - (long long)x.g * n_rb);
+  const long long start = base[lo] + seg * len, stop = start + len;
+  x.next = min(end, stop);
+  x.last = x.next == stop;
+  // the piece's part: this CTA's place among those that share the segment
+  x.s = int((long long)blockIdx.x - (((start + 1) * n_cta + W - 1) / W - 1));
+  x.k_lo = int(pos - start) * kTile;
+  int n_hi = x.kv_len;        // a tree row may see up to the last key
+  if (p.tree_mask == nullptr) {
+    const int last_row = min(x.rows * p.gqa - 1, x.rb * MB + MB - 1) / p.gqa;
+    n_hi = x.kv_len - x.rows + last_row + 1;
+  }
+  x.k_hi = min(int(min((x.next - start) * kTile, (long long)n_hi)), n_hi);
+  x.n_tiles = x.k_hi > x.k_lo ? (x.k_hi - x.k_lo + kTile - 1) / kTile : 0;
+  return x;
+}
+
+__device__ __forceinline__ float log2_scale(float s) {
+  const uint32_t b = __float_as_uint(s);
+  if ((b & 0x7FFFFFu) == 0u && b - 0x00800000u < 0x7F000000u) return float(int(b >> 23) - 127);
+  return __log2f(s);   // 0 gives -inf
+}
+
+// Bytes of a 16-byte chunk that are e4m3 NaN become 0; returns whether there was one.
+__device__ __forceinline__ bool clear_nan8(uint4& u) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t any = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    w[i] &= ~m;
+    any |= m;
+  }
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+  return any != 0u;
+}
+
+// The V row of one key of a landed tile: zeroed, or its NaN codes taken out.
+__device__ __noinline__ bool clean_v_row(uint8_t* slot, int row, bool zero) {
+  bool hit = false;
+  for (int c = 0; c < 16; ++c) {
+    uint4* const a = reinterpret_cast<uint4*>(slot + (c >> 3) * kHalfBytes + row * 128 +
+                                              (((c & 7) ^ (row & 7)) << 4));
+    if (zero) {
+      *a = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      uint4 u = *a;
+      if (clear_nan8(u)) {
+        *a = u;
+        hit = true;
+      }
+    }
+  }
+  return hit;
+}
+
+// Columns [col, col + 16) of one half of O^T times f, in tensor memory (whole warp).
+__device__ __forceinline__ void rescale_cols(uint32_t ta, const float* f) {
+  uint32_t o[16];
+  ptx::tmem_ld16_wait(ta, o);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
+  ptx::tmem_st16_wait(ta, o);
+}
+
+// Two values to e4m3, and what they leave: (lo, hi) becomes (x - e4m3(x)) * step.
+__device__ __forceinline__ uint32_t take_term(float& lo, float& hi, float step) {
+  const uint32_t t = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+  const float2 f = from_e4m3x2(t);
+  lo = (lo - f.x) * step;
+  hi = (hi - f.y) * step;
+  return t;
+}
+
+template <int MB, bool kF16>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const Kv8AttnArgs p) {
+  using C = Cfg<MB, kF16>;
+  extern __shared__ uint8_t smem_raw[];
+  AttnSmem<MB, kF16>& sm = *reinterpret_cast<AttnSmem<MB, kF16>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t tmo = p.ctl.timeout_ns;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- the schedule: tiles before each sequence, and this CTA's share of them
+  int most = 0;   // tiles of the longest sequence
+  for (int b = tid; b < p.B; b += kAttnThreads) {
+    int t0, rows, kv;
+    const bool ok = seq_of(p, b, t0, rows, kv);
+    const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
+    sm.base[b + 1] = (long long)tiles * p.Hkv * ((rows * p.gqa + MB - 1) / MB);
+    most = max(most, tiles);
+    if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+  }
+  if (tid == 0) {
+    sm.base[0] = 0;
+    sm.red[0][0][0] = 0.f;
+    for (int i = 0; i < C::kKS; ++i) {
+      ptx::mbar_init(&sm.k_full[i], 1);
+      ptx::mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kVS; ++i) {
+      ptx::mbar_init(&sm.v_full[i], 1);
+      ptx::mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(&sm.sc_full[i], 32);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.s_full[i], 1);
+      ptx::mbar_init(&sm.p_full[i], kSoftmaxThreads / 32);
+      ptx::mbar_init(&sm.pv_done[i], 1);
+    }
+    ptx::mbar_init(&sm.q_full, kSoftmaxThreads / 32);
+    ptx::mbar_init(&sm.o_full, 1);
+    ptx::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    sm.zero = 0;
+    sm.hit = 0ull;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sm.tmem_base, C::kCols);
+    ptx::tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 0) {   // inclusive sums over the sequences, 32 at a time
+    long long run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      long long v = b0 + lane < p.B ? sm.base[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (b0 + lane < p.B) sm.base[b0 + lane + 1] = run + v;
+      run += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  atomicMax(reinterpret_cast<int*>(&sm.red[0][0][0]), most);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  most = *reinterpret_cast<const int*>(&sm.red[0][0][0]);
+  const long long W = sm.base[p.B];
+  // Shares so long that no segment needs more than `parts` parts, and of one tile at least.
+  long long n_cta = min((long long)gridDim.x, W);
+  if (most > p.parts) n_cta = min(n_cta, max(1LL, W * (p.parts - 2) / most));
+  const bool works = (long long)blockIdx.x < n_cta;
+  const long long pos0 = works ? W * blockIdx.x / n_cta : 0;
+  const long long end = works ? W * (blockIdx.x + 1) / n_cta : 0;
+  __syncthreads();   // red is read before the softmax warps write it
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    // A tile's scales live in a ring of kScaleRing tiles without a release: tile J + 8 is
+    // copied only once S of tile J + 8 - kKS >= J + 5 was issued, which waits for the
+    // softmax of tile J + 3, so tile J's scales have been read.
+    static_assert(kScaleRing >= C::kKS + 3, "scale ring");
+    const int bs = 1 << p.bs_log2, per_tile = kTile >> p.bs_log2;
+    long long J = 0;
+    bool ok = true;
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmK);
+      ptx::prefetch_tmap(&tmV);
+    }
+    for (long long pos = pos0; ok && pos < end;) {
+      const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
+      pos = x.next;
+      const int* const table = p.tables + (long long)x.b * p.max_blocks;
+      int at = x.k_lo + lane * bs;   // first key of this lane's block
+      int blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
+      for (int j = 0; ok && j < x.n_tiles; ++j, ++J) {
+        const bool mine = lane < per_tile && at < x.k_hi;
+        const bool in = blk >= 0 && blk < p.num_blocks;
+        if (mine && !in) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+        // a block outside the pool: past the map's last row, which copies zeros
+        const int row = in ? (blk * p.Hkv + x.g) << p.bs_log2 : (p.num_blocks * p.Hkv) << p.bs_log2;
+        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, mine))) * uint32_t(bs) * 256u;
+        const int cur = blk;
+        at += kTile;
+        blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
+        const int ks = int(J % C::kKS), vs = int(J % C::kVS);
+        int go = 1;
+        if (lane == 0) {
+          if (J >= C::kKS)
+            go = ptx::mbar_wait(&sm.k_empty[ks], uint32_t(J / C::kKS - 1) & 1u, tmo, &sm.abort);
+          if (go) ptx::mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+        }
+        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+        if (!ok) break;
+        if (mine) {
+          uint8_t* const d = sm.k[ks] + lane * bs * 128;
+          ptx::tma_load_2d(d, &tmK, &sm.k_full[ks], 0, row);
+          ptx::tma_load_2d(d + kHalfBytes, &tmK, &sm.k_full[ks], 128, row);
+          const size_t sc = size_t(in ? cur : 0) * p.Hkv + x.g;
+          ptx::cp_async4(ptx::smem_addr(&sm.scale[J % kScaleRing][0][lane]), p.k_scale + sc, in ? 4u : 0u);
+          ptx::cp_async4(ptx::smem_addr(&sm.scale[J % kScaleRing][1][lane]), p.v_scale + sc, in ? 4u : 0u);
+        }
+        ptx::cp_async_mbar_arrive(&sm.sc_full[J % kScaleRing]);
+        if (lane == 0) {
+          if (J >= C::kVS)
+            go = ptx::mbar_wait(&sm.v_empty[vs], uint32_t(J / C::kVS - 1) & 1u, tmo, &sm.abort);
+          if (go) ptx::mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+        }
+        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+        if (!ok) {
+          // K of this tile is on its way: it must land before the CTA ends
+          if (lane == 0) ptx::mbar_wait(&sm.k_full[ks], uint32_t(J / C::kKS) & 1u, tmo, &sm.zero);
+          break;
+        }
+        if (mine) {
+          uint8_t* const d = sm.v[vs] + lane * bs * 128;
+          ptx::tma_load_2d(d, &tmV, &sm.v_full[vs], 0, row);
+          ptx::tma_load_2d(d + kHalfBytes, &tmV, &sm.v_full[vs], 128, row);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      sm.abort = 1;
+      record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+    }
+    ptx::cp_async_wait_all();
+    if (lane == 0) {   // every copy has landed before the CTA ends
+      for (long long c = max(0LL, J - C::kKS); c < J; ++c)
+        ptx::mbar_wait(&sm.k_full[c % C::kKS], uint32_t(c / C::kKS) & 1u, tmo, &sm.zero);
+      for (long long c = max(0LL, J - C::kVS); c < J; ++c)
+        ptx::mbar_wait(&sm.v_full[c % C::kVS], uint32_t(c / C::kVS) & 1u, tmo, &sm.zero);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t qa = ptx::smem_addr(sm.q), pa = ptx::smem_addr(sm.p);
+      long long J = 0;
+      bool ok = true;
+      const auto issue_s = [&](long long n) -> bool {
+        const int ks = int(n % C::kKS);
+        if (!ptx::mbar_wait(&sm.k_full[ks], uint32_t(n / C::kKS) & 1u, tmo, &sm.abort)) return false;
+        ptx::tc_fence_after();
+        const uint32_t ka = ptx::smem_addr(sm.k[ks]);
+        const uint32_t d = tmem + C::kTmS + uint32_t(n & 1) * C::kStep;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_ss_f8(
+              d, ptx::sdesc_sw128(ka + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
+              ptx::sdesc_sw128(qa + (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32, 16, 1024),
+              C::kIdescS, kk > 0);
+        ptx::tc_commit(&sm.s_full[n & 1]);
+        ptx::tc_commit(&sm.k_empty[ks]);
+        return true;
+      };
+      const auto issue_pv = [&](long long n, bool first) -> bool {
+        const int vs = int(n % C::kVS), buf = int(n & 1);
+        if (!ptx::mbar_wait(&sm.p_full[buf], uint32_t(n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!ptx::mbar_wait(&sm.v_full[vs], uint32_t(n / C::kVS) & 1u, tmo, &sm.abort)) return false;
+        ptx::tc_fence_after();
+        const uint32_t va = ptx::smem_addr(sm.v[vs]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_ss_f8(tmem + C::kTmO + h * C::kStep,
+                           ptx::sdesc_sw128(va + h * kHalfBytes + kk * 4096, kHalfBytes, 1024),
+                           ptx::sdesc_plain(pa + buf * (C::kNO * kTile) + kk * 512, 128, 2048),
+                           C::kIdescO, !first || kk > 0);
+        ptx::tc_commit(&sm.pv_done[buf]);
+        ptx::tc_commit(&sm.v_empty[vs]);
+        return true;
+      };
+      uint32_t pc = 0;   // pieces with tiles so far
+      for (long long pos = pos0; ok && pos < end;) {
+        const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
+        pos = x.next;
+        if (x.n_tiles == 0) continue;
+        ok = ptx::mbar_wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        ok = issue_s(J);
+        for (int j = 1; ok && j < x.n_tiles; ++j) {
+          ok = issue_s(J + j);
+          if (ok) ok = issue_pv(J + j - 1, j == 1);
+        }
+        if (ok) ok = issue_pv(J + x.n_tiles - 1, x.n_tiles == 1);
+        if (ok) ptx::tc_commit(&sm.o_full);
+        J += x.n_tiles;
+        ++pc;
+      }
+      if (!ok) {
+        sm.abort = 1;
+        record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+      }
+      // every product issued has to end before tensor memory is given back
+      ptx::tc_commit(&sm.drain);
+      ptx::mbar_wait(&sm.drain, 0, tmo, &sm.zero);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, epilogue
+    const int qd = warp & 3;                   // tensor-memory lanes 32 qd .. 32 qd + 31
+    const int key_in = qd * 32 + lane;         // this thread's key of a tile
+    const int st = tid - 64;                   // 0 .. 127
+    const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
+    const bool tree = p.tree_mask != nullptr;
+    const auto bar = [] { ptx::named_bar_sync(1, kSoftmaxThreads); };
+    long long J = 0;
+    uint32_t pc = 0;
+    bool ok = true;      // this thread's waits; agreed on at barriers before anyone leaves
+    bool stop = false;   // the same in all softmax threads
+    for (long long pos = pos0; !stop && pos < end;) {
+      const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
+      pos = x.next;
+      const int P = x.rows * p.gqa, p0 = x.rb * MB, n_rows = min(MB, P - p0);
+      const int base = x.kv_len - x.rows;
+      const size_t part0 = size_t(x.s) * size_t(p.T) * p.Hq;
+      const auto out_row = [&](int r) {
+        const int pp = p0 + r;
+        return size_t(x.t0 + pp / p.gqa) * p.Hq + size_t(x.g) * p.gqa + pp % p.gqa;
+      };
+      if (x.s < 0 || x.s >= p.parts) {   // cannot happen with shares as cut above
+        if (st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+        if (x.n_tiles == 0) continue;
+      }
+      const bool fits = x.s >= 0 && x.s < p.parts;
+      if (x.last && st == 0 && fits)
+        p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
+      if (x.n_tiles == 0) {   // no row of the block sees a key of the piece
+        if (st < n_rows) p.lse_parts[part0 + out_row(st)] = -INFINITY;
+        continue;
+      }
+      // keys from pr_lo on are seen by some rows of the block only
+      const int pr_lo = max(x.k_lo, tree ? base : base + p0 / p.gqa + 1);
+
+      // ---- Q's terms and the rows' limits (the last piece's products are done)
+      bar();
+      if (st < MB) {
+        int lim = 0;
+        unsigned long long m = 0ull;
+        if (st < n_rows) {
+          const int i = (p0 + st) / p.gqa;
+          lim = tree ? x.kv_len : base + i + 1;
+          if (tree) m = p.tree_mask[x.t0 + i];
+        }
+        sm.lim[st] = lim;
+        sm.mask[st] = m;
+      }
+      if (st == 0) sm.hit = 0ull;
+      {
+        constexpr int kPer = MB / 4;     // rows of each warp
+        uint4 u[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = qd + i * 4;
+          u[i] = r < n_rows ? __ldg(p.q + out_row(r) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int r = qd + i * 4;
+          float f[8];
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 a = unpack_elem2<kF16>(w[c]);
+            f[2 * c] = a.x;
+            f[2 * c + 1] = a.y;
+          }
+          const int e = scale_exp(__reduce_max_sync(0xffffffffu, finite_amax_bits(f)));
+          if (lane == 0) sm.fac[r] = pow2f(e) * kScaleLog2;
+          const float inv = pow2f(-e);
+          // an infinite element makes its row's scores NaN, as in the formula
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
+#pragma unroll
+          for (int t = 0; t < C::kQTerms; ++t) {
+            const int n = t * MB + r;
+            uint2 o;
+            o.x = take_term(f[0], f[1], 16.f);
+            o.x |= take_term(f[2], f[3], 16.f) << 16;
+            o.y = take_term(f[4], f[5], 16.f);
+            o.y |= take_term(f[6], f[7], 16.f) << 16;
+            *reinterpret_cast<uint2*>(sm.q[lane >> 4] + n * 128 +
+                                      ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8) = o;
+          }
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.q_full);
+      bar();   // limits and factors are written
+
+      float ref[MB], ml[MB], l[MB];
+#pragma unroll
+      for (int r = 0; r < MB; ++r) {
+        ref[r] = kNone;
+        ml[r] = kNone;
+        l[r] = 0.f;
+      }
+      for (int j = 0; j < x.n_tiles; ++j, ++J) {
+        const int buf = int(J & 1);
+        const int key = x.k_lo + j * kTile + key_in;
+        const int tile_end = x.k_lo + (j + 1) * kTile;
+        float s[MB];
+        float lv = 0.f;
+        bool need = false;
+        ok = ok && ptx::mbar_wait(&sm.s_full[buf], uint32_t(J >> 1) & 1u, tmo, &sm.abort) &&
+             ptx::mbar_wait(&sm.sc_full[J % kScaleRing], uint32_t(J / kScaleRing) & 1u, tmo, &sm.abort);
+        ok = warp_all(ok);
+        if (ok) {
+          ptx::tc_fence_after();
+          float sk = sm.scale[J % kScaleRing][0][key_in >> p.bs_log2];
+          const float sv = sm.scale[J % kScaleRing][1][key_in >> p.bs_log2];
+          if (key >= x.k_hi) {
+            sk = 0.f;
+          } else {
+            lv = log2_scale(sv);
+          }
+          const uint32_t sa = trow + C::kTmS + uint32_t(buf) * C::kStep;
+          if constexpr (MB == 16) {
+            uint32_t a[32];
+            ptx::tmem_ld32_wait(sa, a);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              s[r] = fmaf(__uint_as_float(a[16 + r]), 0.0625f, __uint_as_float(a[r]));
+            if constexpr (kF16) {
+              uint32_t c[16];
+              ptx::tmem_ld16_wait(sa + 32, c);
+#pragma unroll
+              for (int r = 0; r < 16; ++r) s[r] = fmaf(__uint_as_float(c[r]), 0.00390625f, s[r]);
+            }
+          } else {
+            uint32_t a[64];
+            ptx::tmem_ld64_wait(sa, a);
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+              s[r] = fmaf(__uint_as_float(a[32 + r]), 0.0625f, __uint_as_float(a[r]));
+            if constexpr (kF16) {
+              uint32_t c[32];
+              ptx::tmem_ld32_wait(sa + 64, c);
+#pragma unroll
+              for (int r = 0; r < 32; ++r) s[r] = fmaf(__uint_as_float(c[r]), 0.00390625f, s[r]);
+            }
+          }
+          const bool part_seen = tile_end > pr_lo || tile_end > x.k_hi;
+#pragma unroll
+          for (int r0 = 0; r0 < MB; r0 += 4) {
+            if (r0 >= n_rows) break;
+#pragma unroll
+            for (int r = r0; r < r0 + 4; ++r) {
+              float v = s[r] * sm.fac[r] * sk;
+              if (part_seen) {
+                const bool vis = key < min(sm.lim[r], x.k_hi) &&
+                                 (!tree || key < base || ((sm.mask[r] >> (key - base)) & 1ull));
+                v = vis ? v : -INFINITY;
+              }
+              s[r] = v;
+              need = need || v + lv > ref[r] + kSlack || v > ml[r] + kLSlack;
+            }
+          }
+        }
+        // ---- does a reference have to move (or has a wait run out)?
+        if (ptx::named_bar_or(1, kSoftmaxThreads, need || !ok)) {
+          if (ptx::named_bar_or(1, kSoftmaxThreads, !ok)) {
+            stop = true;
+            break;
+          }
+#pragma unroll
+          for (int r0 = 0; r0 < MB; r0 += 4) {
+            if (r0 >= n_rows) break;
+#pragma unroll
+            for (int r = r0; r < r0 + 4; ++r) {
+              const float a = ptx::warp_max_f32(s[r] + lv), c = ptx::warp_max_f32(s[r]);
+              if (lane == r) {
+                sm.red[0][r][qd] = a;
+                sm.red[1][r][qd] = c;
+              }
+            }
+          }
+          bar();
+          bool move = false;
+          float alpha[MB];
+#pragma unroll
+          for (int r = 0; r < MB; ++r) alpha[r] = 1.f;
+#pragma unroll
+          for (int r0 = 0; r0 < MB; r0 += 4) {
+            if (r0 >= n_rows) break;
+#pragma unroll
+            for (int r = r0; r < r0 + 4; ++r) {
+              const float4 a = *reinterpret_cast<const float4*>(sm.red[0][r]);
+              const float4 c = *reinterpret_cast<const float4*>(sm.red[1][r]);
+              const float ma = fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w));
+              const float mc = fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w));
+              if (ma > ref[r] + kSlack) {
+                alpha[r] = ex2(ref[r] - (ma - kTop));
+                ref[r] = ma - kTop;
+                move = true;
+              }
+              if (mc > ml[r] + kLSlack) {
+                l[r] *= ex2(ml[r] - mc);
+                ml[r] = mc;
+              }
+            }
+          }
+          if (move && j > 0) {   // the same in all threads: references and maxima are
+            ok = warp_all(ptx::mbar_wait(&sm.pv_done[buf ^ 1], uint32_t((J - 1) >> 1) & 1u, tmo,
+                                         &sm.abort));
+            if (ok) {
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int g16 = 0; g16 < MB / 16; ++g16)
+#pragma unroll 1
+                for (int c = 0; c < 2 * kPTerms; ++c)
+                  rescale_cols(trow + C::kTmO + (c / kPTerms) * C::kStep + (c % kPTerms) * MB +
+                                   g16 * 16,
+                               alpha + g16 * 16);
+            }
+          }
+        }
+        // ---- P's terms (PV of tile J - 2 has read this buffer)
+        if (J >= 2)
+          ok = ok && ptx::mbar_wait(&sm.pv_done[buf], uint32_t((J >> 1) - 1) & 1u, tmo, &sm.abort);
+        const bool tail = tile_end > x.k_hi, partly = tile_end > pr_lo;
+        if (tail || partly) {
+          ok = ok && ptx::mbar_wait(&sm.v_full[J % C::kVS], uint32_t(J / C::kVS) & 1u, tmo, &sm.abort);
+          if (ok && (key >= x.k_hi || key >= pr_lo) &&
+              clean_v_row(sm.v[J % C::kVS], key_in, key >= x.k_hi))
+            atomicOr(&sm.hit, 1ull << (key - pr_lo));
+        }
+        ok = warp_all(ok);
+        if (ok) {
+#pragma unroll
+          for (int g16 = 0; g16 < MB / 16; ++g16) {
+            uint32_t w[kPTerms][4];
+#pragma unroll
+            for (int t = 0; t < kPTerms; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[t][i] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = g16 * 16 + 4 * i;
+              if (r >= n_rows) break;
+              float e[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                l[r + c] += ex2(s[r + c] - ml[r + c]);
+                e[c] = ex2(s[r + c] + lv - ref[r + c]);
+              }
+#pragma unroll
+              for (int t = 0; t < kPTerms; ++t)
+                w[t][i] = take_term(e[0], e[1], 32.f) | (take_term(e[2], e[3], 32.f) << 16);
+            }
+#pragma unroll
+            for (int t = 0; t < kPTerms; ++t)
+              *reinterpret_cast<uint4*>(sm.p[buf] + (t * (MB / 16) + g16) * (kTile * 16) + key_in * 16) =
+                  make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.p_full[buf]);
+        }
+      }
+      // ---- the piece's sums and parts
+      if (!stop) {
+        ok = ok && ptx::mbar_wait(&sm.o_full, pc & 1u, tmo, &sm.abort);
+        ok = warp_all(ok);
+#pragma unroll
+        for (int r = 0; r < MB; ++r) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+          if (lane == r) sm.red[0][r][qd] = l[r];
+        }
+        stop = ptx::named_bar_or(1, kSoftmaxThreads, !ok);
+      }
+      if (stop) break;
+      ++pc;
+      ptx::tc_fence_after();
+      const unsigned long long hits = sm.hit;
+#pragma unroll
+      for (int g16 = 0; g16 < MB / 16; ++g16) {
+        float inv[16], ex[16];
+        bool some[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = g16 * 16 + i;
+          const float4 a = *reinterpret_cast<const float4*>(sm.red[0][r]);
+          const float L = (a.x + a.y) + (a.z + a.w);
+          some[i] = fits && r < n_rows && L != 0.f;
+          inv[i] = 1.f / L;
+          ex[i] = ex2(0.5f * (ref[r] - ml[r]));
+          if (fits && st == r && r < n_rows)
+            p.lse_parts[part0 + out_row(r)] = L == 0.f ? -INFINITY : (ml[r] + __log2f(L)) * kLn2;
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[16], b[16], c[16];
+          const uint32_t ta = trow + C::kTmO + h * C::kStep + g16 * 16;
+          ptx::tmem_ld16_wait(ta, a);
+          ptx::tmem_ld16_wait(ta + MB, b);
+          ptx::tmem_ld16_wait(ta + 2 * MB, c);
+          const int dim = h * 128 + key_in;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (!some[i]) continue;
+            const int r = g16 * 16 + i;
+            float o = fmaf(__uint_as_float(c[i]), 1.f / 1024.f,
+                           fmaf(__uint_as_float(b[i]), 1.f / 32.f, __uint_as_float(a[i])));
+            o = o * inv[i] * ex[i] * ex[i];
+            for (unsigned long long m = hits; m != 0ull; m &= m - 1ull) {
+              const int kk = pr_lo + __ffsll(static_cast<long long>(m)) - 1;
+              if (kk >= sm.lim[r] || (tree && kk >= base && !((sm.mask[r] >> (kk - base)) & 1ull)))
+                continue;
+              const int blk = __ldg(p.tables + (long long)x.b * p.max_blocks + (kk >> p.bs_log2));
+              if (blk < 0 || blk >= p.num_blocks) continue;
+              const size_t vrow = ((size_t(blk) * p.Hkv + x.g) << p.bs_log2) + (kk & ((1 << p.bs_log2) - 1));
+              if ((p.v_pool[vrow * 256 + dim] & 0x7Fu) == 0x7Fu) o = __int_as_float(0x7FC00000);
+            }
+            p.o_parts[(part0 + out_row(r)) * 256 + dim] = o;
+          }
+        }
+      }
+      ptx::tc_fence_before();
+    }
+    if (stop && st == 0) {
+      sm.abort = 1;
+      record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) ptx::tmem_dealloc(tmem, C::kCols);
+}
+
+bool encode_pool(EncodeTiledFn fn, CUtensorMap* map, const void* pool, const Kv8AttnArgs& a) {
+  const cuuint64_t dims[2] = {256, cuuint64_t(a.num_blocks) * cuuint64_t(a.Hkv) << a.bs_log2};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {128, cuuint32_t(1) << a.bs_log2};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MB, bool kF16>
+cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                     long long grid, cudaStream_t stream) {
+  const size_t smem = sizeof(AttnSmem<MB, kF16>) + 1024;
+  static_assert(sizeof(AttnSmem<MB, kF16>) + 1024 <= 227 * 1024, "one CTA per SM");
+  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<MB, kF16>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  kv8_attn_kernel<MB, kF16><<<dim3(unsigned(grid)), kAttnThreads, smem, stream>>>(tmK, tmV, a);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    char name[64];
+    std::snprintf(name, sizeof(name), "kv8_attn_kernel<%d,%s>", MB, kF16 ? "fp16" : "bf16");
+    note_launch(name, grid, kAttnThreads, smem);
+  }
+  return e;
+}
+
+}  // namespace
+
+int kv8_rows_per_block(long long packed_rows) { return packed_rows <= 16 ? 16 : 32; }
+
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
+                            bool* encode_failed) {
+  *encode_failed = false;
+  EncodeTiledFn fn = get_encode_fn();
+  CUtensorMap tmK, tmV;
+  if (fn == nullptr || !encode_pool(fn, &tmK, a.k_pool, a) || !encode_pool(fn, &tmV, a.v_pool, a)) {
+    *encode_failed = true;
+    return cudaSuccess;
+  }
+  const int mb = kv8_rows_per_block((long long)a.max_rows * a.gqa);
+  const long long tiles = (a.max_kv_len + kTile - 1) / kTile;
+  const long long most = (long long)a.B * a.Hkv * a.max_rb * tiles;
+  const long long grid = most < sms ? most : sms;
+  if (mb == 16)
+    return f16 ? launch_t<16, true>(a, tmK, tmV, grid, stream)
+               : launch_t<16, false>(a, tmK, tmV, grid, stream);
+  return f16 ? launch_t<32, true>(a, tmK, tmV, grid, stream)
+             : launch_t<32, false>(a, tmK, tmV, grid, stream);
+}
+
+}  // namespace gqa

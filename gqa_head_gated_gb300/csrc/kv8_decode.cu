@@ -1,165 +1,110 @@
-// Gated attention of decode / verify rows over the paged 8-bit cache:
+// Gated attention of decode / verify rows over the paged 8-bit cache: the entry points, the
+// plan, and the merge of the split kernel's parts (kv8_attn.cu holds the mathematics):
 //
-//   s_j = (Q . k_j) * k_scale[block(j), g] / 16      p_j = exp(s_j - m), l = sum_j p_j
-//   out = (sum_j p_j v_j * v_scale[block(j), g]) / l * sigmoid(G)
+//   out = (sum_i w_i O_i) / (sum_i w_i) * sigmoid(G),  w_i = exp(lse_i - max_i lse_i)
 //
-// over the keys a row sees (chain: j < kv_len - rows + i + 1; tree: the keys before the
-// new rows, and new key k where bit k of the row's mask is set).
-//
-// One warp per (row, query head, key split): a lane holds 8 of the 256 dims of q and of
-// the running sum, and the keys go by one after another (online softmax, fp32).
+// over the parts i of the row's segment.  The merge reads only the parts that were written
+// (a count per segment), so that a plan with room for many parts costs a short batch
+// nothing.  It is launched as a programmatic dependent: finding its row, which takes a
+// chain of reads, and the gate overlap the split kernel's last CTAs.
 #include <cuda_runtime.h>
 
+#include "kv8_attn.h"
 #include "kv8_common.cuh"
 
 namespace gqa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kBatch = 8;   // parts whose loads are issued together
 
-struct DecodeParams {
-  const uint4* q;
-  const uint2* k_pool;
-  const uint2* v_pool;
-  const float* k_scale;
-  const float* v_scale;
-  const int* tables;
+struct MergeParams {
+  const float* o_parts;
+  const float* lse_parts;
+  const int* n_parts;
   const int* kv_lens;
   const int* cu_rows;
-  const unsigned long long* tree_mask;
   const uint16_t* gate;
   uint16_t* out;
   float* lse_out;
-  float* o_parts;
-  float* lse_parts;
-  int B, T, Hq, Hkv, num_blocks, bs_log2, max_blocks, max_rows, max_kv_len, splits, split_keys;
-  LaunchCtl ctl;
+  int B, T, Hq, Hkv, gqa, max_rows, max_kv_len, max_rb, rows_per_block, parts;
 };
 
-// The sequence of token t and its row there; false for a token of no (valid) sequence.
-__device__ __forceinline__ bool find_row(const DecodeParams& p, int t, int& b, int& i, int& rows,
-                                         int& kv_len, bool& bad) {
-  bad = false;
-  if (p.cu_rows == nullptr) {
-    b = t;
-    i = 0;
-    rows = 1;
-  } else {
-    int lo = 0, hi = p.B - 1;
+// Merges a row's parts, gates and rounds them: one warp a row, 8 of the 256 columns a lane.
+// Rows of no sequence, or of one that was skipped, are left as they are.
+template <bool kF16>
+__global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const MergeParams p) {
+  const int lane = threadIdx.x & 31;
+  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (n >= p.T * p.Hq) return;
+  const int t = n / p.Hq, h = n - t * p.Hq;
+  int b = t, i = 0, rows = 1;
+  if (p.cu_rows != nullptr) {
+    int lo = 0, hi = p.B - 1;   // last sequence that starts at or before t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (__ldg(p.cu_rows + mid) <= t) lo = mid; else hi = mid - 1;
     }
-    b = lo;
     const int t0 = __ldg(p.cu_rows + lo), t1 = __ldg(p.cu_rows + lo + 1);
+    b = lo;
     i = t - t0;
     rows = t1 - t0;
-    if (i < 0 || t >= t1) return false;
-    bad = t0 < 0 || t1 > p.T || rows > p.max_rows;
+    if (t0 < 0 || i < 0 || t >= t1 || t1 > p.T || rows > p.max_rows) return;
   }
-  kv_len = __ldg(p.kv_lens + b);
-  bad = bad || kv_len < rows || kv_len > p.max_kv_len;
-  return !bad;
-}
-
-template <bool kF16>
-__global__ void __launch_bounds__(kWarps * 32) kv8_rows_kernel(const DecodeParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long n = w / p.splits;
-  const int split = int(w - n * p.splits);
-  if (n >= (long long)p.T * p.Hq) return;
-  const int t = int(n / p.Hq), h = int(n - (long long)t * p.Hq), g = h / (p.Hq / p.Hkv);
-  int b, i, rows, kv_len;
-  bool bad;
-  if (!find_row(p, t, b, i, rows, kv_len, bad)) {
-    if (bad && lane == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-    return;
-  }
-  float q[8], acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  {
-    const uint4 u = __ldg(p.q + size_t(n) * 32 + lane);
-    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-    for (int c = 0; c < 4; ++c) {
-      const float2 f = unpack_elem2<kF16>(x[c]);
-      q[2 * c] = f.x;
-      q[2 * c + 1] = f.y;
-    }
-  }
-  const int base = kv_len - rows, bs = 1 << p.bs_log2;
-  const bool tree = p.tree_mask != nullptr;
-  const unsigned long long mask = tree ? p.tree_mask[t] : 0ull;
-  const int lo = split * p.split_keys;
-  const int hi = min(lo + p.split_keys, tree ? kv_len : base + i + 1);
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    if (tree && j >= base && !((mask >> (j - base)) & 1ull)) continue;
-    const int blk = __ldg(p.tables + (long long)b * p.max_blocks + (j >> p.bs_log2));
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-      break;
-    }
-    const size_t bg = size_t(blk) * p.Hkv + g;
-    const size_t row = (bg * bs + (j & (bs - 1))) * 32 + lane;
-    float k[8], v[8], s = 0.f;
-    from_e4m3x8(__ldg(p.k_pool + row), k);
-    from_e4m3x8(__ldg(p.v_pool + row), v);
-    for (int c = 0; c < 8; ++c) s = fmaf(q[c], k[c], s);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= __ldg(p.k_scale + bg) * (1.f / 16.f);
-    const float m_new = fmaxf(m, s);
-    const float msub = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = __expf(m - msub), e = __expf(s - msub), sv = __ldg(p.v_scale + bg);
-    m = m_new;
-    l = l * alpha + e;
-    for (int c = 0; c < 8; ++c) acc[c] = acc[c] * alpha + e * (v[c] * sv);
-  }
-  const size_t part = size_t(split) * size_t(p.T) * p.Hq + size_t(n);
-  if (lane == 0) p.lse_parts[part] = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + __logf(l);
-  if (l == 0.f) return;
-  float4* const o = reinterpret_cast<float4*>(p.o_parts + part * 256 + lane * 8);
-  o[0] = make_float4(acc[0] / l, acc[1] / l, acc[2] / l, acc[3] / l);
-  o[1] = make_float4(acc[4] / l, acc[5] / l, acc[6] / l, acc[7] / l);
-}
-
-// Merges a row's parts, gates and rounds them: one warp a row.  Rows of no sequence, or of
-// one that was skipped, are left as they are.
-template <bool kF16>
-__global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const DecodeParams p) {
-  const int lane = threadIdx.x & 31;
-  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (n >= p.T * p.Hq) return;
-  int b, i, rows, kv_len;
-  bool bad;
-  if (!find_row(p, n / p.Hq, b, i, rows, kv_len, bad)) return;
-  const size_t stride = size_t(p.T) * p.Hq;
-  float M = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, __ldcg(p.lse_parts + s * stride + n));
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float msub = M == -INFINITY ? 0.f : M;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float ls = __ldcg(p.lse_parts + s * stride + n);
-    if (ls == -INFINITY) continue;
-    const float w = __expf(ls - msub);
-    sum += w;
-    const float4* const src =
-        reinterpret_cast<const float4*>(p.o_parts + (s * stride + n) * 256 + lane * 8);
-    const float4 a = __ldcg(src), c = __ldcg(src + 1);
-    const float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-    for (int k = 0; k < 8; ++k) acc[k] += w * x[k];
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int kv_len = __ldg(p.kv_lens + b);
+  if (kv_len < rows || kv_len > p.max_kv_len) return;
   float gs[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
   if (p.gate != nullptr) {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.gate + size_t(n) * 256 + lane * 8));
     const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 f = unpack_elem2<kF16>(w4[e]);
       gs[2 * e] = gate_sigmoid(f.x);
       gs[2 * e + 1] = gate_sigmoid(f.y);
     }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = h / p.gqa, rb = (i * p.gqa + h - g * p.gqa) / p.rows_per_block;
+  const int cnt = min(__ldcg(p.n_parts + (size_t(b) * p.Hkv + g) * p.max_rb + rb), p.parts);
+  const size_t stride = size_t(p.T) * p.Hq;
+  const float ls0 = lane < cnt ? __ldcg(p.lse_parts + lane * stride + n) : -INFINITY;
+  float M = ls0;   // fmaxf drops a NaN; a NaN part still gets weight NaN below
+  for (int s = lane + 32; s < cnt; s += 32) M = fmaxf(M, __ldcg(p.lse_parts + s * stride + n));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float msub = M == -INFINITY ? 0.f : M;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  for (int s0 = 0; s0 < cnt; s0 += 32) {
+    const int sl = s0 + lane;
+    const float ls = s0 == 0 ? ls0 : sl < cnt ? __ldcg(p.lse_parts + sl * stride + n) : -INFINITY;
+    const float wl = ls == -INFINITY ? 0.f : __expf(ls - msub);
+    const int here = min(32, cnt - s0);
+    for (int s1 = 0; s1 < here; s1 += kBatch) {
+      float w[kBatch];
+      float4 x[kBatch], y[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        w[u] = __shfl_sync(0xffffffffu, wl, min(s1 + u, 31));
+        if (s1 + u >= here) w[u] = 0.f;
+        x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w[u] != 0.f) {
+          const float4* const src = reinterpret_cast<const float4*>(
+              p.o_parts + ((s0 + s1 + u) * stride + n) * 256 + lane * 8);
+          x[u] = __ldcg(src);
+          y[u] = __ldcg(src + 1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        sum += w[u];
+        const float v[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += w[u] * v[k];
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint4 o;
   o.x = pack_elem2<kF16>(acc[0] * inv * gs[0], acc[1] * inv * gs[1]);
   o.y = pack_elem2<kF16>(acc[2] * inv * gs[2], acc[3] * inv * gs[3]);
@@ -170,19 +115,57 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const DecodePara
     p.lse_out[n] = sum == 0.f ? -INFINITY : msub + __logf(sum);
 }
 
-constexpr int kMaxSplits = 16;
-int plan_splits(int max_kv_len, int* split_keys) {
-  int s = (max_kv_len + 511) / 512;
-  if (s > kMaxSplits) s = kMaxSplits;
-  *split_keys = (max_kv_len + s - 1) / s;
-  return s;
+template <bool kF16>
+cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((p.T * p.Hq + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel<kF16>, p);
+  if (e == cudaSuccess)
+    note_launch(kF16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", cfg.gridDim.x,
+                kWarps * 32, 0);
+  return e;
+}
+
+struct Plan {
+  int rows_per_block, max_rb, parts;
+  size_t o_bytes, lse_bytes, bytes;   // workspace: O parts, lse parts, parts per segment
+};
+
+// Part slots per row: so many that the longest sequence alone can spread over every SM, or
+// (large batches, where no sequence need) four times the even share; never more than it
+// has tiles of 128 keys.  The shares are cut on the device so that no segment needs more.
+Plan plan_decode8(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
+  Plan q;
+  const long long packed = (long long)max_rows * (Hq / Hkv), sms = device_sm_count();
+  q.rows_per_block = kv8_rows_per_block(packed);
+  q.max_rb = int((packed + q.rows_per_block - 1) / q.rows_per_block);
+  const long long units = (long long)Hkv * q.max_rb, tiles = (max_kv_len + 127LL) / 128;
+  long long parts = (sms + units - 1) / units + 2;
+  const long long even = 4 * sms / (B * units) + 2;
+  if (parts > (even > 16 ? even : 16)) parts = even > 16 ? even : 16;
+  if (parts > tiles) parts = tiles;
+  if (parts < 3) parts = 3;
+  q.parts = int(parts);
+  const size_t rows = size_t(parts) * T * Hq;
+  q.o_bytes = rows * 256 * sizeof(float);
+  q.lse_bytes = rows * sizeof(float);
+  q.bytes = q.o_bytes + q.lse_bytes + size_t(B) * units * sizeof(int);
+  return q;
 }
 
 int check_sizes(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
   if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_rows < 1 || max_kv_len < 1 ||
       max_rows > max_kv_len)
     return GQA_ERR_INVALID_ARG;
-  if ((long long)T * Hq >= (1LL << 31) || (long long)max_rows * (Hq / Hkv) >= (1LL << 30))
+  if ((long long)T * Hq >= (1LL << 31) ||
+      (long long)max_rows * Hq >= (1LL << 31) || (long long)B * Hkv >= (1LL << 31))
     return GQA_ERR_UNSUPPORTED;
   return GQA_OK;
 }
@@ -210,51 +193,49 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
                         (const void*)kv_lens, (const void*)cu_rows, (const void*)lse_out})
     if (!aligned_to(q, 4)) return GQA_ERR_INVALID_ARG;
   if (!aligned_to(tree_mask, 8)) return GQA_ERR_INVALID_ARG;
-  DecodeParams p{};
-  p.splits = plan_splits(max_kv_len, &p.split_keys);
-  const size_t rows = size_t(T) * Hq;
-  if (workspace == nullptr || workspace_bytes < p.splits * rows * 257 * sizeof(float))
-    return GQA_ERR_WORKSPACE;
+  const Plan plan = plan_decode8(B, T, Hq, Hkv, max_rows, max_kv_len);
+  if (workspace == nullptr || workspace_bytes < plan.bytes) return GQA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return GQA_ERR_INVALID_ARG;
-  p.q = static_cast<const uint4*>(Q);
-  p.k_pool = static_cast<const uint2*>(k_pool);
-  p.v_pool = static_cast<const uint2*>(v_pool);
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.tables = block_tables;
-  p.kv_lens = kv_lens;
-  p.cu_rows = cu_rows;
-  p.tree_mask = tree_mask;
-  p.gate = static_cast<const uint16_t*>(G);
-  p.out = static_cast<uint16_t*>(out);
-  p.lse_out = lse_out;
-  p.o_parts = static_cast<float*>(workspace);
-  p.lse_parts = p.o_parts + p.splits * rows * 256;
-  p.B = B;
-  p.T = T;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.num_blocks = num_blocks;
-  while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
-  p.max_blocks = max_blocks;
-  p.max_rows = max_rows;
-  p.max_kv_len = max_kv_len;
-  if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
-  const long long grid = ((long long)rows * p.splits + kWarps - 1) / kWarps;
-  const long long mgrid = ((long long)rows + kWarps - 1) / kWarps;
-  if (grid >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  Kv8AttnArgs a{};
+  a.q = static_cast<const uint4*>(Q);
+  a.k_pool = static_cast<const uint8_t*>(k_pool);
+  a.v_pool = static_cast<const uint8_t*>(v_pool);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.tree_mask = tree_mask;
+  a.o_parts = static_cast<float*>(workspace);
+  a.lse_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
+  a.n_parts = reinterpret_cast<int*>(static_cast<char*>(workspace) + plan.o_bytes + plan.lse_bytes);
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.gqa = Hq / Hkv;
+  a.num_blocks = num_blocks;
+  while ((1 << a.bs_log2) < block_size) ++a.bs_log2;
+  a.max_blocks = max_blocks;
+  a.max_rows = max_rows;
+  a.max_kv_len = max_kv_len;
+  a.max_rb = plan.max_rb;
+  a.parts = plan.parts;
+  if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (f16) {
-    kv8_rows_kernel<true><<<unsigned(grid), kWarps * 32, 0, s>>>(p);
-    kv8_merge_kernel<true><<<unsigned(mgrid), kWarps * 32, 0, s>>>(p);
-  } else {
-    kv8_rows_kernel<false><<<unsigned(grid), kWarps * 32, 0, s>>>(p);
-    kv8_merge_kernel<false><<<unsigned(mgrid), kWarps * 32, 0, s>>>(p);
+  for (int b0 = 0; b0 < B; b0 += kKv8Seqs) {
+    a.b0 = b0;
+    a.B = B - b0 < kKv8Seqs ? B - b0 : kKv8Seqs;
+    a.tables = block_tables + (long long)b0 * max_blocks;
+    a.kv_lens = kv_lens + b0;
+    a.cu_rows = cu_rows == nullptr ? nullptr : cu_rows + b0;
+    bool encode_failed = false;
+    const cudaError_t e = launch_kv8_attn(a, f16, device_sm_count(), s, &encode_failed);
+    if (encode_failed) return GQA_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return GQA_ERR_CUDA;
   }
-  if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
-  note_launch(f16 ? "kv8_rows_kernel<fp16>" : "kv8_rows_kernel<bf16>", grid, kWarps * 32, 0);
-  note_launch(f16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", mgrid, kWarps * 32, 0);
-  return GQA_OK;
+  const MergeParams m{a.o_parts, a.lse_parts, a.n_parts, kv_lens, cu_rows,
+                      static_cast<const uint16_t*>(G), static_cast<uint16_t*>(out), lse_out,
+                      B, T, Hq, Hkv, a.gqa, max_rows, max_kv_len, plan.max_rb,
+                      plan.rows_per_block, plan.parts};
+  return (f16 ? launch_merge<true>(m, s) : launch_merge<false>(m, s)) == cudaSuccess ? GQA_OK
+                                                                                     : GQA_ERR_CUDA;
 }
 
 }  // namespace
@@ -266,8 +247,7 @@ extern "C" {
 
 size_t gqa_kv8_workspace_size(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
   if (check_sizes(B, T, Hq, Hkv, max_rows, max_kv_len) != GQA_OK) return 0;
-  int c = 0;
-  return size_t(plan_splits(max_kv_len, &c)) * T * Hq * 257 * sizeof(float);
+  return plan_decode8(B, T, Hq, Hkv, max_rows, max_kv_len).bytes;
 }
 
 int gqa_kv8_decode(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
