@@ -52,8 +52,8 @@ namespace {
 constexpr int kTile = 128;                       // keys per tile
 constexpr int kHalfBytes = kTile * 128;          // 128 keys x 128 dims of K or V
 constexpr int kSlotBytes = 2 * kHalfBytes;
-constexpr int kAttnThreads = 192;
-constexpr int kSoftmaxThreads = 128;
+constexpr int kGroupRows = 8;                    // rows of one softmax thread
+constexpr int kGroupThreads = 128;               // one thread per key of a tile
 constexpr int kPTerms = 3;
 constexpr int kScaleRing = 8;      // tiles whose scales are held: see the producer
 constexpr int kMaxTileBlocks = kTile / 16;
@@ -65,6 +65,9 @@ constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
 template <int MB, bool kF16>
 struct Cfg {
   static constexpr int kQTerms = kF16 ? 3 : 2;
+  static constexpr int kGroups = MB / kGroupRows;          // softmax thread groups
+  static constexpr int kSoftmax = kGroups * kGroupThreads;
+  static constexpr int kThreads = 64 + kSoftmax;
   static constexpr int kNS = MB * kQTerms;       // columns of S^T
   static constexpr int kNO = MB * kPTerms;       // columns of each half of O^T
   static constexpr int kKS = 3;                  // K slots
@@ -97,7 +100,7 @@ struct __align__(1024) AttnSmem {
   float fac[MB];
   alignas(16) float red[2][MB][4];         // read as float4
   uint32_t tmem_base;
-  int abort, zero;
+  int abort, zero, stopped;
 };
 
 struct Piece {
@@ -189,13 +192,19 @@ __device__ __noinline__ bool clean_v_row(uint8_t* slot, int row, bool zero) {
   return hit;
 }
 
-// Columns [col, col + 16) of one half of O^T times f, in tensor memory (whole warp).
-__device__ __forceinline__ void rescale_cols(uint32_t ta, const float* f) {
-  uint32_t o[16];
-  ptx::tmem_ld16_wait(ta, o);
+// The three terms (columns t0, t0 + MB, t0 + 2 MB) of 8 rows of one half of O^T times f, in
+// tensor memory (whole warp).
+template <int MB>
+__device__ __forceinline__ void rescale_cols(uint32_t t0, const float (&f)[8]) {
+  uint32_t a[8], b[8], c[8];
+  ptx::tmem_ld8x3_wait(t0, t0 + MB, t0 + 2 * MB, a, b, c);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
-  ptx::tmem_st16_wait(ta, o);
+  for (int i = 0; i < 8; ++i) {
+    a[i] = __float_as_uint(__uint_as_float(a[i]) * f[i]);
+    b[i] = __float_as_uint(__uint_as_float(b[i]) * f[i]);
+    c[i] = __float_as_uint(__uint_as_float(c[i]) * f[i]);
+  }
+  ptx::tmem_st8x3_wait(t0, t0 + MB, t0 + 2 * MB, a, b, c);
 }
 
 // Two values to e4m3, and what they leave: (lo, hi) becomes (x - e4m3(x)) * step.
@@ -207,8 +216,35 @@ __device__ __forceinline__ uint32_t take_term(float& lo, float& hi, float step) 
   return t;
 }
 
+// Two probabilities (at most 2^8) as three e4m3 terms each, steps of 32: the first remainder
+// is exact in fp32 and goes on as fp16, whose 11 bits hold the two terms to come.
+__device__ __forceinline__ void p_terms(float lo, float hi, uint32_t (&t)[kPTerms]) {
+  t[0] = take_term(lo, hi, 32.f);
+  __half2 r = __floats2half2_rn(lo, hi);
+  t[1] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+  const __half2 f(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(t[1]), __NV_E4M3));
+  r = __hmul2(__hsub2(r, f), __float2half2_rn(32.f));
+  t[2] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+}
+
+// A row's output of one dim: NaN when a key that it sees had a NaN there (`hits`: keys from
+// pr_lo on whose V rows had NaN codes taken out).
+__device__ __noinline__ float put_back_nan(const Kv8AttnArgs& p, int b, int g,
+                                           unsigned long long hits, int pr_lo, int lim, bool tree,
+                                           int base, unsigned long long mask, int dim, float o) {
+  for (; hits != 0ull; hits &= hits - 1ull) {
+    const int key = pr_lo + __ffsll(static_cast<long long>(hits)) - 1;
+    if (key >= lim || (tree && key >= base && !((mask >> (key - base)) & 1ull))) continue;
+    const int blk = __ldg(p.tables + (long long)b * p.max_blocks + (key >> p.bs_log2));
+    if (blk < 0 || blk >= p.num_blocks) continue;
+    const size_t row = ((size_t(blk) * p.Hkv + g) << p.bs_log2) + (key & ((1 << p.bs_log2) - 1));
+    if ((p.v_pool[row * 256 + dim] & 0x7Fu) == 0x7Fu) o = __int_as_float(0x7FC00000);
+  }
+  return o;
+}
+
 template <int MB, bool kF16>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(Cfg<MB, kF16>::kThreads, 1)
 kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const Kv8AttnArgs p) {
   using C = Cfg<MB, kF16>;
@@ -221,7 +257,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 
   // ---- the schedule: tiles before each sequence, and this CTA's share of them
   int most = 0;   // tiles of the longest sequence
-  for (int b = tid; b < p.B; b += kAttnThreads) {
+  for (int b = tid; b < p.B; b += C::kThreads) {
     int t0, rows, kv;
     const bool ok = seq_of(p, b, t0, rows, kv);
     const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
@@ -243,14 +279,15 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(&sm.sc_full[i], 32);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.s_full[i], 1);
-      ptx::mbar_init(&sm.p_full[i], kSoftmaxThreads / 32);
+      ptx::mbar_init(&sm.p_full[i], C::kSoftmax / 32);
       ptx::mbar_init(&sm.pv_done[i], 1);
     }
-    ptx::mbar_init(&sm.q_full, kSoftmaxThreads / 32);
+    ptx::mbar_init(&sm.q_full, C::kSoftmax / 32);
     ptx::mbar_init(&sm.o_full, 1);
     ptx::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     sm.zero = 0;
+    sm.stopped = 0;
     sm.hit = 0ull;
     ptx::fence_mbar_init();
   }
@@ -433,42 +470,45 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, epilogue
+    // Group rg of 128 threads has rows 8 rg .. 8 rg + 7 of the block, thread by key.
+    constexpr int kR = kGroupRows;
     const int qd = warp & 3;                   // tensor-memory lanes 32 qd .. 32 qd + 31
+    const int rg = (warp - 2) >> 2;
     const int key_in = qd * 32 + lane;         // this thread's key of a tile
-    const int st = tid - 64;                   // 0 .. 127
-    const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
+    const int st = tid - 64;                   // 0 .. kSoftmax - 1
+    const uint32_t trow = tmem + (uint32_t(qd * 32) << 16) + uint32_t(rg * kR);
     const bool tree = p.tree_mask != nullptr;
-    const auto bar = [] { ptx::named_bar_sync(1, kSoftmaxThreads); };
+    const uint32_t bar_id = 1 + rg;            // barriers 1 .. kGroups; kGroups + 1 for all
+    const auto bar_all = [] { ptx::named_bar_sync(C::kGroups + 1, C::kSoftmax); };
     long long J = 0;
     uint32_t pc = 0;
     bool ok = true;      // this thread's waits; agreed on at barriers before anyone leaves
-    bool stop = false;   // the same in all softmax threads
-    for (long long pos = pos0; !stop && pos < end;) {
+    bool stop = false;   // the same in all threads of a group
+    for (long long pos = pos0; pos < end;) {
       const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
       pos = x.next;
       const int P = x.rows * p.gqa, p0 = x.rb * MB, n_rows = min(MB, P - p0);
+      const int n_mine = min(max(n_rows - rg * kR, 0), kR);   // rows of this group
       const int base = x.kv_len - x.rows;
       const size_t part0 = size_t(x.s) * size_t(p.T) * p.Hq;
       const auto out_row = [&](int r) {
         const int pp = p0 + r;
         return size_t(x.t0 + pp / p.gqa) * p.Hq + size_t(x.g) * p.gqa + pp % p.gqa;
       };
-      if (x.s < 0 || x.s >= p.parts) {   // cannot happen with shares as cut above
-        if (st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-        if (x.n_tiles == 0) continue;
-      }
-      const bool fits = x.s >= 0 && x.s < p.parts;
+      const bool fits = x.s >= 0 && x.s < p.parts;   // always, with shares as cut above
+      if (!fits && st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
       if (x.last && st == 0 && fits)
         p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
       if (x.n_tiles == 0) {   // no row of the block sees a key of the piece
-        if (st < n_rows) p.lse_parts[part0 + out_row(st)] = -INFINITY;
+        if (st < n_rows && fits) p.lse_parts[part0 + out_row(st)] = -INFINITY;
         continue;
       }
       // keys from pr_lo on are seen by some rows of the block only
       const int pr_lo = max(x.k_lo, tree ? base : base + p0 / p.gqa + 1);
 
       // ---- Q's terms and the rows' limits (the last piece's products are done)
-      bar();
+      bar_all();
+      if (sm.stopped) break;   // set before the barrier by a group that gave up
       if (st < MB) {
         int lim = 0;
         unsigned long long m = 0ull;
@@ -482,16 +522,16 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       }
       if (st == 0) sm.hit = 0ull;
       {
-        constexpr int kPer = MB / 4;     // rows of each warp
+        constexpr int kWarpsQ = C::kSoftmax / 32, kPer = MB / kWarpsQ;   // rows of each warp
         uint4 u[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int r = qd + i * 4;
+          const int r = warp - 2 + i * kWarpsQ;
           u[i] = r < n_rows ? __ldg(p.q + out_row(r) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int r = qd + i * 4;
+          const int r = warp - 2 + i * kWarpsQ;
           float f[8];
           const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
@@ -523,11 +563,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.q_full);
-      bar();   // limits and factors are written
+      bar_all();   // limits and factors are written
 
-      float ref[MB], ml[MB], l[MB];
+      float ref[kR], ml[kR], l[kR];
 #pragma unroll
-      for (int r = 0; r < MB; ++r) {
+      for (int r = 0; r < kR; ++r) {
         ref[r] = kNone;
         ml[r] = kNone;
         l[r] = 0.f;
@@ -536,96 +576,86 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int buf = int(J & 1);
         const int key = x.k_lo + j * kTile + key_in;
         const int tile_end = x.k_lo + (j + 1) * kTile;
-        float s[MB];
-        float lv = 0.f;
-        bool need = false;
-        ok = ok && ptx::mbar_wait(&sm.s_full[buf], uint32_t(J >> 1) & 1u, tmo, &sm.abort) &&
-             ptx::mbar_wait(&sm.sc_full[J % kScaleRing], uint32_t(J / kScaleRing) & 1u, tmo, &sm.abort);
-        ok = warp_all(ok);
-        if (ok) {
-          ptx::tc_fence_after();
-          float sk = sm.scale[J % kScaleRing][0][key_in >> p.bs_log2];
-          const float sv = sm.scale[J % kScaleRing][1][key_in >> p.bs_log2];
-          if (key >= x.k_hi) {
-            sk = 0.f;
-          } else {
-            lv = log2_scale(sv);
-          }
-          const uint32_t sa = trow + C::kTmS + uint32_t(buf) * C::kStep;
-          if constexpr (MB == 16) {
-            uint32_t a[32];
-            ptx::tmem_ld32_wait(sa, a);
+        // This group's rows only; a group without rows keeps step with the others.
+        ok = ok && ptx::mbar_wait(&sm.s_full[buf], uint32_t(J >> 1) & 1u, tmo, &sm.abort);
+        uint2 w[kPTerms];
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              s[r] = fmaf(__uint_as_float(a[16 + r]), 0.0625f, __uint_as_float(a[r]));
-            if constexpr (kF16) {
-              uint32_t c[16];
-              ptx::tmem_ld16_wait(sa + 32, c);
-#pragma unroll
-              for (int r = 0; r < 16; ++r) s[r] = fmaf(__uint_as_float(c[r]), 0.00390625f, s[r]);
+        for (int t = 0; t < kPTerms; ++t) w[t] = make_uint2(0u, 0u);
+        if (n_mine > 0) {
+          float s[kR], d[kR];   // log2 scores; with vs, minus p's reference
+          float lv = 0.f;
+          bool need = false;
+          ok = ok && ptx::mbar_wait(&sm.sc_full[J % kScaleRing], uint32_t(J / kScaleRing) & 1u, tmo,
+                                    &sm.abort);
+          ok = warp_all(ok);
+          if (ok) {
+            ptx::tc_fence_after();
+            float sk = sm.scale[J % kScaleRing][0][key_in >> p.bs_log2];
+            const float sv = sm.scale[J % kScaleRing][1][key_in >> p.bs_log2];
+            if (key >= x.k_hi) {
+              sk = 0.f;
+            } else {
+              lv = log2_scale(sv);
             }
-          } else {
-            uint32_t a[64];
-            ptx::tmem_ld64_wait(sa, a);
-#pragma unroll
-            for (int r = 0; r < 32; ++r)
-              s[r] = fmaf(__uint_as_float(a[32 + r]), 0.0625f, __uint_as_float(a[r]));
+            const uint32_t sa = trow + C::kTmS + uint32_t(buf) * C::kStep;
+            uint32_t a[8], b[8];
             if constexpr (kF16) {
-              uint32_t c[32];
-              ptx::tmem_ld32_wait(sa + 64, c);
+              uint32_t c[8];
+              ptx::tmem_ld8x3_wait(sa, sa + MB, sa + 2 * MB, a, b, c);
 #pragma unroll
-              for (int r = 0; r < 32; ++r) s[r] = fmaf(__uint_as_float(c[r]), 0.00390625f, s[r]);
+              for (int r = 0; r < kR; ++r)
+                s[r] = fmaf(__uint_as_float(c[r]), 0.00390625f,
+                            fmaf(__uint_as_float(b[r]), 0.0625f, __uint_as_float(a[r])));
+            } else {
+              ptx::tmem_ld8x2_wait(sa, sa + MB, a, b);
+#pragma unroll
+              for (int r = 0; r < kR; ++r)
+                s[r] = fmaf(__uint_as_float(b[r]), 0.0625f, __uint_as_float(a[r]));
             }
-          }
-          const bool part_seen = tile_end > pr_lo || tile_end > x.k_hi;
 #pragma unroll
-          for (int r0 = 0; r0 < MB; r0 += 4) {
-            if (r0 >= n_rows) break;
+            for (int r = 0; r < kR; ++r) s[r] = s[r] * sm.fac[rg * kR + r] * sk;
+            if (tile_end > pr_lo || tile_end > x.k_hi) {
 #pragma unroll
-            for (int r = r0; r < r0 + 4; ++r) {
-              float v = s[r] * sm.fac[r] * sk;
-              if (part_seen) {
-                const bool vis = key < min(sm.lim[r], x.k_hi) &&
-                                 (!tree || key < base || ((sm.mask[r] >> (key - base)) & 1ull));
-                v = vis ? v : -INFINITY;
+              for (int r = 0; r < kR; ++r) {
+                const bool vis =
+                    key < min(sm.lim[rg * kR + r], x.k_hi) &&
+                    (!tree || key < base || ((sm.mask[rg * kR + r] >> (key - base)) & 1ull));
+                if (!vis) s[r] = -INFINITY;
               }
-              s[r] = v;
-              need = need || v + lv > ref[r] + kSlack || v > ml[r] + kLSlack;
             }
-          }
-        }
-        // ---- does a reference have to move (or has a wait run out)?
-        if (ptx::named_bar_or(1, kSoftmaxThreads, need || !ok)) {
-          if (ptx::named_bar_or(1, kSoftmaxThreads, !ok)) {
-            stop = true;
-            break;
-          }
+            float md = -INFINITY, me = -INFINITY;
 #pragma unroll
-          for (int r0 = 0; r0 < MB; r0 += 4) {
-            if (r0 >= n_rows) break;
+            for (int r = 0; r < kR; ++r) {
+              d[r] = (s[r] - ref[r]) + lv;
+              md = fmaxf(md, d[r]);
+              me = fmaxf(me, s[r] - ml[r]);
+            }
+            need = md > kSlack || me > kLSlack;
+          }
+          // ---- does a reference have to move (or has a wait run out)?
+          if (ptx::named_bar_or(bar_id, kGroupThreads, need || !ok)) {
+            if (ptx::named_bar_or(bar_id, kGroupThreads, !ok)) {
+              stop = true;
+              break;
+            }
 #pragma unroll
-            for (int r = r0; r < r0 + 4; ++r) {
+            for (int r = 0; r < kR; ++r) {
               const float a = ptx::warp_max_f32(s[r] + lv), c = ptx::warp_max_f32(s[r]);
               if (lane == r) {
-                sm.red[0][r][qd] = a;
-                sm.red[1][r][qd] = c;
+                sm.red[0][rg * kR + r][qd] = a;
+                sm.red[1][rg * kR + r][qd] = c;
               }
             }
-          }
-          bar();
-          bool move = false;
-          float alpha[MB];
+            ptx::named_bar_sync(bar_id, kGroupThreads);
+            bool move = false;
+            float alpha[kR];
 #pragma unroll
-          for (int r = 0; r < MB; ++r) alpha[r] = 1.f;
-#pragma unroll
-          for (int r0 = 0; r0 < MB; r0 += 4) {
-            if (r0 >= n_rows) break;
-#pragma unroll
-            for (int r = r0; r < r0 + 4; ++r) {
-              const float4 a = *reinterpret_cast<const float4*>(sm.red[0][r]);
-              const float4 c = *reinterpret_cast<const float4*>(sm.red[1][r]);
+            for (int r = 0; r < kR; ++r) {
+              const float4 a = *reinterpret_cast<const float4*>(sm.red[0][rg * kR + r]);
+              const float4 c = *reinterpret_cast<const float4*>(sm.red[1][rg * kR + r]);
               const float ma = fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w));
               const float mc = fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w));
+              alpha[r] = 1.f;
               if (ma > ref[r] + kSlack) {
                 alpha[r] = ex2(ref[r] - (ma - kTop));
                 ref[r] = ma - kTop;
@@ -635,61 +665,50 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 l[r] *= ex2(ml[r] - mc);
                 ml[r] = mc;
               }
+              d[r] = (s[r] - ref[r]) + lv;
+            }
+            if (move && j > 0) {   // the same in all threads: references and maxima are
+              ok = warp_all(ptx::mbar_wait(&sm.pv_done[buf ^ 1], uint32_t((J - 1) >> 1) & 1u, tmo,
+                                           &sm.abort));
+              if (ok) {
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) rescale_cols<MB>(trow + C::kTmO + h * C::kStep, alpha);
+              }
             }
           }
-          if (move && j > 0) {   // the same in all threads: references and maxima are
-            ok = warp_all(ptx::mbar_wait(&sm.pv_done[buf ^ 1], uint32_t((J - 1) >> 1) & 1u, tmo,
-                                         &sm.abort));
-            if (ok) {
-              ptx::tc_fence_after();
+          // ---- P's terms
 #pragma unroll
-              for (int g16 = 0; g16 < MB / 16; ++g16)
-#pragma unroll 1
-                for (int c = 0; c < 2 * kPTerms; ++c)
-                  rescale_cols(trow + C::kTmO + (c / kPTerms) * C::kStep + (c % kPTerms) * MB +
-                                   g16 * 16,
-                               alpha + g16 * 16);
+          for (int i = 0; i < kR / 4; ++i) {
+            if (4 * i >= n_mine) break;
+            float pr[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              l[4 * i + c] += ex2(s[4 * i + c] - ml[4 * i + c]);
+              pr[c] = ex2(d[4 * i + c]);
             }
+            uint32_t lo[kPTerms], hi[kPTerms];
+            p_terms(pr[0], pr[1], lo);
+            p_terms(pr[2], pr[3], hi);
+#pragma unroll
+            for (int t = 0; t < kPTerms; ++t) (i == 0 ? w[t].x : w[t].y) = lo[t] | (hi[t] << 16);
           }
         }
-        // ---- P's terms (PV of tile J - 2 has read this buffer)
-        if (J >= 2)
-          ok = ok && ptx::mbar_wait(&sm.pv_done[buf], uint32_t((J >> 1) - 1) & 1u, tmo, &sm.abort);
-        const bool tail = tile_end > x.k_hi, partly = tile_end > pr_lo;
-        if (tail || partly) {
+        if (rg == 0 && (tile_end > x.k_hi || tile_end > pr_lo)) {
           ok = ok && ptx::mbar_wait(&sm.v_full[J % C::kVS], uint32_t(J / C::kVS) & 1u, tmo, &sm.abort);
           if (ok && (key >= x.k_hi || key >= pr_lo) &&
               clean_v_row(sm.v[J % C::kVS], key_in, key >= x.k_hi))
             atomicOr(&sm.hit, 1ull << (key - pr_lo));
         }
+        // (PV of tile J - 2 has read this buffer)
+        if (J >= 2)
+          ok = ok && ptx::mbar_wait(&sm.pv_done[buf], uint32_t((J >> 1) - 1) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         if (ok) {
 #pragma unroll
-          for (int g16 = 0; g16 < MB / 16; ++g16) {
-            uint32_t w[kPTerms][4];
-#pragma unroll
-            for (int t = 0; t < kPTerms; ++t)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[t][i] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = g16 * 16 + 4 * i;
-              if (r >= n_rows) break;
-              float e[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                l[r + c] += ex2(s[r + c] - ml[r + c]);
-                e[c] = ex2(s[r + c] + lv - ref[r + c]);
-              }
-#pragma unroll
-              for (int t = 0; t < kPTerms; ++t)
-                w[t][i] = take_term(e[0], e[1], 32.f) | (take_term(e[2], e[3], 32.f) << 16);
-            }
-#pragma unroll
-            for (int t = 0; t < kPTerms; ++t)
-              *reinterpret_cast<uint4*>(sm.p[buf] + (t * (MB / 16) + g16) * (kTile * 16) + key_in * 16) =
-                  make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-          }
+          for (int t = 0; t < kPTerms; ++t)
+            *reinterpret_cast<uint2*>(sm.p[buf] + (t * (MB / 16) + (rg >> 1)) * (kTile * 16) +
+                                      key_in * 16 + (rg & 1) * 8) = w[t];
           ptx::fence_proxy_async_smem();
           ptx::tc_fence_before();
           __syncwarp();
@@ -701,63 +720,56 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ok = ok && ptx::mbar_wait(&sm.o_full, pc & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
 #pragma unroll
-        for (int r = 0; r < MB; ++r) {
+        for (int r = 0; r < kR; ++r) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-          if (lane == r) sm.red[0][r][qd] = l[r];
+          if (lane == r) sm.red[0][rg * kR + r][qd] = l[r];
         }
-        stop = ptx::named_bar_or(1, kSoftmaxThreads, !ok);
+        stop = ptx::named_bar_or(bar_id, kGroupThreads, !ok);
       }
-      if (stop) break;
       ++pc;
+      if (stop) {
+        // Tell the other groups, which stop at the next piece's barrier; their own waits
+        // run out too (this group's arrivals are missing).
+        if (key_in == 0) sm.stopped = 1;
+        continue;
+      }
       ptx::tc_fence_after();
       const unsigned long long hits = sm.hit;
+      if (n_mine > 0) {
+        float inv[kR], ex[kR];
 #pragma unroll
-      for (int g16 = 0; g16 < MB / 16; ++g16) {
-        float inv[16], ex[16];
-        bool some[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = g16 * 16 + i;
-          const float4 a = *reinterpret_cast<const float4*>(sm.red[0][r]);
+        for (int r = 0; r < kR; ++r) {
+          const float4 a = *reinterpret_cast<const float4*>(sm.red[0][rg * kR + r]);
           const float L = (a.x + a.y) + (a.z + a.w);
-          some[i] = fits && r < n_rows && L != 0.f;
-          inv[i] = 1.f / L;
-          ex[i] = ex2(0.5f * (ref[r] - ml[r]));
-          if (fits && st == r && r < n_rows)
-            p.lse_parts[part0 + out_row(r)] = L == 0.f ? -INFINITY : (ml[r] + __log2f(L)) * kLn2;
+          inv[r] = L == 0.f ? 0.f : 1.f / L;
+          ex[r] = ex2(0.5f * (ref[r] - ml[r]));
+          if (fits && key_in == r && r < n_mine)
+            p.lse_parts[part0 + out_row(rg * kR + r)] =
+                L == 0.f ? -INFINITY : (ml[r] + __log2f(L)) * kLn2;
         }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          uint32_t a[16], b[16], c[16];
-          const uint32_t ta = trow + C::kTmO + h * C::kStep + g16 * 16;
-          ptx::tmem_ld16_wait(ta, a);
-          ptx::tmem_ld16_wait(ta + MB, b);
-          ptx::tmem_ld16_wait(ta + 2 * MB, c);
+          uint32_t a[8], b[8], c[8];
+          const uint32_t ta = trow + C::kTmO + h * C::kStep;
+          ptx::tmem_ld8x3_wait(ta, ta + MB, ta + 2 * MB, a, b, c);
           const int dim = h * 128 + key_in;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (!some[i]) continue;
-            const int r = g16 * 16 + i;
+          for (int i = 0; i < kR; ++i) {
+            if (i >= n_mine || !fits) continue;
+            const int r = rg * kR + i;
             float o = fmaf(__uint_as_float(c[i]), 1.f / 1024.f,
                            fmaf(__uint_as_float(b[i]), 1.f / 32.f, __uint_as_float(a[i])));
             o = o * inv[i] * ex[i] * ex[i];
-            for (unsigned long long m = hits; m != 0ull; m &= m - 1ull) {
-              const int kk = pr_lo + __ffsll(static_cast<long long>(m)) - 1;
-              if (kk >= sm.lim[r] || (tree && kk >= base && !((sm.mask[r] >> (kk - base)) & 1ull)))
-                continue;
-              const int blk = __ldg(p.tables + (long long)x.b * p.max_blocks + (kk >> p.bs_log2));
-              if (blk < 0 || blk >= p.num_blocks) continue;
-              const size_t vrow = ((size_t(blk) * p.Hkv + x.g) << p.bs_log2) + (kk & ((1 << p.bs_log2) - 1));
-              if ((p.v_pool[vrow * 256 + dim] & 0x7Fu) == 0x7Fu) o = __int_as_float(0x7FC00000);
-            }
+            if (hits != 0ull)
+              o = put_back_nan(p, x.b, x.g, hits, pr_lo, sm.lim[r], tree, base, sm.mask[r], dim, o);
             p.o_parts[(part0 + out_row(r)) * 256 + dim] = o;
           }
         }
       }
       ptx::tc_fence_before();
     }
-    if (stop && st == 0) {
+    if (stop && key_in == 0) {
       sm.abort = 1;
       record_status(p.ctl.status, GQA_ERR_TIMEOUT);
     }
@@ -785,12 +797,12 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
   cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<MB, kF16>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  kv8_attn_kernel<MB, kF16><<<dim3(unsigned(grid)), kAttnThreads, smem, stream>>>(tmK, tmV, a);
+  kv8_attn_kernel<MB, kF16><<<dim3(unsigned(grid)), Cfg<MB, kF16>::kThreads, smem, stream>>>(tmK, tmV, a);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
     char name[64];
     std::snprintf(name, sizeof(name), "kv8_attn_kernel<%d,%s>", MB, kF16 ? "fp16" : "bf16");
-    note_launch(name, grid, kAttnThreads, smem);
+    note_launch(name, grid, Cfg<MB, kF16>::kThreads, smem);
   }
   return e;
 }
