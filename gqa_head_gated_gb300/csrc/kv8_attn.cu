@@ -97,11 +97,22 @@ struct __align__(1024) AttnSmem {
   unsigned long long mask[MB];
   long long base[kKv8Seqs + 1];            // first tile of each sequence's segments
   int lim[MB];
+  int row[MB];                             // output row (token * Hq + head)
   float fac[MB];
   alignas(16) float red[2][MB][4];         // read as float4
   uint32_t tmem_base;
   int abort, zero, stopped;
 };
+
+// ptx::mbar_wait with the polling loop out of line: the kernel has many waits, and its code
+// has to stay small (inlined, they made it 114 KB, whose instruction fetches took thousands
+// of cycles wherever a path had not run for a while).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t tmo, int* abort) {
+  return ptx::mbar_wait(bar, parity, tmo, abort);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t tmo, int* abort) {
+  return ptx::mbar_try_wait(ptx::smem_addr(bar), parity) || wait_slow(bar, parity, tmo, abort);
+}
 
 struct Piece {
   int b, g, rb, s;        // sequence, KV head, row block, part
@@ -122,7 +133,7 @@ __device__ __forceinline__ bool seq_of(const Kv8AttnArgs& p, int b, int& t0, int
 
 // The piece of this CTA's share that starts at `pos` (the share ends at `end`).
 template <int MB>
-__device__ __forceinline__ Piece piece_at(const Kv8AttnArgs& p, const long long* base, long long pos,
+__device__ __noinline__ Piece piece_at(const Kv8AttnArgs& p, const long long* base, long long pos,
                                           long long end, long long W, long long n_cta) {
   Piece x;
   int lo = 0, hi = p.B - 1;   // last sequence that starts at or before pos
@@ -205,6 +216,23 @@ __device__ __forceinline__ void rescale_cols(uint32_t t0, const float (&f)[8]) {
     c[i] = __float_as_uint(__uint_as_float(c[i]) * f[i]);
   }
   ptx::tmem_st8x3_wait(t0, t0 + MB, t0 + 2 * MB, a, b, c);
+}
+
+// Maxima over the warp of 16 values a thread (NaN left out): lane 2 i gets the i-th.  Each
+// step halves the values that a lane still carries: 16 shuffles (measured: redux.sync.max.f32
+// took 230 cycles a value, 3,700 in all; this about 150).
+__device__ __forceinline__ float warp_max16(float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1) {
+    const bool up = (lane & (2 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 2 * n));
+    }
+  }
+  return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 // Two values to e4m3, and what they leave: (lo, hi) becomes (x - e4m3(x)) * step.
@@ -331,7 +359,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     // softmax of tile J + 3, so tile J's scales have been read.
     static_assert(kScaleRing >= C::kKS + 3, "scale ring");
     const int bs = 1 << p.bs_log2, per_tile = kTile >> p.bs_log2;
-    long long J = 0;
+    uint32_t J = 0;
     bool ok = true;
     if (lane == 0) {
       ptx::prefetch_tmap(&tmK);
@@ -353,11 +381,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int cur = blk;
         at += kTile;
         blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
-        const int ks = int(J % C::kKS), vs = int(J % C::kVS);
+        const uint32_t ks = J % C::kKS, vs = J % C::kVS;
         int go = 1;
         if (lane == 0) {
           if (J >= C::kKS)
-            go = ptx::mbar_wait(&sm.k_empty[ks], uint32_t(J / C::kKS - 1) & 1u, tmo, &sm.abort);
+            go = wait(&sm.k_empty[ks], (J / C::kKS - 1) & 1u, tmo, &sm.abort);
           if (go) ptx::mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
         }
         ok = __shfl_sync(0xffffffffu, go, 0) != 0;
@@ -373,13 +401,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ptx::cp_async_mbar_arrive(&sm.sc_full[J % kScaleRing]);
         if (lane == 0) {
           if (J >= C::kVS)
-            go = ptx::mbar_wait(&sm.v_empty[vs], uint32_t(J / C::kVS - 1) & 1u, tmo, &sm.abort);
+            go = wait(&sm.v_empty[vs], (J / C::kVS - 1) & 1u, tmo, &sm.abort);
           if (go) ptx::mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
         }
         ok = __shfl_sync(0xffffffffu, go, 0) != 0;
         if (!ok) {
           // K of this tile is on its way: it must land before the CTA ends
-          if (lane == 0) ptx::mbar_wait(&sm.k_full[ks], uint32_t(J / C::kKS) & 1u, tmo, &sm.zero);
+          if (lane == 0) wait(&sm.k_full[ks], (J / C::kKS) & 1u, tmo, &sm.zero);
           break;
         }
         if (mine) {
@@ -395,24 +423,24 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
     ptx::cp_async_wait_all();
     if (lane == 0) {   // every copy has landed before the CTA ends
-      for (long long c = max(0LL, J - C::kKS); c < J; ++c)
-        ptx::mbar_wait(&sm.k_full[c % C::kKS], uint32_t(c / C::kKS) & 1u, tmo, &sm.zero);
-      for (long long c = max(0LL, J - C::kVS); c < J; ++c)
-        ptx::mbar_wait(&sm.v_full[c % C::kVS], uint32_t(c / C::kVS) & 1u, tmo, &sm.zero);
+      for (uint32_t c = J - min(J, uint32_t(C::kKS)); c < J; ++c)
+        wait(&sm.k_full[c % C::kKS], (c / C::kKS) & 1u, tmo, &sm.zero);
+      for (uint32_t c = J - min(J, uint32_t(C::kVS)); c < J; ++c)
+        wait(&sm.v_full[c % C::kVS], (c / C::kVS) & 1u, tmo, &sm.zero);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       const uint32_t qa = ptx::smem_addr(sm.q), pa = ptx::smem_addr(sm.p);
-      long long J = 0;
+      uint32_t J = 0;
       bool ok = true;
-      const auto issue_s = [&](long long n) -> bool {
-        const int ks = int(n % C::kKS);
-        if (!ptx::mbar_wait(&sm.k_full[ks], uint32_t(n / C::kKS) & 1u, tmo, &sm.abort)) return false;
+      const auto issue_s = [&](uint32_t n) -> bool {
+        const uint32_t ks = n % C::kKS;
+        if (!wait(&sm.k_full[ks], (n / C::kKS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint32_t ka = ptx::smem_addr(sm.k[ks]);
-        const uint32_t d = tmem + C::kTmS + uint32_t(n & 1) * C::kStep;
+        const uint32_t d = tmem + C::kTmS + (n & 1u) * C::kStep;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           ptx::mma_ss_f8(
@@ -423,10 +451,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ptx::tc_commit(&sm.k_empty[ks]);
         return true;
       };
-      const auto issue_pv = [&](long long n, bool first) -> bool {
-        const int vs = int(n % C::kVS), buf = int(n & 1);
-        if (!ptx::mbar_wait(&sm.p_full[buf], uint32_t(n >> 1) & 1u, tmo, &sm.abort)) return false;
-        if (!ptx::mbar_wait(&sm.v_full[vs], uint32_t(n / C::kVS) & 1u, tmo, &sm.abort)) return false;
+      const auto issue_pv = [&](uint32_t n, bool first) -> bool {
+        const uint32_t vs = n % C::kVS, buf = n & 1u;
+        if (!wait(&sm.p_full[buf], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.v_full[vs], (n / C::kVS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint32_t va = ptx::smem_addr(sm.v[vs]);
 #pragma unroll
@@ -446,15 +474,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
         pos = x.next;
         if (x.n_tiles == 0) continue;
-        ok = ptx::mbar_wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
+        ok = wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
         if (!ok) break;
         ptx::tc_fence_after();
         ok = issue_s(J);
-        for (int j = 1; ok && j < x.n_tiles; ++j) {
-          ok = issue_s(J + j);
-          if (ok) ok = issue_pv(J + j - 1, j == 1);
+        for (int j = 0; ok && j < x.n_tiles; ++j) {
+          if (j + 1 < x.n_tiles) ok = issue_s(J + j + 1);
+          if (ok) ok = issue_pv(J + j, j == 0);
         }
-        if (ok) ok = issue_pv(J + x.n_tiles - 1, x.n_tiles == 1);
         if (ok) ptx::tc_commit(&sm.o_full);
         J += x.n_tiles;
         ++pc;
@@ -465,7 +492,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       }
       // every product issued has to end before tensor memory is given back
       ptx::tc_commit(&sm.drain);
-      ptx::mbar_wait(&sm.drain, 0, tmo, &sm.zero);
+      wait(&sm.drain, 0, tmo, &sm.zero);
     }
     __syncwarp();
   } else {
@@ -479,9 +506,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16) + uint32_t(rg * kR);
     const bool tree = p.tree_mask != nullptr;
     const uint32_t bar_id = 1 + rg;            // barriers 1 .. kGroups; kGroups + 1 for all
-    const auto bar_all = [] { ptx::named_bar_sync(C::kGroups + 1, C::kSoftmax); };
-    long long J = 0;
-    uint32_t pc = 0;
+    const auto bar_all = [] { ptx::named_bar_sync_any(C::kGroups + 1, C::kSoftmax); };
+    uint32_t J = 0, pc = 0;
     bool ok = true;      // this thread's waits; agreed on at barriers before anyone leaves
     bool stop = false;   // the same in all threads of a group
     for (long long pos = pos0; pos < end;) {
@@ -492,8 +518,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const int base = x.kv_len - x.rows;
       const size_t part0 = size_t(x.s) * size_t(p.T) * p.Hq;
       const auto out_row = [&](int r) {
-        const int pp = p0 + r;
-        return size_t(x.t0 + pp / p.gqa) * p.Hq + size_t(x.g) * p.gqa + pp % p.gqa;
+        const int i = (p0 + r) / p.gqa;
+        return (x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + r - i * p.gqa);
       };
       const bool fits = x.s >= 0 && x.s < p.parts;   // always, with shares as cut above
       if (!fits && st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
@@ -518,16 +544,18 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (tree) m = p.tree_mask[x.t0 + i];
         }
         sm.lim[st] = lim;
+        sm.row[st] = st < n_rows ? out_row(st) : 0;
         sm.mask[st] = m;
       }
       if (st == 0) sm.hit = 0ull;
+      bar_all();   // limits and rows are written
       {
         constexpr int kWarpsQ = C::kSoftmax / 32, kPer = MB / kWarpsQ;   // rows of each warp
         uint4 u[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int r = warp - 2 + i * kWarpsQ;
-          u[i] = r < n_rows ? __ldg(p.q + out_row(r) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+          u[i] = r < n_rows ? __ldg(p.q + size_t(sm.row[r]) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -563,7 +591,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.q_full);
-      bar_all();   // limits and factors are written
+      bar_all();   // factors are written
 
       float ref[kR], ml[kR], l[kR];
 #pragma unroll
@@ -573,11 +601,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         l[r] = 0.f;
       }
       for (int j = 0; j < x.n_tiles; ++j, ++J) {
-        const int buf = int(J & 1);
+        const uint32_t buf = J & 1u;
         const int key = x.k_lo + j * kTile + key_in;
         const int tile_end = x.k_lo + (j + 1) * kTile;
         // This group's rows only; a group without rows keeps step with the others.
-        ok = ok && ptx::mbar_wait(&sm.s_full[buf], uint32_t(J >> 1) & 1u, tmo, &sm.abort);
+        ok = ok && wait(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
         uint2 w[kPTerms];
 #pragma unroll
         for (int t = 0; t < kPTerms; ++t) w[t] = make_uint2(0u, 0u);
@@ -585,9 +613,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           float s[kR], d[kR];   // log2 scores; with vs, minus p's reference
           float lv = 0.f;
           bool need = false;
-          ok = ok && ptx::mbar_wait(&sm.sc_full[J % kScaleRing], uint32_t(J / kScaleRing) & 1u, tmo,
+          ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo,
                                     &sm.abort);
           ok = warp_all(ok);
+          __syncwarp();
           if (ok) {
             ptx::tc_fence_after();
             float sk = sm.scale[J % kScaleRing][0][key_in >> p.bs_log2];
@@ -597,7 +626,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             } else {
               lv = log2_scale(sv);
             }
-            const uint32_t sa = trow + C::kTmS + uint32_t(buf) * C::kStep;
+            const uint32_t sa = trow + C::kTmS + buf * C::kStep;
             uint32_t a[8], b[8];
             if constexpr (kF16) {
               uint32_t c[8];
@@ -638,15 +667,18 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               stop = true;
               break;
             }
+            {
+              float v[2 * kR];
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-              const float a = ptx::warp_max_f32(s[r] + lv), c = ptx::warp_max_f32(s[r]);
-              if (lane == r) {
-                sm.red[0][rg * kR + r][qd] = a;
-                sm.red[1][rg * kR + r][qd] = c;
+              for (int r = 0; r < kR; ++r) {
+                v[r] = s[r] + lv;
+                v[kR + r] = s[r];
               }
+              const float m = warp_max16(v);
+              const int i = lane >> 1;
+              if ((lane & 1) == 0) sm.red[i >> 3][rg * kR + (i & 7)][qd] = m;
             }
-            ptx::named_bar_sync(bar_id, kGroupThreads);
+            ptx::named_bar_sync_any(bar_id, kGroupThreads);
             bool move = false;
             float alpha[kR];
 #pragma unroll
@@ -668,8 +700,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               d[r] = (s[r] - ref[r]) + lv;
             }
             if (move && j > 0) {   // the same in all threads: references and maxima are
-              ok = warp_all(ptx::mbar_wait(&sm.pv_done[buf ^ 1], uint32_t((J - 1) >> 1) & 1u, tmo,
+              ok = warp_all(wait(&sm.pv_done[buf ^ 1], ((J - 1) >> 1) & 1u, tmo,
                                            &sm.abort));
+              __syncwarp();
               if (ok) {
                 ptx::tc_fence_after();
 #pragma unroll 1
@@ -695,14 +728,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
         }
         if (rg == 0 && (tile_end > x.k_hi || tile_end > pr_lo)) {
-          ok = ok && ptx::mbar_wait(&sm.v_full[J % C::kVS], uint32_t(J / C::kVS) & 1u, tmo, &sm.abort);
+          ok = ok && wait(&sm.v_full[J % C::kVS], (J / C::kVS) & 1u, tmo, &sm.abort);
           if (ok && (key >= x.k_hi || key >= pr_lo) &&
               clean_v_row(sm.v[J % C::kVS], key_in, key >= x.k_hi))
             atomicOr(&sm.hit, 1ull << (key - pr_lo));
         }
         // (PV of tile J - 2 has read this buffer)
         if (J >= 2)
-          ok = ok && ptx::mbar_wait(&sm.pv_done[buf], uint32_t((J >> 1) - 1) & 1u, tmo, &sm.abort);
+          ok = ok && wait(&sm.pv_done[buf], ((J >> 1) - 1) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         if (ok) {
 #pragma unroll
@@ -717,7 +750,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       }
       // ---- the piece's sums and parts
       if (!stop) {
-        ok = ok && ptx::mbar_wait(&sm.o_full, pc & 1u, tmo, &sm.abort);
+        ok = ok && wait(&sm.o_full, pc & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
@@ -745,11 +778,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           inv[r] = L == 0.f ? 0.f : 1.f / L;
           ex[r] = ex2(0.5f * (ref[r] - ml[r]));
           if (fits && key_in == r && r < n_mine)
-            p.lse_parts[part0 + out_row(rg * kR + r)] =
+            p.lse_parts[part0 + sm.row[rg * kR + r]] =
                 L == 0.f ? -INFINITY : (ml[r] + __log2f(L)) * kLn2;
         }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          __syncwarp();
           uint32_t a[8], b[8], c[8];
           const uint32_t ta = trow + C::kTmO + h * C::kStep;
           ptx::tmem_ld8x3_wait(ta, ta + MB, ta + 2 * MB, a, b, c);
@@ -763,7 +797,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             o = o * inv[i] * ex[i] * ex[i];
             if (hits != 0ull)
               o = put_back_nan(p, x.b, x.g, hits, pr_lo, sm.lim[r], tree, base, sm.mask[r], dim, o);
-            p.o_parts[(part0 + out_row(r)) * 256 + dim] = o;
+            p.o_parts[(part0 + sm.row[r]) * 256 + dim] = o;
           }
         }
       }

@@ -353,6 +353,11 @@ __device__ __forceinline__ void tmem_st16_wait(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
+// The same for warps whose lanes may not be converged (bar.sync wants them to be).
+__device__ __forceinline__ void named_bar_sync_any(uint32_t id, uint32_t count) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Named barrier over `count` threads that also gives each the OR of their predicates.
 __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool v) {
   uint32_t r;
@@ -367,13 +372,6 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool v
       : "r"(id), "r"(count), "r"(uint32_t(v))
       : "memory");
   return r != 0;
-}
-
-// Largest value over the warp's lanes, NaN left out.
-__device__ __forceinline__ float warp_max_f32(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 // Named barrier over `count` threads (count a multiple of 32).
