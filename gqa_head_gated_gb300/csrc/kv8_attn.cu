@@ -93,12 +93,14 @@ struct __align__(1024) AttnSmem {
   uint64_t sc_full[kScaleRing];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_full, drain;
-  unsigned long long hit;                  // NaN V rows taken out: bit of key pr_lo + i
-  unsigned long long mask[MB];
-  long long base[kKv8Seqs + 1];            // first tile of each sequence's segments
-  int lim[MB];
-  int row[MB];                             // output row (token * Hq + head)
-  float fac[MB];
+  // by piece, two in turn
+  unsigned long long hit[2];               // NaN V rows taken out: bit of key pr_lo + i
+  unsigned long long mask[2][MB];          // tree mask of each row
+  int lim[2][MB];                          // keys before this one are seen
+  int row[2][MB];                          // output row (token * Hq + head)
+  float fac[2][MB];                        // scale of the row's Q terms, with log2(e) / 16
+  int4 seq[kKv8Seqs];                      // first token, rows, keys, tiles
+  uint32_t base[kKv8Seqs + 1];             // first tile of each sequence's segments
   alignas(16) float red[2][MB][4];         // read as float4
   uint32_t tmem_base;
   int abort, zero, stopped;
@@ -119,47 +121,45 @@ struct Piece {
   int rows, t0, kv_len;   // of the sequence
   int k_lo, k_hi;         // keys of the piece that some row of the block sees
   int n_tiles;
-  long long next;         // position after the piece
+  uint32_t next;          // position after the piece
   bool last;              // ends its segment
 };
 
-__device__ __forceinline__ bool seq_of(const Kv8AttnArgs& p, int b, int& t0, int& rows, int& kv) {
-  kv = p.kv_lens[b];
-  t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
-  rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
-  return rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
-         kv <= p.max_kv_len;
-}
-
 // The piece of this CTA's share that starts at `pos` (the share ends at `end`).
 template <int MB>
-__device__ __noinline__ Piece piece_at(const Kv8AttnArgs& p, const long long* base, long long pos,
-                                          long long end, long long W, long long n_cta) {
+__device__ __noinline__ Piece piece_at(const Kv8AttnArgs& p, const int4* seqs, const uint32_t* base,
+                                       uint32_t pos, uint32_t end, uint32_t n_cta) {
   Piece x;
   int lo = 0, hi = p.B - 1;   // last sequence that starts at or before pos
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (base[mid] <= pos) lo = mid; else hi = mid - 1;
   }
+  const int4 q = seqs[lo];
   x.b = lo;
-  seq_of(p, lo, x.t0, x.rows, x.kv_len);
-  const int n_rb = (x.rows * p.gqa + MB - 1) / MB;
-  const long long len = (x.kv_len + kTile - 1) / kTile;
-  const long long seg = (pos - base[lo]) / len;
+  x.t0 = q.x;
+  x.rows = q.y;
+  x.kv_len = q.z;
+  const uint32_t len = uint32_t(q.w), n_rb = uint32_t((x.rows * p.gqa + MB - 1) / MB);
+  const uint32_t seg = (pos - base[lo]) / len;
   x.g = int(seg / n_rb);
-  x.rb = int(seg - (long long)x.g * n_rb);
-  const long long start = base[lo] + seg * len, stop = start + len;
-  x.next = min(end, stop);
-  x.last = x.next == stop;
+  x.rb = int(seg - uint32_t(x.g) * n_rb);
+  const uint32_t start = base[lo] + seg * len;
+  x.next = min(end, start + len);
+  x.last = x.next == start + len;
   // the piece's part: this CTA's place among those that share the segment
-  x.s = int((long long)blockIdx.x - (((start + 1) * n_cta + W - 1) / W - 1));
+  x.s = 0;
+  if (pos != start) {
+    const unsigned long long W = base[p.B];
+    x.s = int(blockIdx.x) - int(((start + 1ull) * n_cta + W - 1) / W - 1);
+  }
   x.k_lo = int(pos - start) * kTile;
-  int n_hi = x.kv_len;        // a tree row may see up to the last key
+  x.k_hi = x.kv_len;          // a tree row may see up to the last key
   if (p.tree_mask == nullptr) {
     const int last_row = min(x.rows * p.gqa - 1, x.rb * MB + MB - 1) / p.gqa;
-    n_hi = x.kv_len - x.rows + last_row + 1;
+    x.k_hi = x.kv_len - x.rows + last_row + 1;
   }
-  x.k_hi = min(int(min((x.next - start) * kTile, (long long)n_hi)), n_hi);
+  if (!x.last) x.k_hi = min(x.k_hi, int(x.next - start) * kTile);
   x.n_tiles = x.k_hi > x.k_lo ? (x.k_hi - x.k_lo + kTile - 1) / kTile : 0;
   return x;
 }
@@ -286,10 +286,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   // ---- the schedule: tiles before each sequence, and this CTA's share of them
   int most = 0;   // tiles of the longest sequence
   for (int b = tid; b < p.B; b += C::kThreads) {
-    int t0, rows, kv;
-    const bool ok = seq_of(p, b, t0, rows, kv);
+    const int kv = p.kv_lens[b], t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
+    const int rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
+    const bool ok = rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
+                    kv <= p.max_kv_len;
     const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
-    sm.base[b + 1] = (long long)tiles * p.Hkv * ((rows * p.gqa + MB - 1) / MB);
+    sm.seq[b] = make_int4(t0, rows, kv, tiles);
+    sm.base[b + 1] = uint32_t(tiles) * uint32_t(p.Hkv) *
+                     (tiles > 0 ? uint32_t((rows * p.gqa + MB - 1) / MB) : 0u);
     most = max(most, tiles);
     if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
   }
@@ -316,7 +320,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     sm.abort = 0;
     sm.zero = 0;
     sm.stopped = 0;
-    sm.hit = 0ull;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -325,12 +328,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   }
   __syncthreads();
   if (warp == 0) {   // inclusive sums over the sequences, 32 at a time
-    long long run = 0;
+    uint32_t run = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      long long v = b0 + lane < p.B ? sm.base[b0 + lane + 1] : 0;
+      uint32_t v = b0 + lane < p.B ? sm.base[b0 + lane + 1] : 0u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
       }
       if (b0 + lane < p.B) sm.base[b0 + lane + 1] = run + v;
@@ -343,13 +346,16 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   most = *reinterpret_cast<const int*>(&sm.red[0][0][0]);
-  const long long W = sm.base[p.B];
+  const uint32_t W = sm.base[p.B];
   // Shares so long that no segment needs more than `parts` parts, and of one tile at least.
-  long long n_cta = min((long long)gridDim.x, W);
-  if (most > p.parts) n_cta = min(n_cta, max(1LL, W * (p.parts - 2) / most));
-  const bool works = (long long)blockIdx.x < n_cta;
-  const long long pos0 = works ? W * blockIdx.x / n_cta : 0;
-  const long long end = works ? W * (blockIdx.x + 1) / n_cta : 0;
+  uint32_t n_cta = min(gridDim.x, W);
+  if (most > p.parts)
+    n_cta = min(n_cta, max(1u, uint32_t((unsigned long long)W * uint32_t(p.parts - 2) / uint32_t(most))));
+  uint32_t pos0 = 0, end = 0;
+  if (blockIdx.x < n_cta) {
+    pos0 = uint32_t((unsigned long long)W * blockIdx.x / n_cta);
+    end = uint32_t((unsigned long long)W * (blockIdx.x + 1) / n_cta);
+  }
   __syncthreads();   // red is read before the softmax warps write it
 
   if (warp == 0) {
@@ -365,8 +371,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ptx::prefetch_tmap(&tmK);
       ptx::prefetch_tmap(&tmV);
     }
-    for (long long pos = pos0; ok && pos < end;) {
-      const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
+    for (uint32_t pos = pos0; ok && pos < end;) {
+      const Piece x = piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta);
       pos = x.next;
       const int* const table = p.tables + (long long)x.b * p.max_blocks;
       int at = x.k_lo + lane * bs;   // first key of this lane's block
@@ -470,8 +476,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         return true;
       };
       uint32_t pc = 0;   // pieces with tiles so far
-      for (long long pos = pos0; ok && pos < end;) {
-        const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
+      for (uint32_t pos = pos0; ok && pos < end;) {
+        const Piece x = piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta);
         pos = x.next;
         if (x.n_tiles == 0) continue;
         ok = wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
@@ -510,100 +516,170 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     uint32_t J = 0, pc = 0;
     bool ok = true;      // this thread's waits; agreed on at barriers before anyone leaves
     bool stop = false;   // the same in all threads of a group
-    for (long long pos = pos0; pos < end;) {
-      const Piece x = piece_at<MB>(p, sm.base, pos, end, W, n_cta);
-      pos = x.next;
-      const int P = x.rows * p.gqa, p0 = x.rb * MB, n_rows = min(MB, P - p0);
-      const int n_mine = min(max(n_rows - rg * kR, 0), kR);   // rows of this group
-      const int base = x.kv_len - x.rows;
-      const size_t part0 = size_t(x.s) * size_t(p.T) * p.Hq;
-      const auto out_row = [&](int r) {
+    uint32_t pos = pos0;
+    Piece x;
+    x.n_tiles = 0;
+    // Fetches the share's next piece with tiles into x; false at the share's end.  A piece
+    // without (no row of its block sees one of its keys) has empty parts.
+    const auto fetch = [&]() -> bool {
+      while (pos < end) {
+        x = piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta);
+        pos = x.next;
+        const bool fits = x.s >= 0 && x.s < p.parts;   // always, with shares as cut above
+        if (!fits && st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+        if (x.last && st == 0 && fits)
+          p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
+        if (!fits) x.s = -1;   // nothing of it is written
+        if (x.n_tiles > 0) return true;
+        const int pp = x.rb * MB + st, i = pp / p.gqa;
+        if (st < MB && pp < x.rows * p.gqa && fits)
+          p.lse_parts[size_t(x.s) * size_t(p.T) * p.Hq + size_t(x.t0 + i) * p.Hq + x.g * p.gqa +
+                      (pp - i * p.gqa)] = -INFINITY;
+      }
+      x.n_tiles = 0;
+      return false;
+    };
+    // Q's terms, the rows' limits and places of piece x, into half `par` of the piece arrays;
+    // then the products of the piece may start.  The last piece's S products are done.
+    const auto prepare = [&](uint32_t par) {
+      constexpr int kWarpsQ = C::kSoftmax / 32, kPer = MB / kWarpsQ;   // rows of each warp
+      const int p0 = x.rb * MB, n_rows = min(MB, x.rows * p.gqa - p0);
+      uint4 u[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int r = warp - 2 + k * kWarpsQ;
         const int i = (p0 + r) / p.gqa;
-        return (x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + r - i * p.gqa);
-      };
-      const bool fits = x.s >= 0 && x.s < p.parts;   // always, with shares as cut above
-      if (!fits && st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-      if (x.last && st == 0 && fits)
-        p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
-      if (x.n_tiles == 0) {   // no row of the block sees a key of the piece
-        if (st < n_rows && fits) p.lse_parts[part0 + out_row(st)] = -INFINITY;
-        continue;
-      }
-      // keys from pr_lo on are seen by some rows of the block only
-      const int pr_lo = max(x.k_lo, tree ? base : base + p0 / p.gqa + 1);
-
-      // ---- Q's terms and the rows' limits (the last piece's products are done)
-      bar_all();
-      if (sm.stopped) break;   // set before the barrier by a group that gave up
-      if (st < MB) {
-        int lim = 0;
-        unsigned long long m = 0ull;
-        if (st < n_rows) {
-          const int i = (p0 + st) / p.gqa;
-          lim = tree ? x.kv_len : base + i + 1;
-          if (tree) m = p.tree_mask[x.t0 + i];
+        const int row = (x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + r - i * p.gqa);
+        u[k] = r < n_rows ? __ldg(p.q + size_t(row) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+        if (lane == 0) {
+          sm.row[par][r] = row;
+          sm.lim[par][r] = r >= n_rows ? 0 : tree ? x.kv_len : x.kv_len - x.rows + i + 1;
+          sm.mask[par][r] = tree && r < n_rows ? p.tree_mask[x.t0 + i] : 0ull;
         }
-        sm.lim[st] = lim;
-        sm.row[st] = st < n_rows ? out_row(st) : 0;
-        sm.mask[st] = m;
       }
-      if (st == 0) sm.hit = 0ull;
-      bar_all();   // limits and rows are written
-      {
-        constexpr int kWarpsQ = C::kSoftmax / 32, kPer = MB / kWarpsQ;   // rows of each warp
-        uint4 u[kPer];
+      if (st == 0) sm.hit[par] = 0ull;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = warp - 2 + i * kWarpsQ;
-          u[i] = r < n_rows ? __ldg(p.q + size_t(sm.row[r]) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < kPer; ++k) {
+        const int r = warp - 2 + k * kWarpsQ;
+        float f[8];
+        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 a = unpack_elem2<kF16>(w[c]);
+          f[2 * c] = a.x;
+          f[2 * c + 1] = a.y;
         }
+        const int e = scale_exp(__reduce_max_sync(0xffffffffu, finite_amax_bits(f)));
+        if (lane == 0) sm.fac[par][r] = pow2f(e) * kScaleLog2;
+        const float inv = pow2f(-e);
+        // an infinite element makes its row's scores NaN, as in the formula
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = warp - 2 + i * kWarpsQ;
-          float f[8];
-          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 a = unpack_elem2<kF16>(w[c]);
-            f[2 * c] = a.x;
-            f[2 * c + 1] = a.y;
-          }
-          const int e = scale_exp(__reduce_max_sync(0xffffffffu, finite_amax_bits(f)));
-          if (lane == 0) sm.fac[r] = pow2f(e) * kScaleLog2;
-          const float inv = pow2f(-e);
-          // an infinite element makes its row's scores NaN, as in the formula
-#pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
-#pragma unroll
-          for (int t = 0; t < C::kQTerms; ++t) {
-            const int n = t * MB + r;
-            uint2 o;
-            o.x = take_term(f[0], f[1], 16.f);
-            o.x |= take_term(f[2], f[3], 16.f) << 16;
-            o.y = take_term(f[4], f[5], 16.f);
-            o.y |= take_term(f[6], f[7], 16.f) << 16;
-            *reinterpret_cast<uint2*>(sm.q[lane >> 4] + n * 128 +
-                                      ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8) = o;
-          }
+        for (int t = 0; t < C::kQTerms; ++t) {
+          const int n = t * MB + r;
+          uint2 o;
+          o.x = take_term(f[0], f[1], 16.f);
+          o.x |= take_term(f[2], f[3], 16.f) << 16;
+          o.y = take_term(f[4], f[5], 16.f);
+          o.y |= take_term(f[6], f[7], 16.f) << 16;
+          *reinterpret_cast<uint2*>(sm.q[lane >> 4] + n * 128 +
+                                    ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8) = o;
         }
       }
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.q_full);
-      bar_all();   // factors are written
+    };
 
-      float ref[kR], ml[kR], l[kR];
+    // The piece whose tiles are done and whose parts are due
+    int seq = 0, head = 0, s_idx = 0, n_mine = 0, base = 0, pr_lo = 0;
+    float ref[kR], ml[kR], l[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) ref[r] = ml[r] = l[r] = 0.f;
+    for (bool first = true;; first = false) {
+      // ---- the next piece may start while the last one ends (its S products are done)
+      bool more = false;
+      if (!stop) more = fetch();
+      if (more) prepare(pc & 1u);
+      if (!first) {
+        // ---- the last piece's sums and parts
+        const uint32_t par = (pc - 1u) & 1u;
+        ok = ok && wait(&sm.o_full, par, tmo, &sm.abort);
+        ok = warp_all(ok);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+          if (lane == r) sm.red[0][rg * kR + r][qd] = l[r];
+        }
+        stop = ptx::named_bar_or(bar_id, kGroupThreads, !ok);
+        if (stop) {
+          if (key_in == 0) sm.stopped = 1;
+          if (more) bar_all();
+          break;
+        }
+        ptx::tc_fence_after();
+        const size_t part0 = size_t(s_idx) * size_t(p.T) * p.Hq;
+        const unsigned long long hits = sm.hit[par];
+        if (n_mine > 0) {
+          float inv[kR], ex[kR];
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            const float4 a = *reinterpret_cast<const float4*>(sm.red[0][rg * kR + r]);
+            const float L = (a.x + a.y) + (a.z + a.w);
+            inv[r] = L == 0.f ? 0.f : 1.f / L;
+            ex[r] = ex2(0.5f * (ref[r] - ml[r]));
+            if (s_idx >= 0 && key_in == r && r < n_mine)
+              p.lse_parts[part0 + sm.row[par][rg * kR + r]] =
+                  L == 0.f ? -INFINITY : (ml[r] + __log2f(L)) * kLn2;
+          }
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+            uint32_t a[8], b[8], c[8];
+            const uint32_t ta = trow + C::kTmO + h * C::kStep;
+            ptx::tmem_ld8x3_wait(ta, ta + MB, ta + 2 * MB, a, b, c);
+            const int dim = h * 128 + key_in;
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+              if (i >= n_mine || s_idx < 0) continue;
+              const int r = rg * kR + i;
+              float o = fmaf(__uint_as_float(c[i]), 1.f / 1024.f,
+                             fmaf(__uint_as_float(b[i]), 1.f / 32.f, __uint_as_float(a[i])));
+              o = o * inv[i] * ex[i] * ex[i];
+              if (hits != 0ull)
+                o = put_back_nan(p, seq, head, hits, pr_lo, sm.lim[par][r], tree, base,
+                                 sm.mask[par][r], dim, o);
+              p.o_parts[(part0 + sm.row[par][r]) * 256 + dim] = o;
+            }
+          }
+        }
+        ptx::tc_fence_before();
+      }
+      if (!more) break;
+      bar_all();               // the piece's rows, limits and factors are written
+      if (sm.stopped) break;   // set before the barrier by a group that gave up
+      const uint32_t par = pc & 1u;
+      const int n_tiles = x.n_tiles, k_lo = x.k_lo, k_hi = x.k_hi;
+      seq = x.b;
+      head = x.g;
+      s_idx = x.s;
+      n_mine = min(max(x.rows * p.gqa - x.rb * MB - rg * kR, 0), kR);   // this group's rows
+      base = x.kv_len - x.rows;
+      // keys from pr_lo on are seen by some rows of the block only
+      pr_lo = max(k_lo, tree ? base : base + x.rb * MB / p.gqa + 1);
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         ref[r] = kNone;
         ml[r] = kNone;
         l[r] = 0.f;
       }
-      for (int j = 0; j < x.n_tiles; ++j, ++J) {
+      for (int j = 0; j < n_tiles; ++j, ++J) {
         const uint32_t buf = J & 1u;
-        const int key = x.k_lo + j * kTile + key_in;
-        const int tile_end = x.k_lo + (j + 1) * kTile;
+        const int key = k_lo + j * kTile + key_in;
+        const int tile_end = k_lo + (j + 1) * kTile;
         // This group's rows only; a group without rows keeps step with the others.
         ok = ok && wait(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
         uint2 w[kPTerms];
@@ -613,15 +689,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           float s[kR], d[kR];   // log2 scores; with vs, minus p's reference
           float lv = 0.f;
           bool need = false;
-          ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo,
-                                    &sm.abort);
+          ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
           ok = warp_all(ok);
           __syncwarp();
           if (ok) {
             ptx::tc_fence_after();
             float sk = sm.scale[J % kScaleRing][0][key_in >> p.bs_log2];
             const float sv = sm.scale[J % kScaleRing][1][key_in >> p.bs_log2];
-            if (key >= x.k_hi) {
+            if (key >= k_hi) {
               sk = 0.f;
             } else {
               lv = log2_scale(sv);
@@ -642,13 +717,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 s[r] = fmaf(__uint_as_float(b[r]), 0.0625f, __uint_as_float(a[r]));
             }
 #pragma unroll
-            for (int r = 0; r < kR; ++r) s[r] = s[r] * sm.fac[rg * kR + r] * sk;
-            if (tile_end > pr_lo || tile_end > x.k_hi) {
+            for (int r = 0; r < kR; ++r) s[r] = s[r] * sm.fac[par][rg * kR + r] * sk;
+            if (tile_end > pr_lo || tile_end > k_hi) {
 #pragma unroll
               for (int r = 0; r < kR; ++r) {
                 const bool vis =
-                    key < min(sm.lim[rg * kR + r], x.k_hi) &&
-                    (!tree || key < base || ((sm.mask[rg * kR + r] >> (key - base)) & 1ull));
+                    key < min(sm.lim[par][rg * kR + r], k_hi) &&
+                    (!tree || key < base || ((sm.mask[par][rg * kR + r] >> (key - base)) & 1ull));
                 if (!vis) s[r] = -INFINITY;
               }
             }
@@ -700,8 +775,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               d[r] = (s[r] - ref[r]) + lv;
             }
             if (move && j > 0) {   // the same in all threads: references and maxima are
-              ok = warp_all(wait(&sm.pv_done[buf ^ 1], ((J - 1) >> 1) & 1u, tmo,
-                                           &sm.abort));
+              ok = warp_all(wait(&sm.pv_done[buf ^ 1u], ((J - 1) >> 1) & 1u, tmo, &sm.abort));
               __syncwarp();
               if (ok) {
                 ptx::tc_fence_after();
@@ -727,15 +801,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             for (int t = 0; t < kPTerms; ++t) (i == 0 ? w[t].x : w[t].y) = lo[t] | (hi[t] << 16);
           }
         }
-        if (rg == 0 && (tile_end > x.k_hi || tile_end > pr_lo)) {
+        if (rg == 0 && (tile_end > k_hi || tile_end > pr_lo)) {
           ok = ok && wait(&sm.v_full[J % C::kVS], (J / C::kVS) & 1u, tmo, &sm.abort);
-          if (ok && (key >= x.k_hi || key >= pr_lo) &&
-              clean_v_row(sm.v[J % C::kVS], key_in, key >= x.k_hi))
-            atomicOr(&sm.hit, 1ull << (key - pr_lo));
+          if (ok && (key >= k_hi || key >= pr_lo) &&
+              clean_v_row(sm.v[J % C::kVS], key_in, key >= k_hi))
+            atomicOr(&sm.hit[par], 1ull << (key - pr_lo));
         }
-        // (PV of tile J - 2 has read this buffer)
-        if (J >= 2)
-          ok = ok && wait(&sm.pv_done[buf], ((J >> 1) - 1) & 1u, tmo, &sm.abort);
+        // PV of tile J - 2 has read this buffer: it was issued before S of tile J, whose
+        // completion (s_full) covers every product issued before it.
         ok = warp_all(ok);
         if (ok) {
 #pragma unroll
@@ -748,60 +821,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (lane == 0) ptx::mbar_arrive(&sm.p_full[buf]);
         }
       }
-      // ---- the piece's sums and parts
-      if (!stop) {
-        ok = ok && wait(&sm.o_full, pc & 1u, tmo, &sm.abort);
-        ok = warp_all(ok);
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-          if (lane == r) sm.red[0][rg * kR + r][qd] = l[r];
-        }
-        stop = ptx::named_bar_or(bar_id, kGroupThreads, !ok);
-      }
       ++pc;
       if (stop) {
-        // Tell the other groups, which stop at the next piece's barrier; their own waits
-        // run out too (this group's arrivals are missing).
+        // Tell the other groups, which stop at the next piece's barrier if there is one
+        // (their own waits run out too: this group's arrivals are missing), and be there.
         if (key_in == 0) sm.stopped = 1;
-        continue;
+        if (fetch()) bar_all();
+        break;
       }
-      ptx::tc_fence_after();
-      const unsigned long long hits = sm.hit;
-      if (n_mine > 0) {
-        float inv[kR], ex[kR];
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const float4 a = *reinterpret_cast<const float4*>(sm.red[0][rg * kR + r]);
-          const float L = (a.x + a.y) + (a.z + a.w);
-          inv[r] = L == 0.f ? 0.f : 1.f / L;
-          ex[r] = ex2(0.5f * (ref[r] - ml[r]));
-          if (fits && key_in == r && r < n_mine)
-            p.lse_parts[part0 + sm.row[rg * kR + r]] =
-                L == 0.f ? -INFINITY : (ml[r] + __log2f(L)) * kLn2;
-        }
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          __syncwarp();
-          uint32_t a[8], b[8], c[8];
-          const uint32_t ta = trow + C::kTmO + h * C::kStep;
-          ptx::tmem_ld8x3_wait(ta, ta + MB, ta + 2 * MB, a, b, c);
-          const int dim = h * 128 + key_in;
-#pragma unroll
-          for (int i = 0; i < kR; ++i) {
-            if (i >= n_mine || !fits) continue;
-            const int r = rg * kR + i;
-            float o = fmaf(__uint_as_float(c[i]), 1.f / 1024.f,
-                           fmaf(__uint_as_float(b[i]), 1.f / 32.f, __uint_as_float(a[i])));
-            o = o * inv[i] * ex[i] * ex[i];
-            if (hits != 0ull)
-              o = put_back_nan(p, x.b, x.g, hits, pr_lo, sm.lim[r], tree, base, sm.mask[r], dim, o);
-            p.o_parts[(part0 + sm.row[r]) * 256 + dim] = o;
-          }
-        }
-      }
-      ptx::tc_fence_before();
     }
     if (stop && key_in == 0) {
       sm.abort = 1;
@@ -856,7 +883,7 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_
   }
   const int mb = kv8_rows_per_block((long long)a.max_rows * a.gqa);
   const long long tiles = (a.max_kv_len + kTile - 1) / kTile;
-  const long long most = (long long)a.B * a.Hkv * a.max_rb * tiles;
+  const long long most = (long long)a.B * a.Hkv * a.max_rb * tiles;   // < 2^31: the caller's check
   const long long grid = most < sms ? most : sms;
   if (mb == 16)
     return f16 ? launch_t<16, true>(a, tmK, tmV, grid, stream)

@@ -15,8 +15,10 @@
 namespace gqa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kBatch = 8;   // parts whose loads are issued together
+constexpr int kThreads = 256;
+constexpr int kGroups = 4;     // each takes every fourth part of the row, 4 columns a thread
+constexpr int kBatch = 8;      // parts whose loads a thread issues together
+constexpr int kMaxParts = kThreads;
 
 struct MergeParams {
   const float* o_parts;
@@ -30,13 +32,18 @@ struct MergeParams {
   int B, T, Hq, Hkv, gqa, max_rows, max_kv_len, max_rb, rows_per_block, parts;
 };
 
-// Merges a row's parts, gates and rounds them: one warp a row, 8 of the 256 columns a lane.
-// Rows of no sequence, or of one that was skipped, are left as they are.
+// Merges a row's parts, gates and rounds them: one CTA a row.  Rows of no sequence, or of one
+// that was skipped, are left as they are.  A chain of reads bounds it (the row's sequence,
+// its count of parts, then lse and O side by side), so that a row's parts are spread over
+// four groups of threads with eight loads each in flight: with one warp a row, 39 parts took
+// 13 us, as long as a third of the split kernel at 2 x 131071 keys.
 template <bool kF16>
-__global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const MergeParams p) {
-  const int lane = threadIdx.x & 31;
-  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (n >= p.T * p.Hq) return;
+__global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p) {
+  __shared__ float s_w[kMaxParts];
+  __shared__ float s_red[2][kThreads / 32];
+  __shared__ float4 s_acc[kGroups - 1][64];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = blockIdx.x;
   const int t = n / p.Hq, h = n - t * p.Hq;
   int b = t, i = 0, rows = 1;
   if (p.cu_rows != nullptr) {
@@ -53,73 +60,96 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_merge_kernel(const MergeParam
   }
   const int kv_len = __ldg(p.kv_lens + b);
   if (kv_len < rows || kv_len > p.max_kv_len) return;
-  float gs[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-  if (p.gate != nullptr) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.gate + size_t(n) * 256 + lane * 8));
-    const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_elem2<kF16>(w4[e]);
-      gs[2 * e] = gate_sigmoid(f.x);
-      gs[2 * e + 1] = gate_sigmoid(f.y);
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int grp = tid >> 6, c4 = (tid & 63) * 4;
+  uint2 gate = make_uint2(0u, 0u);
+  if (p.gate != nullptr && grp == 0)
+    gate = __ldg(reinterpret_cast<const uint2*>(p.gate + size_t(n) * 256 + c4));
   const int g = h / p.gqa, rb = (i * p.gqa + h - g * p.gqa) / p.rows_per_block;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int cnt = min(__ldcg(p.n_parts + (size_t(b) * p.Hkv + g) * p.max_rb + rb), p.parts);
   const size_t stride = size_t(p.T) * p.Hq;
-  const float ls0 = lane < cnt ? __ldcg(p.lse_parts + lane * stride + n) : -INFINITY;
-  float M = ls0;   // fmaxf drops a NaN; a NaN part still gets weight NaN below
-  for (int s = lane + 32; s < cnt; s += 32) M = fmaxf(M, __ldcg(p.lse_parts + s * stride + n));
+  // the group's first parts are on their way while the weights are worked out
+  float4 v[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int s = grp + kGroups * u;
+    if (s < cnt)
+      v[u] = __ldcg(reinterpret_cast<const float4*>(p.o_parts + (s * stride + n) * 256 + c4));
+  }
+  const float ls = tid < cnt ? __ldcg(p.lse_parts + tid * stride + n) : -INFINITY;
+  float M = ls;   // fmaxf drops a NaN; a NaN part still gets weight NaN below
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) M = fmaxf(M, s_red[0][k]);
   const float msub = M == -INFINITY ? 0.f : M;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  for (int s0 = 0; s0 < cnt; s0 += 32) {
-    const int sl = s0 + lane;
-    const float ls = s0 == 0 ? ls0 : sl < cnt ? __ldcg(p.lse_parts + sl * stride + n) : -INFINITY;
-    const float wl = ls == -INFINITY ? 0.f : __expf(ls - msub);
-    const int here = min(32, cnt - s0);
-    for (int s1 = 0; s1 < here; s1 += kBatch) {
-      float w[kBatch];
-      float4 x[kBatch], y[kBatch];
+  const float wl = ls == -INFINITY ? 0.f : __expf(ls - msub);
+  s_w[tid] = wl;
+  float sum = wl;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_red[1][warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) sum += s_red[1][k];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = grp; s0 < cnt; s0 += kGroups * kBatch) {
+    if (s0 != grp) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        w[u] = __shfl_sync(0xffffffffu, wl, min(s1 + u, 31));
-        if (s1 + u >= here) w[u] = 0.f;
-        x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w[u] != 0.f) {
-          const float4* const src = reinterpret_cast<const float4*>(
-              p.o_parts + ((s0 + s1 + u) * stride + n) * 256 + lane * 8);
-          x[u] = __ldcg(src);
-          y[u] = __ldcg(src + 1);
-        }
+        const int s = s0 + kGroups * u;
+        if (s < cnt)
+          v[u] = __ldcg(reinterpret_cast<const float4*>(p.o_parts + (s * stride + n) * 256 + c4));
       }
+    }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        sum += w[u];
-        const float v[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += w[u] * v[k];
+    for (int u = 0; u < kBatch; ++u) {
+      const int s = s0 + kGroups * u;
+      const float w = s < cnt ? s_w[s] : 0.f;
+      if (w != 0.f) {   // (an empty part's O was not written)
+        acc.x += w * v[u].x;
+        acc.y += w * v[u].y;
+        acc.z += w * v[u].z;
+        acc.w += w * v[u].w;
       }
     }
   }
+  if (grp > 0) s_acc[grp - 1][tid & 63] = acc;
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int k = 0; k < kGroups - 1; ++k) {
+    const float4 x = s_acc[k][tid];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint4 o;
-  o.x = pack_elem2<kF16>(acc[0] * inv * gs[0], acc[1] * inv * gs[1]);
-  o.y = pack_elem2<kF16>(acc[2] * inv * gs[2], acc[3] * inv * gs[3]);
-  o.z = pack_elem2<kF16>(acc[4] * inv * gs[4], acc[5] * inv * gs[5]);
-  o.w = pack_elem2<kF16>(acc[6] * inv * gs[6], acc[7] * inv * gs[7]);
-  *reinterpret_cast<uint4*>(p.out + size_t(n) * 256 + lane * 8) = o;
-  if (p.lse_out != nullptr && lane == 0)
+  float gs[4] = {1.f, 1.f, 1.f, 1.f};
+  if (p.gate != nullptr) {
+    const float2 a = unpack_elem2<kF16>(gate.x), c = unpack_elem2<kF16>(gate.y);
+    gs[0] = gate_sigmoid(a.x);
+    gs[1] = gate_sigmoid(a.y);
+    gs[2] = gate_sigmoid(c.x);
+    gs[3] = gate_sigmoid(c.y);
+  }
+  uint2 o;
+  o.x = pack_elem2<kF16>(acc.x * inv * gs[0], acc.y * inv * gs[1]);
+  o.y = pack_elem2<kF16>(acc.z * inv * gs[2], acc.w * inv * gs[3]);
+  *reinterpret_cast<uint2*>(p.out + size_t(n) * 256 + c4) = o;
+  if (p.lse_out != nullptr && tid == 0)
     p.lse_out[n] = sum == 0.f ? -INFINITY : msub + __logf(sum);
 }
 
 template <bool kF16>
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((p.T * p.Hq + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3(unsigned(p.T) * unsigned(p.Hq));
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -129,7 +159,7 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel<kF16>, p);
   if (e == cudaSuccess)
     note_launch(kF16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", cfg.gridDim.x,
-                kWarps * 32, 0);
+                kThreads, 0);
   return e;
 }
 
@@ -151,6 +181,7 @@ Plan plan_decode8(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
   const long long even = 4 * sms / (B * units) + 2;
   if (parts > (even > 16 ? even : 16)) parts = even > 16 ? even : 16;
   if (parts > tiles) parts = tiles;
+  if (parts > kMaxParts) parts = kMaxParts;
   if (parts < 3) parts = 3;
   q.parts = int(parts);
   const size_t rows = size_t(parts) * T * Hq;
@@ -219,9 +250,14 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
   a.parts = plan.parts;
   if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  for (int b0 = 0; b0 < B; b0 += kKv8Seqs) {
+  // the kernel counts a launch's key tiles in 31 bits
+  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128);
+  if (per_seq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  const long long fit = ((1LL << 31) - 1) / per_seq;
+  const int step = fit < kKv8Seqs ? int(fit) : kKv8Seqs;
+  for (int b0 = 0; b0 < B; b0 += step) {
     a.b0 = b0;
-    a.B = B - b0 < kKv8Seqs ? B - b0 : kKv8Seqs;
+    a.B = B - b0 < step ? B - b0 : step;
     a.tables = block_tables + (long long)b0 * max_blocks;
     a.kv_lens = kv_lens + b0;
     a.cu_rows = cu_rows == nullptr ? nullptr : cu_rows + b0;
