@@ -311,42 +311,69 @@ def kv_keep(k_cache, v_cache, kv_lens, cu_rows, keep_idx, cu_keep, kv_lens_out=N
                              _stream()), "gqa_kv_keep")
 
 
-def _i32(t, numel, name):
+# The paged 8-bit cache.  A step's calls are short, so their checks are written to cost
+# little: each gives the tensor's address, and the message is made only for a refusal.
+_I32, _F32, _F8 = torch.int32, torch.float32, torch.float8_e4m3fn
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(d):
+    return (_raw_stream(d) if _raw_stream is not None
+            else torch.cuda.current_stream(d).cuda_stream)
+
+
+def _at(t, dtype, shape, d, name):
+    """Address of a contiguous CUDA tensor of this type and shape on device d."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == d and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {numel} entries")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on cuda:{d}, got "
+                     f"{tuple(t.shape)} on {t.device}")
 
 
-def _tables(block_tables, B):
+def _cuda_index(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _tables(block_tables, B, d):
+    """(address, max_blocks) of int32 block_tables [B, max_blocks]."""
     if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
         raise ValueError("block_tables must be an int32 CUDA tensor [B, max_blocks]")
-    _i32(block_tables, B * block_tables.shape[1], "block_tables")
-    return block_tables.shape[1]
+    m = block_tables.shape[1]
+    return _at(block_tables, _I32, (B, m), d, "block_tables"), m
 
 
 def _kv8_pools(k_pool, v_pool, k_scale, v_scale):
-    """(num_blocks, Hkv, block_size) of checked pools and scales."""
-    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        _need(t, torch.float8_e4m3fn, 4, name)
-    N, Hkv, bs, _ = k_pool.shape
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool must have the same shape")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
-            raise TypeError(f"{name} must be a float32 tensor")
-        if tuple(t.shape) != (N, Hkv) or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor [num_blocks, Hkv]")
-    return N, Hkv, bs
+    """Device, (num_blocks, Hkv, block_size) and addresses of checked pools and scales."""
+    d = _cuda_index(k_pool, "k_pool")
+    if k_pool.dim() != 4 or k_pool.shape[3] != HEAD_DIM:
+        raise ValueError(f"k_pool must be [num_blocks, Hkv, block_size, {HEAD_DIM}], got "
+                         f"{tuple(k_pool.shape)}")
+    shape = k_pool.shape
+    N, Hkv, bs, _ = shape
+    return d, N, Hkv, bs, (_at(k_pool, _F8, shape, d, "k_pool"), _at(v_pool, _F8, shape, d, "v_pool"),
+                           _at(k_scale, _F32, (N, Hkv), d, "k_scale"),
+                           _at(v_scale, _F32, (N, Hkv), d, "v_scale"))
 
 
-def _one_device(*tensors):
-    """The tensors' common device, made current for the call."""
-    d = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != d:
-            raise ValueError("the tensors of a call must be on one device")
-    return torch.cuda.device(d)
+def _call(name, d, *args):
+    """Runs an entry point on device d's current stream (its last argument)."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == d:
+        code = fn(*args, _stream_of(d))
+    else:
+        with torch.cuda.device(d):
+            code = fn(*args, _stream_of(d))
+    if code != 0:
+        raise GqaError(code, name)
 
 
 def block_plan(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, block_size, T,
@@ -362,27 +389,18 @@ def block_plan(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, 
     block_size + row; -1 without one) for kv8_append, and the lengths with the new rows for
     kv8_decode.  A sequence that the pool has no blocks for keeps its length, its slots are
     -1, and last_device_status() gives GQA_ERR_NO_BLOCKS (7)."""
-    B = kv_lens.numel()
-    _i32(kv_lens, B, "kv_lens")
-    _i32(cu_rows, B + 1, "cu_rows")
-    max_blocks = _tables(block_tables, B)
-    _i32(n_blocks, B, "n_blocks")
-    _i32(free_list, free_list.numel(), "free_list")
-    _i32(free_count, 1, "free_count")
-    T = int(T)
+    d = _cuda_index(kv_lens, "kv_lens")
+    B, T, N = kv_lens.numel(), int(T), free_list.numel()
     if slots is None:
-        slots = torch.empty(max(T, 0), dtype=torch.int32, device=kv_lens.device)
+        slots = torch.empty(max(T, 0), dtype=_I32, device=kv_lens.device)
     if kv_lens_out is None:
         kv_lens_out = torch.empty_like(kv_lens)
-    _i32(slots, T, "slots")
-    _i32(kv_lens_out, B, "kv_lens_out")
-    with _one_device(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, slots,
-                     kv_lens_out):
-        check(load().gqa_block_plan(_ptr(kv_lens), _ptr(cu_rows), _ptr(block_tables),
-                                    _ptr(n_blocks), _ptr(free_list), _ptr(free_count),
-                                    _ptr(slots), _ptr(kv_lens_out), B, T, max_blocks,
-                                    free_list.numel(), int(block_size), _stream()),
-              "gqa_block_plan")
+    tables, max_blocks = _tables(block_tables, B, d)
+    _call("gqa_block_plan", d, _at(kv_lens, _I32, (B,), d, "kv_lens"),
+          _at(cu_rows, _I32, (B + 1,), d, "cu_rows"), tables,
+          _at(n_blocks, _I32, (B,), d, "n_blocks"), _at(free_list, _I32, (N,), d, "free_list"),
+          _at(free_count, _I32, (1,), d, "free_count"), _at(slots, _I32, (T,), d, "slots"),
+          _at(kv_lens_out, _I32, (B,), d, "kv_lens_out"), B, T, max_blocks, N, int(block_size))
     return slots, kv_lens_out
 
 
@@ -393,17 +411,11 @@ def kv8_append(k_new, v_new, slots, k_pool, v_pool, k_scale, v_scale):
     block and head, kept as large as the block's rows ask (rows that a block holds already
     are rounded again when its scale grows)."""
     sfx = _elem(k_new, "k_new")
-    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
-        _need(t, k_new.dtype, 3, n)
-    N, Hkv, bs = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
-    T = k_new.shape[0]
-    if k_new.shape[1] != Hkv or v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must be [T, Hkv, 256] with the pools' Hkv")
-    _i32(slots, T, "slots")
-    with _one_device(k_new, v_new, slots, k_pool, v_pool, k_scale, v_scale):
-        fn = getattr(load(), "gqa_kv8_append" + sfx)
-        check(fn(_ptr(k_new), _ptr(v_new), _ptr(slots), _ptr(k_pool), _ptr(v_pool),
-                 _ptr(k_scale), _ptr(v_scale), T, Hkv, N, bs, _stream()), "gqa_kv8_append" + sfx)
+    d, N, Hkv, bs, pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    T, shape = k_new.shape[0], (k_new.shape[0], Hkv, HEAD_DIM)
+    _call("gqa_kv8_append" + sfx, d, _at(k_new, k_new.dtype, shape, d, "k_new"),
+          _at(v_new, k_new.dtype, shape, d, "v_new"), _at(slots, _I32, (T,), d, "slots"), *pools, T,
+          Hkv, N, bs)
 
 
 def kv8_keep(k_pool, v_pool, k_scale, v_scale, block_tables, kv_lens, cu_rows, keep_idx, cu_keep,
@@ -411,24 +423,20 @@ def kv8_keep(k_pool, v_pool, k_scale, v_scale, block_tables, kv_lens, cu_rows, k
     """kv_keep() for the paged 8-bit cache: the accepted draft rows (at most 64 per sequence)
     move to the front of each sequence's draft region, as if their values had been appended
     there; writes the new lengths into kv_lens_out when given."""
-    N, Hkv, bs = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
-    B = kv_lens.numel()
-    _i32(kv_lens, B, "kv_lens")
-    max_blocks = _tables(block_tables, B)
-    _i32(cu_rows, B + 1, "cu_rows")
-    _i32(keep_idx, keep_idx.numel(), "keep_idx")
-    _i32(cu_keep, B + 1, "cu_keep")
-    if kv_lens_out is not None:
-        _i32(kv_lens_out, B, "kv_lens_out")
-    with _one_device(k_pool, v_pool, k_scale, v_scale, block_tables, kv_lens, cu_rows, keep_idx,
-                     cu_keep, kv_lens_out):
-        check(load().gqa_kv8_keep(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                                  _ptr(block_tables), _ptr(kv_lens), _ptr(cu_rows),
-                                  _ptr(keep_idx), _ptr(cu_keep), _ptr(kv_lens_out),
-                                  keep_idx.numel(), B, Hkv, N, bs, max_blocks, _stream()), "gqa_kv8_keep")
+    d, N, Hkv, bs, pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    _cuda_index(kv_lens, "kv_lens")
+    _cuda_index(keep_idx, "keep_idx")
+    B, n = kv_lens.numel(), keep_idx.numel()
+    tables, max_blocks = _tables(block_tables, B, d)
+    _call("gqa_kv8_keep", d, *pools, tables, _at(kv_lens, _I32, (B,), d, "kv_lens"),
+          _at(cu_rows, _I32, (B + 1,), d, "cu_rows"), _at(keep_idx, _I32, (n,), d, "keep_idx"),
+          _at(cu_keep, _I32, (B + 1,), d, "cu_keep"),
+          None if kv_lens_out is None else _at(kv_lens_out, _I32, (B,), d, "kv_lens_out"), n, B,
+          Hkv, N, bs, max_blocks)
 
 
 def kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len):
+    """Bytes of workspace that kv8_decode() needs for these sizes (on the current device)."""
     return int(load().gqa_kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len))
 
 
@@ -441,44 +449,35 @@ def kv8_decode(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu
     [B+1] or None (one row per sequence).  Returns out [T,Hq,256]; rows behind cu_rows[B] (a
     padded batch) are left as they were in a given out."""
     sfx = _elem(q, "q")
-    _need(q, q.dtype, 3, "q")
-    N, Hkv, bs = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
-    if g is not None:
-        _need(g, q.dtype, 3, "g")
-        if g.shape != q.shape:
-            raise ValueError("g must have q's shape")
-    T, Hq, _ = q.shape
+    d, N, Hkv, bs, pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError(f"q must be [T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
+    T, Hq, _ = shape = q.shape
+    _cuda_index(kv_lens, "kv_lens")
     B = kv_lens.numel()
-    _i32(kv_lens, B, "kv_lens")
-    max_blocks = _tables(block_tables, B)
-    if cu_rows is not None:
-        _i32(cu_rows, B + 1, "cu_rows")
-    if tree_mask is not None and (tree_mask.dtype != torch.int64 or not tree_mask.is_cuda
-                                  or not tree_mask.is_contiguous() or tree_mask.numel() != T):
-        raise ValueError("tree_mask must be a contiguous int64 CUDA tensor of T entries")
+    tables, max_blocks = _tables(block_tables, B, d)
     if max_kv_len is None:           # synchronises; pass it to avoid the copy
         max_kv_len = max(1, int(kv_lens.max().item()))
     if max_rows is None:
         max_rows = 1 if cu_rows is None else max(1, int((cu_rows[1:] - cu_rows[:-1]).max().item()))
     if out is None:
         out = torch.empty_like(q)
-    _need(out, q.dtype, 3, "out")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
     if workspace is None:    # (a given workspace is checked by the library itself)
-        need = kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len)
+        with torch.cuda.device(d):
+            need = kv8_workspace_size(B, T, Hq, Hkv, max_rows, max_kv_len)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    with _one_device(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu_rows,
-                     tree_mask, workspace, out):
-        fn = getattr(load(), "gqa_kv8_decode" + sfx)
-        code = fn(_ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(g),
-                  _ptr(block_tables), _ptr(kv_lens), _ptr(cu_rows), _ptr(tree_mask), _ptr(out),
-                  _ptr(lse), B, T, Hq, Hkv, N, bs, max_blocks, int(max_rows), int(max_kv_len),
-                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream())
-    check(code, "gqa_kv8_decode" + sfx)
+    elif workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{d}")
+    lse = torch.empty((T, Hq), dtype=_F32, device=q.device) if return_lse else None
+    dt = q.dtype
+    _call("gqa_kv8_decode" + sfx, d, _at(q, dt, shape, d, "q"), *pools,
+          None if g is None else _at(g, dt, shape, d, "g"), tables,
+          _at(kv_lens, _I32, (B,), d, "kv_lens"),
+          None if cu_rows is None else _at(cu_rows, _I32, (B + 1,), d, "cu_rows"),
+          None if tree_mask is None else _at(tree_mask, torch.int64, (T,), d, "tree_mask"),
+          _at(out, dt, shape, d, "out"), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, N,
+          bs, max_blocks, int(max_rows), int(max_kv_len), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return (out, lse) if return_lse else out
 
 

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "device_common.cuh"
 
 namespace gqa {
@@ -76,6 +78,20 @@ cudaError_t launch_decode_split(const DecodeSplitArgs& a, const LaunchCtl& ctl,
 int tc_split_keys_multiple();
 cudaError_t launch_decode_split_tc(const DecodeSplitArgs& a, const LaunchCtl& ctl,
                                    cudaStream_t stream, bool* encode_failed);
+
+// cudaFuncSetAttribute(max dynamic shared memory) once per device and `done` word (one per
+// kernel instance): it costs a launch's host side more than the rest of a short call's checks.
+inline cudaError_t allow_smem_once(std::atomic<unsigned long long>& done, const void* kernel,
+                                   size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit != 0ull && (done.load(std::memory_order_acquire) & bit) != 0ull) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct MergeArgs {
   const float* O_parts;

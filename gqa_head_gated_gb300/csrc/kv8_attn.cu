@@ -855,8 +855,9 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
                      long long grid, cudaStream_t stream) {
   const size_t smem = sizeof(AttnSmem<MB, kF16>) + 1024;
   static_assert(sizeof(AttnSmem<MB, kF16>) + 1024 <= 227 * 1024, "one CTA per SM");
-  cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<MB, kF16>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e =
+      allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_attn_kernel<MB, kF16>), smem);
   if (e != cudaSuccess) return e;
   kv8_attn_kernel<MB, kF16><<<dim3(unsigned(grid)), Cfg<MB, kF16>::kThreads, smem, stream>>>(tmK, tmV, a);
   e = cudaGetLastError();

@@ -208,8 +208,9 @@ extern "C" int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block
   while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
   if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
   const size_t smem = (size_t(5) * B + 1) * sizeof(int);
-  if (cudaFuncSetAttribute(block_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           int((size_t(5) * kMaxSeqs + 1) * sizeof(int))) != cudaSuccess)
+  static std::atomic<unsigned long long> allowed{0};
+  if (allow_smem_once(allowed, reinterpret_cast<const void*>(block_plan_kernel),
+                      (size_t(5) * kMaxSeqs + 1) * sizeof(int)) != cudaSuccess)
     return GQA_ERR_CUDA;
   const unsigned ctas = kMaxCtas;
   cudaLaunchConfig_t cfg = {};
