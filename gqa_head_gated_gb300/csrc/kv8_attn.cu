@@ -70,8 +70,11 @@ struct Cfg {
   static constexpr int kThreads = 64 + kSoftmax;
   static constexpr int kNS = MB * kQTerms;       // columns of S^T
   static constexpr int kNO = MB * kPTerms;       // columns of each half of O^T
-  static constexpr int kKS = 3;                  // K slots
-  static constexpr int kVS = MB == 16 ? 3 : 2;   // V slots
+  // K and V slots of a tile each.  A K slot is free once S has read it, a V slot a softmax
+  // and a product later; with two and three the copies' order (K, V, K, V, ...) is the order
+  // in which slots come free.
+  static constexpr int kKS = MB == 16 ? 3 : 2;
+  static constexpr int kVS = 3;
   static constexpr uint32_t kStep = MB * 4;      // tensor-memory columns of each of
   static constexpr uint32_t kTmS = 0;            // the two S buffers
   static constexpr uint32_t kTmO = 2 * kStep;    // and the two halves of O
@@ -101,9 +104,9 @@ struct __align__(1024) AttnSmem {
   float fac[2][MB];                        // scale of the row's Q terms, with log2(e) / 16
   int4 seq[kKv8Seqs];                      // first token, rows, keys, tiles
   uint32_t base[kKv8Seqs + 1];             // first tile of each sequence's segments
-  alignas(16) float red[2][MB][4];         // read as float4
+  alignas(16) float red[C::kGroups][2 * kGroupRows][4];   // [group][value][warp], read as float4
   uint32_t tmem_base;
-  int abort, zero, stopped;
+  int abort, zero, stopped, failed[C::kGroups];
 };
 
 // ptx::mbar_wait with the polling loop out of line: the kernel has many waits, and its code
@@ -320,6 +323,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     sm.abort = 0;
     sm.zero = 0;
     sm.stopped = 0;
+    for (int i = 0; i < C::kGroups; ++i) sm.failed[i] = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -612,7 +616,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int r = 0; r < kR; ++r) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-          if (lane == r) sm.red[0][rg * kR + r][qd] = l[r];
+          if (lane == r) sm.red[rg][r][qd] = l[r];
         }
         stop = ptx::named_bar_or(bar_id, kGroupThreads, !ok);
         if (stop) {
@@ -627,7 +631,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           float inv[kR], ex[kR];
 #pragma unroll
           for (int r = 0; r < kR; ++r) {
-            const float4 a = *reinterpret_cast<const float4*>(sm.red[0][rg * kR + r]);
+            const float4 a = *reinterpret_cast<const float4*>(sm.red[rg][r]);
             const float L = (a.x + a.y) + (a.z + a.w);
             inv[r] = L == 0.f ? 0.f : 1.f / L;
             ex[r] = ex2(0.5f * (ref[r] - ml[r]));
@@ -737,8 +741,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             need = md > kSlack || me > kLSlack;
           }
           // ---- does a reference have to move (or has a wait run out)?
+          if (!ok) sm.failed[rg] = 1;
           if (ptx::named_bar_or(bar_id, kGroupThreads, need || !ok)) {
-            if (ptx::named_bar_or(bar_id, kGroupThreads, !ok)) {
+            if (sm.failed[rg]) {   // written before the barrier, by this group alone
               stop = true;
               break;
             }
@@ -750,28 +755,24 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 v[kR + r] = s[r];
               }
               const float m = warp_max16(v);
-              const int i = lane >> 1;
-              if ((lane & 1) == 0) sm.red[i >> 3][rg * kR + (i & 7)][qd] = m;
+              if ((lane & 1) == 0) sm.red[rg][lane >> 1][qd] = m;
             }
             ptx::named_bar_sync_any(bar_id, kGroupThreads);
+            // lane 2 i, 2 i + 1: the i-th maximum over the tile
+            const float4 q4 = *reinterpret_cast<const float4*>(sm.red[rg][lane >> 1]);
+            const float top = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
             bool move = false;
             float alpha[kR];
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-              const float4 a = *reinterpret_cast<const float4*>(sm.red[0][rg * kR + r]);
-              const float4 c = *reinterpret_cast<const float4*>(sm.red[1][rg * kR + r]);
-              const float ma = fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w));
-              const float mc = fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w));
-              alpha[r] = 1.f;
-              if (ma > ref[r] + kSlack) {
-                alpha[r] = ex2(ref[r] - (ma - kTop));
-                ref[r] = ma - kTop;
-                move = true;
-              }
-              if (mc > ml[r] + kLSlack) {
-                l[r] *= ex2(ml[r] - mc);
-                ml[r] = mc;
-              }
+              const float ma = __shfl_sync(0xffffffffu, top, 2 * r);
+              const float mc = __shfl_sync(0xffffffffu, top, 2 * (kR + r));
+              const bool up = ma > ref[r] + kSlack, up_l = mc > ml[r] + kLSlack;
+              alpha[r] = up ? ex2(ref[r] - (ma - kTop)) : 1.f;
+              ref[r] = up ? ma - kTop : ref[r];
+              move = move || up;
+              l[r] *= up_l ? ex2(ml[r] - mc) : 1.f;
+              ml[r] = up_l ? mc : ml[r];
               d[r] = (s[r] - ref[r]) + lv;
             }
             if (move && j > 0) {   // the same in all threads: references and maxima are
