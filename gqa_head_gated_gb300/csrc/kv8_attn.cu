@@ -55,7 +55,9 @@ constexpr int kSlotBytes = 2 * kHalfBytes;
 constexpr int kGroupRows = 8;                    // rows of one softmax thread
 constexpr int kGroupThreads = 128;               // one thread per key of a tile
 constexpr int kPTerms = 3;
-constexpr int kScaleRing = 8;      // tiles whose scales are held: see the producer
+constexpr int kScaleRing = 8;      // tiles whose scales are held: see the copies
+constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see the copies
+constexpr int kSwitch = 3;         // what going on to another segment costs, in tiles
 constexpr int kMaxTileBlocks = kTile / 16;
 constexpr float kSlack = 8.f;      // p <= 2^8
 constexpr float kTop = 5.f;        // a moved reference leaves the row's largest p at 2^5
@@ -84,6 +86,13 @@ struct Cfg {
   static constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, kNO, 1, 1, 0);
 };
 
+// A run of key tiles of one segment that one CTA takes.
+struct Piece {
+  int b, g, rb, s;            // sequence, KV head, row block, part (-1: nothing is written)
+  int rows, t0, kv_len;       // of the sequence
+  int k_lo, k_hi, n_tiles;    // keys that some row of the block sees; 0 tiles: the share's end
+};
+
 template <int MB, bool kF16>
 struct __align__(1024) AttnSmem {
   using C = Cfg<MB, kF16>;
@@ -95,6 +104,7 @@ struct __align__(1024) AttnSmem {
   uint64_t k_full[C::kKS], k_empty[C::kKS], v_full[C::kVS], v_empty[C::kVS];
   uint64_t sc_full[kScaleRing];
   uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t piece_full[kPieceRing];
   uint64_t q_full, o_full, drain;
   // by piece, two in turn
   unsigned long long hit[2];               // NaN V rows taken out: bit of key pr_lo + i
@@ -102,11 +112,12 @@ struct __align__(1024) AttnSmem {
   int lim[2][MB];                          // keys before this one are seen
   int row[2][MB];                          // output row (token * Hq + head)
   float fac[2][MB];                        // scale of the row's Q terms, with log2(e) / 16
+  Piece piece[kPieceRing];
   int4 seq[kKv8Seqs];                      // first token, rows, keys, tiles
   uint32_t base[kKv8Seqs + 1];             // first tile of each sequence's segments
   alignas(16) float red[C::kGroups][2 * kGroupRows][4];   // [group][value][warp], read as float4
   uint32_t tmem_base;
-  int abort, zero, stopped, failed[C::kGroups];
+  int abort, zero, failed[C::kGroups];
 };
 
 // ptx::mbar_wait with the polling loop out of line: the kernel has many waits, and its code
@@ -119,20 +130,14 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t tm
   return ptx::mbar_try_wait(ptx::smem_addr(bar), parity) || wait_slow(bar, parity, tmo, abort);
 }
 
-struct Piece {
-  int b, g, rb, s;        // sequence, KV head, row block, part
-  int rows, t0, kv_len;   // of the sequence
-  int k_lo, k_hi;         // keys of the piece that some row of the block sees
-  int n_tiles;
-  uint32_t next;          // position after the piece
-  bool last;              // ends its segment
-};
-
-// The piece of this CTA's share that starts at `pos` (the share ends at `end`).
+// The piece of this CTA's share [.., end) that starts at position `pos`, which moves on behind
+// it.  A segment takes kSwitch positions before those of its tiles: a CTA that goes on to it
+// from another has that much less to do.  `last`: the piece ends its segment.  False: the
+// piece has no position of a tile.
 template <int MB>
-__device__ __noinline__ Piece piece_at(const Kv8AttnArgs& p, const int4* seqs, const uint32_t* base,
-                                       uint32_t pos, uint32_t end, uint32_t n_cta) {
-  Piece x;
+__device__ __forceinline__ bool piece_at(const Kv8AttnArgs& p, const int4* seqs, const uint32_t* base,
+                                         uint32_t& pos, uint32_t end, uint32_t n_cta, Piece& x,
+                                         bool& last) {
   int lo = 0, hi = p.B - 1;   // last sequence that starts at or before pos
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -143,28 +148,30 @@ __device__ __noinline__ Piece piece_at(const Kv8AttnArgs& p, const int4* seqs, c
   x.t0 = q.x;
   x.rows = q.y;
   x.kv_len = q.z;
-  const uint32_t len = uint32_t(q.w), n_rb = uint32_t((x.rows * p.gqa + MB - 1) / MB);
+  const uint32_t len = uint32_t(q.w) + kSwitch, n_rb = uint32_t((x.rows * p.gqa + MB - 1) / MB);
   const uint32_t seg = (pos - base[lo]) / len;
   x.g = int(seg / n_rb);
   x.rb = int(seg - uint32_t(x.g) * n_rb);
-  const uint32_t start = base[lo] + seg * len;
-  x.next = min(end, start + len);
-  x.last = x.next == start + len;
-  // the piece's part: this CTA's place among those that share the segment
+  const uint32_t start = base[lo] + seg * len, first = start + kSwitch;
+  const uint32_t from = max(pos, first);
+  last = end >= start + len;
+  pos = min(end, start + len);
+  if (pos <= from) return false;
+  // the piece's part: this CTA's place among those that have tiles of the segment
   x.s = 0;
-  if (pos != start) {
+  if (from != first) {
     const unsigned long long W = base[p.B];
-    x.s = int(blockIdx.x) - int(((start + 1ull) * n_cta + W - 1) / W - 1);
+    x.s = int(blockIdx.x) - int(((first + 1ull) * n_cta - 1) / W);
   }
-  x.k_lo = int(pos - start) * kTile;
+  x.k_lo = int(from - first) * kTile;
   x.k_hi = x.kv_len;          // a tree row may see up to the last key
   if (p.tree_mask == nullptr) {
     const int last_row = min(x.rows * p.gqa - 1, x.rb * MB + MB - 1) / p.gqa;
     x.k_hi = x.kv_len - x.rows + last_row + 1;
   }
-  if (!x.last) x.k_hi = min(x.k_hi, int(x.next - start) * kTile);
+  if (!last) x.k_hi = min(x.k_hi, int(pos - first) * kTile);
   x.n_tiles = x.k_hi > x.k_lo ? (x.k_hi - x.k_lo + kTile - 1) / kTile : 0;
-  return x;
+  return true;
 }
 
 __device__ __forceinline__ float log2_scale(float s) {
@@ -286,7 +293,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const uint64_t tmo = p.ctl.timeout_ns;
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // ---- the schedule: tiles before each sequence, and this CTA's share of them
+  // ---- the schedule: positions before each sequence, and this CTA's share of them
   int most = 0;   // tiles of the longest sequence
   for (int b = tid; b < p.B; b += C::kThreads) {
     const int kv = p.kv_lens[b], t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
@@ -295,8 +302,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     kv <= p.max_kv_len;
     const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
     sm.seq[b] = make_int4(t0, rows, kv, tiles);
-    sm.base[b + 1] = uint32_t(tiles) * uint32_t(p.Hkv) *
-                     (tiles > 0 ? uint32_t((rows * p.gqa + MB - 1) / MB) : 0u);
+    sm.base[b + 1] = tiles > 0 ? uint32_t(tiles + kSwitch) * uint32_t(p.Hkv) *
+                                     uint32_t((rows * p.gqa + MB - 1) / MB)
+                               : 0u;
     most = max(most, tiles);
     if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
   }
@@ -312,6 +320,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ptx::mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(&sm.sc_full[i], 32);
+    for (int i = 0; i < kPieceRing; ++i) ptx::mbar_init(&sm.piece_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.s_full[i], 1);
       ptx::mbar_init(&sm.p_full[i], C::kSoftmax / 32);
@@ -322,7 +331,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     ptx::mbar_init(&sm.drain, 1);
     sm.abort = 0;
     sm.zero = 0;
-    sm.stopped = 0;
     for (int i = 0; i < C::kGroups; ++i) sm.failed[i] = 0;
     ptx::fence_mbar_init();
   }
@@ -351,7 +359,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const uint32_t tmem = sm.tmem_base;
   most = *reinterpret_cast<const int*>(&sm.red[0][0][0]);
   const uint32_t W = sm.base[p.B];
-  // Shares so long that no segment needs more than `parts` parts, and of one tile at least.
+  // Shares so long that no segment needs more than `parts` parts.
   uint32_t n_cta = min(gridDim.x, W);
   if (most > p.parts)
     n_cta = min(n_cta, max(1u, uint32_t((unsigned long long)W * uint32_t(p.parts - 2) / uint32_t(most))));
@@ -367,7 +375,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     // A tile's scales live in a ring of kScaleRing tiles without a release: tile J + 8 is
     // copied only once S of tile J + 8 - kKS >= J + 5 was issued, which waits for the
     // softmax of tile J + 3, so tile J's scales have been read.
-    static_assert(kScaleRing >= C::kKS + 3, "scale ring");
+    // So with the pieces' descriptions: a piece has a tile at least, so that when piece n + 8
+    // is published the softmax has passed tiles of piece n + 8 - kKS - 3 and with it piece n.
+    static_assert(kScaleRing >= C::kKS + 3 && kPieceRing >= C::kKS + 4, "rings");
     const int bs = 1 << p.bs_log2, per_tile = kTile >> p.bs_log2;
     uint32_t J = 0;
     bool ok = true;
@@ -375,9 +385,37 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ptx::prefetch_tmap(&tmK);
       ptx::prefetch_tmap(&tmV);
     }
+    uint32_t n_pieces = 0;
+    const auto publish = [&](const Piece& x) {
+      if (lane == 0) {
+        sm.piece[n_pieces % kPieceRing] = x;
+        ptx::mbar_arrive(&sm.piece_full[n_pieces % kPieceRing]);
+      }
+      ++n_pieces;
+    };
     for (uint32_t pos = pos0; ok && pos < end;) {
-      const Piece x = piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta);
-      pos = x.next;
+      Piece x;
+      bool last;
+      if (!piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta, x, last)) continue;
+      if (x.s < 0 || x.s >= p.parts) {   // never, with shares as cut above
+        if (lane == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+        x.s = -1;
+      }
+      const int n_rows = min(MB, x.rows * p.gqa - x.rb * MB);
+      {
+        const int pp = x.rb * MB + lane, i = pp / p.gqa;   // lane by row: MB <= 32
+        const size_t row = size_t(x.t0 + i) * p.Hq + x.g * p.gqa + (pp - i * p.gqa);
+        if (lane < n_rows) {
+          if (x.n_tiles == 0 && x.s >= 0)   // no row of the block sees a key of the piece
+            p.lse_parts[size_t(x.s) * size_t(p.T) * p.Hq + row] = -INFINITY;
+          for (int c = 0; c < 4; ++c)       // Q's rows, which the piece's start will wait for
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + row * 32 + c * 8));
+        }
+        if (last && lane == 0 && x.s >= 0)
+          p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
+      }
+      if (x.n_tiles == 0) continue;
+      publish(x);
       const int* const table = p.tables + (long long)x.b * p.max_blocks;
       int at = x.k_lo + lane * bs;   // first key of this lane's block
       int blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
@@ -426,6 +464,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           ptx::tma_load_2d(d + kHalfBytes, &tmV, &sm.v_full[vs], 128, row);
         }
       }
+    }
+    if (ok) {
+      Piece none{};
+      publish(none);   // (the share's end: no tiles)
     }
     if (!ok && lane == 0) {
       sm.abort = 1;
@@ -480,20 +522,21 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         return true;
       };
       uint32_t pc = 0;   // pieces with tiles so far
-      for (uint32_t pos = pos0; ok && pos < end;) {
-        const Piece x = piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta);
-        pos = x.next;
-        if (x.n_tiles == 0) continue;
+      while (ok) {
+        ok = wait(&sm.piece_full[pc % kPieceRing], (pc / kPieceRing) & 1u, tmo, &sm.abort);
+        if (!ok) break;
+        const int n_tiles = sm.piece[pc % kPieceRing].n_tiles;
+        if (n_tiles == 0) break;
         ok = wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
         if (!ok) break;
         ptx::tc_fence_after();
         ok = issue_s(J);
-        for (int j = 0; ok && j < x.n_tiles; ++j) {
-          if (j + 1 < x.n_tiles) ok = issue_s(J + j + 1);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          if (j + 1 < n_tiles) ok = issue_s(J + j + 1);
           if (ok) ok = issue_pv(J + j, j == 0);
         }
         if (ok) ptx::tc_commit(&sm.o_full);
-        J += x.n_tiles;
+        J += n_tiles;
         ++pc;
       }
       if (!ok) {
@@ -515,38 +558,27 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int st = tid - 64;                   // 0 .. kSoftmax - 1
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16) + uint32_t(rg * kR);
     const bool tree = p.tree_mask != nullptr;
-    const uint32_t bar_id = 1 + rg;            // barriers 1 .. kGroups; kGroups + 1 for all
-    const auto bar_all = [] { ptx::named_bar_sync_any(C::kGroups + 1, C::kSoftmax); };
+    const uint32_t bar_id = 1 + rg;            // this group's barrier
     uint32_t J = 0, pc = 0;
-    bool ok = true;      // this thread's waits; agreed on at barriers before anyone leaves
+    // This thread's waits.  A group agrees at its barriers before it leaves; across groups
+    // there are only bounded waits, so that none is left behind at a barrier.
+    bool ok = true;
     bool stop = false;   // the same in all threads of a group
-    uint32_t pos = pos0;
     Piece x;
-    x.n_tiles = 0;
-    // Fetches the share's next piece with tiles into x; false at the share's end.  A piece
-    // without (no row of its block sees one of its keys) has empty parts.
+    // The share's next piece into x; false at the share's end, or when the wait ran out.
+    uint32_t n_fetched = 0;
     const auto fetch = [&]() -> bool {
-      while (pos < end) {
-        x = piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta);
-        pos = x.next;
-        const bool fits = x.s >= 0 && x.s < p.parts;   // always, with shares as cut above
-        if (!fits && st == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-        if (x.last && st == 0 && fits)
-          p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
-        if (!fits) x.s = -1;   // nothing of it is written
-        if (x.n_tiles > 0) return true;
-        const int pp = x.rb * MB + st, i = pp / p.gqa;
-        if (st < MB && pp < x.rows * p.gqa && fits)
-          p.lse_parts[size_t(x.s) * size_t(p.T) * p.Hq + size_t(x.t0 + i) * p.Hq + x.g * p.gqa +
-                      (pp - i * p.gqa)] = -INFINITY;
-      }
-      x.n_tiles = 0;
-      return false;
+      ok = warp_all(ok && wait(&sm.piece_full[n_fetched % kPieceRing], (n_fetched / kPieceRing) & 1u,
+                               tmo, &sm.abort));
+      x = sm.piece[n_fetched % kPieceRing];
+      ++n_fetched;
+      return ok && x.n_tiles > 0;
     };
     // Q's terms, the rows' limits and places of piece x, into half `par` of the piece arrays;
     // then the products of the piece may start.  The last piece's S products are done.
     const auto prepare = [&](uint32_t par) {
       constexpr int kWarpsQ = C::kSoftmax / 32, kPer = MB / kWarpsQ;   // rows of each warp
+      static_assert(kPer == 2, "two rows a warp");
       const int p0 = x.rb * MB, n_rows = min(MB, x.rows * p.gqa - p0);
       uint4 u[kPer];
 #pragma unroll
@@ -562,11 +594,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
       }
       if (st == 0) sm.hit[par] = 0ull;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < kPer; ++k) {
         const int r = warp - 2 + k * kWarpsQ;
         float f[8];
-        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        const uint4 v = k == 0 ? u[0] : u[kPer - 1];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 a = unpack_elem2<kF16>(w[c]);
@@ -579,7 +612,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // an infinite element makes its row's scores NaN, as in the formula
 #pragma unroll
         for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < C::kQTerms; ++t) {
           const int n = t * MB + r;
           uint2 o;
@@ -604,26 +637,24 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     for (int r = 0; r < kR; ++r) ref[r] = ml[r] = l[r] = 0.f;
     for (bool first = true;; first = false) {
       // ---- the next piece may start while the last one ends (its S products are done)
-      bool more = false;
-      if (!stop) more = fetch();
+      const bool more = fetch();
       if (more) prepare(pc & 1u);
+      const uint32_t last_par = (pc - 1u) & 1u;
       if (!first) {
-        // ---- the last piece's sums and parts
-        const uint32_t par = (pc - 1u) & 1u;
-        ok = ok && wait(&sm.o_full, par, tmo, &sm.abort);
-        ok = warp_all(ok);
+        // ---- the last piece's sums
+        ok = warp_all(ok && wait(&sm.o_full, last_par, tmo, &sm.abort));
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
           if (lane == r) sm.red[rg][r][qd] = l[r];
         }
-        stop = ptx::named_bar_or(bar_id, kGroupThreads, !ok);
-        if (stop) {
-          if (key_in == 0) sm.stopped = 1;
-          if (more) bar_all();
-          break;
-        }
+      }
+      stop = ptx::named_bar_or(bar_id, kGroupThreads, !ok);
+      if (stop) break;
+      if (!first) {
+        // ---- and parts
+        const uint32_t par = last_par;
         ptx::tc_fence_after();
         const size_t part0 = size_t(s_idx) * size_t(p.T) * p.Hq;
         const unsigned long long hits = sm.hit[par];
@@ -663,9 +694,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ptx::tc_fence_before();
       }
       if (!more) break;
-      bar_all();               // the piece's rows, limits and factors are written
-      if (sm.stopped) break;   // set before the barrier by a group that gave up
       const uint32_t par = pc & 1u;
+      ok = ok && wait(&sm.q_full, par, tmo, &sm.abort);   // rows, limits, factors are written
       const int n_tiles = x.n_tiles, k_lo = x.k_lo, k_hi = x.k_hi;
       seq = x.b;
       head = x.g;
@@ -823,13 +853,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
       }
       ++pc;
-      if (stop) {
-        // Tell the other groups, which stop at the next piece's barrier if there is one
-        // (their own waits run out too: this group's arrivals are missing), and be there.
-        if (key_in == 0) sm.stopped = 1;
-        if (fetch()) bar_all();
-        break;
-      }
+      if (stop) break;
     }
     if (stop && key_in == 0) {
       sm.abort = 1;

@@ -250,8 +250,8 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
   a.parts = plan.parts;
   if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the kernel counts a launch's key tiles in 31 bits
-  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128);
+  // the kernel counts a launch's positions (a segment's tiles and a few more) in 31 bits
+  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128 + 8);
   if (per_seq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
   const long long fit = ((1LL << 31) - 1) / per_seq;
   const int step = fit < kKv8Seqs ? int(fit) : kKv8Seqs;
