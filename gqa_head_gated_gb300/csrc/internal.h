@@ -93,6 +93,29 @@ inline cudaError_t allow_smem_once(std::atomic<unsigned long long>& done, const 
   return e;
 }
 
+// Launches a kernel as a programmatic dependent of the stream's last one: it may be scheduled
+// while that one drains.  The kernel executes griddepcontrol.wait in every thread before it
+// touches global memory, so that stream order holds.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int block, size_t smem,
+                                    cudaStream_t stream, int cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct MergeArgs {
   const float* O_parts;
   const float* lse_parts;

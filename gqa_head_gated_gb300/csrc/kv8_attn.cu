@@ -291,23 +291,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t tmo = p.ctl.timeout_ns;
-  asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- the schedule: positions before each sequence, and this CTA's share of them
-  int most = 0;   // tiles of the longest sequence
-  for (int b = tid; b < p.B; b += C::kThreads) {
-    const int kv = p.kv_lens[b], t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
-    const int rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
-    const bool ok = rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
-                    kv <= p.max_kv_len;
-    const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
-    sm.seq[b] = make_int4(t0, rows, kv, tiles);
-    sm.base[b + 1] = tiles > 0 ? uint32_t(tiles + kSwitch) * uint32_t(p.Hkv) *
-                                     uint32_t((rows * p.gqa + MB - 1) / MB)
-                               : 0u;
-    most = max(most, tiles);
-    if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-  }
   if (tid == 0) {
     sm.base[0] = 0;
     sm.red[0][0][0] = 0.f;
@@ -337,6 +322,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (warp == 1) {
     ptx::tmem_alloc(&sm.tmem_base, C::kCols);
     ptx::tmem_relinquish();
+  }
+  wait_for_last();
+  let_next_start();   // not before: the merge reads lengths and gate ahead of its own wait
+  int most = 0;   // tiles of the longest sequence
+  for (int b = tid; b < p.B; b += C::kThreads) {
+    const int kv = p.kv_lens[b], t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
+    const int rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
+    const bool ok = rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
+                    kv <= p.max_kv_len;
+    const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
+    sm.seq[b] = make_int4(t0, rows, kv, tiles);
+    sm.base[b + 1] = tiles > 0 ? uint32_t(tiles + kSwitch) * uint32_t(p.Hkv) *
+                                     uint32_t((rows * p.gqa + MB - 1) / MB)
+                               : 0u;
+    most = max(most, tiles);
+    if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
   }
   __syncthreads();
   if (warp == 0) {   // inclusive sums over the sequences, 32 at a time
@@ -884,8 +885,8 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
   cudaError_t e =
       allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_attn_kernel<MB, kF16>), smem);
   if (e != cudaSuccess) return e;
-  kv8_attn_kernel<MB, kF16><<<dim3(unsigned(grid)), Cfg<MB, kF16>::kThreads, smem, stream>>>(tmK, tmV, a);
-  e = cudaGetLastError();
+  e = launch_dependent(kv8_attn_kernel<MB, kF16>, dim3(unsigned(grid)), Cfg<MB, kF16>::kThreads, smem,
+                       stream, 1, tmK, tmV, a);
   if (e == cudaSuccess) {
     char name[64];
     std::snprintf(name, sizeof(name), "kv8_attn_kernel<%d,%s>", MB, kF16 ? "fp16" : "bf16");

@@ -25,6 +25,27 @@ constexpr int kWindow = 64;               // tokens whose runs a CTA writes
 constexpr int kSpan = kWindow + 128;      // the last of them may reach a block further
 constexpr int kRowsPerWarp = kWindow / kWarps;
 
+// Largest |x| of a row's 256 elements (8 a lane) as fp32 bits, NaN and infinities left out;
+// *all: every element is finite.  16-bit magnitudes order as integers, two at a time; the
+// elements are looked at one by one only in a row that holds a NaN or an infinity.
+template <bool kF16>
+__device__ __forceinline__ uint32_t row_amax(uint4 u, bool* all) {
+  constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
+  const uint32_t w[4] = {u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu, u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu};
+  uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+  *all = m < kInf;
+  if (m >= kInf) {
+    m = 0u;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = w[i] & 0xFFFFu, b = w[i] >> 16;
+      m = max(m, max(a < kInf ? a : 0u, b < kInf ? b : 0u));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+  }
+  return __float_as_uint(elem_to_float<kF16>(m));
+}
+
 template <bool kF16>
 __device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -79,6 +100,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   const uint4* const x = p.x[kv];
   uint2* const pool = p.pool[kv];
 
+  let_next_start();
+  wait_for_last();
   // The window's rows are on their way while the runs are worked out.
   uint4 u[kRowsPerWarp];
 #pragma unroll
@@ -124,22 +147,21 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
     return f < kWindow && ((s_start[f >> 5] >> (f & 31)) & 1u) ? f : -1;
   };
   int run[kRowsPerWarp];
+  uint32_t finite = 0u;    // bit k: row k of this warp holds no NaN or infinity
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k) {
-    const int i = warp + k * kWarps;
-    run[k] = run_of(i);
+    run[k] = run_of(warp + k * kWarps);
     if (run[k] < 0) continue;
-    float f[8];
-    unpack8<kF16>(u[k], f);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, finite_amax_bits(f));
+    bool all;
+    const uint32_t m = row_amax<kF16>(u[k], &all);
+    finite |= uint32_t(all) << k;
     if (lane == 0) atomicMax(&s_max[run[k]], m);
   }
   for (int i = kWindow + warp; i < n_span; i += kWarps) {
     const int r = run_of(i);
     if (r < 0) break;   // past the last run
-    float f[8];
-    unpack8<kF16>(__ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), f);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, finite_amax_bits(f));
+    bool all;
+    const uint32_t m = row_amax<kF16>(__ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), &all);
     if (lane == 0) atomicMax(&s_max[r], m);
   }
   __syncthreads();
@@ -159,22 +181,22 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
     *sp = pow2f(e);
   }
   __syncthreads();
-  const auto put = [&](int i, int r, uint4 v) {
+  const auto put = [&](int i, int r, uint4 v, bool all) {
     float f[8];
     unpack8<kF16>(v, f);
     const float inv = pow2f(-s_exp[r]);
 #pragma unroll
     for (int c = 0; c < 8; ++c) f[c] *= inv;
     const int s = s_slot[i + 1];
-    pool[((size_t(s >> p.bs_log2) * p.Hkv + g) * bs + (s & (bs - 1))) * 32 + lane] = to_e4m3x8(f);
+    pool[((size_t(s >> p.bs_log2) * p.Hkv + g) * bs + (s & (bs - 1))) * 32 + lane] = all ? finite_to_e4m3x8(f) : to_e4m3x8(f);
   };
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k)
-    if (run[k] >= 0) put(warp + k * kWarps, run[k], u[k]);
+    if (run[k] >= 0) put(warp + k * kWarps, run[k], u[k], (finite >> k) & 1u);
   for (int i = kWindow + warp; i < n_span; i += kWarps) {
     const int r = run_of(i);
     if (r < 0) break;
-    put(i, r, __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane));
+    put(i, r, __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), false);
   }
   for (int j = 0; j < s_n_grown; ++j) {
     const int r = s_grown[j], s = s_slot[r + 1];
@@ -204,14 +226,16 @@ struct KeepParams {
 // One CTA: one sequence and KV head of K or V.  All kept rows are in registers before
 // the first is written (a block's scale may change while later rows of it are due).
 __global__ void __launch_bounds__(kThreads) kv8_keep_kernel(const KeepParams p) {
-  __shared__ int s_idx[kMaxKeep];
-  __shared__ int s_bad;
+  __shared__ int s_src[kMaxKeep];          // pool row (block * bs + row) of kept row k, and
+  __shared__ int s_dst[kMaxKeep];          // its place
   __shared__ uint32_t s_max[kMaxRuns];
   __shared__ int s_exp[kMaxRuns];
-  __shared__ float s_old;
+  __shared__ float s_old;                  // scale of the rows that stay before the first run
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x, g = blockIdx.y, kv = blockIdx.z;
   const int bs = 1 << p.bs_log2;
+  let_next_start();
+  wait_for_last();
   const int r = p.cu_rows[b + 1] - p.cu_rows[b];
   const int L = p.kv_lens[b];
   const int k0 = p.cu_keep[b], nk = p.cu_keep[b + 1] - k0;
@@ -220,39 +244,43 @@ __global__ void __launch_bounds__(kThreads) kv8_keep_kernel(const KeepParams p) 
   const bool ok = r >= 0 && L >= r && nk >= 0 && nk <= r && nk <= kMaxKeep && k0 >= 0 &&
                   (long long)k0 + nk <= p.n_keep &&
                   (long long)L <= ((long long)p.max_blocks << p.bs_log2);
-  if (tid == 0) s_bad = ok ? 0 : 1;
-  if (tid < kMaxRuns) s_max[tid] = 0u;
-  __syncthreads();
+  bool bad = !ok;
   if (ok && tid < nk) {
     const int i = p.keep_idx[k0 + tid];
-    s_idx[tid] = i;
     const int before = tid == 0 ? -1 : p.keep_idx[k0 + tid - 1];
-    const bool fine = i >= 0 && i < r && i > before;
-    const int src = fine ? table[(base + i) >> p.bs_log2] : -1;
-    const int dst = fine ? table[(base + tid) >> p.bs_log2] : -1;
-    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) s_bad = 1;
+    const int dst = table[(base + tid) >> p.bs_log2];
+    bad = i < 0 || i >= r || i <= before || dst < 0 || dst >= p.num_blocks;
+    const int src = bad ? -1 : table[(base + i) >> p.bs_log2];
+    bad = bad || src < 0 || src >= p.num_blocks;
+    s_src[tid] = (src << p.bs_log2) + ((base + i) & (bs - 1));
+    s_dst[tid] = (dst << p.bs_log2) + ((base + tid) & (bs - 1));
   }
-  __syncthreads();
-  if (s_bad) {
+  if (tid < kMaxRuns) s_max[tid] = 0u;
+  if (__syncthreads_or(bad)) {
     if (tid == 0 && g == 0 && kv == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
     return;
   }
   if (tid == 0 && g == 0 && kv == 0 && p.lens_out != nullptr) p.lens_out[b] = base + nk;
+  if (nk == 0) return;
   uint2* const pool = p.pool[kv];
   float* const scale = p.scale[kv];
-  const auto block_at = [&](int pos) { return size_t(table[pos >> p.bs_log2]) * p.Hkv + g; };
+  // 8-byte units of pool row `at`, and its block's scale
+  const auto row_of = [&](int at) {
+    return ((size_t(at >> p.bs_log2) * p.Hkv + g) * bs + (at & (bs - 1))) * 32;
+  };
+  const auto scale_of = [&](int at) { return scale + size_t(at >> p.bs_log2) * p.Hkv + g; };
   const int run0 = base >> p.bs_log2;
+  const int n_runs = ((base + nk - 1) >> p.bs_log2) - run0 + 1;
   uint2 q[kKeepPerWarp];
   float sc[kKeepPerWarp];
 #pragma unroll
   for (int k = 0; k < kKeepPerWarp; ++k) {
     const int i = warp + k * kWarps;
     if (i >= nk) continue;
-    const int pos = base + s_idx[i];
-    const size_t blk = block_at(pos);
-    q[k] = pool[(blk * bs + (pos & (bs - 1))) * 32 + lane];
-    sc[k] = scale[blk];
+    q[k] = pool[row_of(s_src[i]) + lane];
+    sc[k] = *scale_of(s_src[i]);
   }
+  if (tid == 0) s_old = *scale_of(s_dst[0]);
 #pragma unroll
   for (int k = 0; k < kKeepPerWarp; ++k) {
     const int i = warp + k * kWarps;
@@ -265,34 +293,28 @@ __global__ void __launch_bounds__(kThreads) kv8_keep_kernel(const KeepParams p) 
     if (lane == 0) atomicMax(&s_max[((base + i) >> p.bs_log2) - run0], m);
   }
   __syncthreads();   // every kept row and its scale are read
-  const int n_runs = nk == 0 ? 0 : ((base + nk - 1) >> p.bs_log2) - run0 + 1;
+  const int off0 = base & (bs - 1);
   if (tid < n_runs) {
-    float* const sp = scale + block_at((run0 + tid) << p.bs_log2);
     int e = scale_exp(s_max[tid]);
-    if (tid == 0 && (base & (bs - 1)) != 0) {
-      s_old = *sp;
-      e = max(e, stored_exp(s_old));
-    }
+    if (tid == 0 && off0 != 0) e = max(e, stored_exp(s_old));
     s_exp[tid] = e;
-    *sp = pow2f(e);
+    // the run's first row: kept row 0, or the first one of its block
+    *scale_of(s_dst[tid == 0 ? 0 : ((run0 + tid) << p.bs_log2) - base]) = pow2f(e);
   }
   __syncthreads();
-  if (nk == 0) return;
 #pragma unroll
   for (int k = 0; k < kKeepPerWarp; ++k) {
     const int i = warp + k * kWarps;
     if (i >= nk) continue;
-    const int pos = base + i;
-    const float inv = pow2f(-s_exp[(pos >> p.bs_log2) - run0]);
+    const float inv = pow2f(-s_exp[((base + i) >> p.bs_log2) - run0]);
     float f[8];
     from_e4m3x8(q[k], f);
 #pragma unroll
     for (int c = 0; c < 8; ++c) f[c] = f[c] * sc[k] * inv;
-    pool[(block_at(pos) * bs + (pos & (bs - 1))) * 32 + lane] = to_e4m3x8(f);
+    pool[row_of(s_dst[i]) + lane] = to_e4m3x8(f);
   }
-  const int off0 = base & (bs - 1);
   if (off0 != 0 && pow2f(s_exp[0]) != s_old)
-    rescale_rows(pool + block_at(base) * bs * 32, off0, s_old, s_exp[0]);
+    rescale_rows(pool + row_of(s_dst[0] - off0), off0, s_old, s_exp[0]);
 }
 
 int log2_of(int block_size) {
@@ -331,11 +353,9 @@ int append_impl(bool f16, const void* Knew, const void* Vnew, const int* slots, 
   if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
   const dim3 grid((T + kWindow - 1) / kWindow, Hkv, 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (f16)
-    kv8_append_kernel<true><<<grid, kThreads, 0, s>>>(p);
-  else
-    kv8_append_kernel<false><<<grid, kThreads, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
+  if (launch_dependent(f16 ? kv8_append_kernel<true> : kv8_append_kernel<false>, grid, kThreads, 0,
+                       s, 1, p) != cudaSuccess)
+    return GQA_ERR_CUDA;
   note_launch(f16 ? "kv8_append_kernel<fp16>" : "kv8_append_kernel<bf16>",
               (long long)grid.x * grid.y * grid.z, kThreads, 0);
   return GQA_OK;
@@ -397,8 +417,9 @@ int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
   p.bs_log2 = log2_of(block_size);
   if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
   const dim3 grid(B, Hkv, 2);
-  kv8_keep_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
+  if (launch_dependent(kv8_keep_kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), 1, p) !=
+      cudaSuccess)
+    return GQA_ERR_CUDA;
   note_launch("kv8_keep_kernel", (long long)B * Hkv * 2, kThreads, 0);
   return GQA_OK;
 }

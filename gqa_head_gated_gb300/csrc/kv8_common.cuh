@@ -14,6 +14,17 @@
 namespace gqa {
 namespace {
 
+// The cache's kernels are launched as programmatic dependents, one after another: each lets
+// the next be scheduled early, and waits for the last before it touches global memory.  (The
+// merge alone reads inputs of the call before its wait, so the split kernel before it lets it
+// start only after its own.)
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_last() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 constexpr int kMinScaleExp = -126;   // an all-zero run's scale: the smallest normal power of two
 
 // 2^e for e in [-126, 127].
@@ -66,6 +77,15 @@ __device__ __forceinline__ void from_e4m3x8(uint2 u, float (&f)[8]) {
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&f)[8]) {
   return make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16),
                     to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
+}
+
+// The same for values that are all finite.
+__device__ __forceinline__ uint2 finite_to_e4m3x8(const float (&f)[8]) {
+  const auto two = [](float lo, float hi) -> uint32_t {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+  };
+  return make_uint2(two(f[0], f[1]) | (two(f[2], f[3]) << 16),
+                    two(f[4], f[5]) | (two(f[6], f[7]) << 16));
 }
 
 // Largest |x| of eight values as fp32 bits, NaN and infinities left out.

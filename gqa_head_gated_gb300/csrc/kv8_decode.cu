@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
   __shared__ float4 s_acc[kGroups - 1][64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = blockIdx.x;
+  let_next_start();
   const int t = n / p.Hq, h = n - t * p.Hq;
   int b = t, i = 0, rows = 1;
   if (p.cu_rows != nullptr) {
@@ -56,16 +57,20 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
     b = lo;
     i = t - t0;
     rows = t1 - t0;
-    if (t0 < 0 || i < 0 || t >= t1 || t1 > p.T || rows > p.max_rows) return;
+    if (t0 < 0 || i < 0 || t >= t1 || t1 > p.T || rows > p.max_rows) b = -1;
   }
-  const int kv_len = __ldg(p.kv_lens + b);
-  if (kv_len < rows || kv_len > p.max_kv_len) return;
+  const int kv_len = b < 0 ? -1 : __ldg(p.kv_lens + b);
+  if (kv_len < rows || kv_len > p.max_kv_len) b = -1;
+  if (b < 0) {   // (rows >= 1 where there is a row)
+    wait_for_last();
+    return;
+  }
   const int grp = tid >> 6, c4 = (tid & 63) * 4;
   uint2 gate = make_uint2(0u, 0u);
   if (p.gate != nullptr && grp == 0)
     gate = __ldg(reinterpret_cast<const uint2*>(p.gate + size_t(n) * 256 + c4));
   const int g = h / p.gqa, rb = (i * p.gqa + h - g * p.gqa) / p.rows_per_block;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_last();
   const int cnt = min(__ldcg(p.n_parts + (size_t(b) * p.Hkv + g) * p.max_rb + rb), p.parts);
   const size_t stride = size_t(p.T) * p.Hq;
   // the group's first parts are on their way while the weights are worked out
@@ -147,19 +152,10 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
 
 template <bool kF16>
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.T) * unsigned(p.Hq));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel<kF16>, p);
+  const unsigned rows = unsigned(p.T) * unsigned(p.Hq);
+  const cudaError_t e = launch_dependent(kv8_merge_kernel<kF16>, dim3(rows), kThreads, 0, stream, 1, p);
   if (e == cudaSuccess)
-    note_launch(kF16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", cfg.gridDim.x,
-                kThreads, 0);
+    note_launch(kF16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", rows, kThreads, 0);
   return e;
 }
 

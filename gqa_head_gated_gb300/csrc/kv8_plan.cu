@@ -25,6 +25,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSeqs = 8192;    // sequences a launch plans: 5 words of shared memory each
 constexpr int kMaxCtas = 8;       // the portable cluster size
+constexpr int kUnroll = 4;
 
 struct PlanParams {
   const int* kv_lens;
@@ -96,6 +97,8 @@ block_plan_kernel(const PlanParams p) {
   const int cta = blockIdx.x, ctas = gridDim.x;   // the grid is one cluster
   const long long cap = (long long)p.max_blocks << bs_log2;
 
+  let_next_start();
+  wait_for_last();
   for (int b = tid; b <= B; b += kThreads) s_cu[b] = p.cu_rows[b];
   const int fc_read = *p.free_count;
   const int fc = min(max(fc_read, 0), p.num_blocks);
@@ -162,21 +165,32 @@ block_plan_kernel(const PlanParams p) {
   }
   if (p.T == 0) return;
   ptx::cluster_sync();
-  for (int t = cta * kThreads + tid; t < p.T; t += ctas * kThreads) {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_cu[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    const int have = s_have[lo];
-    int slot = -1;
-    if (have >= 0 && t >= s_cu[lo] && t < s_cu[lo + 1]) {
+  // Slots, kUnroll tokens a thread at a time: their table reads are in flight together.
+  const int per = ctas * kThreads;
+  for (int t0 = cta * kThreads + tid; t0 < p.T; t0 += kUnroll * per) {
+    int row[kUnroll], blk[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int t = t0 + u * per;
+      row[u] = -1;
+      if (t >= p.T) continue;
+      int lo = 0, hi = B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const int have = s_have[lo];
+      if (have < 0 || t < s_cu[lo] || t >= s_cu[lo + 1]) continue;
       const int n = need_of(lo) - have, pos = s_len[lo] + t - s_cu[lo];
-      if (n <= 0 || (long long)s_grow[lo] + n <= avail)
-        slot = (__ldcg(p.tables + (long long)lo * p.max_blocks + (pos >> bs_log2)) << bs_log2) +
-               (pos & (bs - 1));
+      if (n > 0 && (long long)s_grow[lo] + n > avail) continue;
+      row[u] = pos & (bs - 1);
+      blk[u] = __ldcg(p.tables + (long long)lo * p.max_blocks + (pos >> bs_log2));
     }
-    p.slots[t] = slot;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int t = t0 + u * per;
+      if (t < p.T) p.slots[t] = row[u] < 0 ? -1 : (blk[u] << bs_log2) + row[u];
+    }
   }
 }
 
@@ -212,20 +226,12 @@ extern "C" int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block
   if (allow_smem_once(allowed, reinterpret_cast<const void*>(block_plan_kernel),
                       (size_t(5) * kMaxSeqs + 1) * sizeof(int)) != cudaSuccess)
     return GQA_ERR_CUDA;
-  const unsigned ctas = kMaxCtas;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, block_plan_kernel, p) != cudaSuccess) return GQA_ERR_CUDA;
+  // One CTA for a decode step (a barrier of a cluster of one costs little), a full cluster
+  // where there is work to share.
+  const int ctas = B > 2 * kThreads || T > 4 * kThreads ? kMaxCtas : 1;
+  if (launch_dependent(block_plan_kernel, dim3(unsigned(ctas)), kThreads, smem,
+                       static_cast<cudaStream_t>(stream), ctas, p) != cudaSuccess)
+    return GQA_ERR_CUDA;
   note_launch("block_plan_kernel", ctas, kThreads, smem);
   return GQA_OK;
 }

@@ -287,6 +287,60 @@ def test_other_stream_graph_and_two_workspaces():
     assert torch.equal(outs[0], b) and G.last_device_status() == 0
 
 
+def test_a_whole_step_in_one_graph():
+    """Plan, append and decode captured behind copies and in front of them, then replayed with other
+    lengths and rows: each replay equals the same calls made eagerly on a copy of the state."""
+    B, Hq, Hkv, bs, N, width = 4, 12, 2, 32, 40, 8
+    gen = torch.Generator().manual_seed(90)
+    pool = lambda: torch.zeros(N, Hkv, bs, 256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)  # noqa: E731
+
+    def state():
+        return dict(tables=i32([[-1] * width] * B), n=i32([0] * B), free=i32(list(range(N))), fc=i32([N]),
+                    lens=i32([0] * B), k=pool(), v=pool(), ks=torch.ones(N, Hkv, device=DEV),
+                    vs=torch.ones(N, Hkv, device=DEV))
+
+    T = 8
+    cu, out = i32([0] * (B + 1)), torch.zeros(T, Hq, 256, dtype=torch.bfloat16, device=DEV)
+    kn, vn = (torch.zeros(T, Hkv, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q, g = (torch.zeros(T, Hq, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    src = [torch.zeros_like(x) for x in (kn, vn, q, g, cu)]
+    ws = torch.empty(G.kv8_workspace_size(B, T, Hq, Hkv, T, width * bs), dtype=torch.uint8, device=DEV)
+    last = torch.zeros_like(out)
+
+    def step(s, dst):
+        for a, b in zip((kn, vn, q, g, cu), src):
+            a.copy_(b)
+        slots, lens = G.block_plan(s["lens"], cu, s["tables"], s["n"], s["free"], s["fc"], bs, T)
+        G.kv8_append(kn, vn, slots, s["k"], s["v"], s["ks"], s["vs"])
+        G.kv8_decode(q, s["k"], s["v"], s["ks"], s["vs"], g, s["tables"], lens, cu, max_rows=T,
+                     max_kv_len=width * bs, workspace=ws, out=dst)
+        s["lens"].copy_(lens)
+        last.copy_(dst)
+
+    a, b = state(), state()
+    eager = torch.zeros_like(out)
+    step(state(), eager)                      # first use of every kernel, outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a, out)
+    for key in a:                             # (capture runs nothing)
+        a[key].view(torch.uint8).copy_(b[key].view(torch.uint8))
+    for rows in ([3, 1, 4, 0], [1, 1, 1, 1], [0, 2, 0, 6], [1, 0, 5, 1], [2, 2, 2, 2]):
+        fill = [torch.randn(x.shape, generator=gen).to(x.dtype) for x in (kn, vn, q, g)]
+        for d, x in zip(src, fill + [torch.tensor(cu_of(rows), dtype=torch.int32)]):
+            d.copy_(x)
+        out.zero_(), eager.zero_()
+        graph.replay()
+        got = last.clone()
+        step(b, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(got, eager)
+        for key in a:
+            assert torch.equal(a[key].view(torch.uint8), b[key].view(torch.uint8)), key
+    assert G.last_device_status() == 0
+
+
 def test_rounds_of_serving():
     """Plan, append, decode, a tree of drafts, keep, and the next step, all captured state on the GPU:
     the cache equals the oracle's after every step, the rows its attention's."""
