@@ -41,29 +41,16 @@
 
 #include <cstdio>
 
-#include "kv8_attn.h"
-#include "kv8_common.cuh"
-#include "ptx_sm100.cuh"
-#include "tc_common.cuh"
+#include "kv8_attn.cuh"
 
 namespace gqa {
 namespace {
 
-constexpr int kTile = 128;                       // keys per tile
-constexpr int kHalfBytes = kTile * 128;          // 128 keys x 128 dims of K or V
-constexpr int kSlotBytes = 2 * kHalfBytes;
 constexpr int kGroupRows = 8;                    // rows of one softmax thread
 constexpr int kGroupThreads = 128;               // one thread per key of a tile
 constexpr int kPTerms = 3;
-constexpr int kScaleRing = 8;      // tiles whose scales are held: see the copies
-constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see the copies
-constexpr int kSwitch = 3;         // what going on to another segment costs, in tiles
-constexpr int kMaxTileBlocks = kTile / 16;
 constexpr float kSlack = 8.f;      // p <= 2^8
 constexpr float kTop = 5.f;        // a moved reference leaves the row's largest p at 2^5
-constexpr float kLSlack = 64.f;    // l's terms stay below 2^64
-constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
-
 template <int MB, bool kF16>
 struct Cfg {
   static constexpr int kQTerms = kF16 ? 3 : 2;
@@ -86,25 +73,13 @@ struct Cfg {
   static constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, kNO, 1, 1, 0);
 };
 
-// A run of key tiles of one segment that one CTA takes.
-struct Piece {
-  int b, g, rb, s;            // sequence, KV head, row block, part (-1: nothing is written)
-  int rows, t0, kv_len;       // of the sequence
-  int k_lo, k_hi, n_tiles;    // keys that some row of the block sees; 0 tiles: the share's end
-};
-
 template <int MB, bool kF16>
-struct __align__(1024) AttnSmem {
+struct __align__(1024) AttnSmem : RingSmem<Cfg<MB, kF16>::kKS, Cfg<MB, kF16>::kVS> {
   using C = Cfg<MB, kF16>;
-  uint8_t q[2][C::kNS * 128];              // [half of D][column][128 bytes, swizzled]
+  alignas(1024) uint8_t q[2][C::kNS * 128];   // [half of D][column][128 bytes, swizzled]
   uint8_t p[2][C::kNO * kTile];            // [buffer][16 columns][key][16 bytes]
-  uint8_t k[C::kKS][kSlotBytes];
-  uint8_t v[C::kVS][kSlotBytes];
-  float scale[kScaleRing][2][kMaxTileBlocks];
-  uint64_t k_full[C::kKS], k_empty[C::kKS], v_full[C::kVS], v_empty[C::kVS];
-  uint64_t sc_full[kScaleRing];
+  alignas(16) float red[C::kGroups][2 * kGroupRows][4];   // [group][value][warp], read as float4
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t piece_full[kPieceRing];
   uint64_t q_full, o_full, drain;
   // by piece, two in turn
   unsigned long long hit[2];               // NaN V rows taken out: bit of key pr_lo + i
@@ -112,106 +87,8 @@ struct __align__(1024) AttnSmem {
   int lim[2][MB];                          // keys before this one are seen
   int row[2][MB];                          // output row (token * Hq + head)
   float fac[2][MB];                        // scale of the row's Q terms, with log2(e) / 16
-  Piece piece[kPieceRing];
-  int4 seq[kKv8Seqs];                      // first token, rows, keys, tiles
-  uint32_t base[kKv8Seqs + 1];             // first tile of each sequence's segments
-  alignas(16) float red[C::kGroups][2 * kGroupRows][4];   // [group][value][warp], read as float4
-  uint32_t tmem_base;
-  int abort, zero, failed[C::kGroups];
+  int failed[C::kGroups];
 };
-
-// ptx::mbar_wait with the polling loop out of line: the kernel has many waits, and its code
-// has to stay small (inlined, they made it 114 KB, whose instruction fetches took thousands
-// of cycles wherever a path had not run for a while).
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t tmo, int* abort) {
-  return ptx::mbar_wait(bar, parity, tmo, abort);
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t tmo, int* abort) {
-  return ptx::mbar_try_wait(ptx::smem_addr(bar), parity) || wait_slow(bar, parity, tmo, abort);
-}
-
-// The piece of this CTA's share [.., end) that starts at position `pos`, which moves on behind
-// it.  A segment takes kSwitch positions before those of its tiles: a CTA that goes on to it
-// from another has that much less to do.  `last`: the piece ends its segment.  False: the
-// piece has no position of a tile.
-template <int MB>
-__device__ __forceinline__ bool piece_at(const Kv8AttnArgs& p, const int4* seqs, const uint32_t* base,
-                                         uint32_t& pos, uint32_t end, uint32_t n_cta, Piece& x,
-                                         bool& last) {
-  int lo = 0, hi = p.B - 1;   // last sequence that starts at or before pos
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (base[mid] <= pos) lo = mid; else hi = mid - 1;
-  }
-  const int4 q = seqs[lo];
-  x.b = lo;
-  x.t0 = q.x;
-  x.rows = q.y;
-  x.kv_len = q.z;
-  const uint32_t len = uint32_t(q.w) + kSwitch, n_rb = uint32_t((x.rows * p.gqa + MB - 1) / MB);
-  const uint32_t seg = (pos - base[lo]) / len;
-  x.g = int(seg / n_rb);
-  x.rb = int(seg - uint32_t(x.g) * n_rb);
-  const uint32_t start = base[lo] + seg * len, first = start + kSwitch;
-  const uint32_t from = max(pos, first);
-  last = end >= start + len;
-  pos = min(end, start + len);
-  if (pos <= from) return false;
-  // the piece's part: this CTA's place among those that have tiles of the segment
-  x.s = 0;
-  if (from != first) {
-    const unsigned long long W = base[p.B];
-    x.s = int(blockIdx.x) - int(((first + 1ull) * n_cta - 1) / W);
-  }
-  x.k_lo = int(from - first) * kTile;
-  x.k_hi = x.kv_len;          // a tree row may see up to the last key
-  if (p.tree_mask == nullptr) {
-    const int last_row = min(x.rows * p.gqa - 1, x.rb * MB + MB - 1) / p.gqa;
-    x.k_hi = x.kv_len - x.rows + last_row + 1;
-  }
-  if (!last) x.k_hi = min(x.k_hi, int(pos - first) * kTile);
-  x.n_tiles = x.k_hi > x.k_lo ? (x.k_hi - x.k_lo + kTile - 1) / kTile : 0;
-  return true;
-}
-
-__device__ __forceinline__ float log2_scale(float s) {
-  const uint32_t b = __float_as_uint(s);
-  if ((b & 0x7FFFFFu) == 0u && b - 0x00800000u < 0x7F000000u) return float(int(b >> 23) - 127);
-  return __log2f(s);   // 0 gives -inf
-}
-
-// Bytes of a 16-byte chunk that are e4m3 NaN become 0; returns whether there was one.
-__device__ __forceinline__ bool clear_nan8(uint4& u) {
-  uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t any = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t m = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    w[i] &= ~m;
-    any |= m;
-  }
-  u = make_uint4(w[0], w[1], w[2], w[3]);
-  return any != 0u;
-}
-
-// The V row of one key of a landed tile: zeroed, or its NaN codes taken out.
-__device__ __noinline__ bool clean_v_row(uint8_t* slot, int row, bool zero) {
-  bool hit = false;
-  for (int c = 0; c < 16; ++c) {
-    uint4* const a = reinterpret_cast<uint4*>(slot + (c >> 3) * kHalfBytes + row * 128 +
-                                              (((c & 7) ^ (row & 7)) << 4));
-    if (zero) {
-      *a = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      uint4 u = *a;
-      if (clear_nan8(u)) {
-        *a = u;
-        hit = true;
-      }
-    }
-  }
-  return hit;
-}
 
 // The three terms (columns t0, t0 + MB, t0 + 2 MB) of 8 rows of one half of O^T times f, in
 // tensor memory (whole warp).
@@ -245,15 +122,6 @@ __device__ __forceinline__ float warp_max16(float (&v)[16]) {
   return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// Two values to e4m3, and what they leave: (lo, hi) becomes (x - e4m3(x)) * step.
-__device__ __forceinline__ uint32_t take_term(float& lo, float& hi, float step) {
-  const uint32_t t = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-  const float2 f = from_e4m3x2(t);
-  lo = (lo - f.x) * step;
-  hi = (hi - f.y) * step;
-  return t;
-}
-
 // Two probabilities (at most 2^8) as three e4m3 terms each, steps of 32: the first remainder
 // is exact in fp32 and goes on as fp16, whose 11 bits hold the two terms to come.
 __device__ __forceinline__ void p_terms(float lo, float hi, uint32_t (&t)[kPTerms]) {
@@ -263,22 +131,6 @@ __device__ __forceinline__ void p_terms(float lo, float hi, uint32_t (&t)[kPTerm
   const __half2 f(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(t[1]), __NV_E4M3));
   r = __hmul2(__hsub2(r, f), __float2half2_rn(32.f));
   t[2] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
-}
-
-// A row's output of one dim: NaN when a key that it sees had a NaN there (`hits`: keys from
-// pr_lo on whose V rows had NaN codes taken out).
-__device__ __noinline__ float put_back_nan(const Kv8AttnArgs& p, int b, int g,
-                                           unsigned long long hits, int pr_lo, int lim, bool tree,
-                                           int base, unsigned long long mask, int dim, float o) {
-  for (; hits != 0ull; hits &= hits - 1ull) {
-    const int key = pr_lo + __ffsll(static_cast<long long>(hits)) - 1;
-    if (key >= lim || (tree && key >= base && !((mask >> (key - base)) & 1ull))) continue;
-    const int blk = __ldg(p.tables + (long long)b * p.max_blocks + (key >> p.bs_log2));
-    if (blk < 0 || blk >= p.num_blocks) continue;
-    const size_t row = ((size_t(blk) * p.Hkv + g) << p.bs_log2) + (key & ((1 << p.bs_log2) - 1));
-    if ((p.v_pool[row * 256 + dim] & 0x7Fu) == 0x7Fu) o = __int_as_float(0x7FC00000);
-  }
-  return o;
 }
 
 template <int MB, bool kF16>
@@ -292,20 +144,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t tmo = p.ctl.timeout_ns;
 
-  // ---- the schedule: positions before each sequence, and this CTA's share of them
   if (tid == 0) {
-    sm.base[0] = 0;
-    sm.red[0][0][0] = 0.f;
-    for (int i = 0; i < C::kKS; ++i) {
-      ptx::mbar_init(&sm.k_full[i], 1);
-      ptx::mbar_init(&sm.k_empty[i], 1);
-    }
-    for (int i = 0; i < C::kVS; ++i) {
-      ptx::mbar_init(&sm.v_full[i], 1);
-      ptx::mbar_init(&sm.v_empty[i], 1);
-    }
-    for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(&sm.sc_full[i], 32);
-    for (int i = 0; i < kPieceRing; ++i) ptx::mbar_init(&sm.piece_full[i], 1);
+    init_ring(sm);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.s_full[i], 1);
       ptx::mbar_init(&sm.p_full[i], C::kSoftmax / 32);
@@ -314,8 +154,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     ptx::mbar_init(&sm.q_full, C::kSoftmax / 32);
     ptx::mbar_init(&sm.o_full, 1);
     ptx::mbar_init(&sm.drain, 1);
-    sm.abort = 0;
-    sm.zero = 0;
     for (int i = 0; i < C::kGroups; ++i) sm.failed[i] = 0;
     ptx::fence_mbar_init();
   }
@@ -323,165 +161,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     ptx::tmem_alloc(&sm.tmem_base, C::kCols);
     ptx::tmem_relinquish();
   }
-  wait_for_last();
-  let_next_start();   // not before: the merge reads lengths and gate ahead of its own wait
-  int most = 0;   // tiles of the longest sequence
-  for (int b = tid; b < p.B; b += C::kThreads) {
-    const int kv = p.kv_lens[b], t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
-    const int rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
-    const bool ok = rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
-                    kv <= p.max_kv_len;
-    const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
-    sm.seq[b] = make_int4(t0, rows, kv, tiles);
-    sm.base[b + 1] = tiles > 0 ? uint32_t(tiles + kSwitch) * uint32_t(p.Hkv) *
-                                     uint32_t((rows * p.gqa + MB - 1) / MB)
-                               : 0u;
-    most = max(most, tiles);
-    if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-  }
-  __syncthreads();
-  if (warp == 0) {   // inclusive sums over the sequences, 32 at a time
-    uint32_t run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      uint32_t v = b0 + lane < p.B ? sm.base[b0 + lane + 1] : 0u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (b0 + lane < p.B) sm.base[b0 + lane + 1] = run + v;
-      run += __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  atomicMax(reinterpret_cast<int*>(&sm.red[0][0][0]), most);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  most = *reinterpret_cast<const int*>(&sm.red[0][0][0]);
-  const uint32_t W = sm.base[p.B];
-  // Shares so long that no segment needs more than `parts` parts.
-  uint32_t n_cta = min(gridDim.x, W);
-  if (most > p.parts)
-    n_cta = min(n_cta, max(1u, uint32_t((unsigned long long)W * uint32_t(p.parts - 2) / uint32_t(most))));
-  uint32_t pos0 = 0, end = 0;
-  if (blockIdx.x < n_cta) {
-    pos0 = uint32_t((unsigned long long)W * blockIdx.x / n_cta);
-    end = uint32_t((unsigned long long)W * (blockIdx.x + 1) / n_cta);
-  }
-  __syncthreads();   // red is read before the softmax warps write it
+  const Share share = cut_shares<MB>(sm, p);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ copies
-    // A tile's scales live in a ring of kScaleRing tiles without a release: tile J + 8 is
-    // copied only once S of tile J + 8 - kKS >= J + 5 was issued, which waits for the
-    // softmax of tile J + 3, so tile J's scales have been read.
-    // So with the pieces' descriptions: a piece has a tile at least, so that when piece n + 8
-    // is published the softmax has passed tiles of piece n + 8 - kKS - 3 and with it piece n.
-    static_assert(kScaleRing >= C::kKS + 3 && kPieceRing >= C::kKS + 4, "rings");
-    const int bs = 1 << p.bs_log2, per_tile = kTile >> p.bs_log2;
-    uint32_t J = 0;
-    bool ok = true;
-    if (lane == 0) {
-      ptx::prefetch_tmap(&tmK);
-      ptx::prefetch_tmap(&tmV);
-    }
-    uint32_t n_pieces = 0;
-    const auto publish = [&](const Piece& x) {
-      if (lane == 0) {
-        sm.piece[n_pieces % kPieceRing] = x;
-        ptx::mbar_arrive(&sm.piece_full[n_pieces % kPieceRing]);
-      }
-      ++n_pieces;
-    };
-    for (uint32_t pos = pos0; ok && pos < end;) {
-      Piece x;
-      bool last;
-      if (!piece_at<MB>(p, sm.seq, sm.base, pos, end, n_cta, x, last)) continue;
-      if (x.s < 0 || x.s >= p.parts) {   // never, with shares as cut above
-        if (lane == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-        x.s = -1;
-      }
-      const int n_rows = min(MB, x.rows * p.gqa - x.rb * MB);
-      {
-        const int pp = x.rb * MB + lane, i = pp / p.gqa;   // lane by row: MB <= 32
-        const size_t row = size_t(x.t0 + i) * p.Hq + x.g * p.gqa + (pp - i * p.gqa);
-        if (lane < n_rows) {
-          if (x.n_tiles == 0 && x.s >= 0)   // no row of the block sees a key of the piece
-            p.lse_parts[size_t(x.s) * size_t(p.T) * p.Hq + row] = -INFINITY;
-          for (int c = 0; c < 4; ++c)       // Q's rows, which the piece's start will wait for
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + row * 32 + c * 8));
-        }
-        if (last && lane == 0 && x.s >= 0)
-          p.n_parts[(size_t(p.b0 + x.b) * p.Hkv + x.g) * p.max_rb + x.rb] = x.s + 1;
-      }
-      if (x.n_tiles == 0) continue;
-      publish(x);
-      const int* const table = p.tables + (long long)x.b * p.max_blocks;
-      int at = x.k_lo + lane * bs;   // first key of this lane's block
-      int blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
-      for (int j = 0; ok && j < x.n_tiles; ++j, ++J) {
-        const bool mine = lane < per_tile && at < x.k_hi;
-        const bool in = blk >= 0 && blk < p.num_blocks;
-        if (mine && !in) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-        // a block outside the pool: past the map's last row, which copies zeros
-        const int row = in ? (blk * p.Hkv + x.g) << p.bs_log2 : (p.num_blocks * p.Hkv) << p.bs_log2;
-        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, mine))) * uint32_t(bs) * 256u;
-        const int cur = blk;
-        at += kTile;
-        blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
-        const uint32_t ks = J % C::kKS, vs = J % C::kVS;
-        int go = 1;
-        if (lane == 0) {
-          if (J >= C::kKS)
-            go = wait(&sm.k_empty[ks], (J / C::kKS - 1) & 1u, tmo, &sm.abort);
-          if (go) ptx::mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
-        }
-        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-        if (!ok) break;
-        if (mine) {
-          uint8_t* const d = sm.k[ks] + lane * bs * 128;
-          ptx::tma_load_2d(d, &tmK, &sm.k_full[ks], 0, row);
-          ptx::tma_load_2d(d + kHalfBytes, &tmK, &sm.k_full[ks], 128, row);
-          const size_t sc = size_t(in ? cur : 0) * p.Hkv + x.g;
-          ptx::cp_async4(ptx::smem_addr(&sm.scale[J % kScaleRing][0][lane]), p.k_scale + sc, in ? 4u : 0u);
-          ptx::cp_async4(ptx::smem_addr(&sm.scale[J % kScaleRing][1][lane]), p.v_scale + sc, in ? 4u : 0u);
-        }
-        ptx::cp_async_mbar_arrive(&sm.sc_full[J % kScaleRing]);
-        if (lane == 0) {
-          if (J >= C::kVS)
-            go = wait(&sm.v_empty[vs], (J / C::kVS - 1) & 1u, tmo, &sm.abort);
-          if (go) ptx::mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
-        }
-        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-        if (!ok) {
-          // K of this tile is on its way: it must land before the CTA ends
-          if (lane == 0) wait(&sm.k_full[ks], (J / C::kKS) & 1u, tmo, &sm.zero);
-          break;
-        }
-        if (mine) {
-          uint8_t* const d = sm.v[vs] + lane * bs * 128;
-          ptx::tma_load_2d(d, &tmV, &sm.v_full[vs], 0, row);
-          ptx::tma_load_2d(d + kHalfBytes, &tmV, &sm.v_full[vs], 128, row);
-        }
-      }
-    }
-    if (ok) {
-      Piece none{};
-      publish(none);   // (the share's end: no tiles)
-    }
-    if (!ok && lane == 0) {
-      sm.abort = 1;
-      record_status(p.ctl.status, GQA_ERR_TIMEOUT);
-    }
-    ptx::cp_async_wait_all();
-    if (lane == 0) {   // every copy has landed before the CTA ends
-      for (uint32_t c = J - min(J, uint32_t(C::kKS)); c < J; ++c)
-        wait(&sm.k_full[c % C::kKS], (c / C::kKS) & 1u, tmo, &sm.zero);
-      for (uint32_t c = J - min(J, uint32_t(C::kVS)); c < J; ++c)
-        wait(&sm.v_full[c % C::kVS], (c / C::kVS) & 1u, tmo, &sm.zero);
-    }
-    __syncwarp();
+    copy_role<MB>(sm, p, tmK, tmV, share);
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
@@ -866,16 +553,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (warp == 1) ptx::tmem_dealloc(tmem, C::kCols);
 }
 
-bool encode_pool(EncodeTiledFn fn, CUtensorMap* map, const void* pool, const Kv8AttnArgs& a) {
-  const cuuint64_t dims[2] = {256, cuuint64_t(a.num_blocks) * cuuint64_t(a.Hkv) << a.bs_log2};
-  const cuuint64_t strides[1] = {256};
-  const cuuint32_t box[2] = {128, cuuint32_t(1) << a.bs_log2};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MB, bool kF16>
 cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                      long long grid, cudaStream_t stream) {
@@ -897,18 +574,20 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
 
 }  // namespace
 
-int kv8_rows_per_block(long long packed_rows) { return packed_rows <= 16 ? 16 : 32; }
+// 16, 32 or (bf16) 128 packed rows share a tile.  Up to 32 rows the cache's bytes bound the
+// kernels and fewer columns cost less; past 32 a second row block would read the cache again,
+// which the wide kernel's 128 rows do not.
+int kv8_rows_per_block(long long packed_rows, bool f16) {
+  return packed_rows <= 16 ? 16 : packed_rows <= 32 || f16 ? 32 : 128;
+}
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
                             bool* encode_failed) {
-  *encode_failed = false;
-  EncodeTiledFn fn = get_encode_fn();
   CUtensorMap tmK, tmV;
-  if (fn == nullptr || !encode_pool(fn, &tmK, a.k_pool, a) || !encode_pool(fn, &tmV, a.v_pool, a)) {
-    *encode_failed = true;
-    return cudaSuccess;
-  }
-  const int mb = kv8_rows_per_block((long long)a.max_rows * a.gqa);
+  const int mb = kv8_rows_per_block((long long)a.max_rows * a.gqa, f16);
+  if (mb == 128) return launch_kv8_wide(a, sms, stream, encode_failed);
+  *encode_failed = !encode_pools(&tmK, &tmV, a);
+  if (*encode_failed) return cudaSuccess;
   const long long tiles = (a.max_kv_len + kTile - 1) / kTile;
   const long long most = (long long)a.B * a.Hkv * a.max_rb * tiles;   // < 2^31: the caller's check
   const long long grid = most < sms ? most : sms;

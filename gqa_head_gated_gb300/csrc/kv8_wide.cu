@@ -1,0 +1,490 @@
+// The attention of many rows (wide draft trees, prompt chunks; bf16) over the paged 8-bit
+// cache: 128 packed rows (query heads of a KV group x new rows) share each tile.  The
+// mathematics, parts and schedule are kv8_attn.cu's; what differs is the side of the product
+// that the rows take, and the terms:
+//
+//   S [rows, 128 keys] = Q . K^T       A = Q's terms, B = the tile's K, as it lies
+//   O [rows, 256]     += P . V         A = P's terms (tensor memory), B = V, the same bytes
+//
+// Q is two e4m3 terms that add up in one accumulator (t0 + t1, no scale between them: what a
+// row's elements lose is below 2^-19 of its largest).  P is three e5m2 terms, again in one
+// accumulator: e5m2 has 3 bits a term but the range of fp16, so that p <= 2^15 splits into
+// t0 + t1 + t2 with a relative error of 2^-9 (a bf16 P has 2^-9) and an absolute one of 2^-17,
+// 2^-24 of the row's largest when its reference has just moved (to 2^7) and less after.
+// One accumulator for all terms is what leaves room for 128 rows: with e4m3 terms a column
+// or lane each, as the kernel for few rows has them, O alone would take three times 256
+// columns.
+//
+// What bounds it: the tensor pipe, 2 x 1024 x 64 / 128 clocks for S (two terms, K = 32 a step,
+// 64 clocks each) and three times 512 for P.V: 2,560 a tile of 128 keys, 1.33 us, against
+// 1.47 us that its 64 KB take from HBM.  The kernel for few rows reads the cache once for 32
+// rows, so from 33 on this one reads it less often.
+//
+// Roles (320 threads): warp 0 copies, warp 1 issues the products, warps 2..9 are the softmax
+// and epilogue: tensor-memory lane = row, two warps share a quadrant's rows, 64 keys each.
+// TMEM: O 256 columns, S 128 (one buffer: S of the next tile may start once every warp holds
+// its scores in registers), P 3 x 32.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kv8_attn.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kWideThreads = 320;
+constexpr int kWarpsS = 8;             // softmax warps
+constexpr int kQTerms = 2, kPTerms = 3;
+constexpr int kSlots = 2;              // K and V slots of a tile each
+constexpr uint32_t kTmWideO = 0, kTmWideS = 256, kTmWideP = 384;
+constexpr float kWideCap = 15.f;       // p <= 2^15
+constexpr float kWideTop = 7.f;        // a moved reference leaves the row's largest p at 2^7
+constexpr uint32_t kIdescS = ptx::idesc_f32acc(128, 128, 0, 0, 0);
+// A e5m2 (format 1), B e4m3 (format 0), B MN-major
+constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, 256, 0, 1, 0) | (1u << 7);
+
+struct __align__(1024) WideSmem : RingSmem<kSlots, kSlots> {
+  alignas(1024) uint8_t q[kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
+  float2 red[2][2][kRows];                 // [tile parity][half][row]: maxima with vs, without
+  float sum[2][kRows];                     // [half][row]
+  uint64_t s_full, s_free, p_full, pv_done, q_full, o_full, drain;
+  // by piece, two in turn
+  unsigned long long hit[2][2];            // NaN V rows taken out: bits of keys pr_lo + 64 w + i
+  unsigned long long mask[2][kRows];
+  int lim[2][kRows], row[2][kRows];
+  float fac[2][kRows];
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc], 8-bit inputs.
+__device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two probabilities as three e5m2 terms each.  They go as fp16 (a rounding of 2^-12), whose
+// remainders are exact; an e5m2 number is the upper byte of the fp16 of the same value.
+__device__ __forceinline__ void p_terms5(float lo, float hi, uint32_t (&t)[kPTerms]) {
+  __half2 r = __floats2half2_rn(lo, hi);
+#pragma unroll
+  for (int i = 0; i < kPTerms; ++i) {
+    t[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E5M2);
+    if (i + 1 < kPTerms) {
+      const uint32_t w = __byte_perm(t[i], 0u, 0x1404);   // bytes to the halves' upper ones
+      r = __hsub2(r, *reinterpret_cast<const __half2*>(&w));
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kWideThreads, 1)
+kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const Kv8AttnArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  WideSmem& sm = *reinterpret_cast<WideSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t tmo = p.ctl.timeout_ns;
+  if (tid == 0) {
+    init_ring(sm);
+    ptx::mbar_init(&sm.s_full, 1);
+    ptx::mbar_init(&sm.s_free, kWarpsS);
+    ptx::mbar_init(&sm.p_full, kWarpsS);
+    ptx::mbar_init(&sm.pv_done, 1);
+    ptx::mbar_init(&sm.q_full, kWarpsS);
+    ptx::mbar_init(&sm.o_full, 1);
+    ptx::mbar_init(&sm.drain, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sm.tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const Share share = cut_shares<kRows>(sm, p);
+
+  if (warp == 0) {
+    copy_role<kRows>(sm, p, tmK, tmV, share);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t qa = ptx::smem_addr(sm.q);
+      uint32_t J = 0, pc = 0;
+      bool ok = true;
+      const auto issue_s = [&](uint32_t n) -> bool {
+        const uint32_t ks = n % kSlots;
+        if (n > 0 && !wait(&sm.s_free, (n - 1) & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.k_full[ks], (n / kSlots) & 1u, tmo, &sm.abort)) return false;
+        ptx::tc_fence_after();
+        const uint32_t ka = ptx::smem_addr(sm.k[ks]);
+#pragma unroll 1
+        for (int t = 0; t < kQTerms; ++t)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_ss_f8(tmem + kTmWideS,
+                           ptx::sdesc_sw128(qa + t * (2 * kRows * 128) + (kk >> 2) * (kRows * 128) +
+                                                (kk & 3) * 32, 16, 1024),
+                           ptx::sdesc_sw128(ka + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
+                           kIdescS, t > 0 || kk > 0);
+        ptx::tc_commit(&sm.s_full);
+        ptx::tc_commit(&sm.k_empty[ks]);
+        return true;
+      };
+      const auto issue_pv = [&](uint32_t n, bool first) -> bool {
+        const uint32_t vs = n % kSlots;
+        if (!wait(&sm.p_full, n & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.v_full[vs], (n / kSlots) & 1u, tmo, &sm.abort)) return false;
+        ptx::tc_fence_after();
+        const uint32_t va = ptx::smem_addr(sm.v[vs]);
+#pragma unroll 1
+        for (int t = 0; t < kPTerms; ++t)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts_f8(tmem + kTmWideO, tmem + kTmWideP + t * 32 + kk * 8,
+                      ptx::sdesc_sw128(va + kk * 4096, kHalfBytes, 1024), kIdescO,
+                      !first || t > 0 || kk > 0);
+        ptx::tc_commit(&sm.pv_done);
+        ptx::tc_commit(&sm.v_empty[vs]);
+        return true;
+      };
+      while (ok) {
+        ok = wait(&sm.piece_full[pc % kPieceRing], (pc / kPieceRing) & 1u, tmo, &sm.abort);
+        if (!ok) break;
+        const int n_tiles = sm.piece[pc % kPieceRing].n_tiles;
+        if (n_tiles == 0) break;
+        ok = wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        ok = issue_s(J);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          if (j + 1 < n_tiles) ok = issue_s(J + j + 1);
+          if (ok) ok = issue_pv(J + j, j == 0);
+        }
+        if (ok) ptx::tc_commit(&sm.o_full);
+        J += n_tiles;
+        ++pc;
+      }
+      if (!ok) {
+        sm.abort = 1;
+        record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+      }
+      // every product issued has to end before tensor memory is given back
+      ptx::tc_commit(&sm.drain);
+      wait(&sm.drain, 0, tmo, &sm.zero);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, epilogue
+    const int sw = warp - 2;
+    const int half = sw >> 2;                  // keys 64 half .. 64 half + 63 of a tile
+    const int qd = warp & 3;                   // tensor-memory lanes 32 qd .. 32 qd + 31
+    const int r = qd * 32 + lane;              // this thread's row of the block
+    const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
+    const bool tree = p.tree_mask != nullptr;
+    const uint32_t bar_id = 1 + qd;            // the two warps of a quadrant
+    uint32_t J = 0, pc = 0, n_fetched = 0;
+    bool ok = true;      // agreed on by the two warps at their barriers before they leave
+    bool stop = false;
+    Piece x;
+    const auto fetch = [&]() -> bool {
+      ok = warp_all(ok && wait(&sm.piece_full[n_fetched % kPieceRing], (n_fetched / kPieceRing) & 1u,
+                               tmo, &sm.abort));
+      x = sm.piece[n_fetched % kPieceRing];
+      ++n_fetched;
+      return ok && x.n_tiles > 0;
+    };
+    // Q's terms, the rows' limits and places of piece x, into half `par` of the piece arrays;
+    // then the products of the piece may start.  The last piece's S products are done.
+    const auto prepare = [&](uint32_t par) {
+      const int p0 = x.rb * kRows, n_rows = min(kRows, x.rows * p.gqa - p0);
+#pragma unroll 1
+      for (int r0 = sw; r0 < kRows; r0 += 4 * kWarpsS) {
+        uint4 u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = r0 + k * kWarpsS, i = (p0 + rr) / p.gqa;
+          const int row = (x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
+          u[k] = rr < n_rows ? __ldg(p.q + size_t(row) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+          if (lane == 0) {
+            sm.row[par][rr] = row;
+            sm.lim[par][rr] = rr >= n_rows ? 0 : tree ? x.kv_len : x.kv_len - x.rows + i + 1;
+            sm.mask[par][rr] = tree && rr < n_rows ? p.tree_mask[x.t0 + i] : 0ull;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = r0 + k * kWarpsS;
+          float f[8];
+          const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 a = unpack_elem2<false>(w[c]);
+            f[2 * c] = a.x;
+            f[2 * c + 1] = a.y;
+          }
+          const int e = scale_exp(__reduce_max_sync(0xffffffffu, finite_amax_bits(f)));
+          if (lane == 0) sm.fac[par][rr] = pow2f(e) * kScaleLog2;
+          const float inv = pow2f(-e);
+          // an infinite element makes its row's scores NaN, as in the formula
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
+#pragma unroll 1
+          for (int t = 0; t < kQTerms; ++t) {
+            uint2 o;
+            o.x = take_term(f[0], f[1], 1.f);
+            o.x |= take_term(f[2], f[3], 1.f) << 16;
+            o.y = take_term(f[4], f[5], 1.f);
+            o.y |= take_term(f[6], f[7], 1.f) << 16;
+            *reinterpret_cast<uint2*>(sm.q[t][lane >> 4] + rr * 128 +
+                                      ((((lane & 15) >> 1) ^ (rr & 7)) << 4) + (lane & 1) * 8) = o;
+          }
+        }
+      }
+      if (sw == 0 && lane < 2) sm.hit[par][lane] = 0ull;
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.q_full);
+    };
+
+    // The piece whose tiles are done and whose parts are due
+    int seq = 0, head = 0, s_idx = 0, base = 0, pr_lo = 0, n_rows = 0;
+    float ref = kNone, ml = kNone, l = 0.f;
+    for (bool first = true;; first = false) {
+      // ---- the next piece may start while the last one ends (its S products are done)
+      const bool more = fetch();
+      if (more) prepare(pc & 1u);
+      const uint32_t last_par = (pc - 1u) & 1u;
+      if (!first) {
+        ok = warp_all(ok && wait(&sm.o_full, last_par, tmo, &sm.abort));
+        sm.sum[half][r] = l;
+      }
+      stop = ptx::named_bar_or(bar_id, 64, !ok);
+      if (stop) break;
+      if (!first) {
+        // ---- the last piece's parts: this thread's row, 128 of its columns
+        ptx::tc_fence_after();
+        const float L = sm.sum[0][r] + sm.sum[1][r];
+        const float inv = L == 0.f ? 0.f : 1.f / L, ex = ex2(0.5f * (ref - ml));
+        const bool mine = s_idx >= 0 && r < n_rows;
+        const int row = sm.row[last_par][r];
+        const size_t part0 = size_t(s_idx) * size_t(p.T) * p.Hq;
+        if (mine && half == 0)
+          p.lse_parts[part0 + row] = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
+        const unsigned long long h0 = sm.hit[last_par][0], h1 = sm.hit[last_par][1];
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          __syncwarp();
+          uint32_t o[32];
+          ptx::tmem_ld32_wait(trow + kTmWideO + half * 128 + cc * 32, o);
+          if (!mine || L == 0.f) continue;
+          float* const dst = p.o_parts + (part0 + row) * 256 + half * 128 + cc * 32;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = __uint_as_float(o[c + i]) * inv * ex * ex;
+              if ((h0 | h1) != 0ull) {
+                const int dim = half * 128 + cc * 32 + c + i, lim = sm.lim[last_par][r];
+                const unsigned long long m = sm.mask[last_par][r];
+                v[i] = put_back_nan(p, seq, head, h0, pr_lo, lim, tree, base, m, dim, v[i]);
+                v[i] = put_back_nan(p, seq, head, h1, pr_lo + 64, lim, tree, base, m, dim, v[i]);
+              }
+            }
+            *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        ptx::tc_fence_before();
+      }
+      if (!more) break;
+      const uint32_t par = pc & 1u;
+      ok = ok && wait(&sm.q_full, par, tmo, &sm.abort);   // rows, limits, factors are written
+      const int n_tiles = x.n_tiles, k_lo = x.k_lo, k_hi = x.k_hi;
+      seq = x.b;
+      head = x.g;
+      s_idx = x.s;
+      n_rows = min(kRows, x.rows * p.gqa - x.rb * kRows);
+      base = x.kv_len - x.rows;
+      // keys from pr_lo on are seen by some rows of the block only (fewer than 128)
+      pr_lo = max(k_lo, tree ? base : base + x.rb * kRows / p.gqa + 1);
+      const int lim = sm.lim[par][r];
+      const unsigned long long mask = sm.mask[par][r];
+      const float fac = sm.fac[par][r];
+      ref = ml = kNone;
+      l = 0.f;
+      for (int j = 0; j < n_tiles; ++j, ++J) {
+        const int key0 = k_lo + j * kTile + half * 64;
+        const int tile_end = k_lo + (j + 1) * kTile;
+        ok = ok && wait(&sm.s_full, J & 1u, tmo, &sm.abort) &&
+             wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
+        ok = warp_all(ok);
+        __syncwarp();
+        uint32_t s[64];
+        float f[4], lv[4];        // by run of 16 keys: score factor, log2 of the V scale
+        float mp = -INFINITY, ms = -INFINITY;
+        if (ok) {
+          ptx::tc_fence_after();
+          ptx::tmem_ld64_wait(trow + kTmWideS + half * 64, s);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.s_free);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int blk = (half * 64 + i * 16) >> p.bs_log2;
+            const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
+            // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
+            f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
+            lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
+          }
+          if (tile_end > k_hi || tile_end > pr_lo) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const int key = key0 + c;
+              const bool vis = key < min(lim, k_hi) &&
+                               (!tree || key < base || ((mask >> (key - base)) & 1ull));
+              if (!vis) s[c] = 0xFF800000u;   // -inf
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
+#pragma unroll
+            for (int c = 2; c < 16; c += 2) {
+              m0 = fmaxf(m0, __uint_as_float(s[16 * i + c]));
+              m1 = fmaxf(m1, __uint_as_float(s[16 * i + c + 1]));
+            }
+            const float m = fmaxf(m0, m1) * f[i];
+            ms = fmaxf(ms, m);
+            mp = fmaxf(mp, m + lv[i]);
+          }
+          sm.red[J & 1u][half][r] = make_float2(mp, ms);
+        }
+        if (ptx::named_bar_or(bar_id, 64, !ok)) {
+          stop = true;
+          break;
+        }
+        // ---- references (both threads of a row do the same)
+        {
+          const float2 o = sm.red[J & 1u][half ^ 1][r];
+          mp = fmaxf(mp, o.x);
+          ms = fmaxf(ms, o.y);
+        }
+        const bool up = mp > ref + kWideCap, up_l = ms > ml + kLSlack;
+        if (__any_sync(0xffffffffu, up || up_l)) {
+          const float alpha = up ? ex2(ref - (mp - kWideTop)) : 1.f;
+          if (up) ref = mp - kWideTop;
+          if (up_l) {
+            l *= ex2(ml - ms);
+            ml = ms;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, up)) {
+            ok = warp_all(wait(&sm.pv_done, (J - 1) & 1u, tmo, &sm.abort));
+            __syncwarp();
+            if (ok) {
+              ptx::tc_fence_after();
+              rescale_o_cols(trow + kTmWideO + half * 128, alpha);
+            }
+          }
+        }
+        // ---- P's terms
+        uint32_t w[kPTerms][16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = lv[i] - ref;
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float e[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              e[k] = ex2(fmaf(__uint_as_float(s[16 * i + 4 * c + k]), f[i], a));
+              sum += e[k];
+            }
+            uint32_t lo[kPTerms], hi[kPTerms];
+            p_terms5(e[0], e[1], lo);
+            p_terms5(e[2], e[3], hi);
+#pragma unroll
+            for (int t = 0; t < kPTerms; ++t) w[t][4 * i + c] = lo[t] | (hi[t] << 16);
+          }
+          // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
+          // block of tiny values that p hardly sees)
+          const float d = -a - ml;
+          if (__any_sync(0xffffffffu, d > 60.f)) {
+            sum = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              float v = 0.f;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v = k == c ? __uint_as_float(s[16 * i + k]) : v;
+              sum += ex2(fmaf(v, f[i], -ml));
+            }
+            l += sum;
+          } else {
+            l += sum * ex2(d);
+          }
+        }
+        // ---- V rows that some row does not see
+        if (tile_end > k_hi || tile_end > pr_lo) {
+          ok = ok && wait(&sm.v_full[J % kSlots], (J / kSlots) & 1u, tmo, &sm.abort);
+          const int key = k_lo + j * kTile + r;   // thread by key here, half a row each
+          if (ok && (key >= k_hi || key >= pr_lo) &&
+              clean_v_row(sm.v[J % kSlots], r, key >= k_hi, 8 * half, 8 * half + 8))
+            atomicOr(&sm.hit[par][(key - pr_lo) >> 6], 1ull << ((key - pr_lo) & 63));
+          ptx::fence_proxy_async_smem();
+        }
+        if (J > 0) ok = ok && wait(&sm.pv_done, (J - 1) & 1u, tmo, &sm.abort);   // P is free
+        ok = warp_all(ok);
+        __syncwarp();
+        if (ok) {
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < kPTerms; ++t)
+            ptx::tmem_st16_wait(trow + kTmWideP + t * 32 + half * 16, w[t]);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.p_full);
+        }
+      }
+      ++pc;
+      if (stop) break;
+    }
+    if (stop && lane == 0) {
+      sm.abort = 1;
+      record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, int sms, cudaStream_t stream, bool* encode_failed) {
+  CUtensorMap tmK, tmV;
+  *encode_failed = !encode_pools(&tmK, &tmV, a);
+  if (*encode_failed) return cudaSuccess;
+  const long long tiles = (a.max_kv_len + kTile - 1) / kTile;
+  const long long most = (long long)a.B * a.Hkv * a.max_rb * tiles;
+  const long long grid = most < sms ? most : sms;
+  const size_t smem = sizeof(WideSmem) + 1024;
+  static_assert(sizeof(WideSmem) + 1024 <= 227 * 1024, "one CTA per SM");
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_wide_kernel), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kv8_wide_kernel, dim3(unsigned(grid)), kWideThreads, smem, stream, 1, tmK, tmV, a);
+  if (e == cudaSuccess) note_launch("kv8_wide_kernel<bf16>", grid, kWideThreads, smem);
+  return e;
+}
+
+}  // namespace gqa

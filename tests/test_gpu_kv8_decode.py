@@ -63,7 +63,8 @@ def test_decode_head_layouts(Hq, Hkv):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("rows,lens", [([2, 3, 1], [2, 300, 129]), ([4, 0, 4], [4, 5, 600]),
-                                       ([33, 7], [900, 7]), ([130], [400])])
+                                       ([33, 7], [900, 7]), ([130], [400]),
+                                       ([40, 3, 64], [700, 260, 64])])
 def test_chain_verify(rows, lens, dtype):
     c = Cache(lens, 2, 64, seed=46)
     _check(c, rows, 12, 47, dtype)
@@ -106,18 +107,19 @@ def test_long_sequences_and_many():
     _check(c, [1] * 300, 4, 58)
 
 
+@pytest.mark.parametrize("rows", [1, 9])        # 4 packed rows, and 36: the kernel for many
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-def test_block_scales_far_apart(dtype):
+def test_block_scales_far_apart(dtype, rows):
     """Blocks whose values differ by many powers of two: a sink block of tiny values that takes nearly
     all probability next to large ones, and keys whose scores differ by tens."""
     c = Cache([400], 2, 16, seed=59)
     for i, e in enumerate([-60, -7, 3, -30, -7, -20, -7, 0]):
         c.vs[c.tables[0][i]] = 2.0 ** e
         c.ks[c.tables[0][i]] = 2.0 ** [-7, -30, -7, -3, -7, -9, -40, -7][i]
-    q, g = rows_qg(1, 8, 60, dtype)
-    out, lse = _run(c, [1], q, g, lse=True)
+    q, g = rows_qg(rows, 8, 60, dtype)
+    out, lse = _run(c, [rows], q, g, lse=True)
     k, v = c.contiguous()
-    ref, rl = oracle.decode(to_f64(q), k, v, to_f64(g), c.lens)
+    ref, rl = oracle.decode(to_f64(q), k, v, to_f64(g), c.lens, [0, rows])
     # scores reach 2^4 times a usual one: their fp32 error is 16 * LSE_TOL at most
     tol = 16 * LSE_TOL
     assert np.abs(to_f64(lse) - rl).max() <= tol
@@ -126,21 +128,22 @@ def test_block_scales_far_apart(dtype):
     assert np.abs(to_f64(out) - ref).max() <= scale * (4 * u + 2 * tol)
 
 
-def test_a_tail_of_many_small_probabilities_is_not_lost():
+@pytest.mark.parametrize("rows", [1, 16])       # 4 packed rows, and 64: the kernel for many
+def test_a_tail_of_many_small_probabilities_is_not_lost(rows):
     """One key weighs e^8 times as much as each of 20,000 others (head 0), which together outweigh it."""
     n = 20001
     c = Cache([n], 1, 64, seed=61)
     c.k[:] = 0
     c.ks[:] = 1.0
     c.vs[:] = 2.0 ** -6
-    q = torch.zeros(1, 4, 256, dtype=torch.bfloat16)
-    q[0, :, 0] = torch.tensor([1.0, 0.5, 0.25, 0.0])
+    q = torch.zeros(rows, 4, 256, dtype=torch.bfloat16)
+    q[:, :, 0] = torch.tensor([1.0, 0.5, 0.25, 0.0])
     c.k[c.tables[0][0], 0, 7, 0] = int(oracle.e4m3_encode(np.array([128.0]))[0])   # 8 nats over 16 * 1/16
-    g = torch.zeros(1, 4, 256, dtype=torch.bfloat16)
+    g = torch.zeros(rows, 4, 256, dtype=torch.bfloat16)
     for dtype in (torch.bfloat16, torch.float16):
-        out, lse = _run(c, [1], q.to(dtype), g.to(dtype), lse=True)
+        out, lse = _run(c, [rows], q.to(dtype), g.to(dtype), lse=True)
         k, v = c.contiguous()
-        ref, rl = oracle.decode(to_f64(q), k, v, to_f64(g), c.lens)
+        ref, rl = oracle.decode(to_f64(q), k, v, to_f64(g), c.lens, [0, rows])
         assert np.abs(to_f64(lse) - rl).max() <= LSE_TOL
         assert_parity_dtype(out, ref)
 
