@@ -459,6 +459,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             need = md > kSlack || me > kLSlack;
           }
           // ---- does a reference have to move (or has a wait run out)?
+          bool moved = false;
+          float alpha[kR];
           if (!ok) sm.failed[rg] = 1;
           if (ptx::named_bar_or(bar_id, kGroupThreads, need || !ok)) {
             if (sm.failed[rg]) {   // written before the barrier, by this group alone
@@ -480,7 +482,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const float4 q4 = *reinterpret_cast<const float4*>(sm.red[rg][lane >> 1]);
             const float top = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
             bool move = false;
-            float alpha[kR];
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
               const float ma = __shfl_sync(0xffffffffu, top, 2 * r);
@@ -493,15 +494,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               ml[r] = up_l ? mc : ml[r];
               d[r] = (s[r] - ref[r]) + lv;
             }
-            if (move && j > 0) {   // the same in all threads: references and maxima are
-              ok = warp_all(wait(&sm.pv_done[buf ^ 1u], ((J - 1) >> 1) & 1u, tmo, &sm.abort));
-              __syncwarp();
-              if (ok) {
-                ptx::tc_fence_after();
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) rescale_cols<MB>(trow + C::kTmO + h * C::kStep, alpha);
-              }
-            }
+            moved = move && j > 0;   // the same in all threads: references and maxima are
           }
           // ---- P's terms
 #pragma unroll
@@ -518,6 +511,17 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             p_terms(pr[2], pr[3], hi);
 #pragma unroll
             for (int t = 0; t < kPTerms; ++t) (i == 0 ? w[t].x : w[t].y) = lo[t] | (hi[t] << 16);
+          }
+          if (moved) {
+            // O, with PV of tile J - 1 in it, moves to the new references only now: the terms
+            // above were computed while that product ran
+            ok = warp_all(ok && wait(&sm.pv_done[buf ^ 1u], ((J - 1) >> 1) & 1u, tmo, &sm.abort));
+            __syncwarp();
+            if (ok) {
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) rescale_cols<MB>(trow + C::kTmO + h * C::kStep, alpha);
+            }
           }
         }
         if (rg == 0 && (tile_end > k_hi || tile_end > pr_lo)) {

@@ -20,8 +20,9 @@
 // 1.47 us that its 64 KB take from HBM.  The kernel for few rows reads the cache once for 32
 // rows, so from 33 on this one reads it less often.
 //
-// Roles (320 threads): warp 0 copies, warp 1 issues the products, warps 2..9 are the softmax
-// and epilogue: tensor-memory lane = row, two warps share a quadrant's rows, 64 keys each.
+// Roles (576 threads): warp 0 copies, warp 1 issues the products, warps 2..17 are the softmax
+// and epilogue: tensor-memory lane = row, four warps share a quadrant's rows, 32 keys each
+// (with two of 64 keys a tile took 5,300 cycles: the scores of one thread are one chain).
 // TMEM: O 256 columns, S 128 (one buffer: S of the next tile may start once every warp holds
 // its scores in registers), P 3 x 32.
 #include <cuda.h>
@@ -33,8 +34,10 @@ namespace gqa {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kWideThreads = 320;
-constexpr int kWarpsS = 8;             // softmax warps
+constexpr int kWarpsS = 16;            // softmax warps
+constexpr int kWideThreads = 64 + 32 * kWarpsS;
+constexpr int kShare = 4;              // softmax threads of a row
+constexpr int kMine = kTile / kShare;  // keys of each
 constexpr int kQTerms = 2, kPTerms = 3;
 constexpr int kSlots = 2;              // K and V slots of a tile each
 constexpr uint32_t kTmWideO = 0, kTmWideS = 256, kTmWideP = 384;
@@ -46,8 +49,8 @@ constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, 256, 0, 1, 0) | (1u << 7);
 
 struct __align__(1024) WideSmem : RingSmem<kSlots, kSlots> {
   alignas(1024) uint8_t q[kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
-  float2 red[2][2][kRows];                 // [tile parity][half][row]: maxima with vs, without
-  float sum[2][kRows];                     // [half][row]
+  float2 red[2][kShare][kRows];            // [tile parity][quarter][row]: maxima with vs, without
+  float sum[kShare][kRows];                // [quarter][row]
   uint64_t s_full, s_free, p_full, pv_done, q_full, o_full, drain;
   // by piece, two in turn
   unsigned long long hit[2][2];            // NaN V rows taken out: bits of keys pr_lo + 64 w + i
@@ -69,17 +72,35 @@ __device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
-// Two probabilities as three e5m2 terms each.  They go as fp16 (a rounding of 2^-12), whose
-// remainders are exact; an e5m2 number is the upper byte of the fp16 of the same value.
-__device__ __forceinline__ void p_terms5(float lo, float hi, uint32_t (&t)[kPTerms]) {
-  __half2 r = __floats2half2_rn(lo, hi);
+// Four probabilities as three e5m2 terms each, a word of four bytes per term.  They go as
+// fp16 (a rounding of 2^-12), whose remainders are exact.  An e5m2 number is the upper byte of
+// the fp16 of the same value, so rounding to it (half away from zero; the sums stay below
+// 2^16) is an integer add and a mask, for two values at once: the conversion instructions
+// made the terms of a tile take 1,700 cycles.  (A NaN loses its bits here; the row's sum, in
+// fp32, keeps it.)
+__device__ __forceinline__ void p_terms5(float2 lo, float2 hi, uint32_t (&w)[kPTerms]) {
+  __half2 a = __floats2half2_rn(lo.x, lo.y), b = __floats2half2_rn(hi.x, hi.y);
 #pragma unroll
   for (int i = 0; i < kPTerms; ++i) {
-    t[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E5M2);
+    const uint32_t ta = (*reinterpret_cast<const uint32_t*>(&a) + 0x00800080u) & 0xFF00FF00u;
+    const uint32_t tb = (*reinterpret_cast<const uint32_t*>(&b) + 0x00800080u) & 0xFF00FF00u;
+    w[i] = __byte_perm(ta, tb, 0x7531);
     if (i + 1 < kPTerms) {
-      const uint32_t w = __byte_perm(t[i], 0u, 0x1404);   // bytes to the halves' upper ones
-      r = __hsub2(r, *reinterpret_cast<const __half2*>(&w));
+      a = __hsub2(a, *reinterpret_cast<const __half2*>(&ta));
+      b = __hsub2(b, *reinterpret_cast<const __half2*>(&tb));
     }
+  }
+}
+
+// 64 columns of a row of O times f, in tensor memory (whole warp).
+__device__ __noinline__ void rescale_cols64(uint32_t ta, float f) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t o[32];
+    ptx::tmem_ld32_wait(ta + 32 * c, o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+    ptx::tmem_st32_wait(ta + 32 * c, o);
   }
 }
 
@@ -185,26 +206,23 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   } else {
     // ------------------------------------------------------------ softmax, epilogue
     const int sw = warp - 2;
-    const int half = sw >> 2;                  // keys 64 half .. 64 half + 63 of a tile
+    const int qt = sw >> 2;                    // keys 32 qt .. 32 qt + 31 of a tile
     const int qd = warp & 3;                   // tensor-memory lanes 32 qd .. 32 qd + 31
     const int r = qd * 32 + lane;              // this thread's row of the block
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
     const bool tree = p.tree_mask != nullptr;
-    const uint32_t bar_id = 1 + qd;            // the two warps of a quadrant
-    uint32_t J = 0, pc = 0, n_fetched = 0;
-    bool ok = true;      // agreed on by the two warps at their barriers before they leave
+    const uint32_t bar_id = 1 + qd;            // the four warps of a quadrant
+    constexpr int kBar = 32 * kShare;
+    uint32_t J = 0, pc = 0;
+    bool ok = true;      // agreed on by the quadrant's warps at their barriers before they leave
     bool stop = false;
-    Piece x;
-    const auto fetch = [&]() -> bool {
-      ok = warp_all(ok && wait(&sm.piece_full[n_fetched % kPieceRing], (n_fetched / kPieceRing) & 1u,
-                               tmo, &sm.abort));
-      x = sm.piece[n_fetched % kPieceRing];
-      ++n_fetched;
-      return ok && x.n_tiles > 0;
-    };
-    // Q's terms, the rows' limits and places of piece x, into half `par` of the piece arrays;
-    // then the products of the piece may start.  The last piece's S products are done.
-    const auto prepare = [&](uint32_t par) {
+    // Piece n's description stays in its ring until this warp is far past it.
+    const auto piece = [&](uint32_t n) -> const Piece& { return sm.piece[n % kPieceRing]; };
+    // Q's terms, the rows' limits and places of piece n; then its products may start.  The
+    // last piece's S products are done.
+    const auto prepare = [&](uint32_t n) {
+      const uint32_t par = n & 1u;
+      const Piece x = piece(n);
       const int p0 = x.rb * kRows, n_rows = min(kRows, x.rows * p.gqa - p0);
 #pragma unroll 1
       for (int r0 = sw; r0 < kRows; r0 += 4 * kWarpsS) {
@@ -256,52 +274,57 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (lane == 0) ptx::mbar_arrive(&sm.q_full);
     };
 
-    // The piece whose tiles are done and whose parts are due
-    int seq = 0, head = 0, s_idx = 0, base = 0, pr_lo = 0, n_rows = 0;
+    // First key of a piece that some rows of its block do not see (fewer than 128 are like it).
+    const auto part_seen_from = [&](const Piece& x) {
+      const int base = x.kv_len - x.rows;
+      return max(x.k_lo, tree ? base : base + x.rb * kRows / p.gqa + 1);
+    };
     float ref = kNone, ml = kNone, l = 0.f;
     for (bool first = true;; first = false) {
       // ---- the next piece may start while the last one ends (its S products are done)
-      const bool more = fetch();
-      if (more) prepare(pc & 1u);
-      const uint32_t last_par = (pc - 1u) & 1u;
+      ok = warp_all(ok && wait(&sm.piece_full[pc % kPieceRing], (pc / kPieceRing) & 1u, tmo, &sm.abort));
+      const bool more = ok && piece(pc).n_tiles > 0;
+      if (more) prepare(pc);
       if (!first) {
-        ok = warp_all(ok && wait(&sm.o_full, last_par, tmo, &sm.abort));
-        sm.sum[half][r] = l;
+        ok = warp_all(ok && wait(&sm.o_full, (pc - 1u) & 1u, tmo, &sm.abort));
+        sm.sum[qt][r] = l;
       }
-      stop = ptx::named_bar_or(bar_id, 64, !ok);
+      stop = ptx::named_bar_or(bar_id, kBar, !ok);
       if (stop) break;
       if (!first) {
-        // ---- the last piece's parts: this thread's row, 128 of its columns
+        // ---- the last piece's parts: this thread's row, 64 of its columns
         ptx::tc_fence_after();
-        const float L = sm.sum[0][r] + sm.sum[1][r];
+        const Piece& x = piece(pc - 1u);
+        const uint32_t par = (pc - 1u) & 1u;
+        const float L = (sm.sum[0][r] + sm.sum[1][r]) + (sm.sum[2][r] + sm.sum[3][r]);
         const float inv = L == 0.f ? 0.f : 1.f / L, ex = ex2(0.5f * (ref - ml));
-        const bool mine = s_idx >= 0 && r < n_rows;
-        const int row = sm.row[last_par][r];
-        const size_t part0 = size_t(s_idx) * size_t(p.T) * p.Hq;
-        if (mine && half == 0)
-          p.lse_parts[part0 + row] = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
-        const unsigned long long h0 = sm.hit[last_par][0], h1 = sm.hit[last_par][1];
+        const bool mine = x.s >= 0 && x.rb * kRows + r < x.rows * p.gqa;
+        const size_t part = size_t(x.s) * size_t(p.T) * p.Hq + sm.row[par][r];
+        if (mine && qt == 0) p.lse_parts[part] = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < 2; ++cc) {
           __syncwarp();
           uint32_t o[32];
-          ptx::tmem_ld32_wait(trow + kTmWideO + half * 128 + cc * 32, o);
+          ptx::tmem_ld32_wait(trow + kTmWideO + qt * 64 + cc * 32, o);
           if (!mine || L == 0.f) continue;
-          float* const dst = p.o_parts + (part0 + row) * 256 + half * 128 + cc * 32;
+          float* const dst = p.o_parts + part * 256 + qt * 64 + cc * 32;
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[i] = __uint_as_float(o[c + i]) * inv * ex * ex;
-              if ((h0 | h1) != 0ull) {
-                const int dim = half * 128 + cc * 32 + c + i, lim = sm.lim[last_par][r];
-                const unsigned long long m = sm.mask[last_par][r];
-                v[i] = put_back_nan(p, seq, head, h0, pr_lo, lim, tree, base, m, dim, v[i]);
-                v[i] = put_back_nan(p, seq, head, h1, pr_lo + 64, lim, tree, base, m, dim, v[i]);
-              }
-            }
-            *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<float4*>(dst + c) =
+                make_float4(__uint_as_float(o[c]) * inv * ex * ex, __uint_as_float(o[c + 1]) * inv * ex * ex,
+                            __uint_as_float(o[c + 2]) * inv * ex * ex, __uint_as_float(o[c + 3]) * inv * ex * ex);
+        }
+        const unsigned long long h0 = sm.hit[par][0], h1 = sm.hit[par][1];
+        if ((h0 | h1) != 0ull && mine && L != 0.f) {
+          // NaN values that were taken out, put back into what this thread wrote
+          const int base = x.kv_len - x.rows, first_key = part_seen_from(x);
+#pragma unroll 1
+          for (int c = qt * 64; c < qt * 64 + 64; ++c) {
+            float v = p.o_parts[part * 256 + c];
+            v = put_back_nan(p, x.b, x.g, h0, first_key, sm.lim[par][r], tree, base, sm.mask[par][r], c, v);
+            v = put_back_nan(p, x.b, x.g, h1, first_key + 64, sm.lim[par][r], tree, base,
+                             sm.mask[par][r], c, v);
+            p.o_parts[part * 256 + c] = v;
           }
         }
         ptx::tc_fence_before();
@@ -309,46 +332,40 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (!more) break;
       const uint32_t par = pc & 1u;
       ok = ok && wait(&sm.q_full, par, tmo, &sm.abort);   // rows, limits, factors are written
-      const int n_tiles = x.n_tiles, k_lo = x.k_lo, k_hi = x.k_hi;
-      seq = x.b;
-      head = x.g;
-      s_idx = x.s;
-      n_rows = min(kRows, x.rows * p.gqa - x.rb * kRows);
-      base = x.kv_len - x.rows;
-      // keys from pr_lo on are seen by some rows of the block only (fewer than 128)
-      pr_lo = max(k_lo, tree ? base : base + x.rb * kRows / p.gqa + 1);
-      const int lim = sm.lim[par][r];
-      const unsigned long long mask = sm.mask[par][r];
+      const int n_tiles = piece(pc).n_tiles, k_lo = piece(pc).k_lo, k_hi = piece(pc).k_hi;
+      const int pr_lo = part_seen_from(piece(pc));
       const float fac = sm.fac[par][r];
       ref = ml = kNone;
       l = 0.f;
       for (int j = 0; j < n_tiles; ++j, ++J) {
-        const int key0 = k_lo + j * kTile + half * 64;
+        const int key0 = k_lo + j * kTile + qt * kMine;
         const int tile_end = k_lo + (j + 1) * kTile;
-        ok = ok && wait(&sm.s_full, J & 1u, tmo, &sm.abort) &&
-             wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
+        ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
+        uint32_t s[kMine];
+        float f[2], lv[2];        // by run of 16 keys: score factor, log2 of the V scale
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int blk = (qt * kMine + i * 16) >> p.bs_log2;
+          const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
+          // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
+          f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
+          lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
+        }
+        ok = ok && wait(&sm.s_full, J & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         __syncwarp();
-        uint32_t s[64];
-        float f[4], lv[4];        // by run of 16 keys: score factor, log2 of the V scale
         float mp = -INFINITY, ms = -INFINITY;
         if (ok) {
           ptx::tc_fence_after();
-          ptx::tmem_ld64_wait(trow + kTmWideS + half * 64, s);
+          ptx::tmem_ld32_wait(trow + kTmWideS + qt * kMine, s);
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sm.s_free);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int blk = (half * 64 + i * 16) >> p.bs_log2;
-            const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
-            // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
-            f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
-            lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
-          }
           if (tile_end > k_hi || tile_end > pr_lo) {
+            const int lim = sm.lim[par][r], base = piece(pc).kv_len - piece(pc).rows;
+            const unsigned long long mask = sm.mask[par][r];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
+            for (int c = 0; c < kMine; ++c) {
               const int key = key0 + c;
               const bool vis = key < min(lim, k_hi) &&
                                (!tree || key < base || ((mask >> (key - base)) & 1ull));
@@ -356,7 +373,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
 #pragma unroll
             for (int c = 2; c < 16; c += 2) {
@@ -367,67 +384,58 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             ms = fmaxf(ms, m);
             mp = fmaxf(mp, m + lv[i]);
           }
-          sm.red[J & 1u][half][r] = make_float2(mp, ms);
+          sm.red[J & 1u][qt][r] = make_float2(mp, ms);
         }
-        if (ptx::named_bar_or(bar_id, 64, !ok)) {
+        if (ptx::named_bar_or(bar_id, kBar, !ok)) {
           stop = true;
           break;
         }
-        // ---- references (both threads of a row do the same)
-        {
-          const float2 o = sm.red[J & 1u][half ^ 1][r];
+        // ---- references (all threads of a row do the same)
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
+          const float2 o = sm.red[J & 1u][i][r];
           mp = fmaxf(mp, o.x);
           ms = fmaxf(ms, o.y);
         }
         const bool up = mp > ref + kWideCap, up_l = ms > ml + kLSlack;
+        float alpha = 1.f;
+        bool moved = false;      // the same in the whole warp
         if (__any_sync(0xffffffffu, up || up_l)) {
-          const float alpha = up ? ex2(ref - (mp - kWideTop)) : 1.f;
+          alpha = up ? ex2(ref - (mp - kWideTop)) : 1.f;
           if (up) ref = mp - kWideTop;
           if (up_l) {
             l *= ex2(ml - ms);
             ml = ms;
           }
-          if (j > 0 && __any_sync(0xffffffffu, up)) {
-            ok = warp_all(wait(&sm.pv_done, (J - 1) & 1u, tmo, &sm.abort));
-            __syncwarp();
-            if (ok) {
-              ptx::tc_fence_after();
-              rescale_o_cols(trow + kTmWideO + half * 128, alpha);
-            }
-          }
+          moved = j > 0 && __any_sync(0xffffffffu, up);
         }
         // ---- P's terms
-        uint32_t w[kPTerms][16];
+        uint32_t w[kPTerms][kMine / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const float a = lv[i] - ref;
-          float sum = 0.f;
+          const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
+          float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float e[4];
+            const int k = 16 * i + 4 * c;
+            const float2 x0 = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2, a2);
+            const float2 x1 = fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), f2, a2);
+            const float2 e0 = make_float2(ex2(x0.x), ex2(x0.y)), e1 = make_float2(ex2(x1.x), ex2(x1.y));
+            sum2 = add2(sum2, add2(e0, e1));
+            uint32_t t4[kPTerms];
+            p_terms5(e0, e1, t4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e[k] = ex2(fmaf(__uint_as_float(s[16 * i + 4 * c + k]), f[i], a));
-              sum += e[k];
-            }
-            uint32_t lo[kPTerms], hi[kPTerms];
-            p_terms5(e[0], e[1], lo);
-            p_terms5(e[2], e[3], hi);
-#pragma unroll
-            for (int t = 0; t < kPTerms; ++t) w[t][4 * i + c] = lo[t] | (hi[t] << 16);
+            for (int t = 0; t < kPTerms; ++t) w[t][4 * i + c] = t4[t];
           }
+          float sum = sum2.x + sum2.y;
           // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
           // block of tiny values that p hardly sees)
           const float d = -a - ml;
           if (__any_sync(0xffffffffu, d > 60.f)) {
             sum = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-              float v = 0.f;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v = k == c ? __uint_as_float(s[16 * i + k]) : v;
-              sum += ex2(fmaf(v, f[i], -ml));
-            }
+            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
             l += sum;
           } else {
             l += sum * ex2(d);
@@ -436,9 +444,9 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // ---- V rows that some row does not see
         if (tile_end > k_hi || tile_end > pr_lo) {
           ok = ok && wait(&sm.v_full[J % kSlots], (J / kSlots) & 1u, tmo, &sm.abort);
-          const int key = k_lo + j * kTile + r;   // thread by key here, half a row each
+          const int key = k_lo + j * kTile + r;   // thread by key here, a quarter of a row each
           if (ok && (key >= k_hi || key >= pr_lo) &&
-              clean_v_row(sm.v[J % kSlots], r, key >= k_hi, 8 * half, 8 * half + 8))
+              clean_v_row(sm.v[J % kSlots], r, key >= k_hi, 4 * qt, 4 * qt + 4))
             atomicOr(&sm.hit[par][(key - pr_lo) >> 6], 1ull << ((key - pr_lo) & 63));
           ptx::fence_proxy_async_smem();
         }
@@ -447,9 +455,11 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         __syncwarp();
         if (ok) {
           ptx::tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < kPTerms; ++t)
-            ptx::tmem_st16_wait(trow + kTmWideP + t * 32 + half * 16, w[t]);
+          // O, with PV of tile J - 1 in it, moves to the new references only now: the terms
+          // above were computed while that product ran
+          if (moved) rescale_cols64(trow + kTmWideO + qt * 64, alpha);
+          const uint32_t tp = trow + kTmWideP + qt * (kMine / 4);
+          ptx::tmem_st8x3_wait(tp, tp + 32, tp + 64, w[0], w[1], w[2]);
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sm.p_full);
