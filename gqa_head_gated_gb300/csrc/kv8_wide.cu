@@ -34,10 +34,12 @@ namespace gqa {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kWarpsS = 16;            // softmax warps
-constexpr int kWideThreads = 64 + 32 * kWarpsS;
 constexpr int kShare = 4;              // softmax threads of a row
 constexpr int kMine = kTile / kShare;  // keys of each
+constexpr int kRuns = kMine / 16;      // runs of 16 keys, which have one scale each
+constexpr int kCols = 256 / kShare;    // columns of O of each
+constexpr int kWarpsS = 4 * kShare;    // softmax warps
+constexpr int kWideThreads = 64 + 32 * kWarpsS;
 constexpr int kQTerms = 2, kPTerms = 3;
 constexpr int kSlots = 2;              // K and V slots of a tile each
 constexpr uint32_t kTmWideO = 0, kTmWideS = 256, kTmWideP = 384;
@@ -49,8 +51,8 @@ constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, 256, 0, 1, 0) | (1u << 7);
 
 struct __align__(1024) WideSmem : RingSmem<kSlots, kSlots> {
   alignas(1024) uint8_t q[kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
-  float2 red[2][kShare][kRows];            // [tile parity][quarter][row]: maxima with vs, without
-  float sum[kShare][kRows];                // [quarter][row]
+  float2 red[2][kShare][kRows];            // [tile parity][share][row]: maxima with vs, without
+  float sum[kShare][kRows];                // [share][row]
   uint64_t s_full, s_free, p_full, pv_done, q_full, o_full, drain;
   // by piece, two in turn
   unsigned long long hit[2][2];            // NaN V rows taken out: bits of keys pr_lo + 64 w + i
@@ -92,10 +94,10 @@ __device__ __forceinline__ void p_terms5(float2 lo, float2 hi, uint32_t (&w)[kPT
   }
 }
 
-// 64 columns of a row of O times f, in tensor memory (whole warp).
-__device__ __noinline__ void rescale_cols64(uint32_t ta, float f) {
+// kCols columns of a row of O times f, in tensor memory (whole warp).
+__device__ __noinline__ void rescale_o(uint32_t ta, float f) {
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; c < kCols / 32; ++c) {
     uint32_t o[32];
     ptx::tmem_ld32_wait(ta + 32 * c, o);
 #pragma unroll
@@ -206,7 +208,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   } else {
     // ------------------------------------------------------------ softmax, epilogue
     const int sw = warp - 2;
-    const int qt = sw >> 2;                    // keys 32 qt .. 32 qt + 31 of a tile
+    const int qt = sw >> 2;                    // keys kMine qt .. of a tile
     const int qd = warp & 3;                   // tensor-memory lanes 32 qd .. 32 qd + 31
     const int r = qd * 32 + lane;              // this thread's row of the block
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
@@ -292,22 +294,24 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       stop = ptx::named_bar_or(bar_id, kBar, !ok);
       if (stop) break;
       if (!first) {
-        // ---- the last piece's parts: this thread's row, 64 of its columns
+        // ---- the last piece's parts: this thread's row, kCols of its columns
         ptx::tc_fence_after();
         const Piece& x = piece(pc - 1u);
         const uint32_t par = (pc - 1u) & 1u;
-        const float L = (sm.sum[0][r] + sm.sum[1][r]) + (sm.sum[2][r] + sm.sum[3][r]);
+        float L = 0.f;
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) L += sm.sum[i][r];
         const float inv = L == 0.f ? 0.f : 1.f / L, ex = ex2(0.5f * (ref - ml));
         const bool mine = x.s >= 0 && x.rb * kRows + r < x.rows * p.gqa;
         const size_t part = size_t(x.s) * size_t(p.T) * p.Hq + sm.row[par][r];
         if (mine && qt == 0) p.lse_parts[part] = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
 #pragma unroll 1
-        for (int cc = 0; cc < 2; ++cc) {
+        for (int cc = 0; cc < kCols / 32; ++cc) {
           __syncwarp();
           uint32_t o[32];
-          ptx::tmem_ld32_wait(trow + kTmWideO + qt * 64 + cc * 32, o);
+          ptx::tmem_ld32_wait(trow + kTmWideO + qt * kCols + cc * 32, o);
           if (!mine || L == 0.f) continue;
-          float* const dst = p.o_parts + part * 256 + qt * 64 + cc * 32;
+          float* const dst = p.o_parts + part * 256 + qt * kCols + cc * 32;
 #pragma unroll
           for (int c = 0; c < 32; c += 4)
             *reinterpret_cast<float4*>(dst + c) =
@@ -319,7 +323,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           // NaN values that were taken out, put back into what this thread wrote
           const int base = x.kv_len - x.rows, first_key = part_seen_from(x);
 #pragma unroll 1
-          for (int c = qt * 64; c < qt * 64 + 64; ++c) {
+          for (int c = qt * kCols; c < (qt + 1) * kCols; ++c) {
             float v = p.o_parts[part * 256 + c];
             v = put_back_nan(p, x.b, x.g, h0, first_key, sm.lim[par][r], tree, base, sm.mask[par][r], c, v);
             v = put_back_nan(p, x.b, x.g, h1, first_key + 64, sm.lim[par][r], tree, base,
@@ -342,9 +346,9 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int tile_end = k_lo + (j + 1) * kTile;
         ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
         uint32_t s[kMine];
-        float f[2], lv[2];        // by run of 16 keys: score factor, log2 of the V scale
+        float f[kRuns], lv[kRuns];        // by run of 16 keys: score factor, log2 of the V scale
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kRuns; ++i) {
           const int blk = (qt * kMine + i * 16) >> p.bs_log2;
           const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
           // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
@@ -373,7 +377,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < kRuns; ++i) {
             float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
 #pragma unroll
             for (int c = 2; c < 16; c += 2) {
@@ -409,13 +413,22 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
           moved = j > 0 && __any_sync(0xffffffffu, up);
         }
-        // ---- P's terms
-        uint32_t w[kPTerms][kMine / 4];
+        // ---- V rows that some row does not see
+        if (tile_end > k_hi || tile_end > pr_lo) {
+          ok = ok && wait(&sm.v_full[J % kSlots], (J / kSlots) & 1u, tmo, &sm.abort);
+          const int key = k_lo + j * kTile + r;   // thread by key here, its share of the row
+          if (ok && (key >= k_hi || key >= pr_lo) &&
+              clean_v_row(sm.v[J % kSlots], r, key >= k_hi, 16 / kShare * qt, 16 / kShare * (qt + 1)))
+            atomicOr(&sm.hit[par][(key - pr_lo) >> 6], 1ull << ((key - pr_lo) & 63));
+          ptx::fence_proxy_async_smem();
+        }
+        // ---- P's terms, a run of 16 keys at a time
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kRuns; ++i) {
           const float a = lv[i] - ref;
           const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
           float2 sum2 = make_float2(0.f, 0.f);
+          uint32_t w[kPTerms][4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int k = 16 * i + 4 * c;
@@ -426,7 +439,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             uint32_t t4[kPTerms];
             p_terms5(e0, e1, t4);
 #pragma unroll
-            for (int t = 0; t < kPTerms; ++t) w[t][4 * i + c] = t4[t];
+            for (int t = 0; t < kPTerms; ++t) w[t][c] = t4[t];
           }
           float sum = sum2.x + sum2.y;
           // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
@@ -440,26 +453,23 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           } else {
             l += sum * ex2(d);
           }
+          if (i == 0) {
+            // PV of tile J - 1 has read P, and is in O, which moves to the new references only
+            // now: the terms were computed while that product ran
+            if (J > 0) ok = ok && wait(&sm.pv_done, (J - 1) & 1u, tmo, &sm.abort);
+            ok = warp_all(ok);
+            __syncwarp();
+            if (ok) {
+              ptx::tc_fence_after();
+              if (moved) rescale_o(trow + kTmWideO + qt * kCols, alpha);
+            }
+          }
+          if (ok) {
+            const uint32_t tp = trow + kTmWideP + qt * (kMine / 4) + 4 * i;
+            ptx::tmem_st4x3_wait(tp, tp + 32, tp + 64, w[0], w[1], w[2]);
+          }
         }
-        // ---- V rows that some row does not see
-        if (tile_end > k_hi || tile_end > pr_lo) {
-          ok = ok && wait(&sm.v_full[J % kSlots], (J / kSlots) & 1u, tmo, &sm.abort);
-          const int key = k_lo + j * kTile + r;   // thread by key here, a quarter of a row each
-          if (ok && (key >= k_hi || key >= pr_lo) &&
-              clean_v_row(sm.v[J % kSlots], r, key >= k_hi, 4 * qt, 4 * qt + 4))
-            atomicOr(&sm.hit[par][(key - pr_lo) >> 6], 1ull << ((key - pr_lo) & 63));
-          ptx::fence_proxy_async_smem();
-        }
-        if (J > 0) ok = ok && wait(&sm.pv_done, (J - 1) & 1u, tmo, &sm.abort);   // P is free
-        ok = warp_all(ok);
-        __syncwarp();
         if (ok) {
-          ptx::tc_fence_after();
-          // O, with PV of tile J - 1 in it, moves to the new references only now: the terms
-          // above were computed while that product ran
-          if (moved) rescale_cols64(trow + kTmWideO + qt * 64, alpha);
-          const uint32_t tp = trow + kTmWideP + qt * (kMine / 4);
-          ptx::tmem_st8x3_wait(tp, tp + 32, tp + 64, w[0], w[1], w[2]);
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sm.p_full);
