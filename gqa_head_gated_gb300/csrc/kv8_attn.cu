@@ -172,21 +172,21 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
-      const uint32_t qa = ptx::smem_addr(sm.q), pa = ptx::smem_addr(sm.p);
+      const uint64_t qd = ptx::sdesc_sw128(ptx::smem_addr(sm.q), 16, 1024);
+      const uint64_t pd = ptx::sdesc_plain(ptx::smem_addr(sm.p), 128, 2048);
       uint32_t J = 0;
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
         const uint32_t ks = n % C::kKS;
         if (!wait(&sm.k_full[ks], (n / C::kKS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
-        const uint32_t ka = ptx::smem_addr(sm.k[ks]);
+        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
         const uint32_t d = tmem + C::kTmS + (n & 1u) * C::kStep;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_ss_f8(
-              d, ptx::sdesc_sw128(ka + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
-              ptx::sdesc_sw128(qa + (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32, 16, 1024),
-              C::kIdescS, kk > 0);
+          ptx::mma_ss_f8(d, ptx::sdesc_at(kd, (kk >> 2) * kHalfBytes + (kk & 3) * 32),
+                         ptx::sdesc_at(qd, (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32), C::kIdescS,
+                         kk > 0);
         ptx::tc_commit(&sm.s_full[n & 1]);
         ptx::tc_commit(&sm.k_empty[ks]);
         return true;
@@ -196,14 +196,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!wait(&sm.p_full[buf], (n >> 1) & 1u, tmo, &sm.abort)) return false;
         if (!wait(&sm.v_full[vs], (n / C::kVS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
-        const uint32_t va = ptx::smem_addr(sm.v[vs]);
+        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kHalfBytes, 1024);
+        const uint64_t pb = ptx::sdesc_at(pd, buf * (C::kNO * kTile));
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::mma_ss_f8(tmem + C::kTmO + h * C::kStep,
-                           ptx::sdesc_sw128(va + h * kHalfBytes + kk * 4096, kHalfBytes, 1024),
-                           ptx::sdesc_plain(pa + buf * (C::kNO * kTile) + kk * 512, 128, 2048),
+                           ptx::sdesc_at(vd, h * kHalfBytes + kk * 4096), ptx::sdesc_at(pb, kk * 512),
                            C::kIdescO, !first || kk > 0);
         ptx::tc_commit(&sm.pv_done[buf]);
         ptx::tc_commit(&sm.v_empty[vs]);

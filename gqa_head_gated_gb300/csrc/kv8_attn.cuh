@@ -110,10 +110,11 @@ __device__ __forceinline__ bool piece_at(const Kv8AttnArgs& p, const int4* seqs,
   return true;
 }
 
+// log2 of a scale, exactly where it is a normal power of two; 0 gives -inf.  Without a branch.
 __device__ __forceinline__ float log2_scale(float s) {
   const uint32_t b = __float_as_uint(s);
-  if ((b & 0x7FFFFFu) == 0u && b - 0x00800000u < 0x7F000000u) return float(int(b >> 23) - 127);
-  return __log2f(s);   // 0 gives -inf
+  const float e = float(int(b >> 23) - 127), l = __log2f(s);
+  return (b & 0x7FFFFFu) == 0u && b - 0x00800000u < 0x7F000000u ? e : l;
 }
 
 // Bytes of a 16-byte chunk that are e4m3 NaN become 0; returns whether there was one.

@@ -244,6 +244,14 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, ui
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46);
 }
 
+// A matrix descriptor moved on by `bytes` (a constant multiple of 16; the start address stays
+// below 2^18): one add, where making it anew takes a dozen instructions of the issuing thread.
+__device__ __forceinline__ uint64_t sdesc_at(uint64_t d, uint32_t bytes) {
+  uint32_t lo = uint32_t(d), hi = uint32_t(d >> 32);
+  lo += bytes >> 4;
+  return (uint64_t(hi) << 32) | lo;
+}
+
 // 32 lanes x 8 consecutive columns at two (three) addresses -> registers, waited once.
 __device__ __forceinline__ void tmem_ld8x2_wait(uint32_t t0, uint32_t t1, uint32_t (&a)[8],
                                                 uint32_t (&b)[8]) {
