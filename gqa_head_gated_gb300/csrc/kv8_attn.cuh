@@ -22,7 +22,10 @@ constexpr int kHalfBytes = kTile * 128;          // 128 keys x 128 dims of K or 
 constexpr int kSlotBytes = 2 * kHalfBytes;
 constexpr int kScaleRing = 8;      // tiles whose scales are held: see the copies
 constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see the copies
-constexpr int kSwitch = 3;         // what going on to another segment costs, in tiles
+// What going on to another segment costs a CTA, in tiles, where it has kLongShare tiles or more
+// (with short shares it would only unsettle them: one tile each is best then).
+constexpr int kSwitch = 3;
+constexpr uint32_t kLongShare = 8;
 constexpr int kMaxTileBlocks = kTile / 16;
 constexpr float kLSlack = 64.f;    // l's terms stay below 2^64
 constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
@@ -46,6 +49,7 @@ struct RingSmem {
   Piece piece[kPieceRing];
   int4 seq[kKv8Seqs];                      // first token, rows, keys, tiles
   uint32_t base[kKv8Seqs + 1];             // first position of each sequence's segments
+  uint32_t segs[kKv8Seqs + 1];             // segments before each sequence
   uint32_t tmem_base;
   int most;                                // tiles of the longest sequence
   int abort, zero;
@@ -53,7 +57,7 @@ struct RingSmem {
 
 // This CTA's share [pos, end) of the launch's positions, cut into n_cta shares.
 struct Share {
-  uint32_t pos, end, n_cta;
+  uint32_t pos, end, n_cta, lead;   // lead: positions of a segment before its tiles
 };
 
 // ptx::mbar_wait with the polling loop out of line: the kernel has many waits, and its code
@@ -67,13 +71,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t tm
 }
 
 // The piece of this CTA's share [.., end) that starts at position `pos`, which moves on behind
-// it.  A segment takes kSwitch positions before those of its tiles: a CTA that goes on to it
+// it.  A segment takes `lead` positions before those of its tiles: a CTA that goes on to it
 // from another has that much less to do.  `last`: the piece ends its segment.  False: the
 // piece has no position of a tile.
 template <int MB>
 __device__ __forceinline__ bool piece_at(const Kv8AttnArgs& p, const int4* seqs, const uint32_t* base,
-                                         uint32_t& pos, uint32_t end, uint32_t n_cta, Piece& x,
-                                         bool& last) {
+                                         uint32_t& pos, const Share& share, Piece& x, bool& last) {
+  const uint32_t end = share.end;
   int lo = 0, hi = p.B - 1;   // last sequence that starts at or before pos
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -84,11 +88,11 @@ __device__ __forceinline__ bool piece_at(const Kv8AttnArgs& p, const int4* seqs,
   x.t0 = q.x;
   x.rows = q.y;
   x.kv_len = q.z;
-  const uint32_t len = uint32_t(q.w) + kSwitch, n_rb = uint32_t((x.rows * p.gqa + MB - 1) / MB);
+  const uint32_t len = uint32_t(q.w) + share.lead, n_rb = uint32_t((x.rows * p.gqa + MB - 1) / MB);
   const uint32_t seg = (pos - base[lo]) / len;
   x.g = int(seg / n_rb);
   x.rb = int(seg - uint32_t(x.g) * n_rb);
-  const uint32_t start = base[lo] + seg * len, first = start + kSwitch;
+  const uint32_t start = base[lo] + seg * len, first = start + share.lead;
   const uint32_t from = max(pos, first);
   last = end >= start + len;
   pos = min(end, start + len);
@@ -97,7 +101,7 @@ __device__ __forceinline__ bool piece_at(const Kv8AttnArgs& p, const int4* seqs,
   x.s = 0;
   if (from != first) {
     const unsigned long long W = base[p.B];
-    x.s = int(blockIdx.x) - int(((first + 1ull) * n_cta - 1) / W);
+    x.s = int(blockIdx.x) - int(((first + 1ull) * share.n_cta - 1) / W);
   }
   x.k_lo = int(from - first) * kTile;
   x.k_hi = x.kv_len;          // a tree row may see up to the last key
@@ -203,6 +207,13 @@ __device__ __forceinline__ Share cut_shares(RingSmem<KS, VS>& sm, const Kv8AttnA
   const int tid = threadIdx.x, lane = tid & 31;
   wait_for_last();
   let_next_start();   // not before: the merge reads lengths and gate ahead of its own wait
+  // All of Q is on its way to L2 while the shares are cut (a piece's start reads its rows).
+  if (p.b0 == 0) {
+    const size_t lines = size_t(p.T) * p.Hq * 4;   // 128 bytes each
+    for (size_t i = size_t(blockIdx.x) * blockDim.x + tid; i < lines && i < (size_t(1) << 17);
+         i += size_t(gridDim.x) * blockDim.x)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + i * 8));
+  }
   for (int b = tid; b < p.B; b += blockDim.x) {
     const int kv = p.kv_lens[b], t0 = p.cu_rows ? p.cu_rows[b] : p.b0 + b;
     const int rows = p.cu_rows ? p.cu_rows[b + 1] - t0 : 1;
@@ -210,30 +221,44 @@ __device__ __forceinline__ Share cut_shares(RingSmem<KS, VS>& sm, const Kv8AttnA
                     kv <= p.max_kv_len;
     const int tiles = ok && rows > 0 ? (kv + kTile - 1) / kTile : 0;
     sm.seq[b] = make_int4(t0, rows, kv, tiles);
-    sm.base[b + 1] = tiles > 0 ? uint32_t(tiles + kSwitch) * uint32_t(p.Hkv) *
-                                     uint32_t((rows * p.gqa + MB - 1) / MB)
-                               : 0u;
+    const uint32_t segs = tiles > 0 ? uint32_t(p.Hkv) * uint32_t((rows * p.gqa + MB - 1) / MB) : 0u;
+    sm.base[b + 1] = uint32_t(tiles) * segs;
+    sm.segs[b + 1] = segs;
     if (tiles > 0) atomicMax(&sm.most, tiles);
     if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
   }
   __syncthreads();
+  Share x{0, 0, 0, 0};
   if (tid < 32) {   // inclusive sums over the sequences, 32 at a time
-    uint32_t run = 0;
+    uint32_t run = 0, runs = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       uint32_t v = b0 + lane < p.B ? sm.base[b0 + lane + 1] : 0u;
+      uint32_t w = b0 + lane < p.B ? sm.segs[b0 + lane + 1] : 0u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o), t = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) {
+          v += u;
+          w += t;
+        }
       }
-      if (b0 + lane < p.B) sm.base[b0 + lane + 1] = run + v;
+      if (b0 + lane < p.B) {
+        sm.base[b0 + lane + 1] = run + v;
+        sm.segs[b0 + lane + 1] = runs + w;
+      }
       run += __shfl_sync(0xffffffffu, v, 31);
+      runs += __shfl_sync(0xffffffffu, w, 31);
     }
+    // (this warp's own writes) each sequence's leads go before its tiles
+    __syncwarp();
+    if (run >= kLongShare * gridDim.x)
+      for (int b = lane; b < p.B; b += 32) sm.base[b + 1] += kSwitch * sm.segs[b + 1];
   }
   __syncthreads();
   const uint32_t W = sm.base[p.B];
+  x.lead = W > 0 && W >= kLongShare * gridDim.x + kSwitch * sm.segs[p.B] ? kSwitch : 0;
+  x.n_cta = min(gridDim.x, W);
   // Shares so long that no segment needs more than `parts` parts.
-  Share x{0, 0, min(gridDim.x, W)};
   if (sm.most > p.parts)
     x.n_cta = min(x.n_cta, max(1u, uint32_t((unsigned long long)W * uint32_t(p.parts - 2) /
                                             uint32_t(sm.most))));
@@ -277,7 +302,7 @@ __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArg
   for (uint32_t pos = share.pos; ok && pos < share.end;) {
     Piece x;
     bool last;
-    if (!piece_at<MB>(p, sm.seq, sm.base, pos, share.end, share.n_cta, x, last)) continue;
+    if (!piece_at<MB>(p, sm.seq, sm.base, pos, share, x, last)) continue;
     if (x.s < 0 || x.s >= p.parts) {   // never, with shares as cut above
       if (lane == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
       x.s = -1;

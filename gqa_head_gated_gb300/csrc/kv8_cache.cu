@@ -81,10 +81,10 @@ __device__ __forceinline__ void rescale_rows(uint2* block, int n, float s_old, i
 
 // One CTA: the runs that start in its window of 64 tokens, for one KV head of K or V.
 // A token's run is the tokens before it in the same block; a run is at most one block.
-// Every warp keeps its 8 window rows in registers between the maximum and the rounding;
-// rows of the last run past the window are read twice.
+// Every warp keeps 8 of the first 64 rows in registers between the maximum and the rounding;
+// rows of the last run past them are read twice.
 template <bool kF16>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendParams p) {
   __shared__ int s_slot[kSpan + 1];          // slot of token w0 - 1 + i
   __shared__ uint32_t s_start[kSpan / 32];   // bit i: token w0 + i starts a run
   __shared__ uint32_t s_break[kSpan / 32];   // bit i: token w0 + i starts a run or is in none
@@ -97,18 +97,11 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   const int w0 = blockIdx.x * kWindow, g = blockIdx.y, kv = blockIdx.z;
   const int bs = 1 << p.bs_log2;
   const int n_span = min(kWindow + bs, p.T - w0);   // tokens from w0 on that matter here
-  const uint4* const x = p.x[kv];
-  uint2* const pool = p.pool[kv];
+  const uint4* const x = kv == 0 ? p.x[0] : p.x[1];
+  uint2* const pool = kv == 0 ? p.pool[0] : p.pool[1];
 
   let_next_start();
   wait_for_last();
-  // The window's rows are on their way while the runs are worked out.
-  uint4 u[kRowsPerWarp];
-#pragma unroll
-  for (int k = 0; k < kRowsPerWarp; ++k) {
-    const int t = w0 + warp + k * kWarps;
-    if (t < p.T) u[k] = __ldg(x + (size_t(t) * p.Hkv + g) * 32 + lane);
-  }
   for (int i = tid; i < kSpan + 1; i += kThreads) {
     const int t = w0 - 1 + i;
     s_slot[i] = t >= 0 && i <= n_span ? __ldg(p.slots + t) : -1;
@@ -136,6 +129,15 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
     }
   }
   __syncthreads();
+  // Rows before the first run belong to the window before; the 64 from it on are loaded now.
+  const uint64_t starts = (uint64_t(s_start[1]) << 32) | s_start[0];
+  const int i0 = starts == 0ull ? kSpan : __ffsll(static_cast<long long>(starts)) - 1;
+  uint4 u[kRowsPerWarp];
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    const int i = i0 + warp + k * kWarps;
+    if (i < n_span) u[k] = __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane);
+  }
   // First token of token w0 + i's run, -1 when it is in no run that starts in the window.
   const auto run_of = [&](int i) -> int {
     if (i >= n_span) return -1;
@@ -150,14 +152,14 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   uint32_t finite = 0u;    // bit k: row k of this warp holds no NaN or infinity
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k) {
-    run[k] = run_of(warp + k * kWarps);
+    run[k] = run_of(i0 + warp + k * kWarps);
     if (run[k] < 0) continue;
     bool all;
     const uint32_t m = row_amax<kF16>(u[k], &all);
     finite |= uint32_t(all) << k;
     if (lane == 0) atomicMax(&s_max[run[k]], m);
   }
-  for (int i = kWindow + warp; i < n_span; i += kWarps) {
+  for (int i = i0 + kWindow + warp; i < n_span; i += kWarps) {
     const int r = run_of(i);
     if (r < 0) break;   // past the last run
     bool all;
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   __syncthreads();
   if (tid < kWindow && ((s_start[tid >> 5] >> (tid & 31)) & 1u)) {
     const int s = s_slot[tid + 1];
-    float* const sp = p.scale[kv] + size_t(s >> p.bs_log2) * p.Hkv + g;
+    float* const sp = (kv == 0 ? p.scale[0] : p.scale[1]) + size_t(s >> p.bs_log2) * p.Hkv + g;
     int e = scale_exp(s_max[tid]);
     if ((s & (bs - 1)) != 0) {
       const float old = *sp;
@@ -192,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams
   };
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k)
-    if (run[k] >= 0) put(warp + k * kWarps, run[k], u[k], (finite >> k) & 1u);
-  for (int i = kWindow + warp; i < n_span; i += kWarps) {
+    if (run[k] >= 0) put(i0 + warp + k * kWarps, run[k], u[k], (finite >> k) & 1u);
+  for (int i = i0 + kWindow + warp; i < n_span; i += kWarps) {
     const int r = run_of(i);
     if (r < 0) break;
     put(i, r, __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), false);
@@ -225,7 +227,7 @@ struct KeepParams {
 
 // One CTA: one sequence and KV head of K or V.  All kept rows are in registers before
 // the first is written (a block's scale may change while later rows of it are due).
-__global__ void __launch_bounds__(kThreads) kv8_keep_kernel(const KeepParams p) {
+__global__ void __launch_bounds__(kThreads, 6) kv8_keep_kernel(const KeepParams p) {
   __shared__ int s_src[kMaxKeep];          // pool row (block * bs + row) of kept row k, and
   __shared__ int s_dst[kMaxKeep];          // its place
   __shared__ uint32_t s_max[kMaxRuns];
@@ -262,8 +264,8 @@ __global__ void __launch_bounds__(kThreads) kv8_keep_kernel(const KeepParams p) 
   }
   if (tid == 0 && g == 0 && kv == 0 && p.lens_out != nullptr) p.lens_out[b] = base + nk;
   if (nk == 0) return;
-  uint2* const pool = p.pool[kv];
-  float* const scale = p.scale[kv];
+  uint2* const pool = kv == 0 ? p.pool[0] : p.pool[1];
+  float* const scale = kv == 0 ? p.scale[0] : p.scale[1];
   // 8-byte units of pool row `at`, and its block's scale
   const auto row_of = [&](int at) {
     return ((size_t(at >> p.bs_log2) * p.Hkv + g) * bs + (at & (bs - 1))) * 32;

@@ -93,7 +93,7 @@ block_plan_kernel(const PlanParams p) {
   int* const s_have = s_len + B;       // blocks held, -1 for a sequence that breaks the bounds
   int* const s_rel = s_have + B;       // blocks to release, then their exclusive sums
   int* const s_grow = s_rel + B;       // blocks to take, then their exclusive sums
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int cta = blockIdx.x, ctas = gridDim.x;   // the grid is one cluster
   const long long cap = (long long)p.max_blocks << bs_log2;
 
@@ -126,31 +126,66 @@ block_plan_kernel(const PlanParams p) {
   };
   // Every CTA has read the lengths, counts and the stack's height.
   ptx::cluster_sync();
+  // The last sequence whose first rank (exclusive sum) is at most k: the one with rank k.
+  const auto owner = [&](const int* sums, int k) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sums[mid] <= k) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  const int per = ctas * kThreads, first = cta * kThreads + tid;
   if (total.x > 0) {
-    for (int b = cta * kWarps + (tid >> 5); b < B; b += ctas * kWarps) {
-      if (s_have[b] < 0) continue;
-      const int need = need_of(b), n = s_have[b] - need;
-      int* const row = p.tables + (long long)b * p.max_blocks + need;
-      for (int i = lane; i < n; i += 32) {
-        const int at = fc + total.x - 1 - (s_rel[b] + i);
-        if (at < p.num_blocks) p.free_list[at] = row[i];
-        row[i] = -1;
+    for (int k0 = first; k0 < total.x; k0 += kUnroll * per) {
+      int blk[kUnroll];
+      int* at[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int k = k0 + u * per;
+        if (k >= total.x) continue;
+        const int b = owner(s_rel, k);
+        at[u] = p.tables + (long long)b * p.max_blocks + need_of(b) + (k - s_rel[b]);
+        blk[u] = *at[u];
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int k = k0 + u * per;
+        if (k >= total.x) continue;
+        const int to = fc + total.x - 1 - k;
+        if (to < p.num_blocks) p.free_list[to] = blk[u];
+        *at[u] = -1;
       }
     }
     ptx::cluster_sync();
   }
-  for (int b = cta * kWarps + (tid >> 5); b < B; b += ctas * kWarps) {
+  // (sequences that are not served come last, so that ranks below `avail` tell them apart but
+  // for the first of them, whose blocks would fit in part)
+  for (int k0 = first; k0 < min(total.y, avail); k0 += kUnroll * per) {
+    int blk[kUnroll], own[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = k0 + u * per;
+      if (k >= min(total.y, avail)) continue;
+      own[u] = owner(s_grow, k);
+      blk[u] = __ldcg(p.free_list + avail - 1 - k);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = k0 + u * per;
+      if (k >= min(total.y, avail)) continue;
+      const int b = own[u], have = s_have[b], n = need_of(b) - have;
+      if ((long long)s_grow[b] + n <= avail)
+        p.tables[(long long)b * p.max_blocks + have + (k - s_grow[b])] = blk[u];
+    }
+  }
+  for (int b = first; b < B; b += per) {
     const int have = s_have[b];
     const int need = have < 0 ? 0 : need_of(b), n = need - have;
     const bool served = have >= 0 && (n <= 0 || (long long)s_grow[b] + n <= avail);
-    if (served) {
-      int* const row = p.tables + (long long)b * p.max_blocks + have;
-      for (int i = lane; i < n; i += 32) row[i] = __ldcg(p.free_list + avail - 1 - (s_grow[b] + i));
-      if (lane == 0 && n != 0) p.n_blocks[b] = need;
-    } else if (have >= 0 && lane == 0) {
-      record_status(p.ctl.status, GQA_ERR_NO_BLOCKS);
-    }
-    if (lane == 0) p.lens_out[b] = s_len[b] + (served ? s_cu[b + 1] - s_cu[b] : 0);
+    if (served && n != 0) p.n_blocks[b] = need;
+    if (have >= 0 && !served) record_status(p.ctl.status, GQA_ERR_NO_BLOCKS);
+    p.lens_out[b] = s_len[b] + (served ? s_cu[b + 1] - s_cu[b] : 0);
   }
   if (cta == 0 && tid == 0) {
     // The served sequences are those before the first that does not fit (and those that
@@ -166,19 +201,14 @@ block_plan_kernel(const PlanParams p) {
   if (p.T == 0) return;
   ptx::cluster_sync();
   // Slots, kUnroll tokens a thread at a time: their table reads are in flight together.
-  const int per = ctas * kThreads;
-  for (int t0 = cta * kThreads + tid; t0 < p.T; t0 += kUnroll * per) {
+  for (int t0 = first; t0 < p.T; t0 += kUnroll * per) {
     int row[kUnroll], blk[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int t = t0 + u * per;
       row[u] = -1;
       if (t >= p.T) continue;
-      int lo = 0, hi = B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_cu[mid] <= t) lo = mid; else hi = mid - 1;
-      }
+      const int lo = owner(s_cu, t);
       const int have = s_have[lo];
       if (have < 0 || t < s_cu[lo] || t >= s_cu[lo + 1]) continue;
       const int n = need_of(lo) - have, pos = s_len[lo] + t - s_cu[lo];
