@@ -315,6 +315,8 @@ def kv_keep(k_cache, v_cache, kv_lens, cu_rows, keep_idx, cu_keep, kv_lens_out=N
 # little: each gives the tensor's address, and the message is made only for a refusal.
 _I32, _F32, _F8 = torch.int32, torch.float32, torch.float8_e4m3fn
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_entry = {}     # entry points by name
 
 
 def _stream_of(d):
@@ -324,9 +326,12 @@ def _stream_of(d):
 
 def _at(t, dtype, shape, d, name):
     """Address of a contiguous CUDA tensor of this type and shape on device d."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == d and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == d
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -338,9 +343,10 @@ def _at(t, dtype, shape, d, name):
 def _cuda_index(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return d
 
 
 def _tables(block_tables, B, d):
@@ -354,25 +360,27 @@ def _tables(block_tables, B, d):
 def _kv8_pools(k_pool, v_pool, k_scale, v_scale):
     """Device, (num_blocks, Hkv, block_size) and addresses of checked pools and scales."""
     d = _cuda_index(k_pool, "k_pool")
-    if k_pool.dim() != 4 or k_pool.shape[3] != HEAD_DIM:
-        raise ValueError(f"k_pool must be [num_blocks, Hkv, block_size, {HEAD_DIM}], got "
-                         f"{tuple(k_pool.shape)}")
     shape = k_pool.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM:
+        raise ValueError(f"k_pool must be [num_blocks, Hkv, block_size, {HEAD_DIM}], got "
+                         f"{tuple(shape)}")
     N, Hkv, bs, _ = shape
-    return d, N, Hkv, bs, (_at(k_pool, _F8, shape, d, "k_pool"), _at(v_pool, _F8, shape, d, "v_pool"),
-                           _at(k_scale, _F32, (N, Hkv), d, "k_scale"),
-                           _at(v_scale, _F32, (N, Hkv), d, "v_scale"))
+    scales = (N, Hkv)
+    return (d, N, Hkv, bs, _at(k_pool, _F8, shape, d, "k_pool"), _at(v_pool, _F8, shape, d, "v_pool"),
+            _at(k_scale, _F32, scales, d, "k_scale"), _at(v_scale, _F32, scales, d, "v_scale"))
 
 
 def _call(name, d, *args):
     """Runs an entry point on device d's current stream (its last argument)."""
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == d:
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(load(), name)
+    if _current_device() == d:
         code = fn(*args, _stream_of(d))
     else:
         with torch.cuda.device(d):
             code = fn(*args, _stream_of(d))
-    if code != 0:
+    if code:
         raise GqaError(code, name)
 
 
@@ -411,7 +419,7 @@ def kv8_append(k_new, v_new, slots, k_pool, v_pool, k_scale, v_scale):
     block and head, kept as large as the block's rows ask (rows that a block holds already
     are rounded again when its scale grows)."""
     sfx = _elem(k_new, "k_new")
-    d, N, Hkv, bs, pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
     T, shape = k_new.shape[0], (k_new.shape[0], Hkv, HEAD_DIM)
     _call("gqa_kv8_append" + sfx, d, _at(k_new, k_new.dtype, shape, d, "k_new"),
           _at(v_new, k_new.dtype, shape, d, "v_new"), _at(slots, _I32, (T,), d, "slots"), *pools, T,
@@ -423,7 +431,7 @@ def kv8_keep(k_pool, v_pool, k_scale, v_scale, block_tables, kv_lens, cu_rows, k
     """kv_keep() for the paged 8-bit cache: the accepted draft rows (at most 64 per sequence)
     move to the front of each sequence's draft region, as if their values had been appended
     there; writes the new lengths into kv_lens_out when given."""
-    d, N, Hkv, bs, pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
     _cuda_index(kv_lens, "kv_lens")
     _cuda_index(keep_idx, "keep_idx")
     B, n = kv_lens.numel(), keep_idx.numel()
@@ -449,7 +457,7 @@ def kv8_decode(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu
     [B+1] or None (one row per sequence).  Returns out [T,Hq,256]; rows behind cu_rows[B] (a
     padded batch) are left as they were in a given out."""
     sfx = _elem(q, "q")
-    d, N, Hkv, bs, pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
     if q.dim() != 3 or q.shape[2] != HEAD_DIM:
         raise ValueError(f"q must be [T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
     T, Hq, _ = shape = q.shape

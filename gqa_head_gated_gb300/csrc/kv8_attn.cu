@@ -39,8 +39,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <cstdio>
-
 #include "kv8_attn.cuh"
 
 namespace gqa {
@@ -569,9 +567,10 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
   e = launch_dependent(kv8_attn_kernel<MB, kF16>, dim3(unsigned(grid)), Cfg<MB, kF16>::kThreads, smem,
                        stream, 1, tmK, tmV, a);
   if (e == cudaSuccess) {
-    char name[64];
-    std::snprintf(name, sizeof(name), "kv8_attn_kernel<%d,%s>", MB, kF16 ? "fp16" : "bf16");
-    note_launch(name, grid, Cfg<MB, kF16>::kThreads, smem);
+    static const char* const kNames[2][2] = {
+        {"kv8_attn_kernel<16,bf16>", "kv8_attn_kernel<16,fp16>"},
+        {"kv8_attn_kernel<32,bf16>", "kv8_attn_kernel<32,fp16>"}};
+    note_launch(kNames[MB == 32][kF16], grid, Cfg<MB, kF16>::kThreads, smem);
   }
   return e;
 }
