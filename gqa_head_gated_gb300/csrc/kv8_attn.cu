@@ -577,18 +577,18 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
 
 }  // namespace
 
-// 16, 32 or (bf16) 128 packed rows share a tile.  Up to 32 rows the cache's bytes bound the
-// kernels and fewer columns cost less; past 32 a second row block would read the cache again,
-// which the wide kernel's 128 rows do not.
-int kv8_rows_per_block(long long packed_rows, bool f16) {
-  return packed_rows <= 16 ? 16 : packed_rows <= 32 || f16 ? 32 : 128;
+// 16, 32 or 128 packed rows share a tile.  Up to 32 rows the cache's bytes bound the kernels
+// and fewer columns cost less; past 32 a second row block would read the cache again, which
+// the wide kernel's 128 rows do not (its own comment has both sides measured).
+int kv8_rows_per_block(long long packed_rows) {
+  return packed_rows <= 16 ? 16 : packed_rows <= 32 ? 32 : 128;
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
                             bool* encode_failed) {
   CUtensorMap tmK, tmV;
-  const int mb = kv8_rows_per_block((long long)a.max_rows * a.gqa, f16);
-  if (mb == 128) return launch_kv8_wide(a, sms, stream, encode_failed);
+  const int mb = kv8_rows_per_block((long long)a.max_rows * a.gqa);
+  if (mb == 128) return launch_kv8_wide(a, f16, sms, stream, encode_failed);
   *encode_failed = !encode_pools(&tmK, &tmV, a);
   if (*encode_failed) return cudaSuccess;
   const long long tiles = (a.max_kv_len + kTile - 1) / kTile;

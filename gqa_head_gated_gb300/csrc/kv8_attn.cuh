@@ -22,9 +22,13 @@ constexpr int kHalfBytes = kTile * 128;          // 128 keys x 128 dims of K or 
 constexpr int kSlotBytes = 2 * kHalfBytes;
 constexpr int kScaleRing = 8;      // tiles whose scales are held: see the copies
 constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see the copies
-// What going on to another segment costs a CTA, in tiles, where it has kLongShare tiles or more
-// (with short shares it would only unsettle them: one tile each is best then).
-constexpr int kSwitch = 3;
+// What going on to another segment costs a CTA, in tiles (its end and start, and the first
+// tiles, whose references still move), where shares have kLongShare tiles or more (with short
+// ones it would only unsettle them: one tile each is best then).  Swept over 1, 3, 5, 7, 9 and
+// 12: 16 x 32768 decode 92.2, 89.4, 89.9, 90.7, 90.3, 90.3 us; chain verify (32 rows) 87.1,
+// 85.3, 82.6, 80.6, 80.1, 81.0; tree verify (128 rows) 182, 178, 174, 172, 173, 174.
+template <int MB>
+constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB == 32 ? 9 : 8; }
 constexpr uint32_t kLongShare = 8;
 constexpr int kMaxTileBlocks = kTile / 16;
 constexpr float kLSlack = 64.f;    // l's terms stay below 2^64
@@ -252,11 +256,11 @@ __device__ __forceinline__ Share cut_shares(RingSmem<KS, VS>& sm, const Kv8AttnA
     // (this warp's own writes) each sequence's leads go before its tiles
     __syncwarp();
     if (run >= kLongShare * gridDim.x)
-      for (int b = lane; b < p.B; b += 32) sm.base[b + 1] += kSwitch * sm.segs[b + 1];
+      for (int b = lane; b < p.B; b += 32) sm.base[b + 1] += switch_tiles<MB>() * sm.segs[b + 1];
   }
   __syncthreads();
   const uint32_t W = sm.base[p.B];
-  x.lead = W > 0 && W >= kLongShare * gridDim.x + kSwitch * sm.segs[p.B] ? kSwitch : 0;
+  x.lead = W > 0 && W >= kLongShare * gridDim.x + switch_tiles<MB>() * sm.segs[p.B] ? switch_tiles<MB>() : 0;
   x.n_cta = min(gridDim.x, W);
   // Shares so long that no segment needs more than `parts` parts.
   if (sm.most > p.parts)

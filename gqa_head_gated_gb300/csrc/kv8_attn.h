@@ -28,12 +28,13 @@ struct Kv8AttnArgs {
 };
 
 // Packed rows (query heads of a group x new rows) that a segment of the kernel takes.
-int kv8_rows_per_block(long long packed_rows, bool f16);
+int kv8_rows_per_block(long long packed_rows);
 
 // a.B <= kKv8Seqs, a.parts >= 3, B * Hkv * max_rb * (tiles of 128 keys in max_kv_len) < 2^31.
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
                             bool* encode_failed);
-// The kernel for 128 packed rows (bf16; launch_kv8_attn picks it).
-cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, int sms, cudaStream_t stream, bool* encode_failed);
+// The kernel for 128 packed rows (launch_kv8_attn picks it).
+cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
+                            bool* encode_failed);
 
 }  // namespace gqa

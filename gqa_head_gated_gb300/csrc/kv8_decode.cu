@@ -167,10 +167,10 @@ struct Plan {
 // Part slots per row: so many that the longest sequence alone can spread over every SM, or
 // (large batches, where no sequence need) four times the even share; never more than it
 // has tiles of 128 keys.  The shares are cut on the device so that no segment needs more.
-Plan plan_decode8(bool f16, int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
+Plan plan_decode8(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
   Plan q;
   const long long packed = (long long)max_rows * (Hq / Hkv), sms = device_sm_count();
-  q.rows_per_block = kv8_rows_per_block(packed, f16);
+  q.rows_per_block = kv8_rows_per_block(packed);
   q.max_rb = int((packed + q.rows_per_block - 1) / q.rows_per_block);
   const long long units = (long long)Hkv * q.max_rb, tiles = (max_kv_len + 127LL) / 128;
   long long parts = (sms + units - 1) / units + 2;
@@ -221,7 +221,7 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
                         (const void*)kv_lens, (const void*)cu_rows, (const void*)lse_out})
     if (!aligned_to(q, 4)) return GQA_ERR_INVALID_ARG;
   if (!aligned_to(tree_mask, 8)) return GQA_ERR_INVALID_ARG;
-  const Plan plan = plan_decode8(f16, B, T, Hq, Hkv, max_rows, max_kv_len);
+  const Plan plan = plan_decode8(B, T, Hq, Hkv, max_rows, max_kv_len);
   if (workspace == nullptr || workspace_bytes < plan.bytes) return GQA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return GQA_ERR_INVALID_ARG;
   Kv8AttnArgs a{};
@@ -248,7 +248,7 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
   if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // the kernel counts a launch's positions (a segment's tiles and a few more) in 31 bits
-  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128 + 8);
+  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128 + 16);
   if (per_seq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
   const long long fit = ((1LL << 31) - 1) / per_seq;
   const int step = fit < kKv8Seqs ? int(fit) : kKv8Seqs;
@@ -280,10 +280,7 @@ extern "C" {
 
 size_t gqa_kv8_workspace_size(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len) {
   if (check_sizes(B, T, Hq, Hkv, max_rows, max_kv_len) != GQA_OK) return 0;
-  // enough for either element type
-  const size_t a = plan_decode8(false, B, T, Hq, Hkv, max_rows, max_kv_len).bytes;
-  const size_t b = plan_decode8(true, B, T, Hq, Hkv, max_rows, max_kv_len).bytes;
-  return a > b ? a : b;
+  return plan_decode8(B, T, Hq, Hkv, max_rows, max_kv_len).bytes;
 }
 
 int gqa_kv8_decode(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,

@@ -1,30 +1,32 @@
-// The attention of many rows (wide draft trees, prompt chunks; bf16) over the paged 8-bit
-// cache: 128 packed rows (query heads of a KV group x new rows) share each tile.  The
-// mathematics, parts and schedule are kv8_attn.cu's; what differs is the side of the product
-// that the rows take, and the terms:
+// The attention of many rows (wide draft trees, prompt chunks) over the paged 8-bit cache: 128
+// packed rows (query heads of a KV group x new rows) share each tile.  The mathematics, parts
+// and schedule are kv8_attn.cu's; what differs is the side of the product that the rows take,
+// and the terms:
 //
 //   S [rows, 128 keys] = Q . K^T       A = Q's terms, B = the tile's K, as it lies
 //   O [rows, 256]     += P . V         A = P's terms (tensor memory), B = V, the same bytes
 //
-// Q is two e4m3 terms that add up in one accumulator (t0 + t1, no scale between them: what a
-// row's elements lose is below 2^-19 of its largest).  P is three e5m2 terms, again in one
-// accumulator: e5m2 has 3 bits a term but the range of fp16, so that p <= 2^15 splits into
-// t0 + t1 + t2 with a relative error of 2^-9 (a bf16 P has 2^-9) and an absolute one of 2^-17,
-// 2^-24 of the row's largest when its reference has just moved (to 2^7) and less after.
-// One accumulator for all terms is what leaves room for 128 rows: with e4m3 terms a column
-// or lane each, as the kernel for few rows has them, O alone would take three times 256
-// columns.
+// Q is e4m3 terms (two for a bf16's 8 bits, three for an fp16's 11) that add up in one
+// accumulator, with no scale between them: what a row's elements lose is below 2^-19 of its
+// largest.  P is e5m2 terms, again in one accumulator: e5m2 has 3 bits a term but the range of
+// fp16, so that p <= 2^15 splits into three (four) terms with a relative error of 2^-9 (2^-12),
+// a bf16 (fp16) P's own, and an absolute one of 2^-17: 2^-24 of the row's largest when its
+// reference has just moved (to 2^7) and less after.  One accumulator for all terms is what
+// leaves room for 128 rows: with e4m3 terms a column or lane each, as the kernel for few rows
+// has them, O alone would take three times 256 columns.
 //
-// What bounds it: the tensor pipe, 2 x 1024 x 64 / 128 clocks for S (two terms, K = 32 a step,
-// 64 clocks each) and three times 512 for P.V: 2,560 a tile of 128 keys, 1.33 us, against
-// 1.47 us that its 64 KB take from HBM.  The kernel for few rows reads the cache once for 32
-// rows, so from 33 on this one reads it less often.
+// What bounds it: the softmax's instructions.  The tensor pipe has 2 x 8 products of 64 clocks
+// for S and 3 x 4 of 128 for P.V, 2,560 a tile of 128 keys (1.33 us; HBM: 1.47), but a tile
+// takes about 4,200 cycles: each of 16 warps computes 32 x 32 probabilities and their terms,
+// about 12 instructions each, and the four warps of a scheduler share it (two warps of 64 keys
+// each took 4,900, with conversion instructions for the terms 5,300).
+// The kernel for few rows reads the cache once for 32 rows; 36 packed rows and more are faster
+// here (8 trees of 1 to 32 rows x 8 heads: 314 us there in row blocks of 32, 171 here).
 //
 // Roles (576 threads): warp 0 copies, warp 1 issues the products, warps 2..17 are the softmax
-// and epilogue: tensor-memory lane = row, four warps share a quadrant's rows, 32 keys each
-// (with two of 64 keys a tile took 5,300 cycles: the scores of one thread are one chain).
+// and epilogue: tensor-memory lane = row, four warps share a quadrant's rows, 32 keys each.
 // TMEM: O 256 columns, S 128 (one buffer: S of the next tile may start once every warp holds
-// its scores in registers), P 3 x 32.
+// its scores in registers), P 32 for each term.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -40,8 +42,13 @@ constexpr int kRuns = kMine / 16;      // runs of 16 keys, which have one scale 
 constexpr int kCols = 256 / kShare;    // columns of O of each
 constexpr int kWarpsS = 4 * kShare;    // softmax warps
 constexpr int kWideThreads = 64 + 32 * kWarpsS;
-constexpr int kQTerms = 2, kPTerms = 3;
-constexpr int kSlots = 2;              // K and V slots of a tile each
+template <bool kF16>
+struct WideCfg {
+  static constexpr int kQTerms = kF16 ? 3 : 2, kPTerms = kF16 ? 4 : 3;
+  // K and V slots.  One K slot is enough: S is done early in a tile's softmax, and the next K
+  // lands while that goes on; fp16's third Q term takes the other's place.
+  static constexpr int kKS = kF16 ? 1 : 2, kVS = 2;
+};
 constexpr uint32_t kTmWideO = 0, kTmWideS = 256, kTmWideP = 384;
 constexpr float kWideCap = 15.f;       // p <= 2^15
 constexpr float kWideTop = 7.f;        // a moved reference leaves the row's largest p at 2^7
@@ -49,8 +56,9 @@ constexpr uint32_t kIdescS = ptx::idesc_f32acc(128, 128, 0, 0, 0);
 // A e5m2 (format 1), B e4m3 (format 0), B MN-major
 constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, 256, 0, 1, 0) | (1u << 7);
 
-struct __align__(1024) WideSmem : RingSmem<kSlots, kSlots> {
-  alignas(1024) uint8_t q[kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
+template <bool kF16>
+struct __align__(1024) WideSmem : RingSmem<WideCfg<kF16>::kKS, WideCfg<kF16>::kVS> {
+  alignas(1024) uint8_t q[WideCfg<kF16>::kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
   float2 red[2][kShare][kRows];            // [tile parity][share][row]: maxima with vs, without
   float sum[kShare][kRows];                // [share][row]
   uint64_t s_full, s_free, p_full, pv_done, q_full, o_full, drain;
@@ -74,12 +82,13 @@ __device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
-// Four probabilities as three e5m2 terms each, a word of four bytes per term.  They go as
+// Four probabilities as e5m2 terms, a word of four bytes per term.  They go as
 // fp16 (a rounding of 2^-12), whose remainders are exact.  An e5m2 number is the upper byte of
 // the fp16 of the same value, so rounding to it (half away from zero; the sums stay below
 // 2^16) is an integer add and a mask, for two values at once: the conversion instructions
 // made the terms of a tile take 1,700 cycles.  (A NaN loses its bits here; the row's sum, in
 // fp32, keeps it.)
+template <int kPTerms>
 __device__ __forceinline__ void p_terms5(float2 lo, float2 hi, uint32_t (&w)[kPTerms]) {
   __half2 a = __floats2half2_rn(lo.x, lo.y), b = __floats2half2_rn(hi.x, hi.y);
 #pragma unroll
@@ -106,12 +115,15 @@ __device__ __noinline__ void rescale_o(uint32_t ta, float f) {
   }
 }
 
+template <bool kF16>
 __global__ void __launch_bounds__(kWideThreads, 1)
 kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const Kv8AttnArgs p) {
+  using C = WideCfg<kF16>;
+  constexpr int kPTerms = C::kPTerms, kQTerms = C::kQTerms;
   extern __shared__ uint8_t smem_raw[];
-  WideSmem& sm = *reinterpret_cast<WideSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~uintptr_t(1023));
+  WideSmem<kF16>& sm = *reinterpret_cast<WideSmem<kF16>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t tmo = p.ctl.timeout_ns;
   if (tid == 0) {
@@ -140,41 +152,39 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
-      const uint32_t qa = ptx::smem_addr(sm.q);
+      const uint64_t qd = ptx::sdesc_sw128(ptx::smem_addr(sm.q), 16, 1024);
       uint32_t J = 0, pc = 0;
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
-        const uint32_t ks = n % kSlots;
+        const uint32_t ks = n % C::kKS;
         if (n > 0 && !wait(&sm.s_free, (n - 1) & 1u, tmo, &sm.abort)) return false;
-        if (!wait(&sm.k_full[ks], (n / kSlots) & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.k_full[ks], (n / C::kKS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
-        const uint32_t ka = ptx::smem_addr(sm.k[ks]);
-#pragma unroll 1
+        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
+#pragma unroll
         for (int t = 0; t < kQTerms; ++t)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             ptx::mma_ss_f8(tmem + kTmWideS,
-                           ptx::sdesc_sw128(qa + t * (2 * kRows * 128) + (kk >> 2) * (kRows * 128) +
-                                                (kk & 3) * 32, 16, 1024),
-                           ptx::sdesc_sw128(ka + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
-                           kIdescS, t > 0 || kk > 0);
+                           ptx::sdesc_at(qd, t * (2 * kRows * 128) + (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
+                           ptx::sdesc_at(kd, (kk >> 2) * kHalfBytes + (kk & 3) * 32), kIdescS,
+                           t > 0 || kk > 0);
         ptx::tc_commit(&sm.s_full);
         ptx::tc_commit(&sm.k_empty[ks]);
         return true;
       };
       const auto issue_pv = [&](uint32_t n, bool first) -> bool {
-        const uint32_t vs = n % kSlots;
+        const uint32_t vs = n % C::kVS;
         if (!wait(&sm.p_full, n & 1u, tmo, &sm.abort)) return false;
-        if (!wait(&sm.v_full[vs], (n / kSlots) & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.v_full[vs], (n / C::kVS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
-        const uint32_t va = ptx::smem_addr(sm.v[vs]);
-#pragma unroll 1
+        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kHalfBytes, 1024);
+#pragma unroll
         for (int t = 0; t < kPTerms; ++t)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts_f8(tmem + kTmWideO, tmem + kTmWideP + t * 32 + kk * 8,
-                      ptx::sdesc_sw128(va + kk * 4096, kHalfBytes, 1024), kIdescO,
-                      !first || t > 0 || kk > 0);
+            mma_ts_f8(tmem + kTmWideO, tmem + kTmWideP + t * 32 + kk * 8, ptx::sdesc_at(vd, kk * 4096),
+                      kIdescO, !first || t > 0 || kk > 0);
         ptx::tc_commit(&sm.pv_done);
         ptx::tc_commit(&sm.v_empty[vs]);
         return true;
@@ -247,7 +257,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float2 a = unpack_elem2<false>(w[c]);
+            const float2 a = unpack_elem2<kF16>(w[c]);
             f[2 * c] = a.x;
             f[2 * c + 1] = a.y;
           }
@@ -415,10 +425,10 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         // ---- V rows that some row does not see
         if (tile_end > k_hi || tile_end > pr_lo) {
-          ok = ok && wait(&sm.v_full[J % kSlots], (J / kSlots) & 1u, tmo, &sm.abort);
+          ok = ok && wait(&sm.v_full[J % C::kVS], (J / C::kVS) & 1u, tmo, &sm.abort);
           const int key = k_lo + j * kTile + r;   // thread by key here, its share of the row
           if (ok && (key >= k_hi || key >= pr_lo) &&
-              clean_v_row(sm.v[J % kSlots], r, key >= k_hi, 16 / kShare * qt, 16 / kShare * (qt + 1)))
+              clean_v_row(sm.v[J % C::kVS], r, key >= k_hi, 16 / kShare * qt, 16 / kShare * (qt + 1)))
             atomicOr(&sm.hit[par][(key - pr_lo) >> 6], 1ull << ((key - pr_lo) & 63));
           ptx::fence_proxy_async_smem();
         }
@@ -466,7 +476,9 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
           if (ok) {
             const uint32_t tp = trow + kTmWideP + qt * (kMine / 4) + 4 * i;
-            ptx::tmem_st4x3_wait(tp, tp + 32, tp + 64, w[0], w[1], w[2]);
+#pragma unroll
+            for (int t = 0; t < kPTerms; ++t) ptx::tmem_st4(tp + 32 * t, w[t]);
+            ptx::tmem_wait_st();
           }
         }
         if (ok) {
@@ -488,23 +500,33 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
+template <bool kF16>
+cudaError_t launch_wide_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          long long grid, cudaStream_t stream) {
+  const size_t smem = sizeof(WideSmem<kF16>) + 1024;
+  static_assert(sizeof(WideSmem<kF16>) + 1024 <= 227 * 1024, "one CTA per SM");
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_wide_kernel<kF16>), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kv8_wide_kernel<kF16>, dim3(unsigned(grid)), kWideThreads, smem, stream, 1, tmK,
+                       tmV, a);
+  if (e == cudaSuccess)
+    note_launch(kF16 ? "kv8_wide_kernel<fp16>" : "kv8_wide_kernel<bf16>", grid, kWideThreads, smem);
+  return e;
+}
+
 }  // namespace
 
-cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, int sms, cudaStream_t stream, bool* encode_failed) {
+cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
+                            bool* encode_failed) {
   CUtensorMap tmK, tmV;
   *encode_failed = !encode_pools(&tmK, &tmV, a);
   if (*encode_failed) return cudaSuccess;
   const long long tiles = (a.max_kv_len + kTile - 1) / kTile;
   const long long most = (long long)a.B * a.Hkv * a.max_rb * tiles;
   const long long grid = most < sms ? most : sms;
-  const size_t smem = sizeof(WideSmem) + 1024;
-  static_assert(sizeof(WideSmem) + 1024 <= 227 * 1024, "one CTA per SM");
-  static std::atomic<unsigned long long> allowed{0};
-  cudaError_t e = allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_wide_kernel), smem);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(kv8_wide_kernel, dim3(unsigned(grid)), kWideThreads, smem, stream, 1, tmK, tmV, a);
-  if (e == cudaSuccess) note_launch("kv8_wide_kernel<bf16>", grid, kWideThreads, smem);
-  return e;
+  return f16 ? launch_wide_t<true>(a, tmK, tmV, grid, stream)
+             : launch_wide_t<false>(a, tmK, tmV, grid, stream);
 }
 
 }  // namespace gqa

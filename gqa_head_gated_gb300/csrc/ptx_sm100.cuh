@@ -293,17 +293,14 @@ __device__ __forceinline__ void tmem_st8x3_wait(uint32_t t0, uint32_t t1, uint32
       : "memory");
 }
 
-// 32 lanes x 4 columns at three addresses <- registers, waited once.
-__device__ __forceinline__ void tmem_st4x3_wait(uint32_t t0, uint32_t t1, uint32_t t2,
-                                                const uint32_t (&a)[4], const uint32_t (&b)[4],
-                                                const uint32_t (&c)[4]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%3,%4,%5,%6};\n"
-      "tcgen05.st.sync.aligned.32x32b.x4.b32 [%1], {%7,%8,%9,%10};\n"
-      "tcgen05.st.sync.aligned.32x32b.x4.b32 [%2], {%11,%12,%13,%14};\n"
-      "tcgen05.wait::st.sync.aligned;\n" ::"r"(t0),
-      "r"(t1), "r"(t2), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3])
-      : "memory");
+// 32 lanes x 4 columns <- 4 registers per thread; tmem_wait_st waits for all of them.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // 32 lanes x 32 consecutive 32-bit columns -> 32 registers per thread, waited.
