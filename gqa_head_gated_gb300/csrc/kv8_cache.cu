@@ -66,9 +66,8 @@ struct AppendParams {
   LaunchCtl ctl;
 };
 
-// Rounds a block's first n rows again, from scale `s_old` to 2^e (one warp a row).
-__device__ __forceinline__ void rescale_rows(uint2* block, int n, float s_old, int e) {
-  const float inv = pow2f(-e);
+// Rounds a block's first n rows again, from scale `s_old` to 1 / inv (one warp a row).
+__device__ __forceinline__ void rescale_rows(uint2* block, int n, float s_old, float inv) {
   for (int r = threadIdx.x >> 5; r < n; r += kWarps) {
     uint2* const a = block + r * 32 + (threadIdx.x & 31);
     float f[8];
@@ -88,8 +87,10 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
   __shared__ int s_slot[kSpan + 1];          // slot of token w0 - 1 + i
   __shared__ uint32_t s_start[kSpan / 32];   // bit i: token w0 + i starts a run
   __shared__ uint32_t s_break[kSpan / 32];   // bit i: token w0 + i starts a run or is in none
+  __shared__ int s_run[kSpan];               // first token of token w0 + i's run, -1: none here
+  __shared__ int s_row[kSpan];               // its pool row ((block * Hkv + g) * bs + row)
   __shared__ uint32_t s_max[kWindow];        // by run (its first token): largest |x|, then
-  __shared__ int s_exp[kWindow];             // the exponent of its scale
+  __shared__ float s_inv[kWindow];           // one over its scale
   __shared__ float s_old[kWindow];           // the scale that the rows before it have
   __shared__ int s_grown[kWindow];
   __shared__ int s_n_grown;
@@ -138,16 +139,21 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
     const int i = i0 + warp + k * kWarps;
     if (i < n_span) u[k] = __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane);
   }
-  // First token of token w0 + i's run, -1 when it is in no run that starts in the window.
-  const auto run_of = [&](int i) -> int {
-    if (i >= n_span) return -1;
-    int w = i >> 5;
-    uint32_t m = s_break[w] & (0xffffffffu >> (31 - (i & 31)));
-    while (m == 0u && w > 0) m = s_break[--w];
-    if (m == 0u) return -1;
-    const int f = w * 32 + 31 - __clz(m);
-    return f < kWindow && ((s_start[f >> 5] >> (f & 31)) & 1u) ? f : -1;
-  };
+  if (tid < kSpan) {
+    int f = -1;
+    if (tid < n_span) {
+      int w = tid >> 5;
+      uint32_t m = s_break[w] & (0xffffffffu >> (31 - (tid & 31)));
+      while (m == 0u && w > 0) m = s_break[--w];
+      if (m != 0u) f = w * 32 + 31 - __clz(m);
+      if (f >= kWindow || (f >= 0 && !((s_start[f >> 5] >> (f & 31)) & 1u))) f = -1;
+    }
+    const int s = s_slot[tid + 1];
+    s_run[tid] = f;
+    s_row[tid] = f < 0 ? 0 : (((s >> p.bs_log2) * p.Hkv + g) << p.bs_log2) + (s & (bs - 1));
+  }
+  __syncthreads();
+  const auto run_of = [&](int i) -> int { return i < n_span ? s_run[i] : -1; };
   int run[kRowsPerWarp];
   uint32_t finite = 0u;    // bit k: row k of this warp holds no NaN or infinity
 #pragma unroll
@@ -179,18 +185,17 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
         s_grown[atomicAdd(&s_n_grown, 1)] = tid;
       }
     }
-    s_exp[tid] = e;
+    s_inv[tid] = inv_pow2f(e);
     *sp = pow2f(e);
   }
   __syncthreads();
   const auto put = [&](int i, int r, uint4 v, bool all) {
     float f[8];
     unpack8<kF16>(v, f);
-    const float inv = pow2f(-s_exp[r]);
+    const float inv = s_inv[r];
 #pragma unroll
     for (int c = 0; c < 8; ++c) f[c] *= inv;
-    const int s = s_slot[i + 1];
-    pool[((size_t(s >> p.bs_log2) * p.Hkv + g) * bs + (s & (bs - 1))) * 32 + lane] = all ? finite_to_e4m3x8(f) : to_e4m3x8(f);
+    pool[size_t(s_row[i]) * 32 + lane] = all ? finite_to_e4m3x8(f) : to_e4m3x8(f);
   };
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k)
@@ -201,9 +206,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
     put(i, r, __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), false);
   }
   for (int j = 0; j < s_n_grown; ++j) {
-    const int r = s_grown[j], s = s_slot[r + 1];
-    rescale_rows(pool + (size_t(s >> p.bs_log2) * p.Hkv + g) * bs * 32, s & (bs - 1), s_old[r],
-                 s_exp[r]);
+    const int r = s_grown[j], n = s_row[r] & (bs - 1);
+    rescale_rows(pool + size_t(s_row[r] - n) * 32, n, s_old[r], s_inv[r]);
   }
 }
 
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv8_keep_kernel(const KeepParams 
   __shared__ int s_src[kMaxKeep];          // pool row (block * bs + row) of kept row k, and
   __shared__ int s_dst[kMaxKeep];          // its place
   __shared__ uint32_t s_max[kMaxRuns];
-  __shared__ int s_exp[kMaxRuns];
+  __shared__ float s_inv[kMaxRuns];
   __shared__ float s_old;                  // scale of the rows that stay before the first run
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x, g = blockIdx.y, kv = blockIdx.z;
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv8_keep_kernel(const KeepParams 
   if (tid < n_runs) {
     int e = scale_exp(s_max[tid]);
     if (tid == 0 && off0 != 0) e = max(e, stored_exp(s_old));
-    s_exp[tid] = e;
+    s_inv[tid] = inv_pow2f(e);
     // the run's first row: kept row 0, or the first one of its block
     *scale_of(s_dst[tid == 0 ? 0 : ((run0 + tid) << p.bs_log2) - base]) = pow2f(e);
   }
@@ -308,15 +312,15 @@ __global__ void __launch_bounds__(kThreads, 6) kv8_keep_kernel(const KeepParams 
   for (int k = 0; k < kKeepPerWarp; ++k) {
     const int i = warp + k * kWarps;
     if (i >= nk) continue;
-    const float inv = pow2f(-s_exp[((base + i) >> p.bs_log2) - run0]);
+    const float inv = s_inv[((base + i) >> p.bs_log2) - run0];
     float f[8];
     from_e4m3x8(q[k], f);
 #pragma unroll
     for (int c = 0; c < 8; ++c) f[c] = f[c] * sc[k] * inv;
     pool[row_of(s_dst[i]) + lane] = to_e4m3x8(f);
   }
-  if (off0 != 0 && pow2f(s_exp[0]) != s_old)
-    rescale_rows(pool + row_of(s_dst[0] - off0), off0, s_old, s_exp[0]);
+  if (off0 != 0 && s_old * s_inv[0] != 1.f)
+    rescale_rows(pool + row_of(s_dst[0] - off0), off0, s_old, s_inv[0]);
 }
 
 int log2_of(int block_size) {

@@ -30,6 +30,11 @@ constexpr int kMinScaleExp = -126;   // an all-zero run's scale: the smallest no
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
+// 2^-e for the same range; 2^-127 is a subnormal.
+__device__ __forceinline__ float inv_pow2f(int e) {
+  return e == 127 ? __uint_as_float(0x400000u) : pow2f(-e);
+}
+
 // Least e >= -126 with a <= 448 * 2^e, from the bits of a finite a >= 0.  448 is
 // 1.75 * 2^8, so with a = m * 2^x (1 <= m < 2) e is x - 8 for m <= 1.75, else x - 7.
 __device__ __forceinline__ int scale_exp(uint32_t a_bits) {
