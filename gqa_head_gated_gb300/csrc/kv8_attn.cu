@@ -79,12 +79,12 @@ struct __align__(1024) AttnSmem : RingSmem<Cfg<MB, kF16>::kKS, Cfg<MB, kF16>::kV
   alignas(16) float red[C::kGroups][2 * kGroupRows][4];   // [group][value][warp], read as float4
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_full, drain;
-  // by piece, two in turn
-  unsigned long long hit[2];               // NaN V rows taken out: bit of key pr_lo + i
-  unsigned long long mask[2][MB];          // tree mask of each row
-  int lim[2][MB];                          // keys before this one are seen
-  int row[2][MB];                          // output row (token * Hq + head)
-  float fac[2][MB];                        // scale of the row's Q terms, with log2(e) / 16
+  // by piece, kRowSets in turn
+  unsigned long long hit[kRowSets];        // NaN V rows taken out: bit of key pr_lo + i
+  unsigned long long mask[kRowSets][MB];   // tree mask of each row
+  int lim[kRowSets][MB];                   // keys before this one are seen
+  int row[kRowSets][MB];                   // output row (token * Hq + head)
+  float fac[kRowSets][MB];                     // scale of the row's Q terms, with log2(e) / 16
   int failed[C::kGroups];
 };
 
@@ -260,7 +260,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ++n_fetched;
       return ok && x.n_tiles > 0;
     };
-    // Q's terms, the rows' limits and places of piece x, into half `par` of the piece arrays;
+    // Q's terms, the rows' limits and places of piece x, into set `par` of the piece arrays;
     // then the products of the piece may start.  The last piece's S products are done.
     const auto prepare = [&](uint32_t par) {
       constexpr int kWarpsQ = C::kSoftmax / 32, kPer = MB / kWarpsQ;   // rows of each warp
@@ -324,11 +324,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     for (bool first = true;; first = false) {
       // ---- the next piece may start while the last one ends (its S products are done)
       const bool more = fetch();
-      if (more) prepare(pc & 1u);
-      const uint32_t last_par = (pc - 1u) & 1u;
+      if (more) prepare(pc % kRowSets);
       if (!first) {
         // ---- the last piece's sums
-        ok = warp_all(ok && wait(&sm.o_full, last_par, tmo, &sm.abort));
+        ok = warp_all(ok && wait(&sm.o_full, (pc - 1u) & 1u, tmo, &sm.abort));
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
 #pragma unroll
@@ -340,7 +339,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (stop) break;
       if (!first) {
         // ---- and parts
-        const uint32_t par = last_par;
+        const uint32_t par = (pc - 1u) % kRowSets;
         ptx::tc_fence_after();
         const size_t part0 = size_t(s_idx) * size_t(p.T) * p.Hq;
         const unsigned long long hits = sm.hit[par];
@@ -380,8 +379,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ptx::tc_fence_before();
       }
       if (!more) break;
-      const uint32_t par = pc & 1u;
-      ok = ok && wait(&sm.q_full, par, tmo, &sm.abort);   // rows, limits, factors are written
+      const uint32_t par = pc % kRowSets;
+      ok = ok && wait(&sm.q_full, pc & 1u, tmo, &sm.abort);   // rows, limits, factors are written
       const int n_tiles = x.n_tiles, k_lo = x.k_lo, k_hi = x.k_hi;
       seq = x.b;
       head = x.g;

@@ -31,6 +31,10 @@ template <int MB>
 constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB == 32 ? 9 : 8; }
 constexpr uint32_t kLongShare = 8;
 constexpr int kMaxTileBlocks = kTile / 16;
+// Pieces whose rows, limits and masks are held.  prepare() of piece n may run while another
+// group still writes the parts of n - 2 (when n - 1 has one tile, nothing in between waits for
+// all groups), but not n - 3: the parts of n - 2 are written once all have passed its tiles.
+constexpr uint32_t kRowSets = 4;
 constexpr float kLSlack = 64.f;    // l's terms stay below 2^64
 constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
 

@@ -222,6 +222,9 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
     if (!aligned_to(q, 4)) return GQA_ERR_INVALID_ARG;
   if (!aligned_to(tree_mask, 8)) return GQA_ERR_INVALID_ARG;
   const Plan plan = plan_decode8(B, T, Hq, Hkv, max_rows, max_kv_len);
+  // the kernel counts a launch's positions (a segment's tiles and a few more) in 31 bits
+  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128 + 16);
+  if (per_seq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < plan.bytes) return GQA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 16)) return GQA_ERR_INVALID_ARG;
   Kv8AttnArgs a{};
@@ -247,9 +250,6 @@ int decode_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool,
   a.parts = plan.parts;
   if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the kernel counts a launch's positions (a segment's tiles and a few more) in 31 bits
-  const long long per_seq = (long long)Hkv * plan.max_rb * ((max_kv_len + 127LL) / 128 + 16);
-  if (per_seq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
   const long long fit = ((1LL << 31) - 1) / per_seq;
   const int step = fit < kKv8Seqs ? int(fit) : kKv8Seqs;
   for (int b0 = 0; b0 < B; b0 += step) {

@@ -244,7 +244,8 @@ extern "C" int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block
                         (const void*)n_blocks, (const void*)free_list, (const void*)free_count,
                         (const void*)slots, (const void*)kv_lens_out})
     if (!aligned_to(q, 4)) return GQA_ERR_INVALID_ARG;
-  if (B > kMaxSeqs || (long long)B * max_blocks >= (1LL << 31) ||
+  // (T and the entries stay far enough below 2^31 for sums with strides and the pool's blocks)
+  if (B > kMaxSeqs || T >= (1 << 30) || (long long)B * max_blocks >= (1LL << 30) ||
       (long long)max_blocks * block_size >= (1LL << 31))
     return GQA_ERR_UNSUPPORTED;
   PlanParams p{kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, slots, kv_lens_out,

@@ -62,11 +62,11 @@ struct __align__(1024) WideSmem : RingSmem<WideCfg<kF16>::kKS, WideCfg<kF16>::kV
   float2 red[2][kShare][kRows];            // [tile parity][share][row]: maxima with vs, without
   float sum[kShare][kRows];                // [share][row]
   uint64_t s_full, s_free, p_full, pv_done, q_full, o_full, drain;
-  // by piece, two in turn
-  unsigned long long hit[2][2];            // NaN V rows taken out: bits of keys pr_lo + 64 w + i
-  unsigned long long mask[2][kRows];
-  int lim[2][kRows], row[2][kRows];
-  float fac[2][kRows];
+  // by piece, kRowSets in turn
+  unsigned long long hit[kRowSets][2];     // NaN V rows taken out: bits of keys pr_lo + 64 w + i
+  unsigned long long mask[kRowSets][kRows];
+  int lim[kRowSets][kRows], row[kRowSets][kRows];
+  float fac[kRowSets][kRows];
 };
 
 // D[tmem] (+)= A[tmem] * B[smem desc], 8-bit inputs.
@@ -233,7 +233,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     // Q's terms, the rows' limits and places of piece n; then its products may start.  The
     // last piece's S products are done.
     const auto prepare = [&](uint32_t n) {
-      const uint32_t par = n & 1u;
+      const uint32_t par = n % kRowSets;
       const Piece x = piece(n);
       const int p0 = x.rb * kRows, n_rows = min(kRows, x.rows * p.gqa - p0);
 #pragma unroll 1
@@ -307,7 +307,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // ---- the last piece's parts: this thread's row, kCols of its columns
         ptx::tc_fence_after();
         const Piece& x = piece(pc - 1u);
-        const uint32_t par = (pc - 1u) & 1u;
+        const uint32_t par = (pc - 1u) % kRowSets;
         float L = 0.f;
 #pragma unroll
         for (int i = 0; i < kShare; ++i) L += sm.sum[i][r];
@@ -344,8 +344,8 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ptx::tc_fence_before();
       }
       if (!more) break;
-      const uint32_t par = pc & 1u;
-      ok = ok && wait(&sm.q_full, par, tmo, &sm.abort);   // rows, limits, factors are written
+      const uint32_t par = pc % kRowSets;
+      ok = ok && wait(&sm.q_full, pc & 1u, tmo, &sm.abort);   // rows, limits, factors are written
       const int n_tiles = piece(pc).n_tiles, k_lo = piece(pc).k_lo, k_hi = piece(pc).k_hi;
       const int pr_lo = part_seen_from(piece(pc));
       const float fac = sm.fac[par][r];

@@ -66,7 +66,7 @@ def _plan(lib, **kw):
     (dict(tab=None), 1), (dict(nb=None), 1), (dict(fl=None), 1), (dict(fc=None), 1),
     (dict(slots=None), 1), (dict(out=None), 1), (dict(tab=50), 1), (dict(out=130), 1),
     (dict(B=8193), 2), (dict(N=1 << 30, bs=128), 2), (dict(B=4096, mb=1 << 20), 2),
-    (dict(mb=1 << 28), 2),
+    (dict(mb=1 << 28), 2), (dict(T=1 << 30), 2), (dict(B=2048, mb=1 << 19), 2),
 ])
 def test_plan_rejects_before_launch(lib, kw, code):
     assert _plan(lib, **kw) == code
@@ -127,6 +127,7 @@ def _decode(lib, **kw):
     (dict(out=None), 1), (dict(out=168), 1), (dict(lse=2), 1), (dict(ws=None), 5),
     (dict(wsb=64), 5), (dict(ws=184), 1), (dict(N=1 << 27), 2), (dict(T=1 << 28, Hq=8), 2),
     (dict(tm=192, mr=65, mk=128, mb=8), 2), (dict(T=0, q=None), 0),
+    (dict(mk=1 << 30, mb=1 << 27), 2), (dict(Hkv=1 << 16, Hq=1 << 16, N=1, mk=1 << 23, mb=1 << 20), 2),
 ])
 def test_decode_rejects_before_launch(lib, kw, code):
     assert _decode(lib, **kw) == [code, code]
