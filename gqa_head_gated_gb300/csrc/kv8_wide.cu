@@ -93,8 +93,9 @@ __device__ __forceinline__ void p_terms5(float2 lo, float2 hi, uint32_t (&w)[kPT
   __half2 a = __floats2half2_rn(lo.x, lo.y), b = __floats2half2_rn(hi.x, hi.y);
 #pragma unroll
   for (int i = 0; i < kPTerms; ++i) {
-    const uint32_t ta = (*reinterpret_cast<const uint32_t*>(&a) + 0x00800080u) & 0xFF00FF00u;
-    const uint32_t tb = (*reinterpret_cast<const uint32_t*>(&b) + 0x00800080u) & 0xFF00FF00u;
+    const uint32_t up = i + 1 < kPTerms ? 0u : 0x00800080u;
+    const uint32_t ta = (*reinterpret_cast<const uint32_t*>(&a) + up) & 0xFF00FF00u;
+    const uint32_t tb = (*reinterpret_cast<const uint32_t*>(&b) + up) & 0xFF00FF00u;
     w[i] = __byte_perm(ta, tb, 0x7531);
     if (i + 1 < kPTerms) {
       a = __hsub2(a, *reinterpret_cast<const __half2*>(&ta));
@@ -354,18 +355,10 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       for (int j = 0; j < n_tiles; ++j, ++J) {
         const int key0 = k_lo + j * kTile + qt * kMine;
         const int tile_end = k_lo + (j + 1) * kTile;
-        ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
         uint32_t s[kMine];
         float f[kRuns], lv[kRuns];        // by run of 16 keys: score factor, log2 of the V scale
-#pragma unroll
-        for (int i = 0; i < kRuns; ++i) {
-          const int blk = (qt * kMine + i * 16) >> p.bs_log2;
-          const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
-          // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
-          f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
-          lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
-        }
-        ok = ok && wait(&sm.s_full, J & 1u, tmo, &sm.abort);
+        ok = ok && wait(&sm.s_full, J & 1u, tmo, &sm.abort) &&
+             wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         __syncwarp();
         float mp = -INFINITY, ms = -INFINITY;
@@ -375,6 +368,14 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sm.s_free);
+#pragma unroll
+          for (int i = 0; i < kRuns; ++i) {
+            const int blk = (qt * kMine + i * 16) >> p.bs_log2;
+            const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
+            // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
+            f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
+            lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
+          }
           if (tile_end > k_hi || tile_end > pr_lo) {
             const int lim = sm.lim[par][r], base = piece(pc).kv_len - piece(pc).rows;
             const unsigned long long mask = sm.mask[par][r];
@@ -437,6 +438,16 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int i = 0; i < kRuns; ++i) {
           const float a = lv[i] - ref;
           const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
+          // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
+          // block of tiny values that p hardly sees)
+          const float d = -a - ml;
+          const bool far = __any_sync(0xffffffffu, d > 60.f);
+          if (far) {
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
+            l += sum;
+          }
           float2 sum2 = make_float2(0.f, 0.f);
           uint32_t w[kPTerms][4];
 #pragma unroll
@@ -451,18 +462,8 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
             for (int t = 0; t < kPTerms; ++t) w[t][c] = t4[t];
           }
-          float sum = sum2.x + sum2.y;
-          // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
-          // block of tiny values that p hardly sees)
-          const float d = -a - ml;
-          if (__any_sync(0xffffffffu, d > 60.f)) {
-            sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
-            l += sum;
-          } else {
-            l += sum * ex2(d);
-          }
+          const float sum = sum2.x + sum2.y;
+          if (!far) l += sum * ex2(d);
           if (i == 0) {
             // PV of tile J - 1 has read P, and is in O, which moves to the new references only
             // now: the terms were computed while that product ran
