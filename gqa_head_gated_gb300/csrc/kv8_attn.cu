@@ -166,7 +166,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const Share share = cut_shares<MB>(sm, p);
 
   if (warp == 0) {
-    copy_role<MB>(sm, p, tmK, tmV, share);
+    copy_role<MB, false>(sm, p, tmK, tmV, share);
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {

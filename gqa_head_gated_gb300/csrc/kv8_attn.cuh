@@ -286,7 +286,10 @@ __device__ __forceinline__ Share cut_shares(RingSmem<KS, VS>& sm, const Kv8AttnA
 // J + 3, so tile J's scales have been read.  So with the pieces' descriptions: a piece has a
 // tile at least, so that when piece n + 8 is published the softmax has passed tiles of piece
 // n + 8 - KS - 3 and with it piece n.
-template <int MB, int KS, int VS>
+//
+// kLead: V of a tile is copied behind K of the next one, for a kernel whose products of scores
+// run further ahead than its V slots do.
+template <int MB, bool kLead, int KS, int VS>
 __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArgs& p,
                                           const CUtensorMap& tmK, const CUtensorMap& tmV,
                                           const Share& share) {
@@ -301,6 +304,27 @@ __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArg
     ptx::prefetch_tmap(&tmV);
   }
   uint32_t n_pieces = 0;
+  // V of tile n, a block of this lane's from map row `row`, `bytes` in all
+  uint32_t n_v = 0;      // tiles whose V copies are issued
+  int v_row = 0;
+  uint32_t v_bytes = 0;
+  bool v_mine = false;
+  const auto copy_v = [&]() -> bool {
+    const uint32_t vs = n_v % VS;
+    int go = 1;
+    if (lane == 0) {
+      if (n_v >= VS) go = wait(&sm.v_empty[vs], (n_v / VS - 1) & 1u, tmo, &sm.abort);
+      if (go) ptx::mbar_arrive_expect_tx(&sm.v_full[vs], v_bytes);
+    }
+    if (__shfl_sync(0xffffffffu, go, 0) == 0) return false;
+    if (v_mine) {
+      uint8_t* const d = sm.v[vs] + lane * bs * 128;
+      ptx::tma_load_2d(d, &tmV, &sm.v_full[vs], 0, v_row);
+      ptx::tma_load_2d(d + kHalfBytes, &tmV, &sm.v_full[vs], 128, v_row);
+    }
+    ++n_v;
+    return true;
+  };
   const auto publish = [&](const Piece& x) {
     if (lane == 0) {
       sm.piece[n_pieces % kPieceRing] = x;
@@ -332,7 +356,7 @@ __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArg
     const int* const table = p.tables + (long long)x.b * p.max_blocks;
     int at = x.k_lo + lane * bs;   // first key of this lane's block
     int blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
-    for (int j = 0; ok && j < x.n_tiles; ++j, ++J) {
+    for (int j = 0; ok && j < x.n_tiles; ++j) {
       const bool mine = lane < per_tile && at < x.k_hi;
       const bool in = blk >= 0 && blk < p.num_blocks;
       if (mine && !in) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
@@ -342,7 +366,7 @@ __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArg
       const int cur = blk;
       at += kTile;
       blk = lane < per_tile && at < x.k_hi ? __ldg(table + (at >> p.bs_log2)) : 0;
-      const uint32_t ks = J % KS, vs = J % VS;
+      const uint32_t ks = J % KS;
       int go = 1;
       if (lane == 0) {
         if (J >= KS)
@@ -360,24 +384,15 @@ __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArg
         ptx::cp_async4(ptx::smem_addr(&sm.scale[J % kScaleRing][1][lane]), p.v_scale + sc, in ? 4u : 0u);
       }
       ptx::cp_async_mbar_arrive(&sm.sc_full[J % kScaleRing]);
-      if (lane == 0) {
-        if (J >= VS)
-          go = wait(&sm.v_empty[vs], (J / VS - 1) & 1u, tmo, &sm.abort);
-        if (go) ptx::mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
-      }
-      ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-      if (!ok) {
-        // K of this tile is on its way: it must land before the CTA ends
-        if (lane == 0) wait(&sm.k_full[ks], (J / KS) & 1u, tmo, &sm.zero);
-        break;
-      }
-      if (mine) {
-        uint8_t* const d = sm.v[vs] + lane * bs * 128;
-        ptx::tma_load_2d(d, &tmV, &sm.v_full[vs], 0, row);
-        ptx::tma_load_2d(d + kHalfBytes, &tmV, &sm.v_full[vs], 128, row);
-      }
+      ++J;   // (K of this tile is on its way)
+      if (kLead && J > 1) ok = copy_v();
+      v_row = row;
+      v_bytes = bytes;
+      v_mine = mine;
+      if (!kLead) ok = copy_v();
     }
   }
+  if (kLead && ok && J > 0) ok = copy_v();
   if (ok) {
     Piece none{};
     publish(none);   // (the share's end: no tiles)
@@ -390,7 +405,7 @@ __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArg
   if (lane == 0) {   // every copy has landed before the CTA ends
     for (uint32_t c = J - min(J, uint32_t(KS)); c < J; ++c)
       wait(&sm.k_full[c % KS], (c / KS) & 1u, tmo, &sm.zero);
-    for (uint32_t c = J - min(J, uint32_t(VS)); c < J; ++c)
+    for (uint32_t c = n_v - min(n_v, uint32_t(VS)); c < n_v; ++c)
       wait(&sm.v_full[c % VS], (c / VS) & 1u, tmo, &sm.zero);
   }
   __syncwarp();

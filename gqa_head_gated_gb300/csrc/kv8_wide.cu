@@ -36,11 +36,13 @@ namespace gqa {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kShare = 4;              // softmax threads of a row
-constexpr int kMine = kTile / kShare;  // keys of each
-constexpr int kRuns = kMine / 16;      // runs of 16 keys, which have one scale each
-constexpr int kCols = 256 / kShare;    // columns of O of each
-constexpr int kWarpsS = 4 * kShare;    // softmax warps
+constexpr int kTeams = 2;              // a team of 8 warps takes every other tile
+constexpr int kHalves = 2;             // softmax threads of a row in a team
+constexpr int kMine = kTile / kHalves; // keys of each
+constexpr int kWarpsS = 4 * kTeams * kHalves;   // softmax warps
+constexpr int kWarpsTeam = kWarpsS / kTeams;
+constexpr int kShare = kTeams * kHalves;        // warps of a quadrant, which share the epilogue
+constexpr int kCols = 256 / kShare;    // columns of O of each there
 constexpr int kWideThreads = 64 + 32 * kWarpsS;
 template <bool kF16>
 struct WideCfg {
@@ -49,7 +51,7 @@ struct WideCfg {
   // lands while that goes on; fp16's third Q term takes the other's place.
   static constexpr int kKS = kF16 ? 1 : 2, kVS = 2;
 };
-constexpr uint32_t kTmWideO = 0, kTmWideS = 256, kTmWideP = 384;
+constexpr uint32_t kTmWideO = 0, kTmWideS = 256;   // two buffers of 128 columns for S and P
 constexpr float kWideCap = 15.f;       // p <= 2^15
 constexpr float kWideTop = 7.f;        // a moved reference leaves the row's largest p at 2^7
 constexpr uint32_t kIdescS = ptx::idesc_f32acc(128, 128, 0, 0, 0);
@@ -59,9 +61,10 @@ constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, 256, 0, 1, 0) | (1u << 7);
 template <bool kF16>
 struct __align__(1024) WideSmem : RingSmem<WideCfg<kF16>::kKS, WideCfg<kF16>::kVS> {
   alignas(1024) uint8_t q[WideCfg<kF16>::kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
-  float2 red[2][kShare][kRows];            // [tile parity][share][row]: maxima with vs, without
+  float2 red[kTeams][kHalves][kRows];      // by row: maxima with vs, without
+  float2 refs[2][kRows];                   // [tile parity][row]: the references after the tile
   float sum[kShare][kRows];                // [share][row]
-  uint64_t s_full, s_free, p_full, pv_done, q_full, o_full, drain;
+  uint64_t s_full[2], p_full[2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
   // by piece, kRowSets in turn
   unsigned long long hit[kRowSets][2];     // NaN V rows taken out: bits of keys pr_lo + 64 w + i
   unsigned long long mask[kRowSets][kRows];
@@ -104,10 +107,10 @@ __device__ __forceinline__ void p_terms5(float2 lo, float2 hi, uint32_t (&w)[kPT
   }
 }
 
-// kCols columns of a row of O times f, in tensor memory (whole warp).
-__device__ __noinline__ void rescale_o(uint32_t ta, float f) {
+// Half of a row of O times f, in tensor memory (whole warp).
+__device__ __forceinline__ void rescale_o(uint32_t ta, float f) {
 #pragma unroll 1
-  for (int c = 0; c < kCols / 32; ++c) {
+  for (int c = 0; c < 256 / kHalves / 32; ++c) {
     uint32_t o[32];
     ptx::tmem_ld32_wait(ta + 32 * c, o);
 #pragma unroll
@@ -129,10 +132,13 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const uint64_t tmo = p.ctl.timeout_ns;
   if (tid == 0) {
     init_ring(sm);
-    ptx::mbar_init(&sm.s_full, 1);
-    ptx::mbar_init(&sm.s_free, kWarpsS);
-    ptx::mbar_init(&sm.p_full, kWarpsS);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.s_full[i], 1);
+      ptx::mbar_init(&sm.p_full[i], kWarpsTeam);
+      for (int k = 0; k < 4; ++k) ptx::mbar_init(&sm.ref_full[i][k], kHalves);
+    }
     ptx::mbar_init(&sm.pv_done, 1);
+    ptx::mbar_init(&sm.o_free, kWarpsS);
     ptx::mbar_init(&sm.q_full, kWarpsS);
     ptx::mbar_init(&sm.o_full, 1);
     ptx::mbar_init(&sm.drain, 1);
@@ -149,7 +155,7 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const Share share = cut_shares<kRows>(sm, p);
 
   if (warp == 0) {
-    copy_role<kRows>(sm, p, tmK, tmV, share);
+    copy_role<kRows, true>(sm, p, tmK, tmV, share);
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
@@ -158,7 +164,6 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
         const uint32_t ks = n % C::kKS;
-        if (n > 0 && !wait(&sm.s_free, (n - 1) & 1u, tmo, &sm.abort)) return false;
         if (!wait(&sm.k_full[ks], (n / C::kKS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
@@ -166,17 +171,17 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int t = 0; t < kQTerms; ++t)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            ptx::mma_ss_f8(tmem + kTmWideS,
+            ptx::mma_ss_f8(tmem + kTmWideS + (n & 1u) * 128,
                            ptx::sdesc_at(qd, t * (2 * kRows * 128) + (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
                            ptx::sdesc_at(kd, (kk >> 2) * kHalfBytes + (kk & 3) * 32), kIdescS,
                            t > 0 || kk > 0);
-        ptx::tc_commit(&sm.s_full);
+        ptx::tc_commit(&sm.s_full[n & 1u]);
         ptx::tc_commit(&sm.k_empty[ks]);
         return true;
       };
       const auto issue_pv = [&](uint32_t n, bool first) -> bool {
         const uint32_t vs = n % C::kVS;
-        if (!wait(&sm.p_full, n & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.p_full[n & 1u], (n >> 1) & 1u, tmo, &sm.abort)) return false;
         if (!wait(&sm.v_full[vs], (n / C::kVS) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kHalfBytes, 1024);
@@ -184,8 +189,8 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int t = 0; t < kPTerms; ++t)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts_f8(tmem + kTmWideO, tmem + kTmWideP + t * 32 + kk * 8, ptx::sdesc_at(vd, kk * 4096),
-                      kIdescO, !first || t > 0 || kk > 0);
+            mma_ts_f8(tmem + kTmWideO, tmem + kTmWideS + (n & 1u) * 128 + kk * 32 + t * 8,
+                      ptx::sdesc_at(vd, kk * 4096), kIdescO, !first || t > 0 || kk > 0);
         ptx::tc_commit(&sm.pv_done);
         ptx::tc_commit(&sm.v_empty[vs]);
         return true;
@@ -199,9 +204,13 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok) break;
         ptx::tc_fence_after();
         ok = issue_s(J);
+        if (ok && n_tiles > 1) ok = issue_s(J + 1);
+        // O of the last piece has been read by every warp
+        if (ok && pc > 0) ok = wait(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
         for (int j = 0; ok && j < n_tiles; ++j) {
-          if (j + 1 < n_tiles) ok = issue_s(J + j + 1);
-          if (ok) ok = issue_pv(J + j, j == 0);
+          ok = issue_pv(J + j, j == 0);
+          // S of tile j + 2 goes where P of tile j lies: products run in the order of issue
+          if (ok && j + 2 < n_tiles) ok = issue_s(J + j + 2);
         }
         if (ok) ptx::tc_commit(&sm.o_full);
         J += n_tiles;
@@ -219,15 +228,20 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   } else {
     // ------------------------------------------------------------ softmax, epilogue
     const int sw = warp - 2;
-    const int qt = sw >> 2;                    // keys kMine qt .. of a tile
+    const int qt = sw >> 2;                    // this warp among its quadrant's
+    const uint32_t team = qt & 1;              // tiles of this parity
+    const int half = qt >> 1;                  // keys kMine half .. of a tile
     const int qd = warp & 3;                   // tensor-memory lanes 32 qd .. 32 qd + 31
     const int r = qd * 32 + lane;              // this thread's row of the block
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
     const bool tree = p.tree_mask != nullptr;
     const uint32_t bar_id = 1 + qd;            // the four warps of a quadrant
-    constexpr int kBar = 32 * kShare;
+    const uint32_t pair_id = 5 + 2 * qd + team;   // those of a team
+    constexpr int kBar = 32 * kShare, kPairBar = 32 * kHalves;
     uint32_t J = 0, pc = 0;
-    bool ok = true;      // agreed on by the quadrant's warps at their barriers before they leave
+    // This warp's waits.  A pair agrees at its barrier in each tile; a pair that leaves there
+    // takes the quadrant's next barrier on its way, so that the other one leaves at that.
+    bool ok = true;
     bool stop = false;
     // Piece n's description stays in its ring until this warp is far past it.
     const auto piece = [&](uint32_t n) -> const Piece& { return sm.piece[n % kPieceRing]; };
@@ -299,7 +313,13 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const bool more = ok && piece(pc).n_tiles > 0;
       if (more) prepare(pc);
       if (!first) {
-        ok = warp_all(ok && wait(&sm.o_full, (pc - 1u) & 1u, tmo, &sm.abort));
+        const uint32_t last = (J - 1u) & 1u, phase = ((J - 1u) >> 1) & 1u;
+        ok = warp_all(ok && wait(&sm.ref_full[last][qd], phase, tmo, &sm.abort) &&
+                      wait(&sm.o_full, (pc - 1u) & 1u, tmo, &sm.abort));
+        const float2 fin = sm.refs[last][r];
+        ref = fin.x;
+        l *= ex2(ml - fin.y);
+        ml = fin.y;
         sm.sum[qt][r] = l;
       }
       stop = ptx::named_bar_or(bar_id, kBar, !ok);
@@ -343,153 +363,182 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
         }
         ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.o_free);
       }
       if (!more) break;
       const uint32_t par = pc % kRowSets;
       ok = ok && wait(&sm.q_full, pc & 1u, tmo, &sm.abort);   // rows, limits, factors are written
-      const int n_tiles = piece(pc).n_tiles, k_lo = piece(pc).k_lo, k_hi = piece(pc).k_hi;
-      const int pr_lo = part_seen_from(piece(pc));
+      const int n_tiles = piece(pc).n_tiles;
+      // tiles from this one on have keys that some rows do not see
+      const int part_from = (min(piece(pc).k_hi, part_seen_from(piece(pc))) - piece(pc).k_lo) / kTile;
       const float fac = sm.fac[par][r];
       ref = ml = kNone;
       l = 0.f;
+      // Bit c: this thread's row sees key `key0` + c of the piece.
+      const auto seen = [&](int key0) -> uint32_t {
+        const Piece& x = piece(pc);
+        const int n = min(sm.lim[par][r], x.k_hi) - key0;
+        uint32_t bits = n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
+        if (tree) {
+          const int o = key0 - (x.kv_len - x.rows);
+          const unsigned long long m = sm.mask[par][r];
+          bits &= o >= 0 ? (o < 64 ? uint32_t(m >> o) : 0u)
+                         : o > -32 ? (uint32_t(m) << -o) | ((1u << -o) - 1u) : 0xffffffffu;
+        }
+        return bits;
+      };
+      const auto hide = [&](uint32_t (&s)[32], int key0) {
+        const uint32_t bits = seen(key0);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!((bits >> c) & 1u)) s[c] = 0xFF800000u;   // -inf
+      };
       for (int j = 0; j < n_tiles; ++j, ++J) {
-        const int key0 = k_lo + j * kTile + qt * kMine;
-        const int tile_end = k_lo + (j + 1) * kTile;
-        uint32_t s[kMine];
-        float f[kRuns], lv[kRuns];        // by run of 16 keys: score factor, log2 of the V scale
-        ok = ok && wait(&sm.s_full, J & 1u, tmo, &sm.abort) &&
-             wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
+        const uint32_t buf = J & 1u;
+        if (buf != team) continue;
+        const bool part = j >= part_from;
+        const uint32_t ts = trow + kTmWideS + buf * 128 + half * kMine;
+        ok = ok && wait(&sm.sc_full[J % kScaleRing], (J / kScaleRing) & 1u, tmo, &sm.abort);
+        float f[kMine / 16], lv[kMine / 16];   // by run of 16 keys: score factor, log2 of the V scale
+#pragma unroll
+        for (int i = 0; i < kMine / 16; ++i) {
+          const int blk = (half * kMine + i * 16) >> p.bs_log2;
+          // (of blocks behind the last key no scale was copied)
+          const bool in = !part || piece(pc).k_lo + j * kTile + half * kMine + i * 16 < piece(pc).k_hi;
+          // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
+          f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
+          lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
+        }
+        ok = ok && wait(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         __syncwarp();
         float mp = -INFINITY, ms = -INFINITY;
         if (ok) {
           ptx::tc_fence_after();
-          ptx::tmem_ld32_wait(trow + kTmWideS + qt * kMine, s);
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.s_free);
 #pragma unroll
-          for (int i = 0; i < kRuns; ++i) {
-            const int blk = (qt * kMine + i * 16) >> p.bs_log2;
-            const bool in = key0 + i * 16 < k_hi;   // (else no scale was copied)
-            // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
-            f[i] = fminf(fmaxf(fac * (in ? sm.scale[J % kScaleRing][0][blk] : 1.f), 1e-37f), 3e38f);
-            lv[i] = in ? log2_scale(sm.scale[J % kScaleRing][1][blk]) : 0.f;
-          }
-          if (tile_end > k_hi || tile_end > pr_lo) {
-            const int lim = sm.lim[par][r], base = piece(pc).kv_len - piece(pc).rows;
-            const unsigned long long mask = sm.mask[par][r];
+          for (int h = 0; h < kMine / 32; ++h) {
+            uint32_t s[32];
+            ptx::tmem_ld32_wait(ts + 32 * h, s);
+            if (part) hide(s, piece(pc).k_lo + j * kTile + half * kMine + 32 * h);
 #pragma unroll
-            for (int c = 0; c < kMine; ++c) {
-              const int key = key0 + c;
-              const bool vis = key < min(lim, k_hi) &&
-                               (!tree || key < base || ((mask >> (key - base)) & 1ull));
-              if (!vis) s[c] = 0xFF800000u;   // -inf
+            for (int i = 0; i < 2; ++i) {
+              float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
+#pragma unroll
+              for (int c = 2; c < 16; c += 2) {
+                m0 = fmaxf(m0, __uint_as_float(s[16 * i + c]));
+                m1 = fmaxf(m1, __uint_as_float(s[16 * i + c + 1]));
+              }
+              const float m = fmaxf(m0, m1) * f[2 * h + i];
+              ms = fmaxf(ms, m);
+              mp = fmaxf(mp, m + lv[2 * h + i]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < kRuns; ++i) {
-            float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
-#pragma unroll
-            for (int c = 2; c < 16; c += 2) {
-              m0 = fmaxf(m0, __uint_as_float(s[16 * i + c]));
-              m1 = fmaxf(m1, __uint_as_float(s[16 * i + c + 1]));
-            }
-            const float m = fmaxf(m0, m1) * f[i];
-            ms = fmaxf(ms, m);
-            mp = fmaxf(mp, m + lv[i]);
-          }
-          sm.red[J & 1u][qt][r] = make_float2(mp, ms);
+          sm.red[team][half][r] = make_float2(mp, ms);
         }
-        if (ptx::named_bar_or(bar_id, kBar, !ok)) {
+        if (ptx::named_bar_or(pair_id, kPairBar, !ok)) {
           stop = true;
           break;
         }
-        // ---- references (all threads of a row do the same)
-#pragma unroll
-        for (int i = 0; i < kShare; ++i) {
-          const float2 o = sm.red[J & 1u][i][r];
+        {
+          const float2 o = sm.red[team][half ^ 1][r];
           mp = fmaxf(mp, o.x);
           ms = fmaxf(ms, o.y);
         }
-        const bool up = mp > ref + kWideCap, up_l = ms > ml + kLSlack;
-        float alpha = 1.f;
-        bool moved = false;      // the same in the whole warp
-        if (__any_sync(0xffffffffu, up || up_l)) {
-          alpha = up ? ex2(ref - (mp - kWideTop)) : 1.f;
-          if (up) ref = mp - kWideTop;
-          if (up_l) {
-            l *= ex2(ml - ms);
-            ml = ms;
-          }
-          moved = j > 0 && __any_sync(0xffffffffu, up);
+        // ---- references: those after the last tile, moved on (both threads of a row do the same)
+        float2 at = make_float2(kNone, kNone);
+        if (j > 0) {
+          ok = warp_all(ok && wait(&sm.ref_full[buf ^ 1u][qd], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
+          at = sm.refs[buf ^ 1u][r];
         }
+        const bool up = mp > at.x + kWideCap, up_l = ms > at.y + kLSlack;
+        ref = up ? mp - kWideTop : at.x;
+        if (up_l) at.y = ms;
+        if (half == 0) sm.refs[buf][r] = make_float2(ref, at.y);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.ref_full[buf][qd]);
+        l *= ex2(ml - at.y);
+        ml = at.y;
+        const bool moved = j > 0 && __any_sync(0xffffffffu, up);
+        const float alpha = up ? ex2(at.x - ref) : 1.f;
         // ---- V rows that some row does not see
-        if (tile_end > k_hi || tile_end > pr_lo) {
+        if (part) {
           ok = ok && wait(&sm.v_full[J % C::kVS], (J / C::kVS) & 1u, tmo, &sm.abort);
-          const int key = k_lo + j * kTile + r;   // thread by key here, its share of the row
+          const int k_hi = piece(pc).k_hi, pr_lo = part_seen_from(piece(pc));
+          const int key = piece(pc).k_lo + j * kTile + r;   // thread by key here, its half of the row
           if (ok && (key >= k_hi || key >= pr_lo) &&
-              clean_v_row(sm.v[J % C::kVS], r, key >= k_hi, 16 / kShare * qt, 16 / kShare * (qt + 1)))
+              clean_v_row(sm.v[J % C::kVS], r, key >= k_hi, 16 / kHalves * half, 16 / kHalves * (half + 1)))
             atomicOr(&sm.hit[par][(key - pr_lo) >> 6], 1ull << ((key - pr_lo) & 63));
           ptx::fence_proxy_async_smem();
+          ok = warp_all(ok);
+          __syncwarp();
         }
-        // ---- P's terms, a run of 16 keys at a time
+        // ---- P's terms, a run of 16 keys at a time: those of 32 keys go where their scores were
+        if (ok) {
 #pragma unroll
-        for (int i = 0; i < kRuns; ++i) {
-          const float a = lv[i] - ref;
-          const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
-          // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
-          // block of tiny values that p hardly sees)
-          const float d = -a - ml;
-          const bool far = __any_sync(0xffffffffu, d > 60.f);
-          if (far) {
-            float sum = 0.f;
+          for (int h = 0; h < kMine / 32; ++h) {
+            uint32_t s[32];
+            ptx::tmem_ld32_wait(ts + 32 * h, s);
+            if (part) hide(s, piece(pc).k_lo + j * kTile + half * kMine + 32 * h);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
-            l += sum;
-          }
-          float2 sum2 = make_float2(0.f, 0.f);
-          uint32_t w[kPTerms][4];
+            for (int i = 0; i < 2; ++i) {
+              const float fi = f[2 * h + i], a = lv[2 * h + i] - ref;
+              const float2 f2 = make_float2(fi, fi), a2 = make_float2(a, a);
+              // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them (a
+              // block of tiny values that p hardly sees)
+              const float d = -a - ml;
+              const bool far = __any_sync(0xffffffffu, d > 60.f);
+              if (far) {
+                float sum = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int k = 16 * i + 4 * c;
-            const float2 x0 = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2, a2);
-            const float2 x1 = fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), f2, a2);
-            const float2 e0 = make_float2(ex2(x0.x), ex2(x0.y)), e1 = make_float2(ex2(x1.x), ex2(x1.y));
-            sum2 = add2(sum2, add2(e0, e1));
-            uint32_t t4[kPTerms];
-            p_terms5(e0, e1, t4);
+                for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), fi, -ml));
+                l += sum;
+              }
+              float2 sum2 = make_float2(0.f, 0.f);
+              uint32_t w[kPTerms][4];
 #pragma unroll
-            for (int t = 0; t < kPTerms; ++t) w[t][c] = t4[t];
-          }
-          const float sum = sum2.x + sum2.y;
-          if (!far) l += sum * ex2(d);
-          if (i == 0) {
-            // PV of tile J - 1 has read P, and is in O, which moves to the new references only
-            // now: the terms were computed while that product ran
-            if (J > 0) ok = ok && wait(&sm.pv_done, (J - 1) & 1u, tmo, &sm.abort);
-            ok = warp_all(ok);
-            __syncwarp();
-            if (ok) {
-              ptx::tc_fence_after();
-              if (moved) rescale_o(trow + kTmWideO + qt * kCols, alpha);
+              for (int c = 0; c < 4; ++c) {
+                const int k = 16 * i + 4 * c;
+                const float2 x0 = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2, a2);
+                const float2 x1 = fma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), f2, a2);
+                const float2 e0 = make_float2(ex2(x0.x), ex2(x0.y)), e1 = make_float2(ex2(x1.x), ex2(x1.y));
+                sum2 = add2(sum2, add2(e0, e1));
+                uint32_t t4[kPTerms];
+                p_terms5(e0, e1, t4);
+#pragma unroll
+                for (int t = 0; t < kPTerms; ++t) w[t][c] = t4[t];
+              }
+              if (!far) l += (sum2.x + sum2.y) * ex2(d);
+#pragma unroll
+              for (int t = 0; t < kPTerms; ++t) ptx::tmem_st4(ts + 32 * h + 8 * t + 4 * i, w[t]);
             }
           }
+          ptx::tmem_wait_st();
+        }
+        if (moved) {
+          // O, with PV of tile J - 1 in it, moves to the new references only now: the terms
+          // were computed while that product ran
+          ok = warp_all(ok && wait(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
+          __syncwarp();
           if (ok) {
-            const uint32_t tp = trow + kTmWideP + qt * (kMine / 4) + 4 * i;
-#pragma unroll
-            for (int t = 0; t < kPTerms; ++t) ptx::tmem_st4(tp + 32 * t, w[t]);
-            ptx::tmem_wait_st();
+            ptx::tc_fence_after();
+            rescale_o(trow + kTmWideO + half * (256 / kHalves), alpha);
           }
         }
         if (ok) {
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.p_full);
+          if (lane == 0) ptx::mbar_arrive(&sm.p_full[buf]);
         }
       }
+      // S of the last tile, be it the other team's, has read Q before the next piece's is written
+      if (!stop)
+        ok = warp_all(ok && wait(&sm.s_full[(J - 1u) & 1u], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
       ++pc;
-      if (stop) break;
+      if (stop) {
+        ptx::named_bar_or(bar_id, kBar, true);
+        break;
+      }
     }
     if (stop && lane == 0) {
       sm.abort = 1;
