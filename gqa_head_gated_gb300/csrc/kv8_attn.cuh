@@ -26,7 +26,7 @@ constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see th
 // tiles, whose references still move), where shares have kLongShare tiles or more (with short
 // ones it would only unsettle them: one tile each is best then).  Swept over 1, 3, 5, 7, 9 and
 // 12: 16 x 32768 decode 92.2, 89.4, 89.9, 90.7, 90.3, 90.3 us; chain verify (32 rows) 87.1,
-// 85.3, 82.6, 80.6, 80.1, 81.0; tree verify (128 rows) 182, 178, 174, 172, 173, 174.
+// 85.3, 82.6, 80.6, 80.1, 81.0; tree verify (128 rows) over 2, 4, 6 and 8: 154, 151, 152, 149.
 template <int MB>
 constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB == 32 ? 9 : 8; }
 constexpr uint32_t kLongShare = 8;
@@ -288,7 +288,7 @@ __device__ __forceinline__ Share cut_shares(RingSmem<KS, VS>& sm, const Kv8AttnA
 // n + 8 - KS - 3 and with it piece n.
 //
 // kLead: V of a tile is copied behind K of the next one, for a kernel whose products of scores
-// run further ahead than its V slots do.
+// run further ahead than its V slots do (tree verify 158.6 us without, 156.3 with).
 template <int MB, bool kLead, int KS, int VS>
 __device__ __forceinline__ void copy_role(RingSmem<KS, VS>& sm, const Kv8AttnArgs& p,
                                           const CUtensorMap& tmK, const CUtensorMap& tmV,

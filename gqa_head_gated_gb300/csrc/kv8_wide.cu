@@ -15,18 +15,30 @@
 // leaves room for 128 rows: with e4m3 terms a column or lane each, as the kernel for few rows
 // has them, O alone would take three times 256 columns.
 //
-// What bounds it: the softmax's instructions.  The tensor pipe has 2 x 8 products of 64 clocks
-// for S and 3 x 4 of 128 for P.V, 2,560 a tile of 128 keys (1.33 us; HBM: 1.47), but a tile
-// takes about 4,200 cycles: each of 16 warps computes 32 x 32 probabilities and their terms,
-// about 12 instructions each, and the four warps of a scheduler share it (two warps of 64 keys
-// each took 4,900, with conversion instructions for the terms 5,300).
-// The kernel for few rows reads the cache once for 32 rows; 36 packed rows and more are faster
-// here (8 trees of 1 to 32 rows x 8 heads: 314 us there in row blocks of 32, 171 here).
+// What bounds it: the softmax's latency beside the tensor pipe.  A tile has 2 x 8 products of 64
+// clocks for S and 3 x 4 of 128 for P.V, 2,560 clocks (shared memory: 2,250 for their operands
+// and the copies; HBM: 2,800 for 64 KB), and takes about 3,800.  The rows of a draft tree
+// that pass 128 packed rows read the cache once more, through L2 or HBM.
 //
-// Roles (576 threads): warp 0 copies, warp 1 issues the products, warps 2..17 are the softmax
-// and epilogue: tensor-memory lane = row, four warps share a quadrant's rows, 32 keys each.
-// TMEM: O 256 columns, S 128 (one buffer: S of the next tile may start once every warp holds
-// its scores in registers), P 32 for each term.
+// Two teams of 8 warps take the tiles in turn, so that one's softmax runs beside the other's and
+// beside the products.  That takes two buffers of scores, for which tensor memory has room
+// only because a tile's P goes where its scores were: each warp loads 32 keys' scores and
+// stores their terms over them.  S of tile J + 2 is issued behind P.V of tile J, whose P it
+// overwrites.  The references pass from tile to tile through shared memory (ref_full), and a
+// row's l is kept apart in the four warps that share it.  Measured, 8 trees of 1 to 32 rows x 8
+// heads, keys 4 K to 64 K: 149 us (548 MB, 3.9 TB/s at 128-row blocks); all 16 warps on one
+// tile at a time, 32 keys each, 163 us; terms by conversion instructions, not by masks, took
+// a tile 5,300 cycles for 4,200.  With a limit of 96 registers a thread, code that makes
+// values live across a call (a rescale out of line) costs 30 us in spills.
+//
+// The kernel for few rows reads the cache once for 32 rows; 36 packed rows and more are faster
+// here (the same trees: 314 us there in row blocks of 32), 24 are not (8 x 4 draft rows x 6
+// heads: 80 us there, 93 here).
+//
+// Roles (576 threads): warp 0 copies (K a tile ahead of V: S runs two tiles ahead of P.V), warp 1
+// issues the products, warps 2..17 are the softmax and epilogue: tensor-memory lane = row, two
+// warps of a team share a quadrant's rows, 64 keys each.
+// TMEM: O 256 columns, two buffers of 128 for S and, 8 columns a term and 32 keys, P.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -64,6 +76,7 @@ struct __align__(1024) WideSmem : RingSmem<WideCfg<kF16>::kKS, WideCfg<kF16>::kV
   float2 red[kTeams][kHalves][kRows];      // by row: maxima with vs, without
   float2 refs[2][kRows];                   // [tile parity][row]: the references after the tile
   float sum[kShare][kRows];                // [share][row]
+  // by tile parity: scores done; terms stored; by quadrant, references published and read
   uint64_t s_full[2], p_full[2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
   // by piece, kRowSets in turn
   unsigned long long hit[kRowSets][2];     // NaN V rows taken out: bits of keys pr_lo + 64 w + i
