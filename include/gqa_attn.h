@@ -275,7 +275,7 @@ int gqa_launch_log(gqa_launch_info* out, int max_entries);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word that the
- * kernels set (GQA_ERR_TIMEOUT, GQA_ERR_DEVICE_RANGE); GQA_OK when clear.
+ * kernels set (GQA_ERR_TIMEOUT, GQA_ERR_DEVICE_RANGE, GQA_ERR_NO_BLOCKS); GQA_OK when clear.
  * Returns GQA_ERR_CUDA if the synchronisation fails.
  */
 int gqa_last_device_status(gqa_stream_t stream);
@@ -427,6 +427,8 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  *   its keys i*block_size .. (i+1)*block_size - 1.  No block belongs to two sequences that
  *   one call writes: its contents are unspecified after such a call (no access is out of
  *   range).  A block that is only read may be shared.
+ * The calls are launched as programmatic dependents of what is before them on the stream, and
+ * keep stream order.
  * num_blocks * Hkv * block_size < 2^31 and max_blocks * block_size < 2^31
  * (GQA_ERR_UNSUPPORTED above); the pools themselves may pass 2^32 bytes.
  *
@@ -448,7 +450,8 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  *     (kv_lens[b] when b was not served).  May be kv_lens itself.
  * A sequence that breaks the bounds (a negative length or count, more than max_blocks
  * blocks, cu_rows that fall or pass T) is not served and keeps its blocks, and
- * GQA_ERR_DEVICE_RANGE is recorded.  B <= 8192 (GQA_ERR_UNSUPPORTED above).
+ * GQA_ERR_DEVICE_RANGE is recorded.  B <= 8192, T < 2^30 and B * max_blocks < 2^30
+ * (GQA_ERR_UNSUPPORTED above).
  */
 int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block_tables, int* n_blocks,
                    int* free_list, int* free_count, int* slots, int* kv_lens_out, int B, int T,
@@ -477,8 +480,8 @@ int gqa_kv8_append_f16(const void* Knew, const void* Vnew, const int* slots, voi
  * cu_keep, strictly increasing draft-row indices, at most 64 per sequence) move to positions
  * kv_lens[b] - r_b + k.  The result is that of appending the values which the kept rows
  * stand for behind the first kv_lens[b] - r_b keys, by gqa_kv8_append's rule; rows behind
- * the last kept one hold no key any more.  n_keep: entries of keep_idx.  kv_lens_out: NULL or int32 [B] (not kv_lens),
- * receiving kv_lens[b] - r_b + (number kept).  A sequence with an invalid list or table
+ * the last kept one hold no key any more.  n_keep: entries of keep_idx.  kv_lens_out: NULL or
+ * int32 [B] (not kv_lens), receiving kv_lens[b] - r_b + (number kept).  A sequence with an invalid list or table
  * entry is left untouched and GQA_ERR_DEVICE_RANGE is recorded.
  */
 int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
@@ -500,7 +503,9 @@ int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
  * (a stale row of a block included) never changes its output; a NaN that it sees
  * propagates.  A Q row that holds NaN or +-Inf gives NaN.
  * workspace: gqa_kv8_workspace_size() bytes, 16-byte aligned; calls that may overlap on the
- * GPU need one each.
+ * GPU need one each.  Scores are fp32: q . k * scale / 16 has to stay in its range.
+ * max_kv_len < 2^30 and, for 128-key tiles, Hkv * row blocks * tiles of a sequence < 2^31
+ * (GQA_ERR_UNSUPPORTED above; the size is then 0 or of no use).
  */
 size_t gqa_kv8_workspace_size(int B, int T, int Hq, int Hkv, int max_rows, int max_kv_len);
 int gqa_kv8_decode(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
