@@ -61,14 +61,16 @@ struct Cfg {
   static constexpr int kGroups = MB / kGroupRows;          // softmax thread groups
   static constexpr int kSoftmax = kGroups * kGroupThreads;
   static constexpr int kThreads = 64 + kSoftmax;
-  static constexpr int kNS = MB * kQTerms;       // columns of S^T
-  static constexpr int kNO = MB * kPTerms;       // columns of each half of O^T
+  // columns of S^T and of each half of O^T, whole 16s (a column more than there are terms holds
+  // nothing that is read)
+  static constexpr int kNS = (MB * kQTerms + 15) / 16 * 16;
+  static constexpr int kNO = (MB * kPTerms + 15) / 16 * 16;
   // K and V slots of a tile each.  A K slot is free once S has read it, a V slot a softmax
   // and a product later; with two and three the copies' order (K, V, K, V, ...) is the order
   // in which slots come free.
   static constexpr int kKS = MB == 16 ? 3 : 2;
   static constexpr int kVS = 3;
-  static constexpr uint32_t kStep = MB * 4;      // tensor-memory columns of each of
+  static constexpr uint32_t kStep = MB == 16 ? 64 : 128;   // tensor-memory columns of each of
   static constexpr uint32_t kTmS = 0;            // the two S buffers
   static constexpr uint32_t kTmO = 2 * kStep;    // and the two halves of O
   static constexpr uint32_t kCols = 4 * kStep;
@@ -538,9 +540,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ok = warp_all(ok);
         if (ok) {
 #pragma unroll
-          for (int t = 0; t < kPTerms; ++t)
-            *reinterpret_cast<uint2*>(sm.p[buf] + (t * (MB / 16) + (rg >> 1)) * (kTile * 16) +
-                                      key_in * 16 + (rg & 1) * 8) = w[t];
+          for (int t = 0; t < kPTerms; ++t) {
+            const int c8 = t * C::kGroups + rg;   // which 8 columns
+            *reinterpret_cast<uint2*>(sm.p[buf] + (c8 >> 1) * (kTile * 16) + key_in * 16 +
+                                      (c8 & 1) * 8) = w[t];
+          }
           ptx::fence_proxy_async_smem();
           ptx::tc_fence_before();
           __syncwarp();
@@ -572,10 +576,11 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
   e = launch_dependent(kv8_attn_kernel<MB, kF16>, dim3(unsigned(grid)), Cfg<MB, kF16>::kThreads, smem,
                        stream, 1, tmK, tmV, a);
   if (e == cudaSuccess) {
-    static const char* const kNames[2][2] = {
+    static const char* const kNames[3][2] = {
         {"kv8_attn_kernel<16,bf16>", "kv8_attn_kernel<16,fp16>"},
+        {"kv8_attn_kernel<24,bf16>", "kv8_attn_kernel<24,fp16>"},
         {"kv8_attn_kernel<32,bf16>", "kv8_attn_kernel<32,fp16>"}};
-    note_launch(kNames[MB == 32][kF16], grid, Cfg<MB, kF16>::kThreads, smem);
+    note_launch(kNames[MB / 8 - 2][kF16], grid, Cfg<MB, kF16>::kThreads, smem);
   }
   return e;
 }
@@ -586,7 +591,7 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
 // second row block would read the cache again, which the wide kernel's 128 rows do not (its
 // own comment has both sides measured).
 int kv8_rows_per_block(long long packed_rows) {
-  return packed_rows <= 16 ? 16 : packed_rows <= 32 ? 32 : 128;
+  return packed_rows <= 16 ? 16 : packed_rows <= 24 ? 24 : packed_rows <= 32 ? 32 : 128;
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_t stream,
@@ -602,6 +607,9 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, bool f16, int sms, cudaStream_
   if (mb == 16)
     return f16 ? launch_t<16, true>(a, tmK, tmV, grid, stream)
                : launch_t<16, false>(a, tmK, tmV, grid, stream);
+  if (mb == 24)
+    return f16 ? launch_t<24, true>(a, tmK, tmV, grid, stream)
+               : launch_t<24, false>(a, tmK, tmV, grid, stream);
   return f16 ? launch_t<32, true>(a, tmK, tmV, grid, stream)
              : launch_t<32, false>(a, tmK, tmV, grid, stream);
 }

@@ -28,7 +28,7 @@ constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see th
 // 12: 16 x 32768 decode 92.2, 89.4, 89.9, 90.7, 90.3, 90.3 us; chain verify (32 rows) 87.1,
 // 85.3, 82.6, 80.6, 80.1, 81.0; tree verify (128 rows) over 2, 4, 6 and 8: 154, 151, 152, 149.
 template <int MB>
-constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB == 32 ? 9 : 8; }
+constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB <= 32 ? 9 : 8; }
 constexpr uint32_t kLongShare = 8;
 constexpr int kMaxTileBlocks = kTile / 16;
 // Pieces whose rows, limits and masks are held.  prepare() of piece n may run while another

@@ -26,9 +26,9 @@ def _ref(c, rows, q, g, mask=None):
     return oracle.decode_tree(to_f64(q), k, v, to_f64(g), c.lens, cu_of(rows), mask)[0]
 
 
-# 8, 20 and 40 packed rows: one kernel each
+# 8, 20, 28 and 40 packed rows: one kernel each
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("Hq,rows", [(16, 2), (16, 5), (32, 5)])
+@pytest.mark.parametrize("Hq,rows", [(16, 2), (16, 5), (16, 7), (32, 5)])
 def test_many_sequences_of_one_tile(Hq, rows, dtype):
     """A CTA goes through several segments of a single tile, one after another: each row's result is
     its own, every time."""
@@ -61,7 +61,7 @@ def test_more_sequences_than_one_launch_takes():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("rows", [1, 5, 9])
+@pytest.mark.parametrize("rows", [1, 3, 4, 5, 9])
 @pytest.mark.parametrize("n", [127, 128, 129, 255, 256, 257])
 def test_ends_of_tiles(n, rows, dtype):
     c = Cache([n, n + 128 * 9, rows], 2, 128, seed=106)
