@@ -27,7 +27,7 @@
 // by more than 2^8 (2^64), which one barrier per tile detects; then the warps exchange
 // maxima and O is rescaled in tensor memory.
 //
-// Roles (64 + 128 threads for 8 rows: 320 or 576): warp 0 copies (TMA, a block per box; scales by
+// Roles (64 + 128 threads for 8 rows: 320, 448 or 576): warp 0 copies (TMA, a block per box; scales by
 // cp.async), warp 1 issues the products, the others are the softmax and epilogue, a group of
 // 128 threads (key by thread) for every 8 rows.  A group agrees at its own barrier whether a
 // reference moves; between groups there are only bounded waits, so that one that gives up
@@ -35,8 +35,8 @@
 //
 // Measured (HBM copies run at 6.78 TB/s): 16 sequences of 32768 keys, 4 rows of a group, 89 us
 // for 555 MB (92 %); 2 of 131071 keys in fp16, 53 us for 268 MB (75 %: a launch, a start and a
-// merge are 13 us of it); 8 x 4 draft rows, 24 packed, 80 us for 303 MB (56 %), where the
-// softmax of 32 rows a tile is the limit.  kTop 5, 3 and 1 are as fast; 5 keeps more of the
+// merge are 13 us of it); 8 x 4 draft rows, 24 packed, 74 us for 303 MB (60 %), where
+// tiles whose references move (1,500 clocks more, by a barrier and the rescale) hold the copies up.  kTop 5, 3 and 1 are as fast; 5 keeps more of the
 // small probabilities.
 //
 // A key that a row does not see has p = 0 by selection.  V rows past the last visible key
@@ -587,7 +587,8 @@ cudaError_t launch_t(const Kv8AttnArgs& a, const CUtensorMap& tmK, const CUtenso
 
 }  // namespace
 
-// 16, 32 or 128 packed rows share a tile.  Up to 32 rows fewer columns cost less; past 32 a
+// 16, 24, 32 or 128 packed rows share a tile.  Up to 32 rows fewer columns cost less (8 x 4 draft
+// rows x 6 heads, 24 packed: 74 us in tiles of 24, 80 of 32, 93 of 128); past 32 a
 // second row block would read the cache again, which the wide kernel's 128 rows do not (its
 // own comment has both sides measured).
 int kv8_rows_per_block(long long packed_rows) {

@@ -33,7 +33,7 @@
 //
 // The kernel for few rows reads the cache once for 32 rows; 36 packed rows and more are faster
 // here (the same trees: 314 us there in row blocks of 32), 24 are not (8 x 4 draft rows x 6
-// heads: 80 us there, 93 here).
+// heads: 74 us there, 93 here).
 //
 // Roles (576 threads): warp 0 copies (K a tile ahead of V: S runs two tiles ahead of P.V), warp 1
 // issues the products, warps 2..17 are the softmax and epilogue: tensor-memory lane = row, two
