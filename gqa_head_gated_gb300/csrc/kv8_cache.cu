@@ -33,25 +33,28 @@ constexpr int kWindow = 64;               // tokens whose runs a CTA writes
 constexpr int kSpan = kWindow + 128;      // the last of them may reach a block further
 constexpr int kRowsPerWarp = kWindow / kWarps;
 
-// Largest |x| of a row's 256 elements (8 a lane) as fp32 bits, NaN and infinities left out;
-// *all: every element is finite.  16-bit magnitudes order as integers, two at a time; the
-// elements are looked at one by one only in a row that holds a NaN or an infinity.
+// 16-bit magnitudes order as integers: the largest two of a lane's 8 elements, side by side.
+__device__ __forceinline__ uint32_t lane_amax(uint4 u) {
+  return __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                  __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+}
+
+// The larger of the two over the warp.
+__device__ __forceinline__ uint32_t warp_amax(uint32_t m) {
+  return __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+}
+
+// Largest |x| of a row, NaN and infinities left out.
 template <bool kF16>
-__device__ __forceinline__ uint32_t row_amax(uint4 u, bool* all) {
+__device__ __forceinline__ uint32_t finite_row_amax(uint4 u) {
   constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
   const uint32_t w[4] = {u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu, u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu};
-  uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-  m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-  *all = m < kInf;
-  if (m >= kInf) {
-    m = 0u;
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = w[i] & 0xFFFFu, b = w[i] >> 16;
-      m = max(m, max(a < kInf ? a : 0u, b < kInf ? b : 0u));
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
+  uint32_t m = 0u;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0xFFFFu, b = w[i] >> 16;
+    m = max(m, max(a < kInf ? a : 0u, b < kInf ? b : 0u));
   }
-  return __float_as_uint(elem_to_float<kF16>(m));
+  return __reduce_max_sync(0xffffffffu, m);
 }
 
 template <bool kF16>
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
   __shared__ uint32_t s_break[kSpan / 32];   // bit i: token w0 + i starts a run or is in none
   __shared__ int s_run[kSpan];               // first token of token w0 + i's run, -1: none here
   __shared__ int s_row[kSpan];               // its pool row ((block * Hkv + g) * bs + row)
-  __shared__ uint32_t s_max[kWindow];        // by run (its first token): largest |x|, then
+  __shared__ uint32_t s_max[kWindow];        // by run (its first token): largest |x|, 16 bits
   __shared__ float s_inv[kWindow];           // one over its scale
   __shared__ float s_old[kWindow];           // the scale that the rows before it have
   __shared__ int s_grown[kWindow];
@@ -163,28 +166,43 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
   __syncthreads();
   const auto run_of = [&](int i) -> int { return i < n_span ? s_run[i] : -1; };
   int run[kRowsPerWarp];
-  uint32_t finite = 0u;    // bit k: row k of this warp holds no NaN or infinity
+  constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
+  bool finite = true;      // no row of this warp holds a NaN or an infinity
+  uint32_t m = 0u;         // maxima of the lane's elements in the run of the last rows
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) run[k] = run_of(i0 + warp + k * kWarps);
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k) {
-    run[k] = run_of(i0 + warp + k * kWarps);
     if (run[k] < 0) continue;
-    bool all;
-    const uint32_t m = row_amax<kF16>(u[k], &all);
-    finite |= uint32_t(all) << k;
-    if (lane == 0) atomicMax(&s_max[run[k]], m);
+    m = __vmaxu2(m, lane_amax(u[k]));
+    if (k + 1 < kRowsPerWarp && run[k + 1] == run[k]) continue;
+    const uint32_t a = warp_amax(m);
+    m = 0u;
+    finite = finite && a < kInf;
+    if (a < kInf && lane == 0) atomicMax(&s_max[run[k]], a);
+  }
+  if (!finite) {           // the same in all lanes: rows one by one, without such elements
+#pragma unroll 1
+    for (int i = i0 + warp; i < i0 + kWindow; i += kWarps) {
+      const int r = run_of(i);
+      if (r < 0) continue;
+      const uint32_t a = finite_row_amax<kF16>(__ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane));
+      if (lane == 0) atomicMax(&s_max[r], a);
+    }
   }
   for (int i = i0 + kWindow + warp; i < n_span; i += kWarps) {
     const int r = run_of(i);
     if (r < 0) break;   // past the last run
-    bool all;
-    const uint32_t m = row_amax<kF16>(__ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane), &all);
-    if (lane == 0) atomicMax(&s_max[r], m);
+    const uint4 v = __ldg(x + (size_t(w0 + i) * p.Hkv + g) * 32 + lane);
+    uint32_t a = warp_amax(lane_amax(v));
+    if (a >= kInf) a = finite_row_amax<kF16>(v);
+    if (lane == 0) atomicMax(&s_max[r], a);
   }
   __syncthreads();
   if (tid < kWindow && ((s_start[tid >> 5] >> (tid & 31)) & 1u)) {
     const int s = s_slot[tid + 1];
     float* const sp = (kv == 0 ? p.scale[0] : p.scale[1]) + size_t(s >> p.bs_log2) * p.Hkv + g;
-    int e = scale_exp(s_max[tid]);
+    int e = scale_exp(__float_as_uint(elem_to_float<kF16>(s_max[tid])));
     if ((s & (bs - 1)) != 0) {
       const float old = *sp;
       e = max(e, stored_exp(old));
@@ -202,12 +220,16 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
     unpack8<kF16>(v, f);
     const float inv = s_inv[r];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] *= inv;
+    for (int c = 0; c < 8; c += 2) {
+      const float2 y = mul2(make_float2(f[c], f[c + 1]), make_float2(inv, inv));
+      f[c] = y.x;
+      f[c + 1] = y.y;
+    }
     pool[size_t(s_row[i]) * 32 + lane] = all ? finite_to_e4m3x8(f) : to_e4m3x8(f);
   };
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k)
-    if (run[k] >= 0) put(i0 + warp + k * kWarps, run[k], u[k], (finite >> k) & 1u);
+    if (run[k] >= 0) put(i0 + warp + k * kWarps, run[k], u[k], finite);
   for (int i = i0 + kWindow + warp; i < n_span; i += kWarps) {
     const int r = run_of(i);
     if (r < 0) break;
