@@ -12,11 +12,11 @@
 // behind the first len - r keys.
 //
 // An append of a prompt should be bound by HBM (2 bytes read and 1 written a value) and is by
-// issue slots: 107 instructions a row of 256 values and warp, of which the conversions are
-// a third, at 54 % of the slots.  8192 rows of 4 heads, K and V: 13.0 us for 50 MB (57 % of the
-// copy rate; floor 7.4), 12 chunks of 2731 rows of 2 heads 21.7 for 101 MB (68 %).  With 4 CTAs
+// issue slots and latency: 91 instructions a row of 256 values and warp, of which the conversions
+// are a third, at 51 % of the slots.  8192 rows of 4 heads, K and V: 11.8 us for 50 MB (63 % of the
+// copy rate; floor 7.4), 12 chunks of 2731 rows of 2 heads 20.5 for 101 MB (73 %).  With 4 CTAs
 // of 256 threads an SM each warp holds 8 rows between the maximum and the rounding; 5 and 6 CTAs
-// spill (16.3, 19.0 us), 512 threads with 4 rows a warp took 14.0.  A step's call, 16 rows, is
+// spill (16.3, 19.0 us where 4 took 13.0), 512 threads with 4 rows a warp took 14.0.  A step's call, 16 rows, is
 // bound by latency: 3.3 us on the GPU (a chain of reads: slot, scale, row, and a launch).
 // keep of 128 sequences' drafts takes 7.1 us on the GPU for 8.4 MB, again such a chain: list,
 // table, rows, and the block's rows once more where a scale grew.
