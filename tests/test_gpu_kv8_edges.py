@@ -206,3 +206,34 @@ def test_cache_calls_on_another_stream_and_no_allocation():
     assert G.last_device_status() == 0
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hq,rows", [(129, 1), (200, 1), (256, 3)])
+def test_groups_wider_than_a_row_block(Hq, rows):
+    c = Cache([400, rows], 1, 64, seed=121)
+    q, g = rows_qg(2 * rows, Hq, 122)
+    out = _call(c, [rows] * 2, q.to(DEV), g.to(DEV))
+    assert_parity_dtype(out, _ref(c, [rows] * 2, q, g))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows", [1, 4, 9])
+def test_scales_of_zero_and_the_smallest(rows, dtype):
+    """Blocks whose K scale is 0 (scores of 0), whose V scale is 0 or 2^-126, and a sequence that has
+    no other: as the values say."""
+    c = Cache([700, 90, 300], 2, 32, seed=123)
+    t0, t1, t2 = c.tables
+    c.ks[t0[2:9:3]] = 0.0
+    c.vs[t0[1]], c.vs[t0[4]], c.vs[t0[5], 0] = 0.0, 2.0**-126, 0.0
+    for i in range(-(-90 // 32)):
+        c.vs[t1[i]] = 0.0
+    for i in range(-(-300 // 32)):
+        c.ks[t2[i]] = 0.0
+    q, g = rows_qg(3 * rows, 12, 124, dtype)
+    out, lse = _call(c, [rows] * 3, q.to(DEV), g.to(DEV), return_lse=True)
+    ref = _ref(c, [rows] * 3, q, g)
+    assert_parity_dtype(out, ref)
+    assert torch.all(out[rows:2 * rows] == 0) and G.last_device_status() == 0
+    # scores of 0: lse is ln of the keys seen, exact to an fp32 logarithm of a sum of ones
+    seen = torch.arange(300 - rows + 1, 301, dtype=torch.float64)
+    assert (lse[2 * rows:].double().cpu() - seen.log()[:, None]).abs().max() <= 1e-5
