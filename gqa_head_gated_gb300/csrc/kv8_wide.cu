@@ -59,8 +59,8 @@ constexpr int kWideThreads = 64 + 32 * kWarpsS;
 template <bool kF16>
 struct WideCfg {
   static constexpr int kQTerms = kF16 ? 3 : 2, kPTerms = kF16 ? 4 : 3;
-  // K and V slots.  One K slot is enough: S is done early in a tile's softmax, and the next K
-  // lands while that goes on; fp16's third Q term takes the other's place.
+  // K and V slots.  One K slot does: the next K lands while the teams' softmax goes on; fp16's
+  // third Q term takes the other's place.
   static constexpr int kKS = kF16 ? 1 : 2, kVS = 2;
 };
 constexpr uint32_t kTmWideO = 0, kTmWideS = 256;   // two buffers of 128 columns for S and P
