@@ -26,10 +26,10 @@ constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see th
 // tiles, whose references still move), where shares have kLongShare tiles or more (with short
 // ones it would only unsettle them: one tile each is best then).  Swept over 1, 3, 5, 7, 9 and
 // 12: 16 x 32768 decode (16 rows) 92.2, 89.4, 89.9, 90.7, 90.3, 90.3 us; over 3, 6, 9 and 12:
-// chain verify (24 rows) 78.6, 75.5, 74.0, 74.8; over 2, 4, 6 and 8: tree verify (128 rows) 154,
-// 151, 152, 149.
+// chain verify (24 rows) 78.6, 75.5, 74.0, 74.8; over 3, 5 and 8: tree verify (128 rows) 149.8,
+// 147.8, 149.4.
 template <int MB>
-constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB <= 32 ? 9 : 8; }
+constexpr uint32_t switch_tiles() { return MB == 16 ? 4 : MB <= 32 ? 9 : 5; }
 constexpr uint32_t kLongShare = 8;
 constexpr int kMaxTileBlocks = kTile / 16;
 // Pieces whose rows, limits and masks are held.  prepare() of piece n may run while another

@@ -264,6 +264,12 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const uint32_t par = n % kRowSets;
       const Piece x = piece(n);
       const int p0 = x.rb * kRows, n_rows = min(kRows, x.rows * p.gqa - p0);
+      if (sw < kRows / 32) {   // thread by row
+        const int rr = sw * 32 + lane, i = (p0 + rr) / p.gqa;
+        sm.row[par][rr] = (x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
+        sm.lim[par][rr] = rr >= n_rows ? 0 : tree ? x.kv_len : x.kv_len - x.rows + i + 1;
+        sm.mask[par][rr] = tree && rr < n_rows ? p.tree_mask[x.t0 + i] : 0ull;
+      }
 #pragma unroll 1
       for (int r0 = sw; r0 < kRows; r0 += 4 * kWarpsS) {
         uint4 u[4];
@@ -272,11 +278,6 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const int rr = r0 + k * kWarpsS, i = (p0 + rr) / p.gqa;
           const int row = (x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
           u[k] = rr < n_rows ? __ldg(p.q + size_t(row) * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
-          if (lane == 0) {
-            sm.row[par][rr] = row;
-            sm.lim[par][rr] = rr >= n_rows ? 0 : tree ? x.kv_len : x.kv_len - x.rows + i + 1;
-            sm.mask[par][rr] = tree && rr < n_rows ? p.tree_mask[x.t0 + i] : 0ull;
-          }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -349,19 +350,40 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const bool mine = x.s >= 0 && x.rb * kRows + r < x.rows * p.gqa;
         const size_t part = size_t(x.s) * size_t(p.T) * p.Hq + sm.row[par][r];
         if (mine && qt == 0) p.lse_parts[part] = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
+        // Four lanes have 8 columns of a row (two rows) of each load; they exchange two, so that
+        // a lane stores 16 bytes and the four 64 bytes in a row.
+        const int ok_row = mine && L != 0.f;
 #pragma unroll 1
-        for (int cc = 0; cc < kCols / 32; ++cc) {
+        for (int n = 0; n < 2 * kCols / 32; ++n) {
+          const int r16 = (n & 1) * 16, col = qt * kCols + (n >> 1) * 32;
           __syncwarp();
-          uint32_t o[32];
-          ptx::tmem_ld32_wait(trow + kTmWideO + qt * kCols + cc * 32, o);
-          if (!mine || L == 0.f) continue;
-          float* const dst = p.o_parts + part * 256 + qt * kCols + cc * 32;
+          uint32_t o[16];
+          ptx::tmem_ld16x256_x4_wait(trow + (uint32_t(r16) << 16) + kTmWideO + col, o);
 #pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<float4*>(dst + c) =
-                make_float4(__uint_as_float(o[c]) * inv * ex * ex, __uint_as_float(o[c + 1]) * inv * ex * ex,
-                            __uint_as_float(o[c + 2]) * inv * ex * ex, __uint_as_float(o[c + 3]) * inv * ex * ex);
+          for (int h = 0; h < 2; ++h) {
+            const int of = r16 + h * 8 + (lane >> 2);      // the row, as a lane of the warp
+            const float iv = __shfl_sync(0xffffffffu, inv, of), ev = __shfl_sync(0xffffffffu, ex, of);
+            const bool in = __shfl_sync(0xffffffffu, ok_row, of) != 0;
+            const size_t at = size_t(x.s) * size_t(p.T) * p.Hq + sm.row[par][qd * 32 + of];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {                  // columns 16 k .. 16 k + 15
+              float a[4];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t lo = o[8 * k + 2 * h + c], hi = o[8 * k + 4 + 2 * h + c];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? lo : hi, 1);
+                a[c] = __uint_as_float((lane & 1) ? got : lo);
+                a[2 + c] = __uint_as_float((lane & 1) ? hi : got);
+              }
+              if (in)
+                *reinterpret_cast<float4*>(p.o_parts + at * 256 + col + 16 * k + (lane & 1) * 8 +
+                                           (lane & 2) * 2) =
+                    make_float4(a[0] * iv * ev * ev, a[1] * iv * ev * ev, a[2] * iv * ev * ev,
+                                a[3] * iv * ev * ev);
+            }
+          }
         }
+        __syncwarp();
         const unsigned long long h0 = sm.hit[par][0], h1 = sm.hit[par][1];
         if ((h0 | h1) != 0ull && mine && L != 0.f) {
           // NaN values that were taken out, put back into what this thread wrote
