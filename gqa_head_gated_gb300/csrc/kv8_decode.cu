@@ -16,7 +16,7 @@ namespace gqa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = 4;     // each takes every fourth part of the row, 4 columns a thread
+constexpr int kGroups = 4;     // of 64 threads, 4 columns a thread
 constexpr int kBatch = 8;      // parts whose loads a thread issues together
 constexpr int kMaxParts = kThreads;
 
@@ -37,13 +37,21 @@ struct MergeParams {
 // its count of parts, then lse and O side by side), so that a row's parts are spread over
 // four groups of threads with eight loads each in flight: with one warp a row, 39 parts took
 // 13 us, as long as a third of the split kernel at 2 x 131071 keys.
-template <bool kF16>
+//
+// With more rows than the SMs hold CTAs for, and so few parts a row, a group takes a row of its
+// own (kOwn) and the chains of four rows run side by side.  A whole call, 250 sequences of 120
+// keys x 8 rows x 16 heads: 95 us so, 194 with a CTA a row; 64 of 1500 keys 61 and 86; 200 of 300
+// keys x 1 row 39 and 50.
+template <bool kF16, bool kOwn>
 __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p) {
   __shared__ float s_w[kMaxParts];
   __shared__ float s_red[2][kThreads / 32];
   __shared__ float4 s_acc[kGroups - 1][64];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = blockIdx.x;
+  constexpr int kSplit = kOwn ? 1 : kGroups;   // groups of a row
+  const int grp = tid >> 6, c4 = (tid & 63) * 4, pg = kOwn ? 0 : grp;
+  const int rows_all = p.T * p.Hq, n = kOwn ? min(blockIdx.x * kGroups + grp, rows_all - 1) : blockIdx.x;
+  bool live = !kOwn || blockIdx.x * kGroups + grp < rows_all;
   let_next_start();
   const int t = n / p.Hq, h = n - t * p.Hq;
   int b = t, i = 0, rows = 1;
@@ -62,33 +70,37 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
   const int kv_len = b < 0 ? -1 : __ldg(p.kv_lens + b);
   if (kv_len < rows || kv_len > p.max_kv_len) b = -1;
   if (b < 0) {   // (rows >= 1 where there is a row)
-    wait_for_last();
-    return;
+    if (!kOwn) {
+      wait_for_last();
+      return;
+    }
+    live = false;
   }
-  const int grp = tid >> 6, c4 = (tid & 63) * 4;
   uint2 gate = make_uint2(0u, 0u);
-  if (p.gate != nullptr && grp == 0)
+  if (p.gate != nullptr && pg == 0)
     gate = __ldg(reinterpret_cast<const uint2*>(p.gate + size_t(n) * 256 + c4));
   const int g = h / p.gqa, rb = (i * p.gqa + h - g * p.gqa) / p.rows_per_block;
   wait_for_last();
-  const int cnt = min(__ldcg(p.n_parts + (size_t(b) * p.Hkv + g) * p.max_rb + rb), p.parts);
+  const int cnt =
+      live ? min(__ldcg(p.n_parts + (size_t(b) * p.Hkv + g) * p.max_rb + rb), p.parts) : 0;
   const size_t stride = size_t(p.T) * p.Hq;
   // the group's first parts are on their way while the weights are worked out
   float4 v[kBatch];
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    const int s = grp + kGroups * u;
+    const int s = pg + kSplit * u;
     if (s < cnt)
       v[u] = __ldcg(reinterpret_cast<const float4*>(p.o_parts + (s * stride + n) * 256 + c4));
   }
-  const float ls = tid < cnt ? __ldcg(p.lse_parts + tid * stride + n) : -INFINITY;
+  const int mine = kOwn ? tid & 63 : tid;   // the part whose weight this thread works out
+  const float ls = mine < cnt ? __ldcg(p.lse_parts + mine * stride + n) : -INFINITY;
   float M = ls;   // fmaxf drops a NaN; a NaN part still gets weight NaN below
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) s_red[0][warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) M = fmaxf(M, s_red[0][k]);
+  for (int k = 0; k < 2 * kSplit; ++k) M = fmaxf(M, s_red[0][kOwn ? 2 * grp + k : k]);
   const float msub = M == -INFINITY ? 0.f : M;
   const float wl = ls == -INFINITY ? 0.f : __expf(ls - msub);
   s_w[tid] = wl;
@@ -99,21 +111,21 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
   __syncthreads();
   sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) sum += s_red[1][k];
+  for (int k = 0; k < 2 * kSplit; ++k) sum += s_red[1][kOwn ? 2 * grp + k : k];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = grp; s0 < cnt; s0 += kGroups * kBatch) {
-    if (s0 != grp) {
+  for (int s0 = pg; s0 < cnt; s0 += kSplit * kBatch) {
+    if (s0 != pg) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int s = s0 + kGroups * u;
+        const int s = s0 + kSplit * u;
         if (s < cnt)
           v[u] = __ldcg(reinterpret_cast<const float4*>(p.o_parts + (s * stride + n) * 256 + c4));
       }
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int s = s0 + kGroups * u;
-      const float w = s < cnt ? s_w[s] : 0.f;
+      const int s = s0 + kSplit * u;
+      const float w = s < cnt ? s_w[kOwn ? grp * 64 + s : s] : 0.f;
       if (w != 0.f) {   // (an empty part's O was not written)
         acc.x += w * v[u].x;
         acc.y += w * v[u].y;
@@ -122,16 +134,20 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
       }
     }
   }
-  if (grp > 0) s_acc[grp - 1][tid & 63] = acc;
-  __syncthreads();
-  if (grp > 0) return;
+  if (kOwn) {
+    if (!live) return;
+  } else {
+    if (grp > 0) s_acc[grp - 1][tid & 63] = acc;
+    __syncthreads();
+    if (grp > 0) return;
 #pragma unroll
-  for (int k = 0; k < kGroups - 1; ++k) {
-    const float4 x = s_acc[k][tid];
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float4 x = s_acc[k][tid];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   float gs[4] = {1.f, 1.f, 1.f, 1.f};
@@ -146,16 +162,20 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
   o.x = pack_elem2<kF16>(acc.x * inv * gs[0], acc.y * inv * gs[1]);
   o.y = pack_elem2<kF16>(acc.z * inv * gs[2], acc.w * inv * gs[3]);
   *reinterpret_cast<uint2*>(p.out + size_t(n) * 256 + c4) = o;
-  if (p.lse_out != nullptr && tid == 0)
+  if (p.lse_out != nullptr && c4 == 0)
     p.lse_out[n] = sum == 0.f ? -INFINITY : msub + __logf(sum);
 }
 
 template <bool kF16>
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   const unsigned rows = unsigned(p.T) * unsigned(p.Hq);
-  const cudaError_t e = launch_dependent(kv8_merge_kernel<kF16>, dim3(rows), kThreads, 0, stream, 1, p);
+  const bool own = p.parts <= 64 && rows > 2048u / kThreads * unsigned(device_sm_count());
+  const unsigned grid = own ? (rows + kGroups - 1) / kGroups : rows;
+  const cudaError_t e =
+      launch_dependent(own ? kv8_merge_kernel<kF16, true> : kv8_merge_kernel<kF16, false>, dim3(grid),
+                       kThreads, 0, stream, 1, p);
   if (e == cudaSuccess)
-    note_launch(kF16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", rows, kThreads, 0);
+    note_launch(kF16 ? "kv8_merge_kernel<fp16>" : "kv8_merge_kernel<bf16>", grid, kThreads, 0);
   return e;
 }
 

@@ -26,7 +26,7 @@
 // stores their terms over them.  S of tile J + 2 is issued behind P.V of tile J, whose P it
 // overwrites.  The references pass from tile to tile through shared memory (ref_full), and a
 // row's l is kept apart in the four warps that share it.  Measured, 8 trees of 1 to 32 rows x 8
-// heads, keys 4 K to 64 K: 149 us (548 MB, 3.9 TB/s at 128-row blocks); all 16 warps on one
+// heads, keys 4 K to 64 K: 145 us (548 MB, 4 TB/s at 128-row blocks); all 16 warps on one
 // tile at a time, 32 keys each, 163 us; terms by conversion instructions, not by masks, took
 // a tile 5,300 cycles for 4,200.  With a limit of 96 registers a thread, code that makes
 // values live across a call (a rescale out of line) costs 30 us in spills.

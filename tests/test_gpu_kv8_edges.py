@@ -237,3 +237,20 @@ def test_scales_of_zero_and_the_smallest(rows, dtype):
     # scores of 0: lse is ln of the keys seen, exact to an fp32 logarithm of a sum of ones
     seen = torch.arange(300 - rows + 1, 301, dtype=torch.float64)
     assert (lse[2 * rows:].double().cpu() - seen.log()[:, None]).abs().max() <= 1e-5
+
+
+def test_skipped_rows_of_a_large_batch():
+    """More rows than the GPU holds CTAs for: those of a skipped sequence and behind the last stay."""
+    rows = [3] * 60
+    c = Cache([50 + i for i in range(60)], 1, 16, seed=125)
+    q, g = rows_qg(183, 16, 126)
+    out = torch.full((183, 16, 256), 7.0, dtype=q.dtype, device=DEV)
+    lens = list(c.lens)
+    lens[20] = 2                                          # fewer keys than new rows: skipped
+    G.kv8_decode(q.to(DEV), *c.device()[:4], g.to(DEV), i32(c.tables), i32(lens), i32(cu_of(rows)), max_rows=3,
+                 max_kv_len=max(c.lens), out=out)
+    assert G.last_device_status() == 6
+    assert torch.all(out[60:63] == 7) and torch.all(out[180:] == 7)
+    ref = _ref(c, rows, q[:180], g[:180])
+    keep = [i for i in range(180) if not 60 <= i < 63]
+    assert_parity_dtype(out[keep], ref[keep])
