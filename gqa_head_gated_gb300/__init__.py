@@ -417,7 +417,9 @@ def kv8_append(k_new, v_new, slots, k_pool, v_pool, k_scale, v_scale):
     (int32 [T], from block_plan; -1 skips a row).  k_pool, v_pool: float8_e4m3fn [num_blocks,
     Hkv, block_size, 256]; k_scale, v_scale: float32 [num_blocks, Hkv], one power of two per
     block and head, kept as large as the block's rows ask (rows that a block holds already
-    are rounded again when its scale grows)."""
+    are rounded again when its scale grows).  Rows of one block have increasing slots; a row
+    that repeats an earlier one's is skipped, and last_device_status() gives
+    GQA_ERR_DEVICE_RANGE (6)."""
     sfx = _elem(k_new, "k_new")
     d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
     T, shape = k_new.shape[0], (k_new.shape[0], Hkv, HEAD_DIM)

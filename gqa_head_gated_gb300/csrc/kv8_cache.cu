@@ -8,13 +8,15 @@
 //   rows before the run are rounded again by 2^(e_old - e) where the scale grew
 //   q    = e4m3(x * 2^-e), nearest even; NaN and +-Inf are stored as NaN (e4m3 has no
 //          infinity, and a saturated one would pass for a number)
+// Several runs of a call in one block follow one another in order.
 // keep is the same rule applied to the kept rows' values, as if they had been appended
 // behind the first len - r keys.
 //
 // An append of a prompt should be bound by HBM (2 bytes read and 1 written a value) and is by
 // issue slots and latency: 91 instructions a row of 256 values and warp, of which the conversions
-// are a third, at 51 % of the slots.  8192 rows of 4 heads, K and V: 11.8 us for 50 MB (63 % of the
-// copy rate; floor 7.4), 12 chunks of 2731 rows of 2 heads 20.5 for 101 MB (73 %).  With 4 CTAs
+// are a third, at 51 % of the slots.  8192 rows of 4 heads, K and V: 12.0 us for 50 MB (62 % of the
+// copy rate; floor 7.4), 12 chunks of 2731 rows of 2 heads 23.7 for 101 MB (63 %; 20.5 when the
+// ends of a sequence did not look for other rows of their block).  With 4 CTAs
 // of 256 threads an SM each warp holds 8 rows between the maximum and the rounding; 5 and 6 CTAs
 // spill (16.3, 19.0 us where 4 took 13.0), 512 threads with 4 rows a warp took 14.0.  A step's call, 16 rows, is
 // bound by latency: 3.3 us on the GPU (a chain of reads: slot, scale, row, and a launch).
@@ -89,12 +91,161 @@ __device__ __forceinline__ void rescale_rows(uint2* block, int n, float s_old, f
   }
 }
 
+// A call may have several runs in one block: rows that are skipped in the middle of a sequence,
+// sequences whose tokens alternate.  Each rounds the rows before it again, so that they go one
+// after another: the CTA that has the block's first run takes all of them, the others leave
+// theirs to it.  A run that starts at the block's first row has none before it, one that ends at
+// its last row none behind it (rows of a block increase with the token), so that a prompt's
+// windows look at the call's other tokens only at the ends of a sequence.
+constexpr int kHash = kThreads;           // lists of a window's runs by block
+constexpr int kContinues = 1;             // there is an earlier run in the block: left to its CTA
+constexpr int kFollowed = 2;              // a later token of the call is in the block
+constexpr int kRepeats = 4;               // an earlier token has this row or one behind it: no place
+
+constexpr int kFew = 2;                   // runs that are asked for one by one
+constexpr int kAhead = 8, kAsk = 16;      // tokens whose slots a thread loads together
+
+struct Ask {
+  int lo, hi;                // tokens
+  unsigned slot;             // first of the block
+};
+
+struct WindowRuns {
+  int head[kHash];           // first run of the list, -1: none
+  int next[kWindow];
+  int end[kWindow];          // by run (its first token): the token behind its last
+  int state[kWindow];
+  int found, len;            // of the block that is followed
+  int n_asks;
+  Ask ask[2 * kFew];
+};
+
+// All threads: is any token in one of the few ranges in the block asked for?  A load and one
+// instruction a token, where look_around() takes about ten: 12 prompt chunks of 2731 rows, whose
+// 24 ends each go through 32,772 slots, 23.7 us so and 35.3 by look_around() alone; 8 loads
+// together 24.8, 24 (spills) 27.1.
+__device__ __noinline__ bool any_in_block(const int* slots, unsigned bs, const WindowRuns& w) {
+  unsigned m = ~0u;
+  for (int a = 0; a < w.n_asks; ++a) {
+    const Ask q = w.ask[a];
+    for (int t = q.lo + int(threadIdx.x); t < q.hi; t += kAsk * kThreads) {
+      unsigned s[kAsk];
+#pragma unroll
+      for (int k = 0; k < kAsk; ++k)
+        s[k] = t + k * kThreads < q.hi ? unsigned(__ldg(slots + t + k * kThreads)) : ~0u;
+#pragma unroll
+      for (int k = 0; k < kAsk; ++k) m = __viaddmin_u32(s[k], 0u - q.slot, m);
+    }
+  }
+  return __syncthreads_or(m < bs);
+}
+
+// All threads: sets kContinues, kFollowed and kRepeats, from every token of the call, for the runs
+// of this window (`mine`: one starts at token w0 + tid) that may have others in their block.
+__device__ __noinline__ void look_around(const int* slots, int T, int w0, unsigned n_slots,
+                                         int bs_log2, const int* s_slot, bool mine, WindowRuns& w) {
+  const int tid = threadIdx.x;
+  if (mine) w.next[tid] = atomicExch(&w.head[(s_slot[tid + 1] >> bs_log2) % kHash], tid);
+  __syncthreads();
+  for (int t0 = tid; t0 < T; t0 += kAhead * kThreads) {
+    int slot[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      slot[k] = t0 + k * kThreads < T ? __ldg(slots + t0 + k * kThreads) : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int s = slot[k], i = t0 + k * kThreads - w0;
+      if (unsigned(s) >= n_slots) continue;
+      for (int f = w.head[(s >> bs_log2) % kHash]; f >= 0; f = w.next[f]) {
+        const int first = s_slot[f + 1];
+        if ((s >> bs_log2) != (first >> bs_log2)) continue;
+        if (i >= w.end[f]) atomicOr(&w.state[f], kFollowed);
+        if (i < f && (first & ((1 << bs_log2) - 1)) != 0)
+          atomicOr(&w.state[f], s < first ? kContinues : kContinues | kRepeats);
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// All threads: the later runs, from token `t` on, in the block of `slot`, whose rows up to that
+// one are written.
+template <bool kF16>
+__device__ __noinline__ void follow_block(const AppendParams& p, const uint4* x, uint2* pool,
+                                          float* scale, int slot, int t, int g, bool record,
+                                          WindowRuns& w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bs = 1 << p.bs_log2, blk = slot >> p.bs_log2;
+  const size_t block = size_t(blk) * p.Hkv + g;
+  uint2* const rows = pool + (block << p.bs_log2) * 32;
+  const auto inside = [&](int i) {
+    const int s = __ldg(p.slots + i);
+    return s >= 0 && (s >> p.bs_log2) == blk;
+  };
+  int most = slot & (bs - 1);              // last row that a token of the call had so far
+  while (t < p.T) {
+    __syncthreads();
+    if (tid == 0) w.found = p.T;
+    __syncthreads();
+    for (; t < p.T; t += 8 * kThreads) {   // the next token in the block
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        const int i = t + k * kThreads + tid;
+        if (i < p.T && inside(i)) {
+          atomicMin(&w.found, i);
+          break;
+        }
+      }
+      __syncthreads();
+      const bool hit = w.found < p.T;
+      __syncthreads();                     // read by all before the next ones are looked at
+      if (hit) break;
+    }
+    t = w.found;
+    if (t >= p.T) return;
+    const int row = __ldg(p.slots + t) & (bs - 1);
+    const bool start = !inside(t - 1);     // (t > 0: it comes behind a run)
+    if (tid == 0) w.len = bs - row;
+    __syncthreads();
+    if (tid < bs - row && (t + tid >= p.T || __ldg(p.slots + t + tid) != __ldg(p.slots + t) + tid))
+      atomicMin(&w.len, tid);
+    __syncthreads();
+    const int n = w.len;
+    if (start && row > most) {
+      if (tid == 0) w.found = 0;           // here: largest |x|
+      __syncthreads();
+      for (int i = warp; i < n; i += kWarps) {
+        const uint32_t a =
+            finite_row_amax<kF16>(__ldg(x + (size_t(t + i) * p.Hkv + g) * 32 + lane));
+        if (lane == 0) atomicMax(&w.found, int(a));
+      }
+      const float old = scale[block];
+      __syncthreads();
+      const int e = max(scale_exp(__float_as_uint(elem_to_float<kF16>(uint32_t(w.found)))), stored_exp(old));
+      const float inv = inv_pow2f(e);
+      if (tid == 0) scale[block] = pow2f(e);
+      if (pow2f(e) != old) rescale_rows(rows, row, old, inv);
+      for (int i = warp; i < n; i += kWarps) {
+        float f[8];
+        unpack8<kF16>(__ldg(x + (size_t(t + i) * p.Hkv + g) * 32 + lane), f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] *= inv;
+        rows[(row + i) * 32 + lane] = to_e4m3x8(f);
+      }
+    } else if (start && row == 0 && record) {
+      record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);   // the block is begun twice
+    }
+    most = max(most, row + n - 1);
+    t += n;
+  }
+}
+
 // One CTA: the runs that start in its window of 64 tokens, for one KV head of K or V.
 // A token's run is the tokens before it in the same block; a run is at most one block.
 // Every warp keeps 8 of the first 64 rows in registers between the maximum and the rounding;
 // rows of the last run past them are read twice.
 template <bool kF16>
-__global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ int s_slot[kSpan + 1];          // slot of token w0 - 1 + i
   __shared__ uint32_t s_start[kSpan / 32];   // bit i: token w0 + i starts a run
   __shared__ uint32_t s_break[kSpan / 32];   // bit i: token w0 + i starts a run or is in none
@@ -105,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
   __shared__ float s_old[kWindow];           // the scale that the rows before it have
   __shared__ int s_grown[kWindow];
   __shared__ int s_n_grown;
+  __shared__ WindowRuns s_runs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int w0 = blockIdx.x * kWindow, g = blockIdx.y, kv = blockIdx.z;
   const int bs = 1 << p.bs_log2;
@@ -118,8 +270,12 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
     const int t = w0 - 1 + i;
     s_slot[i] = t >= 0 && i <= n_span ? __ldg(p.slots + t) : -1;
   }
-  if (tid < kWindow) s_max[tid] = 0u;
-  if (tid == 0) s_n_grown = 0;
+  if (tid < kWindow) {
+    s_max[tid] = 0u;
+    s_runs.state[tid] = 0;
+  }
+  s_runs.head[tid] = -1;
+  if (tid == 0) s_n_grown = s_runs.n_asks = 0;
   __syncthreads();
   const long long n_slots = (long long)p.num_blocks << p.bs_log2;
   if (tid < kSpan) {   // kSpan / 32 whole warps
@@ -143,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
   __syncthreads();
   // Rows before the first run belong to the window before; the 64 from it on are loaded now.
   const uint64_t starts = (uint64_t(s_start[1]) << 32) | s_start[0];
+  const bool starts_run = tid < kWindow && ((starts >> tid) & 1ull);
   const int i0 = starts == 0ull ? kSpan : __ffsll(static_cast<long long>(starts)) - 1;
   uint4 u[kRowsPerWarp];
 #pragma unroll
@@ -163,7 +320,40 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
     s_run[tid] = f;
     s_row[tid] = f < 0 ? 0 : (((s >> p.bs_log2) * p.Hkv + g) << p.bs_log2) + (s & (bs - 1));
   }
-  __syncthreads();
+  bool other = false;   // other tokens of the call may be in the block of the run that starts here
+  if (starts_run) {
+    int end = tid + 1;
+    for (; end < kSpan; end = (end | 31) + 1) {
+      const uint32_t m = s_break[end >> 5] >> (end & 31);
+      if (m != 0u) {
+        end += __ffs(int(m)) - 1;
+        break;
+      }
+    }
+    const int row = s_slot[tid + 1] & (bs - 1);
+    s_runs.end[tid] = end;
+    const int block = s_slot[tid + 1] - row;
+    if (row != 0 && w0 + tid > 0) {
+      other = true;
+      const int a = atomicAdd(&s_runs.n_asks, 1);
+      if (a < 2 * kFew) s_runs.ask[a] = Ask{0, w0 + tid, unsigned(block)};
+    }
+    if (row + end - tid < bs && w0 + end < p.T) {
+      other = true;
+      const int a = atomicAdd(&s_runs.n_asks, 1);
+      if (a < 2 * kFew) s_runs.ask[a] = Ask{w0 + end, p.T, unsigned(block)};
+    }
+  }
+  const int n_other = __syncthreads_count(other);
+  bool looked = n_other > 0;   // the same in all threads, as all of what follows
+  if (looked && n_other <= kFew) looked = any_in_block(p.slots, unsigned(bs), s_runs);
+  if (looked) {
+    look_around(p.slots, p.T, w0, unsigned(n_slots), p.bs_log2, s_slot, other, s_runs);
+    if (starts_run && (s_runs.state[tid] & kRepeats) && g == 0 && kv == 0)
+      record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+    if (tid < n_span && s_run[tid] >= 0 && (s_runs.state[s_run[tid]] & kContinues)) s_run[tid] = -1;
+    __syncthreads();
+  }
   const auto run_of = [&](int i) -> int { return i < n_span ? s_run[i] : -1; };
   int run[kRowsPerWarp];
   constexpr uint32_t kInf = kF16 ? 0x7C00u : 0x7F80u;
@@ -199,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
     if (lane == 0) atomicMax(&s_max[r], a);
   }
   __syncthreads();
-  if (tid < kWindow && ((s_start[tid >> 5] >> (tid & 31)) & 1u)) {
+  if (starts_run && !(s_runs.state[tid] & kContinues)) {
     const int s = s_slot[tid + 1];
     float* const sp = (kv == 0 ? p.scale[0] : p.scale[1]) + size_t(s >> p.bs_log2) * p.Hkv + g;
     int e = scale_exp(__float_as_uint(elem_to_float<kF16>(s_max[tid])));
@@ -238,6 +428,13 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const AppendPar
   for (int j = 0; j < s_n_grown; ++j) {
     const int r = s_grown[j], n = s_row[r] & (bs - 1);
     rescale_rows(pool + size_t(s_row[r] - n) * 32, n, s_old[r], s_inv[r]);
+  }
+  if (!looked) return;
+  for (int f = 0; f < kWindow; ++f) {
+    if (!((starts >> f) & 1ull) || (s_runs.state[f] & (kContinues | kFollowed)) != kFollowed) continue;
+    __syncthreads();   // the run's rows, those before them and its scale are written
+    follow_block<kF16>(p, x, pool, kv == 0 ? p.scale[0] : p.scale[1],
+                       s_slot[s_runs.end[f]], w0 + s_runs.end[f], g, g == 0 && kv == 0, s_runs);
   }
 }
 
@@ -365,7 +562,8 @@ int append_impl(bool f16, const void* Knew, const void* Vnew, const int* slots, 
   if (T < 0) return GQA_ERR_INVALID_ARG;
   const int st = check_kv8_pool(num_blocks, Hkv, block_size);
   if (st != GQA_OK) return st;
-  if (Hkv > 65535 || (long long)T * Hkv >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  // (token indexes run a few windows past T)
+  if (Hkv > 65535 || (long long)T * Hkv >= (1LL << 31) - kAsk * kThreads) return GQA_ERR_UNSUPPORTED;
   if (T == 0) return GQA_OK;
   if (Knew == nullptr || Vnew == nullptr || slots == nullptr || k_pool == nullptr ||
       v_pool == nullptr || k_scale == nullptr || v_scale == nullptr)

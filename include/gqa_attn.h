@@ -465,8 +465,13 @@ int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block_tables, in
  *   e    = E when the run starts at the block's first row, else max(the stored scale's, E)
  *   the block's rows before the run are rounded again when its scale grew
  *   q    = x * 2^-e rounded to e4m3, nearest even; NaN and +-Inf are stored as NaN.
- * A slot outside the pool, or in the block of the token before it but not right behind it,
- * is skipped with the run that it starts, and GQA_ERR_DEVICE_RANGE is recorded.
+ * Several runs in one block (rows of -1 between them, sequences whose tokens alternate) are
+ * taken in the order of their tokens.  The rows of a block increase with the token: a slot
+ * outside the pool, one in the block of the token before it but not right behind it, and one
+ * at or before a row that an earlier token of the call has in its block is skipped with the
+ * run that it starts, and GQA_ERR_DEVICE_RANGE is recorded.  (A block's first row comes once,
+ * and before its others: the block's contents are unspecified after a call that gives it
+ * behind another row or twice; no access is out of range.)
  */
 int gqa_kv8_append(const void* Knew, const void* Vnew, const int* slots, void* k_pool, void* v_pool,
                    float* k_scale, float* v_scale, int T, int Hkv, int num_blocks, int block_size,
