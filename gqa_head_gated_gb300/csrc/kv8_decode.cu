@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
   for (int k = 0; k < 2 * kSplit; ++k) M = fmaxf(M, s_red[0][kOwn ? 2 * grp + k : k]);
   const float msub = M == -INFINITY ? 0.f : M;
   const float wl = ls == -INFINITY ? 0.f : __expf(ls - msub);
-  s_w[tid] = wl;
+  s_w[tid] = ls == -INFINITY ? -1.f : wl;   // -1: the part saw no key, and its O was not written
   float sum = wl;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(kThreads) kv8_merge_kernel(const MergeParams p
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int s = s0 + kSplit * u;
-      const float w = s < cnt ? s_w[kOwn ? grp * 64 + s : s] : 0.f;
-      if (w != 0.f) {   // (an empty part's O was not written)
+      const float w = s < cnt ? s_w[kOwn ? grp * 64 + s : s] : -1.f;
+      if (!(w < 0.f)) {   // a weight of 0 counts: its O may hold a NaN that the row sees
         acc.x += w * v[u].x;
         acc.y += w * v[u].y;
         acc.z += w * v[u].z;
