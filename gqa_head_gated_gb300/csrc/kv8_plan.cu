@@ -86,6 +86,35 @@ __device__ int2 scan2(int* a, int* b, int n, int2* part) {
   return total;
 }
 
+// Where row offsets fall, rows of one sequence may be rows of another: of those that keep the
+// bounds, one that starts before the end of any before it is refused.  Warp 0, 32 sequences at a
+// time, with the largest end so far.
+__device__ __noinline__ void drop_overlaps(const int* s_cu, int* s_have, int* s_rel, int* s_grow,
+                                           int B, int* status) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int end = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + lane;
+      const bool in = b < B && s_have[b] >= 0;
+      int most = in ? s_cu[b + 1] : 0;   // largest end up to and with b
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, most, o);
+        if (lane >= o) most = max(most, x);
+      }
+      const int before = __shfl_up_sync(0xffffffffu, most, 1);
+      if (in && s_cu[b] < max(end, lane > 0 ? before : 0)) {
+        s_have[b] = -1;
+        s_rel[b] = s_grow[b] = 0;
+        if (status != nullptr) record_status(status, GQA_ERR_DEVICE_RANGE);
+      }
+      end = max(end, __shfl_sync(0xffffffffu, most, 31));
+    }
+  }
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(kThreads)
 block_plan_kernel(const PlanParams p) {
   extern __shared__ int smem[];
@@ -106,8 +135,10 @@ block_plan_kernel(const PlanParams p) {
   const int fc_read = *p.free_count;
   const int fc = min(max(fc_read, 0), p.num_blocks);
   __syncthreads();
+  bool down = false;   // row offsets that fall
   for (int b = tid; b < B; b += kThreads) {
     const int len = p.kv_lens[b], have = p.n_blocks[b];
+    down = down || s_cu[b + 1] < s_cu[b];
     const long long end = (long long)len + s_cu[b + 1] - s_cu[b];
     const bool ok = len >= 0 && s_cu[b] >= 0 && s_cu[b + 1] >= s_cu[b] && s_cu[b + 1] <= p.T &&
                     end <= cap && have >= 0 && have <= p.max_blocks;
@@ -118,7 +149,8 @@ block_plan_kernel(const PlanParams p) {
     s_grow[b] = ok ? max(need - have, 0) : 0;
     if (!ok && cta == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
   }
-  __syncthreads();
+  const bool falls = __syncthreads_or(down);   // the same in every CTA
+  if (falls) drop_overlaps(s_cu, s_have, s_rel, s_grow, B, cta == 0 ? p.ctl.status : nullptr);
   const int2 total = scan2(s_rel, s_grow, B, part);
   const int avail = min(fc + total.x, p.num_blocks);
   if (cta == 0 && tid == 0 && (fc != fc_read || fc + (long long)total.x > p.num_blocks))
@@ -202,6 +234,20 @@ block_plan_kernel(const PlanParams p) {
     *p.free_count = avail - (lo < B ? s_grow[lo] : total.y);
   }
   if (p.T == 0) return;
+  if (falls) {   // no order to search in: a warp goes through a sequence's rows
+    for (int t = first; t < p.T; t += per) p.slots[t] = -1;
+    ptx::cluster_sync();
+    for (int b = first >> 5; b < B; b += per >> 5) {
+      const int have = s_have[b], n = have < 0 ? 0 : need_of(b) - have;
+      if (have < 0 || (n > 0 && (long long)s_grow[b] + n > avail)) continue;
+      for (int t = s_cu[b] + (tid & 31); t < s_cu[b + 1]; t += 32) {
+        const int pos = s_len[b] + t - s_cu[b];
+        const int blk = __ldcg(p.tables + (long long)b * p.max_blocks + (pos >> bs_log2));
+        p.slots[t] = (blk << bs_log2) + (pos & (bs - 1));
+      }
+    }
+    return;
+  }
   ptx::cluster_sync();
   // Slots, kUnroll tokens a thread at a time: their table reads are in flight together.
   for (int t0 = first; t0 < p.T; t0 += kUnroll * per) {

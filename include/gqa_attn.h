@@ -449,8 +449,9 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  *   kv_lens_out: int32 [B]: kv_lens[b] + r_b, what gqa_kv8_decode takes after the append
  *     (kv_lens[b] when b was not served).  May be kv_lens itself.
  * A sequence that breaks the bounds (a negative length or count, more than max_blocks
- * blocks, cu_rows that fall or pass T) is not served and keeps its blocks, and
- * GQA_ERR_DEVICE_RANGE is recorded.  B <= 8192, T < 2^30 and B * max_blocks < 2^30
+ * blocks, cu_rows that fall or pass T), or one whose rows start before the end of an earlier
+ * sequence that keeps them, is not served and keeps its blocks, and GQA_ERR_DEVICE_RANGE is
+ * recorded.  B <= 8192, T < 2^30 and B * max_blocks < 2^30
  * (GQA_ERR_UNSUPPORTED above).
  */
 int gqa_block_plan(const int* kv_lens, const int* cu_rows, int* block_tables, int* n_blocks,
