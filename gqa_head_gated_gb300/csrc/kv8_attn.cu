@@ -16,8 +16,8 @@
 //   q = 2^e (t0 + t1 / 16 (+ t2 / 256)): 2 terms hold a bf16's 8 bits, 3 an fp16's 11
 //     (each step of 16 is the 4 bits that e4m3 rounds to; elements below 2^-18 of the
 //     row's largest lose bits, an absolute error of 2^-23 of that, 2^-27 in fp16);
-//   p = t0 + t1 / 32 + t2 / 1024, p <= 256: relative error 2^-12, and what is dropped is
-//     below 2^-20, 2^-25 of the row's largest p.
+//   p = t0 + t1 / 32 + t2 / 1024, p <= 256: relative error 2^-13, and what is dropped is
+//     below 2^-20, 2^-25 of the row's largest p when its reference has just moved.
 //
 // The softmax thread of key j holds S^T's lane j: its block's scales are two scalars of
 // the thread, the visible-key test is one comparison per row, and block sizes cost
@@ -26,6 +26,13 @@
 // large ones loses no bits), l uses ml_r, for s.  They move only when a key passes them
 // by more than 2^8 (2^64), which one barrier per tile detects; then the warps exchange
 // maxima and O is rescaled in tensor memory.
+// What a key loses below 2^-25 of the largest p adds up over the keys that a piece has: to 2^-12
+// over 64 tiles.  In a longer piece ref_r goes down again where the keys stay far below it, so that
+// 131071 keys of which each weighs e^-18 of one other come out as they should (they were lost or
+// doubled: 2^-26).  40 sequences of 65536 keys whose scores have a deviation of 8 nats in one key
+// of a hundred: 769 us with it, 781 without, for one row; 974 and 818 for four, whose references
+// such keys keep moving both ways; shares of 64 tiles and less are as they were but for a
+// register (8 x 4 draft rows 75.1 us, 74.2 before).
 //
 // Roles (64 + 128 threads for 8 rows: 320, 448 or 576): warp 0 copies (TMA, a block per box; scales by
 // cp.async), warp 1 issues the products, the others are the softmax and epilogue, a group of
@@ -55,6 +62,12 @@ constexpr int kGroupThreads = 128;               // one thread per key of a tile
 constexpr int kPTerms = 3;
 constexpr float kSlack = 8.f;      // p <= 2^8
 constexpr float kTop = 5.f;        // a moved reference leaves the row's largest p at 2^5
+// One that has come to stand too high goes down again, to where a tile's largest p is 1: when that
+// was below 2^kFall, and above 2^-kDrop of the highest reference: of keys below, 2^-31 of the row's
+// largest p, a million weigh 2^-11 of it.  (It keeps O finite, too.)  Looked at in a piece's second
+// tile and every 32nd from there, and in the one behind a rise of 2^kJump past all before.
+constexpr float kFall = -8.f, kDrop = 26.f, kJump = 8.f;
+constexpr int kLook = 32;
 template <int MB, bool kF16>
 struct Cfg {
   static constexpr int kQTerms = kF16 ? 3 : 2;
@@ -403,6 +416,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ml[r] = kNone;
         l[r] = 0.f;
       }
+      float peak = kNone;   // lanes 2 r, 2 r + 1: the highest that ref[r] was
+      bool look = false;    // the next tile's maxima are wanted (the same in all threads)
       for (int j = 0; j < n_tiles; ++j, ++J) {
         const uint32_t buf = J & 1u;
         const int key = k_lo + j * kTile + key_in;
@@ -461,7 +476,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               md = fmaxf(md, d[r]);
               me = fmaxf(me, s[r] - ml[r]);
             }
-            need = md > kSlack || me > kLSlack;
+            need = md > kSlack || me > kLSlack ||
+                   (n_tiles > kLongPiece && (look || (j & (kLook - 1)) == 1));
           }
           // ---- does a reference have to move (or has a wait run out)?
           bool moved = false;
@@ -498,6 +514,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               l[r] *= up_l ? ex2(ml[r] - mc) : 1.f;
               ml[r] = up_l ? mc : ml[r];
               d[r] = (s[r] - ref[r]) + lv;
+            }
+            if (n_tiles > kLongPiece) {
+              look = false;
+#pragma unroll
+              for (int r = 0; r < kR; ++r) {
+                const float ma = __shfl_sync(0xffffffffu, top, 2 * r);
+                const float pk = __shfl_sync(0xffffffffu, peak, 2 * r);
+                look = look || ref[r] > pk + kJump;
+                if (ma < ref[r] + kFall && ma > pk - kDrop) {
+                  alpha[r] = ex2(ref[r] - ma);
+                  ref[r] = ma;
+                  d[r] = (s[r] - ref[r]) + lv;
+                  move = true;
+                }
+                if ((lane >> 1) == r) peak = fmaxf(pk, ref[r]);
+              }
             }
             moved = move && j > 0;   // the same in all threads: references and maxima are
           }

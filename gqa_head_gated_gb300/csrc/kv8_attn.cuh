@@ -38,6 +38,7 @@ constexpr int kMaxTileBlocks = kTile / 16;
 // would do; a power of two keeps the remainder cheap (tree verify 195 us with 3, 172 with 4).
 constexpr uint32_t kRowSets = 4;
 constexpr float kLSlack = 64.f;    // l's terms stay below 2^64
+constexpr int kLongPiece = 64;     // tiles from which on p's references may go down again
 constexpr float kNone = -3.0e38f;  // reference of a row that has seen no key
 
 // A run of key tiles of one segment that one CTA takes.

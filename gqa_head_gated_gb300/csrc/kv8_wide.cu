@@ -10,8 +10,11 @@
 // accumulator, with no scale between them: what a row's elements lose is below 2^-19 of its
 // largest.  P is e5m2 terms, again in one accumulator: e5m2 has 3 bits a term but the range of
 // fp16, so that p <= 2^15 splits into three (four) terms with a relative error of 2^-9 (2^-12),
-// a bf16 (fp16) P's own, and an absolute one of 2^-17: 2^-24 of the row's largest when its
-// reference has just moved (to 2^7) and less after.  One accumulator for all terms is what
+// a bf16 (fp16) P's own, and an absolute one of 2^-17: 2^-26 of the row's largest when its
+// reference has just moved (to 2^9; 2^7 and 2^8 are as fast) and less after.  In pieces of more than
+// 64 tiles the reference goes down again where the keys stay far below it, as in kv8_attn.cu (40
+// trees of 16 rows x 6 heads over 65536 keys, one in a hundred with 8 times the score: 1,205 us,
+// 1,128 without).  One accumulator for all terms is what
 // leaves room for 128 rows: with e4m3 terms a column or lane each, as the kernel for few rows
 // has them, O alone would take three times 256 columns.
 //
@@ -26,7 +29,7 @@
 // stores their terms over them.  S of tile J + 2 is issued behind P.V of tile J, whose P it
 // overwrites.  The references pass from tile to tile through shared memory (ref_full), and a
 // row's l is kept apart in the four warps that share it.  Measured, 8 trees of 1 to 32 rows x 8
-// heads, keys 4 K to 64 K: 145 us (548 MB, 4 TB/s at 128-row blocks); all 16 warps on one
+// heads, keys 4 K to 64 K: 148 us (548 MB, 4 TB/s at 128-row blocks); all 16 warps on one
 // tile at a time, 32 keys each, 163 us; terms by conversion instructions, not by masks, took
 // a tile 5,300 cycles for 4,200.  With a limit of 96 registers a thread, code that makes
 // values live across a call (a rescale out of line) costs 30 us in spills.
@@ -65,7 +68,12 @@ struct WideCfg {
 };
 constexpr uint32_t kTmWideO = 0, kTmWideS = 256;   // two buffers of 128 columns for S and P
 constexpr float kWideCap = 15.f;       // p <= 2^15
-constexpr float kWideTop = 7.f;        // a moved reference leaves the row's largest p at 2^7
+constexpr float kWideTop = 9.f;        // a moved reference leaves the row's largest p at 2^9
+// One that has come to stand too high goes down again, to where a tile's largest p is 2^kWideLow: when
+// that was below 2^kWideFall and above 2^-kWideDrop of the highest reference (2^-31 of the row's
+// largest p, as in kv8_attn.cu), in a piece's second tile and every 16th from there.
+constexpr float kWideFall = -6.f, kWideDrop = 22.f, kWideLow = 5.f;
+constexpr int kWideLook = 16;
 constexpr uint32_t kIdescS = ptx::idesc_f32acc(128, 128, 0, 0, 0);
 // A e5m2 (format 1), B e4m3 (format 0), B MN-major
 constexpr uint32_t kIdescO = ptx::idesc_f32acc(128, 256, 0, 1, 0) | (1u << 7);
@@ -75,6 +83,7 @@ struct __align__(1024) WideSmem : RingSmem<WideCfg<kF16>::kKS, WideCfg<kF16>::kV
   alignas(1024) uint8_t q[WideCfg<kF16>::kQTerms][2][kRows * 128];   // [term][half of D][row][128 bytes, swizzled]
   float2 red[kTeams][kHalves][kRows];      // by row: maxima with vs, without
   float2 refs[2][kRows];                   // [tile parity][row]: the references after the tile
+  float peak[kRows];                       // and the highest that p's was
   float sum[kShare][kRows];                // [share][row]
   // by tile parity: scores done; terms stored; by quadrant, references published and read
   uint64_t s_full[2], p_full[2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
@@ -488,14 +497,21 @@ kv8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         const bool up = mp > at.x + kWideCap, up_l = ms > at.y + kLSlack;
         ref = up ? mp - kWideTop : at.x;
+        if (n_tiles > kLongPiece) {
+          if ((j & (kWideLook - 1)) == 1 && mp < at.x + kWideFall &&
+              mp > sm.peak[r] - kWideDrop)
+            ref = mp - kWideLow;
+          // (a row that falls here does not rise: its peak is not read in this tile)
+          if (half == 0 && (j == 0 || up)) sm.peak[r] = j == 0 ? ref : fmaxf(sm.peak[r], ref);
+        }
         if (up_l) at.y = ms;
         if (half == 0) sm.refs[buf][r] = make_float2(ref, at.y);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.ref_full[buf][qd]);
         l *= ex2(ml - at.y);
         ml = at.y;
-        const bool moved = j > 0 && __any_sync(0xffffffffu, up);
-        const float alpha = up ? ex2(at.x - ref) : 1.f;
+        const bool moved = j > 0 && __any_sync(0xffffffffu, ref != at.x);
+        const float alpha = ex2(at.x - ref);
         // ---- V rows that some row does not see
         if (part) {
           ok = ok && wait(&sm.v_full[J % C::kVS], (J / C::kVS) & 1u, tmo, &sm.abort);

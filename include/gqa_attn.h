@@ -508,6 +508,11 @@ int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
  * GQA_ERR_DEVICE_RANGE is recorded.  A NaN in the row of a key that a row does not see
  * (a stale row of a block included) never changes its output; a NaN that it sees
  * propagates.  A Q row that holds NaN or +-Inf gives NaN.
+ * A key's probability enters the product with V in 8-bit terms: off by 2^-13 of itself (more
+ * than 32 packed rows - new rows x Hq / Hkv -: by half a step of the type, bf16 2^-8, fp16
+ * 2^-11) and by 2^-25 of the largest beside it.  Over a stretch of 8192 keys that is 2^-12 of
+ * V's largest at most; over longer ones the terms follow the keys as long as those are above
+ * 2^-31 of the largest (a million of such weigh 2^-11 of it).
  * workspace: gqa_kv8_workspace_size() bytes, 16-byte aligned; calls that may overlap on the
  * GPU need one each.  Scores are fp32: q . k * scale / 16 has to stay in its range.
  * max_kv_len < 2^30 and, for 128-key tiles, Hkv * row blocks * tiles of a sequence < 2^31
