@@ -9,8 +9,8 @@
 // Q is e4m3 terms (two for a bf16's 8 bits, three for an fp16's 11) that add up in one
 // accumulator, with no scale between them: what a row's elements lose is below 2^-19 of its
 // largest.  P is e5m2 terms, again in one accumulator: e5m2 has 3 bits a term but the range of
-// fp16, so that p <= 2^15 splits into three (four) terms with a relative error of 2^-9 (2^-12),
-// a bf16 (fp16) P's own, and an absolute one of 2^-17: 2^-26 of the row's largest when its
+// fp16, so that p <= 2^15 splits into three (four) terms with a relative error of 2^-8.8 (2^-11)
+// at most, a bf16 (fp16) P's own, and an absolute one of 2^-17: 2^-26 of the row's largest when its
 // reference has just moved (to 2^9; 2^7 and 2^8 are as fast) and less after.  In pieces of more than
 // 64 tiles the reference goes down again where the keys stay far below it, as in kv8_attn.cu (40
 // trees of 16 rows x 6 heads over 65536 keys, one in a hundred with 8 times the score: 1,205 us,
@@ -108,17 +108,20 @@ __device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint
 }
 
 // Four probabilities as e5m2 terms, a word of four bytes per term.  They go as
-// fp16 (a rounding of 2^-12), whose remainders are exact.  An e5m2 number is the upper byte of
-// the fp16 of the same value, so rounding to it (half away from zero; the sums stay below
-// 2^16) is an integer add and a mask, for two values at once: the conversion instructions
-// made the terms of a tile take 1,700 cycles.  (A NaN loses its bits here; the row's sum, in
-// fp32, keeps it.)
+// fp16 (a rounding of 2^-11 at most), whose remainders are exact.  An e5m2 number is the upper
+// byte of the fp16 of the same value, so rounding to it is an integer add and a mask, for two
+// values at once (the sums stay below 2^16): the conversion instructions made the terms of a
+// tile take 1,700 cycles.  The last of a bf16's three terms has two bits to round, so that one
+// value in four lies half way: even keys go down there and odd ones up, which leaves a mean of
+// 4e-7 (all up: 1.6e-4 too much of V, beside an exact sum of the weights).  Four terms for bf16
+// too took the draft trees 167 us for 148.  (A NaN loses its bits
+// here; the row's sum, in fp32, keeps it.)
 template <int kPTerms>
 __device__ __forceinline__ void p_terms5(float2 lo, float2 hi, uint32_t (&w)[kPTerms]) {
   __half2 a = __floats2half2_rn(lo.x, lo.y), b = __floats2half2_rn(hi.x, hi.y);
 #pragma unroll
   for (int i = 0; i < kPTerms; ++i) {
-    const uint32_t up = i + 1 < kPTerms ? 0u : 0x00800080u;
+    const uint32_t up = i + 1 < kPTerms ? 0u : 0x0080007Fu;
     const uint32_t ta = (*reinterpret_cast<const uint32_t*>(&a) + up) & 0xFF00FF00u;
     const uint32_t tb = (*reinterpret_cast<const uint32_t*>(&b) + up) & 0xFF00FF00u;
     w[i] = __byte_perm(ta, tb, 0x7531);
