@@ -95,7 +95,8 @@ inline cudaError_t allow_smem_once(std::atomic<unsigned long long>& done, const 
 
 // Launches a kernel as a programmatic dependent of the stream's last one: it may be scheduled
 // while that one drains.  The kernel executes griddepcontrol.wait in every thread before it
-// touches global memory, so that stream order holds.
+// touches global memory, so that stream order holds.  (One reads inputs of its call before: the
+// merge of kv8_decode.cu, which the split kernel before it lets start only behind its own wait.)
 template <typename... P, typename... A>
 inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int block, size_t smem,
                                     cudaStream_t stream, int cluster, const A&... args) {

@@ -115,15 +115,18 @@ struct WindowRuns {
   int next[kWindow];
   int end[kWindow];          // by run (its first token): the token behind its last
   int state[kWindow];
-  int found, len;            // of the block that is followed
+  uint32_t followed[kWindow / 32];   // runs whose blocks' later ones are taken here
+  int found, len;                    // of such a block
   int n_asks;
   Ask ask[2 * kFew];
 };
 
 // All threads: is any token in one of the few ranges in the block asked for?  A load and one
 // instruction a token, where look_around() takes about ten: 12 prompt chunks of 2731 rows, whose
-// 24 ends each go through 32,772 slots, 23.7 us so and 35.3 by look_around() alone; 8 loads
-// together 24.8, 24 (spills) 27.1.
+// 24 ends each go through 32,772 slots, 23.7 us so and 28.7 by look_around() alone; 8 loads
+// together 24.8, 24 (spills) 27.1.  (256 sequences of 128 rows 66.7, and 50.3 when nobody looked; 128
+// of 32 rows, by look_around(), 17.5 and 13.4.  With the CTAs of a window as a cluster that shares
+// its tokens, the same three: 23.9, 72.9, 17.5, and a prompt of 8192 rows 12.3 for 12.0.)
 __device__ __noinline__ bool any_in_block(const int* slots, unsigned bs, const WindowRuns& w) {
   unsigned m = ~0u;
   for (int a = 0; a < w.n_asks; ++a) {
@@ -346,12 +349,23 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const __grid_co
   }
   const int n_other = __syncthreads_count(other);
   bool looked = n_other > 0;   // the same in all threads, as all of what follows
+  if (looked) {
+    // the rows' loads (32 lines a warp) wait behind this: they are on their way to L2 meanwhile
+    const int i = i0 + warp + (lane >> 2) * kWarps;
+    if (i < n_span)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (size_t(w0 + i) * p.Hkv + g) * 32 + (lane & 3) * 8));
+  }
   if (looked && n_other <= kFew) looked = any_in_block(p.slots, unsigned(bs), s_runs);
   if (looked) {
     look_around(p.slots, p.T, w0, unsigned(n_slots), p.bs_log2, s_slot, other, s_runs);
     if (starts_run && (s_runs.state[tid] & kRepeats) && g == 0 && kv == 0)
       record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
     if (tid < n_span && s_run[tid] >= 0 && (s_runs.state[s_run[tid]] & kContinues)) s_run[tid] = -1;
+    if (tid < kWindow) {
+      const uint32_t m = __ballot_sync(
+          0xffffffffu, starts_run && (s_runs.state[tid] & (kContinues | kFollowed)) == kFollowed);
+      if (lane == 0) s_runs.followed[warp] = m;
+    }
     __syncthreads();
   }
   const auto run_of = [&](int i) -> int { return i < n_span ? s_run[i] : -1; };
@@ -430,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const __grid_co
     rescale_rows(pool + size_t(s_row[r] - n) * 32, n, s_old[r], s_inv[r]);
   }
   if (!looked) return;
-  for (int f = 0; f < kWindow; ++f) {
-    if (!((starts >> f) & 1ull) || (s_runs.state[f] & (kContinues | kFollowed)) != kFollowed) continue;
+  for (uint64_t left = (uint64_t(s_runs.followed[1]) << 32) | s_runs.followed[0]; left != 0ull;
+       left &= left - 1ull) {
+    const int f = __ffsll(static_cast<long long>(left)) - 1;
     __syncthreads();   // the run's rows, those before them and its scale are written
     follow_block<kF16>(p, x, pool, kv == 0 ? p.scale[0] : p.scale[1],
                        s_slot[s_runs.end[f]], w0 + s_runs.end[f], g, g == 0 && kv == 0, s_runs);
