@@ -19,7 +19,7 @@
 // ends of a sequence did not look for other rows of their block).  With 4 CTAs
 // of 256 threads an SM each warp holds 8 rows between the maximum and the rounding; 5 and 6 CTAs
 // spill (16.3, 19.0 us where 4 took 13.0), 512 threads with 4 rows a warp took 14.0.  A step's call, 16 rows, is
-// bound by latency: 3.3 us on the GPU (a chain of reads: slot, scale, row, and a launch).
+// bound by latency: 3.6 us on the GPU (a chain of reads: slot, scale, row, and a launch).
 // keep of 128 sequences' drafts takes 7.1 us on the GPU for 8.4 MB, again such a chain: list,
 // table, rows, and the block's rows once more where a scale grew.
 #include <cuda_runtime.h>
@@ -345,6 +345,14 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const __grid_co
       other = true;
       const int a = atomicAdd(&s_runs.n_asks, 1);
       if (a < 2 * kFew) s_runs.ask[a] = Ask{w0 + end, p.T, unsigned(block)};
+    }
+  }
+  if (p.T <= 32 && warp == 0) {   // a small step: the lanes have all of its tokens
+    const int s = s_slot[lane + 1];
+    const uint32_t same = __match_any_sync(0xffffffffu, s >= 0 && s < n_slots ? s >> p.bs_log2 : -1 - lane);
+    if (other) {
+      const int end = s_runs.end[lane];
+      other = ((same & ((1u << lane) - 1u)) | (end < 32 ? same >> end : 0u)) != 0u;
     }
   }
   const int n_other = __syncthreads_count(other);
