@@ -391,7 +391,8 @@ def block_plan(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, 
     Sequence b holds kv_lens[b] keys and gets cu_rows[b+1] - cu_rows[b] new rows; after the
     call it owns exactly the blocks that they need.  int32 CUDA tensors, updated in place:
     block_tables [B, max_blocks], n_blocks [B], free_list [num_blocks] and free_count [1] (a
-    stack).  Surplus blocks go back first (length 0 and no rows: a finished request), then
+    stack).  No block is in two tables or in a table and the stack: blocks that sequences share
+    have no owner here.  Surplus blocks go back first (length 0 and no rows: a finished request), then
     growing sequences take theirs in order.  T: rows in the batch, cu_rows[B] or more.
     Returns (slots int32 [T], kv_lens_out int32 [B]): the place of each new row (block *
     block_size + row; -1 without one) for kv8_append, and the lengths with the new rows for

@@ -25,7 +25,8 @@ constexpr int kPieceRing = 8;      // pieces whose descriptions are held: see th
 // What going on to another segment costs a CTA, in tiles (its end and start, and the first
 // tiles, whose references still move), where shares have kLongShare tiles or more (with short
 // ones it would only unsettle them: one tile each is best then).  Swept over 1, 3, 5, 7, 9 and
-// 12: 16 x 32768 decode (16 rows) 92.2, 89.4, 89.9, 90.7, 90.3, 90.3 us; over 3, 6, 9 and 12:
+// 12: 16 x 32768 decode (16 rows) 92.2, 89.4, 89.9, 90.7, 90.3, 90.3 us, and over 3, 4 and 5: 88.3,
+// 88.6, 88.8 (2 x 131071: 52.8 with each); over 3, 6, 9 and 12:
 // chain verify (24 rows) 78.6, 75.5, 74.0, 74.8; over 3, 5 and 8: tree verify (128 rows) 149.8,
 // 147.8, 149.4.
 template <int MB>

@@ -426,7 +426,8 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  * block_tables: int32 [B, max_blocks]: entry i of sequence b is the pool block that holds
  *   its keys i*block_size .. (i+1)*block_size - 1.  No block belongs to two sequences that
  *   one call writes: its contents are unspecified after such a call (no access is out of
- *   range).  A block that is only read may be shared.
+ *   range).  A block that is only read may be shared by the tables that gqa_kv8_decode reads;
+ *   gqa_block_plan does not count owners, so its tables share none.
  * The calls are launched as programmatic dependents of what is before them on the stream, and
  * keep stream order.
  * num_blocks * Hkv * block_size < 2^31 and max_blocks * block_size < 2^31
@@ -434,8 +435,10 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  *
  * gqa_block_plan: block tables and slot maps from request lengths, on the device.  After it
  * sequence b owns exactly ceil((kv_lens[b] + r_b) / block_size) blocks, r_b = cu_rows[b+1] -
- * cu_rows[b] new rows: a finished request is one with length 0 and no rows, refused drafts
- * are given back by the next call with the shorter length.
+ * cu_rows[b] new rows, and no other sequence or the free list has them: a block that is in two
+ * tables (a shared prompt) would be released twice and handed to two sequences.  A finished
+ * request is one with length 0 and no rows, refused drafts are given back by the next call
+ * with the shorter length.
  *   n_blocks: int32 [B], blocks that b owns (block_tables[b, 0 .. n_blocks[b])); updated.
  *   free_list: int32 [num_blocks], free_count: int32 [1]: a stack of free blocks, its top
  *     at free_list[free_count - 1]; updated.
@@ -503,7 +506,9 @@ int gqa_kv8_keep(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
  * max_rows (at most 64 with tree_mask) and max_kv_len bound r_b and kv_lens[b].
  * T may exceed cu_rows[B] (a padded batch): rows behind the last sequence, and those of a
  * sequence that breaks the bounds (skipped, GQA_ERR_DEVICE_RANGE recorded), are left as
- * they were in out and lse_out.  A row that sees no key gives zeros, lse -inf.
+ * they were in out and lse_out.  Where cu_rows falls, which records it too, so may rows of the
+ * sequences on either side be, and rows that two sequences claim are unspecified.  A row that
+ * sees no key gives zeros, lse -inf.
  * A table entry outside the pool reads as keys and values of zero, and
  * GQA_ERR_DEVICE_RANGE is recorded.  A NaN in the row of a key that a row does not see
  * (a stale row of a block included) never changes its output; a NaN that it sees
