@@ -42,9 +42,9 @@
 //
 // Measured (HBM copies run at 6.78 TB/s): 16 sequences of 32768 keys, 4 rows of a group, 89 us
 // for 555 MB (92 %); 2 of 131071 keys in fp16, 53 us for 268 MB (75 %: a launch, a start and a
-// merge are 13 us of it); 8 x 4 draft rows, 24 packed, 74 us for 303 MB (60 %), where
-// tiles whose references move (1,500 clocks more, by a barrier and the rescale) hold the copies up.  kTop 5, 3 and 1 are as fast; 5 keeps more of the
-// small probabilities.
+// merge are 13 us of it); 8 x 4 draft rows, 24 packed, 75 us for 303 MB (60 %), where tiles
+// whose references move (1,500 clocks more, by a barrier and the rescale) hold the copies up.
+// kTop 5, 3 and 1 are as fast; 5 keeps more of the small probabilities.
 //
 // A key that a row does not see has p = 0 by selection.  V rows past the last visible key
 // of a tile are zeroed in shared memory, and NaN codes of keys that only some rows see are

@@ -13,8 +13,8 @@
 // behind the first len - r keys.
 //
 // An append of a prompt should be bound by HBM (2 bytes read and 1 written a value) and is by
-// issue slots and latency: 91 instructions a row of 256 values and warp, of which the conversions
-// are a third, at 51 % of the slots.  8192 rows of 4 heads, K and V: 12.0 us for 50 MB (62 % of the
+// issue slots and latency: 100 instructions a row of 256 values and warp, of which the conversions
+// are a third, at 55 % of the slots.  8192 rows of 4 heads, K and V: 12.0 us for 50 MB (62 % of the
 // copy rate; floor 7.4), 12 chunks of 2731 rows of 2 heads 23.7 for 101 MB (63 %; 20.5 when the
 // ends of a sequence did not look for other rows of their block).  With 4 CTAs
 // of 256 threads an SM each warp holds 8 rows between the maximum and the rounding; 5 and 6 CTAs

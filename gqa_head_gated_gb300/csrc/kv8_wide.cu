@@ -14,8 +14,8 @@
 // reference has just moved (to 2^9; 2^7 and 2^8 are as fast) and less after.  In pieces of more than
 // 64 tiles the reference goes down again where the keys stay far below it, as in kv8_attn.cu (40
 // trees of 16 rows x 6 heads over 65536 keys, one in a hundred with 8 times the score: 1,205 us,
-// 1,128 without).  One accumulator for all terms is what
-// leaves room for 128 rows: with e4m3 terms a column or lane each, as the kernel for few rows
+// 1,128 without).  One accumulator for all terms is what leaves
+// room for 128 rows: with e4m3 terms a column or lane each, as the kernel for few rows
 // has them, O alone would take three times 256 columns.
 //
 // What bounds it: the softmax's latency beside the tensor pipe.  A tile has 2 x 8 products of 64
@@ -29,7 +29,7 @@
 // stores their terms over them.  S of tile J + 2 is issued behind P.V of tile J, whose P it
 // overwrites.  The references pass from tile to tile through shared memory (ref_full), and a
 // row's l is kept apart in the four warps that share it.  Measured, 8 trees of 1 to 32 rows x 8
-// heads, keys 4 K to 64 K: 148 us (548 MB, 4 TB/s at 128-row blocks); all 16 warps on one
+// heads, keys 4 K to 64 K: 150 us (548 MB, 3.7 TB/s at 128-row blocks); all 16 warps on one
 // tile at a time, 32 keys each, 163 us; terms by conversion instructions, not by masks, took
 // a tile 5,300 cycles for 4,200.  With a limit of 96 registers a thread, code that makes
 // values live across a call (a rescale out of line) costs 30 us in spills.
