@@ -129,7 +129,8 @@ struct WindowRuns {
 // its tokens, the same three: 23.9, 72.9, 17.5, and a prompt of 8192 rows 12.3 for 12.0.)
 __device__ __noinline__ bool any_in_block(const int* slots, unsigned bs, const WindowRuns& w) {
   unsigned m = ~0u;
-  for (int a = 0; a < w.n_asks; ++a) {
+  const int n = min(w.n_asks, 2 * kFew);
+  for (int a = 0; a < n; ++a) {
     const Ask q = w.ask[a];
     for (int t = q.lo + int(threadIdx.x); t < q.hi; t += kAsk * kThreads) {
       unsigned s[kAsk];
@@ -363,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_append_kernel(const __grid_co
     if (i < n_span)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (size_t(w0 + i) * p.Hkv + g) * 32 + (lane & 3) * 8));
   }
-  if (looked && n_other <= kFew) looked = any_in_block(p.slots, unsigned(bs), s_runs);
+  // (the list holds what kFew runs ask; a step of 32 tokens has its answer)
+  if (looked && n_other <= kFew && p.T > 32) looked = any_in_block(p.slots, unsigned(bs), s_runs);
   if (looked) {
     look_around(p.slots, p.T, w0, unsigned(n_slots), p.bs_log2, s_slot, other, s_runs);
     if (starts_run && (s_runs.state[tid] & kRepeats) && g == 0 && kv == 0)

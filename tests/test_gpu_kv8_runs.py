@@ -58,6 +58,18 @@ def test_sequences_whose_tokens_alternate(B, n, bs, dtype):
     assert _append(c, x, y, slots) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("B", [2, 5, 11, 20, 30])
+def test_a_small_step_of_many_sequences(B, dtype):
+    """A row each of up to 30 sequences, and behind them another of one or two."""
+    c = Cache([5 + b for b in range(B)], 2, 64, seed=145, room=8)
+    slots = [_slots(c, b, 5 + b, 1)[0] for b in range(B)]
+    for again in ([0], [B - 2], [B // 2, 0]):
+        more = slots + [_slots(c, b, 6 + b, 1)[0] for b in again]
+        x, y = _spread(len(more), 2, 146, dtype, big=[len(more) - 1])
+        assert _append(c, x, y, more) == 0
+
+
 def test_every_third_row_skipped_and_far_apart():
     """A sequence with a third of its rows left out, and a block whose second run lies thousands of
     tokens behind its first."""
