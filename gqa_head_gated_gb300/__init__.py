@@ -20,7 +20,8 @@ from ._lib import GqaError, check, load  # noqa: F401
 HEAD_DIM = 256
 
 __all__ = ["prefill", "prefill_pair", "masked", "decode", "verify_tree", "kv_append", "kv_keep", "block_plan",
-           "kv8_append", "kv8_keep", "kv8_decode", "kv8_workspace_size", "decode_plan", "decode_split", "lse_merge",
+           "kv8_append", "kv8_keep", "kv8_decode", "kv8_workspace_size", "kv8_prefill",
+           "kv8_prefill_workspace_size", "decode_plan", "decode_split", "lse_merge",
            "decode_workspace_size", "last_device_status", "set_wait_timeout_ns",
            "selftest_wait_timeout", "decode_noalloc", "launch_log", "GqaError",
            "load"]
@@ -486,6 +487,49 @@ def kv8_decode(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu
           _at(kv_lens, _I32, (B,), d, "kv_lens"),
           None if cu_rows is None else _at(cu_rows, _I32, (B + 1,), d, "cu_rows"),
           None if tree_mask is None else _at(tree_mask, torch.int64, (T,), d, "tree_mask"),
+          _at(out, dt, shape, d, "out"), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, N,
+          bs, max_blocks, int(max_rows), int(max_kv_len), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return (out, lse) if return_lse else out
+
+
+def kv8_prefill_workspace_size():
+    """Bytes of workspace that kv8_prefill() needs, whatever the sizes (on the current device)."""
+    return int(load().gqa_kv8_prefill_workspace_size())
+
+
+def kv8_prefill(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu_rows,
+                max_rows=None, max_kv_len=None, workspace=None, out=None, return_lse=False):
+    """Prompt chunks over the paged 8-bit cache: kv8_decode() for many new rows a sequence, without
+    a tree.  New row i of sequence b sees the keys before the chunk and the chunk's first i + 1, which
+    kv8_append() has put into the cache.  q, g: [T,Hq,256] bf16 or fp16; kv_lens int32 [B] counts the
+    new rows; cu_rows int32 [B+1].  workspace: kv8_prefill_workspace_size() bytes (about 40 MB).
+    Returns out [T,Hq,256]; rows behind cu_rows[B] are left as they were in a given out."""
+    sfx = _elem(q, "q")
+    d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError(f"q must be [T, Hq, {HEAD_DIM}], got {tuple(q.shape)}")
+    T, Hq, _ = shape = q.shape
+    _cuda_index(kv_lens, "kv_lens")
+    B = kv_lens.numel()
+    tables, max_blocks = _tables(block_tables, B, d)
+    if max_kv_len is None:           # synchronises; pass it to avoid the copy
+        max_kv_len = max(1, int(kv_lens.max().item()))
+    if max_rows is None:
+        max_rows = max(1, int((cu_rows[1:] - cu_rows[:-1]).max().item()))
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:    # (a given workspace is checked by the library itself)
+        with torch.cuda.device(d):
+            need = kv8_prefill_workspace_size()
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{d}")
+    lse = torch.empty((T, Hq), dtype=_F32, device=q.device) if return_lse else None
+    dt = q.dtype
+    _call("gqa_kv8_prefill" + sfx, d, _at(q, dt, shape, d, "q"), *pools,
+          None if g is None else _at(g, dt, shape, d, "g"), tables,
+          _at(kv_lens, _I32, (B,), d, "kv_lens"), _at(cu_rows, _I32, (B + 1,), d, "cu_rows"),
           _at(out, dt, shape, d, "out"), None if lse is None else lse.data_ptr(), B, T, Hq, Hkv, N,
           bs, max_blocks, int(max_rows), int(max_kv_len), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())

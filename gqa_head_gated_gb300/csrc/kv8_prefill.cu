@@ -1,0 +1,1080 @@
+// Attention of prompt chunks over the paged 8-bit cache, on CTA pairs (tcgen05 .cta_group::2):
+//
+//   out[t] = softmax_j(q[t] . K[j] / 16, j <= base + i) V * sigmoid(g[t]),   K[j] = k_pool row * scale
+//
+// for every new row i of every sequence (base = kv_len - rows).  A segment is 256 packed rows (query
+// heads of a KV group x new rows, heads innermost) of one sequence; each CTA of a pair has 128 of
+// them, and the two share each tile of 128 keys: CTA r brings keys 64 r .. of K and dims 128 r .. of V.
+//
+// The products are 16-bit ones.  An e4m3 number is an fp16 number, so K and V enter as they are
+// stored and their scales stay apart: K's goes into the scores (fp32, per run of 16 keys), V's into the
+// exponent of the probability, p = 2^(score + log2 vs - ref).  Q goes as fp16 times a power of two
+// per row: exact for what lies within 2^-23 of the row's largest element, off by 2^-33 of that below.
+// p goes as fp16: off by 2^-11 of itself, and by 2^-25 where the row's largest is 2^9 at least (a
+// reference moves when p would pass 2^15, and then leaves the largest at 2^9).  The row's sum l is taken
+// from the fp32 probabilities against a reference of its own, without the V scales.
+//
+// What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (8-bit terms, as the kernels
+// for few rows have them, would take 2560), beside 1024 clocks of ex2.
+//
+// The segments' tiles (only those that some row sees) are laid end to end and cut into equal shares,
+// one a pair.  A piece that is a whole segment goes straight to `out`; the pieces of a segment that is
+// cut leave fp32 parts, two a pair at most, that kv8_join_kernel puts together.
+//
+// Roles (448 threads): warp 0 schedules (pieces, block numbers and scales of the tiles), warp 1 of the even
+// CTA issues the products, warps 2..5 convert K and V into shared memory, warps 6..13 are softmax and
+// epilogue (row = tensor-memory lane, 64 keys a thread).
+// TMEM: O 256 columns, two buffers of 128 for S and P.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kv8_attn.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kPairRows = 256;                  // packed rows of a segment
+constexpr int kConvWarp = 2, kConvWarps = 4;    // first warp of each role
+constexpr int kSoftWarp = kConvWarp + kConvWarps;
+constexpr int kThreadsC = 32 * (kSoftWarp + 8);
+constexpr int kSlotC = 32768;                   // half a tile of K or V in fp16
+constexpr int kGroup = 4;                       // tiles that the scheduler looks up together
+constexpr int kGroups = 4;                      // groups held
+constexpr int kTiles = kGroup * kGroups;
+constexpr int kPieces = 32;                     // more than tiles held, and every piece has one
+constexpr int kHitSets = 4;                     // pieces whose NaN keys are held
+constexpr int kHitWords = kPairRows / 32;       // keys that only some rows of a segment see: < 256
+constexpr uint32_t kLead = 3;                   // what a segment costs beside its tiles, in tiles
+constexpr int kSnap = 4;                        // a cut this close to a segment's end is made there
+constexpr float kCap = 15.f, kTop = 9.f;        // p <= 2^15; a moved reference leaves 2^9
+constexpr uint32_t kTmOc = 0, kTmSc = 256;
+constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);
+constexpr uint32_t kIdescOc = ptx::idesc_f32acc(256, 256, 0, 1, 0);
+
+struct ChunkArgs {
+  const uint4* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const uint16_t* gate;
+  const int* tables;
+  const int* kv_lens;
+  const int* cu_rows;
+  uint16_t* out;
+  float* lse;
+  float* o_parts;      // [2 * pairs][256][256]
+  float* lse_parts;    // [2 * pairs][256]
+  int* cuts;           // [pairs][8]: see the scheduler
+  int B, T, Hkv, Hq, gqa, num_blocks, bs_log2, max_blocks, max_rows, max_kv_len, pairs;
+  LaunchCtl ctl;
+};
+
+// A place in the row of all segments: sequence, KV head, row block, tile.
+struct Cut {
+  int b, g, rb, t;
+};
+
+struct ChunkPiece {
+  int b, g, rb, rows, t0, base;   // base: keys before the new rows
+  int part;                    // -1: a whole segment
+};
+
+struct TileRec {
+  int key0, k_hi, pr_lo;       // first key; keys from k_hi on are not there; from pr_lo on not all rows see
+  int g, n_tiles, piece;       // n_tiles of the piece that starts here; 0: the end of the share
+  int first, last;             // of its piece
+  int blk[8];                  // by run of 16 keys: block, scale of K, log2 of V's
+  float ks[8], lv[8];
+};
+
+struct __align__(1024) ChunkSmem {
+  uint8_t q[4 * 128 * 128];
+  uint8_t k[2][kSlotC], v[2][kSlotC];
+  TileRec rec[kTiles];
+  ChunkPiece piece[kPieces];
+  float2 red[2][2][128];                  // [tile parity][half][row]: maxima with vs, without
+  float sum[2][128];
+  float fac[2][128];                      // by piece parity
+  uint32_t hit[kHitSets][kHitWords];
+  uint64_t rec_full[kGroups], rec_empty[kGroups];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], pv_done, q_full, o_full, o_free, drain;
+  uint64_t hit_full[kHitSets];
+  int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
+  uint32_t cost[kKv8Seqs], at[kKv8Seqs + 1];   // of one KV head; of all, before each sequence
+  uint32_t tmem_base;
+  int abort, zero;
+};
+static_assert(sizeof(ChunkSmem) + 1024 <= 227 * 1024, "one CTA per SM");
+
+// Tiles that some row of row block rb sees.
+__device__ __forceinline__ int tiles_of(const int4& s, int rb, int gqa) {
+  const int rows = min(s.y, ((rb + 1) * kPairRows - 1) / gqa + 1);
+  return (s.z - s.y + rows + kTile - 1) / kTile;
+}
+
+// The cut at position pos of the launch's segments (whole warp): at a segment's end where one is near.
+__device__ Cut cut_at(const ChunkSmem& sm, const ChunkArgs& p, uint32_t pos) {
+  const int lane = threadIdx.x & 31;
+  if (pos >= sm.at[p.B]) return Cut{p.B, 0, 0, 0};
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sm.at[mid] <= pos) lo = mid; else hi = mid - 1;
+  }
+  const int4 s = sm.seq[lo];
+  uint32_t rest = pos - sm.at[lo];
+  Cut c{lo, int(rest / sm.cost[lo]), 0, 0};
+  rest -= uint32_t(c.g) * sm.cost[lo];
+  int n = 0;
+  for (int rb0 = 0;; rb0 += 32) {   // (the last row block's sum is the cost, which rest is below)
+    const uint32_t own = rb0 + lane < s.w ? uint32_t(tiles_of(s, rb0 + lane, p.gqa)) + kLead : 0u;
+    uint32_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    const uint32_t over = __ballot_sync(0xffffffffu, sum > rest);
+    if (over != 0u || rb0 + 32 >= s.w) {
+      const int w = over != 0u ? __ffs(over) - 1 : 31;
+      c.rb = rb0 + w;
+      const uint32_t before = __shfl_sync(0xffffffffu, sum - own, w);
+      n = int(__shfl_sync(0xffffffffu, own, w)) - int(kLead);
+      c.t = int(rest - before) - int(kLead);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (c.t <= kSnap) {
+    c.t = 0;
+  } else if (n - c.t <= kSnap) {
+    c.t = 0;
+    if (++c.rb == s.w) {
+      c.rb = 0;
+      if (++c.g == p.Hkv) {
+        c.g = 0;
+        do ++c.b; while (c.b < p.B && sm.at[c.b + 1] == sm.at[c.b]);   // (sequences without rows)
+      }
+    }
+  }
+  return c;
+}
+
+__device__ __forceinline__ bool before(const Cut& a, const Cut& b) {
+  return a.b != b.b ? a.b < b.b : a.g != b.g ? a.g < b.g : a.rb != b.rb ? a.rb < b.rb : a.t < b.t;
+}
+
+// 16 e4m3 values to fp16.
+__device__ __forceinline__ void to_f16x16(const uint4& u, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n"
+        "  .reg .b16 l, h;\n"
+        "  mov.b32 {l, h}, %2;\n"
+        "  cvt.rn.f16x2.e4m3x2 %0, l;\n"
+        "  cvt.rn.f16x2.e4m3x2 %1, h;\n"
+        "}\n"
+        : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+        : "r"(w[i]));
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ bool wait_rec(ChunkSmem& sm, uint32_t J, uint64_t tmo) {
+  const uint32_t G = J / kGroup;
+  return wait(&sm.rec_full[G % kGroups], (G / kGroups) & 1u, tmo, &sm.abort);
+}
+
+// The dims of 128 from `dim` on in which a hit key that this row sees has a NaN: NaN in the row's output
+// (rare).  part: its fp32 part, else out: its 16-bit output.
+__device__ __noinline__ void put_back(const ChunkArgs& p, const uint32_t* hit, int b, int g, int pr_lo,
+                                      int lim, int dim, float* part, uint16_t* out, uint16_t nan16) {
+  for (int w = 0; w < kHitWords; ++w)
+    for (uint32_t bits = hit[w]; bits != 0u; bits &= bits - 1u) {
+      const int key = pr_lo + 32 * w + __ffs(bits) - 1;
+      if (key >= lim) continue;
+      const int blk = __ldg(p.tables + (long long)b * p.max_blocks + (key >> p.bs_log2));
+      if (blk < 0 || blk >= p.num_blocks) continue;
+      const size_t row = ((size_t(blk) * p.Hkv + g) << p.bs_log2) + (key & ((1 << p.bs_log2) - 1));
+#pragma unroll 1
+      for (int c = dim; c < dim + 128; ++c)
+        if ((p.v_pool[row * 256 + c] & 0x7Fu) == 0x7Fu) {
+          if (part != nullptr) part[c] = __int_as_float(0x7FC00000); else out[c] = nan16;
+        }
+    }
+}
+
+template <bool kF16>
+__global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_constant__ ChunkArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t tmo = p.ctl.timeout_ns;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool lead = rank == 0;
+  const int pair = int(blockIdx.x) >> 1;
+  if (tid == 0) {
+    for (int i = 0; i < kGroups; ++i) {
+      ptx::mbar_init(&sm.rec_full[i], 1);
+      ptx::mbar_init(&sm.rec_empty[i], 12);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.k_full[i], 8);
+      ptx::mbar_init(&sm.v_full[i], 8);
+      ptx::mbar_init(&sm.k_empty[i], 1);
+      ptx::mbar_init(&sm.v_empty[i], 1);
+      ptx::mbar_init(&sm.s_full[i], 1);
+      ptx::mbar_init(&sm.p_full[i], 16);
+    }
+    ptx::mbar_init(&sm.pv_done, 1);
+    ptx::mbar_init(&sm.q_full, 16);
+    ptx::mbar_init(&sm.o_full, 1);
+    ptx::mbar_init(&sm.o_free, 16);
+    ptx::mbar_init(&sm.drain, 1);
+    for (int i = 0; i < kHitSets; ++i) ptx::mbar_init(&sm.hit_full[i], 8);
+    sm.abort = 0;
+    sm.zero = 0;
+    sm.at[0] = 0;
+    ptx::fence_mbar_init();
+  }
+  if (tid < kHitSets * kHitWords) (&sm.hit[0][0])[tid] = 0u;
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&sm.tmem_base, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  wait_for_last();
+  let_next_start();
+  // ---- what each sequence costs
+  for (int b = tid; b < p.B; b += kThreadsC) {
+    const int kv = p.kv_lens[b], t0 = p.cu_rows[b], rows = p.cu_rows[b + 1] - t0;
+    const bool ok = rows >= 0 && rows <= p.max_rows && t0 >= 0 && rows <= p.T - t0 && kv >= rows &&
+                    kv <= p.max_kv_len;
+    const int n_rb = ok ? int(((long long)rows * p.gqa + kPairRows - 1) / kPairRows) : 0;
+    sm.seq[b] = make_int4(t0, rows, kv, n_rb);
+    if (!ok && blockIdx.x == 0) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+  }
+  __syncthreads();
+  for (int b = warp; b < p.B; b += kThreadsC / 32) {
+    const int4 s = sm.seq[b];
+    uint32_t sum = 0;
+    for (int rb = lane; rb < s.w; rb += 32) sum += uint32_t(tiles_of(s, rb, p.gqa)) + kLead;
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) sm.cost[b] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {   // inclusive sums over the sequences, 32 at a time
+    uint32_t run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      uint32_t v = b0 + lane < p.B ? sm.cost[b0 + lane] * uint32_t(p.Hkv) : 0u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (b0 + lane < p.B) sm.at[b0 + lane + 1] = run + v;
+      run += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();   // both CTAs' barriers exist before any arrive reaches them
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const auto lead_bar = [&](uint64_t* bar) { return ptx::mapa_shared(ptx::smem_addr(bar), 0); };
+
+  if (warp < kConvWarp) {
+    if (warp == 0) {
+      // ---------------------------------------------------------- schedule
+      const unsigned long long W = sm.at[p.B];
+      const uint32_t n = uint32_t(min((unsigned long long)p.pairs, W));
+      Cut at{p.B, 0, 0, 0}, end = at;
+      if (uint32_t(pair) < n) {
+        at = cut_at(sm, p, uint32_t(W * pair / n));
+        end = cut_at(sm, p, uint32_t(W * (pair + 1) / n));
+      }
+      // cuts[0..1]: whether this pair's first piece goes on with a segment (1) and ends it (2); the
+      // rest: the segment that its last piece starts and does not end
+      int first_state = 0, starts = 0;
+      ChunkPiece open{0, 0, 0, 0, 0, 0, -1};
+      uint32_t J = 0, n_pieces = 0;
+      bool ok = true, done = false;
+      int4 s = make_int4(0, 0, 0, 0);
+      int t = 0, t_end = 0, pr_lo = 0, k_hi = 0;
+      bool in_piece = false, fresh = false;
+      while (!done) {
+        // this group's tiles: every lane goes through them, and keeps its own
+        TileRec r;
+        r.n_tiles = 0;
+        r.key0 = r.k_hi = r.pr_lo = r.g = r.piece = r.first = r.last = 0;
+        int my_b = 0;
+        const uint32_t G = J / kGroup;
+        if (G >= kGroups) {
+          ok = warp_all(wait(&sm.rec_empty[G % kGroups], (G / kGroups - 1) & 1u, tmo, &sm.abort));
+          if (!ok) break;
+        }
+        for (int q = 0; q < kGroup && !done; ++q) {
+          if (!in_piece) {
+            if (!before(at, end)) {
+              done = true;
+              break;
+            }
+            s = sm.seq[at.b];
+            const int all = tiles_of(s, at.rb, p.gqa);
+            const bool ends = at.b != end.b || at.g != end.g || at.rb != end.rb;
+            t = at.t;
+            t_end = ends ? all : end.t;
+            const int rows_to = min(s.y, ((at.rb + 1) * kPairRows - 1) / p.gqa + 1);
+            k_hi = s.z - s.y + rows_to;
+            pr_lo = s.z - s.y + at.rb * kPairRows / p.gqa + 1;
+            ChunkPiece x{at.b, at.g, at.rb, s.y, s.x, s.z - s.y, -1};
+            if (t != 0) {
+              x.part = 2 * pair;
+              first_state = ends ? 2 : 1;
+            } else if (!ends) {
+              x.part = 2 * pair + 1;
+              starts = 1;
+              open = x;
+            }
+            if (lane == 0) sm.piece[n_pieces % kPieces] = x;
+            in_piece = fresh = true;
+          }
+          if ((lane >> 3) == q) {
+            r.key0 = t * kTile;
+            r.k_hi = k_hi;
+            r.pr_lo = pr_lo;
+            r.g = at.g;
+            r.n_tiles = t_end - t;
+            r.piece = int(n_pieces);
+            r.first = fresh;
+            r.last = t + 1 == t_end;
+            my_b = at.b;
+          }
+          fresh = false;
+          if (++t == t_end) {
+            in_piece = false;
+            ++n_pieces;
+            at.t = 0;
+            if (++at.rb == s.w) {
+              at.rb = 0;
+              if (++at.g == p.Hkv) {
+                at.g = 0;
+                do ++at.b; while (at.b < p.B && sm.seq[at.b].w == 0);
+              }
+            }
+          }
+        }
+        // block and scales of run lane & 7 of this lane's tile
+        TileRec& o = sm.rec[(J + (lane >> 3)) % kTiles];
+        const int u = lane & 7, key = r.key0 + 16 * u;
+        int blk = -1;
+        float ks = 1.f, lv = 0.f;
+        if (r.n_tiles > 0 && key < r.k_hi) {
+          blk = __ldg(p.tables + (long long)my_b * p.max_blocks + (key >> p.bs_log2));
+          if (blk >= 0 && blk < p.num_blocks) {
+            ks = __ldg(p.k_scale + size_t(blk) * p.Hkv + r.g);
+            lv = log2_scale(__ldg(p.v_scale + size_t(blk) * p.Hkv + r.g));
+          } else {
+            blk = -1;   // reads as zeros
+            record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+          }
+        }
+        o.blk[u] = blk;
+        o.ks[u] = ks;
+        o.lv[u] = lv;
+        if (u == 0) {
+          o.key0 = r.key0;
+          o.k_hi = r.k_hi;
+          o.pr_lo = r.pr_lo;
+          o.g = r.g;
+          o.n_tiles = r.n_tiles;
+          o.piece = r.piece;
+          o.first = r.first;
+          o.last = r.last;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.rec_full[G % kGroups]);
+        J += kGroup;
+        if (done) break;
+        // (a group that the share's end fills exactly is followed by one that says so)
+      }
+      if (lane == 0 && lead && pair < p.pairs) {
+        int* const c = p.cuts + 8 * pair;
+        c[0] = first_state;
+        c[1] = starts;
+        c[2] = open.g;
+        c[3] = open.rb;
+        c[4] = open.rows;
+        c[5] = open.t0;
+      }
+      if (!ok && lane == 0) {
+        sm.abort = 1;
+        record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+      }
+    } else if (warp == 1 && lead && lane == 0) {
+      // ---------------------------------------------------------- products
+      const uint64_t qd = ptx::sdesc_sw128(ptx::smem_addr(sm.q), 16, 1024);
+      uint32_t J = 0, pc = 0;
+      bool ok = true;
+      const auto issue_s = [&](uint32_t n) -> bool {
+        const uint32_t ks = n & 1u;
+        if (!wait(&sm.k_full[ks], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        ptx::tc_fence_after();
+        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk)
+          ptx::mma_ss_pair(tmem + kTmSc + ks * 128, ptx::sdesc_at(qd, (kk >> 2) * 16384 + (kk & 3) * 32),
+                           ptx::sdesc_at(kd, (kk >> 2) * 8192 + (kk & 3) * 32), kIdescSc, kk > 0);
+        ptx::tc_commit_pair(&sm.s_full[ks], 3);
+        ptx::tc_commit_pair(&sm.k_empty[ks], 3);
+        return true;
+      };
+      const auto issue_pv = [&](uint32_t n, bool first) -> bool {
+        const uint32_t vs = n & 1u;
+        if (!wait(&sm.p_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!wait(&sm.v_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        ptx::tc_fence_after();
+        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), 16384, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + vs * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                           ptx::sdesc_at(vd, kk * 2048), kIdescOc, !first || kk > 0);
+        ptx::tc_commit_pair(&sm.pv_done, 3);
+        ptx::tc_commit_pair(&sm.v_empty[vs], 3);
+        return true;
+      };
+      while (ok) {
+        ok = wait_rec(sm, J, tmo);
+        if (!ok) break;
+        const int n_tiles = sm.rec[J % kTiles].n_tiles;
+        if (n_tiles == 0) break;
+        ok = wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        ok = issue_s(J);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          if (j + 1 < n_tiles) ok = issue_s(J + j + 1);
+          // O of the last piece has been read by every warp
+          if (ok && j == 0 && pc > 0) ok = wait(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
+          if (ok) ok = issue_pv(J + j, j == 0);
+        }
+        if (ok) ptx::tc_commit_pair(&sm.o_full, 3);
+        J += n_tiles;
+        ++pc;
+      }
+      if (!ok) {
+        sm.abort = 1;
+        record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+      }
+      // every product issued has to end before tensor memory is given back
+      ptx::tc_commit_pair(&sm.drain, 1);
+      wait(&sm.drain, 0, tmo, &sm.zero);
+    }
+    __syncwarp();
+  } else if (warp < kSoftWarp) {
+    // ------------------------------------------------------------ conversion
+    const int w = warp - kConvWarp;
+    const int bs_mask = (1 << p.bs_log2) - 1;
+    const uint32_t peer_hit = ptx::mapa_shared(ptx::smem_addr(&sm.hit[0][0]), rank ^ 1u);
+    bool ok = true;
+    // Items K0, K1, V0, K2, V1, ..: item i is V of tile i / 2 - 1 for even i > 0, K of the others.
+    // An item's eight loads a thread are on their way while the last one is converted.
+    uint4 u[2][8];
+    const auto k_row = [&](int s) { return s * 8 + w * 2 + (lane >> 4); };    // of this CTA's 64 keys
+    const auto v_row = [&](int s) { return s * 16 + w * 4 + (lane >> 3); };   // of the tile's 128
+    const auto load = [&](uint32_t J, bool is_v, uint4 (&d)[8]) -> bool {
+      if (!warp_all(ok && wait_rec(sm, J, tmo))) {
+        ok = false;
+        return false;
+      }
+      const TileRec& r = sm.rec[J % kTiles];
+      if (r.n_tiles == 0) return false;
+      const uint8_t* const pool =
+          is_v ? p.v_pool + 128 * rank + (lane & 7) * 16 : p.k_pool + (lane & 15) * 16;
+      const int g = r.g, key0 = r.key0, k_hi = r.k_hi;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int row = is_v ? v_row(s) : 64 * int(rank) + k_row(s), key = key0 + row;
+        const int blk = r.blk[row >> 4];
+        d[s] = make_uint4(0u, 0u, 0u, 0u);
+        if (key < k_hi && blk >= 0)
+          d[s] = __ldg(reinterpret_cast<const uint4*>(
+              pool + (((size_t(blk) * p.Hkv + g) << p.bs_log2) + (key & bs_mask)) * 256));
+      }
+      return true;
+    };
+    const auto store = [&](uint32_t J, bool is_v, uint4 (&d)[8]) {
+      const uint32_t sl = J & 1u;
+      if (J >= 2)
+        ok = warp_all(ok && wait(is_v ? &sm.v_empty[sl] : &sm.k_empty[sl], ((J >> 1) - 1u) & 1u, tmo,
+                                 &sm.abort));
+      if (!ok) return;
+      const TileRec& r = sm.rec[J % kTiles];
+      if (is_v && r.key0 + kTile > r.pr_lo) {
+        // V rows that some rows do not see: their NaN are taken out, and noted in both CTAs
+        const int key0 = r.key0, pr_lo = r.pr_lo, set = r.piece % kHitSets;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const int key = key0 + v_row(s);
+          if (key >= pr_lo && clear_nan8(d[s])) {
+            const int h = key - pr_lo;
+            atomicOr(&sm.hit[set][h >> 5], 1u << (h & 31));
+            asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(
+                             peer_hit + uint32_t(set * kHitWords + (h >> 5)) * 4u),
+                         "r"(1u << (h & 31))
+                         : "memory");
+          }
+        }
+      }
+      const bool odd = (lane & 4) != 0;   // the two chunks' order: 8 lanes' stores meet no bank twice
+      uint8_t* const slot = is_v ? sm.v[sl] : sm.k[sl];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int row = is_v ? v_row(s) : k_row(s);
+        const int c16 = is_v ? lane & 7 : lane & 15;
+        uint8_t* const at = slot + (c16 >> 2) * (is_v ? 16384 : 8192) + row * 128;
+        uint4 lo, hi;
+        to_f16x16(d[s], lo, hi);
+        const int c = (c16 & 3) * 2, x = row & 7;
+        *reinterpret_cast<uint4*>(at + (((odd ? c + 1 : c) ^ x) << 4)) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(at + (((odd ? c : c + 1) ^ x) << 4)) = odd ? lo : hi;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive_cluster(lead_bar(is_v ? &sm.v_full[sl] : &sm.k_full[sl]));
+        if (is_v) {
+          if (r.last) {
+            uint64_t* const h = &sm.hit_full[r.piece % kHitSets];
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 0));
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 1));
+          }
+          // the group's last tile has been read
+          if (J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
+        }
+      }
+      __syncwarp();
+    };
+    // two items a round, so that the buffers are fixed: V of tile J and K of tile J + 2
+    bool more = load(0, false, u[0]);
+    if (more) {
+      bool next = load(1, false, u[1]);
+      store(0, false, u[0]);
+      load(0, true, u[0]);
+      if (next) store(1, false, u[1]);
+      for (uint32_t J = 0; ok; ++J) {
+        const bool after = next && load(J + 2, false, u[1]);
+        store(J, true, u[0]);
+        if (!next) break;
+        load(J + 1, true, u[0]);
+        if (after) store(J + 2, false, u[1]);
+        next = after;
+      }
+    }
+    if (!ok && lane == 0) {
+      sm.abort = 1;
+      record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, epilogue
+    const int sw = warp - kSoftWarp, half = sw >> 2, qd = warp & 3, row = qd * 32 + lane;
+    const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
+    const uint32_t bar_id = 1 + qd;   // the two warps of a quadrant
+    uint32_t J = 0, pc = 0;
+    bool ok = true;
+    // Q's rows of piece n as fp16; then its products may start.  (The last piece's S products are done.)
+    const auto prepare = [&](uint32_t n) {
+      const ChunkPiece& x = sm.piece[n % kPieces];
+      const int p0 = x.rb * kPairRows + int(rank) * 128, n_rows = min(128, x.rows * p.gqa - p0);
+#pragma unroll 1
+      for (int r0 = sw; r0 < 128; r0 += 32) {
+        uint4 u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = r0 + 8 * k, i = (p0 + rr) / p.gqa;
+          const size_t at = size_t(x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
+          u[k] = rr < n_rows ? __ldg(p.q + at * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = r0 + 8 * k;
+          float f[8];
+          const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 a = unpack_elem2<kF16>(w[c]);
+            f[2 * c] = a.x;
+            f[2 * c + 1] = a.y;
+          }
+          const int e = scale_exp(__reduce_max_sync(0xffffffffu, finite_amax_bits(f)));
+          if (lane == 0) sm.fac[n & 1u][rr] = pow2f(e) * kScaleLog2;
+          const float inv = inv_pow2f(e);
+          // an infinite element makes its row's scores NaN, as in the formula
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
+          uint4 o;
+          o.x = pack_half2(f[0], f[1]);
+          o.y = pack_half2(f[2], f[3]);
+          o.z = pack_half2(f[4], f[5]);
+          o.w = pack_half2(f[6], f[7]);
+          *reinterpret_cast<uint4*>(sm.q + (lane >> 3) * 16384 + rr * 128 +
+                                    (((lane & 7) ^ (rr & 7)) << 4)) = o;
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(lead_bar(&sm.q_full));
+    };
+
+    ok = warp_all(wait_rec(sm, 0, tmo));
+    bool more = ok && sm.rec[0].n_tiles > 0;
+    if (more) prepare(0);
+    // All softmax warps meet here once before the first piece and once in each: one that gives up
+    // comes once more on its way out, and the others leave with it.
+    bool stop = ptx::named_bar_or(9, 256, !ok);
+    while (more && !stop) {
+      const int n_tiles = sm.rec[J % kTiles].n_tiles;
+      const ChunkPiece x = sm.piece[pc % kPieces];
+      const int pk = x.rb * kPairRows + int(rank) * 128 + row, i_new = pk / p.gqa;
+      const bool mine = pk < x.rows * p.gqa;
+      const int lim = mine ? x.base + i_new + 1 : 0;
+      const float fac = sm.fac[pc & 1u][row];
+      float ref = kNone, ml = kNone, l = 0.f;
+      for (int j = 0; j < n_tiles; ++j, ++J) {
+        const uint32_t buf = J & 1u;
+        ok = ok && wait_rec(sm, J, tmo) && wait(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
+        ok = warp_all(ok);
+        __syncwarp();
+        const TileRec& r = sm.rec[J % kTiles];
+        const uint32_t ts = trow + kTmSc + buf * 128 + half * 64;
+        uint32_t s[64];
+        float f[4], lv[4];
+        float mp = -INFINITY, ms = -INFINITY;
+        if (ok) {
+          ptx::tc_fence_after();
+          ptx::tmem_ld64_wait(ts, s);
+          const float4 k4 = *reinterpret_cast<const float4*>(&r.ks[4 * half]);
+          const float4 v4 = *reinterpret_cast<const float4*>(&r.lv[4 * half]);
+          const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+          lv[0] = v4.x;
+          lv[1] = v4.y;
+          lv[2] = v4.z;
+          lv[3] = v4.w;
+          const int key0 = r.key0 + half * 64;
+          if (key0 + 64 > lim) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (key0 + c >= lim) s[c] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
+            f[i] = fminf(fmaxf(fac * kk[i], 1e-37f), 3e38f);
+            float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
+#pragma unroll
+            for (int c = 2; c < 16; c += 2) {
+              m0 = fmaxf(m0, __uint_as_float(s[16 * i + c]));
+              m1 = fmaxf(m1, __uint_as_float(s[16 * i + c + 1]));
+            }
+            const float m = fmaxf(m0, m1) * f[i];
+            ms = fmaxf(ms, m);
+            mp = fmaxf(mp, m + lv[i]);
+          }
+          sm.red[buf][half][row] = make_float2(mp, ms);
+        }
+        if (ptx::named_bar_or(bar_id, 64, !ok)) {
+          stop = true;
+          break;
+        }
+        {
+          const float2 o = sm.red[buf][half ^ 1][row];
+          mp = fmaxf(mp, o.x);
+          ms = fmaxf(ms, o.y);
+        }
+        // ---- references (both threads of a row do the same)
+        float alpha = 1.f;
+        if (mp > ref + kCap) {
+          alpha = ex2(ref - (mp - kTop));
+          ref = mp - kTop;
+        }
+        if (ms > ml + kLSlack) {
+          l *= ex2(ml - ms);
+          ml = ms;
+        }
+        const bool moved = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+        // ---- P goes where the scores were
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk2[8];
+          const float a = lv[i] - ref;
+          const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
+          // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them
+          const float d = -a - ml;
+          const bool far = __any_sync(0xffffffffu, d > 60.f);
+          if (far) {
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
+            l += sum;
+          }
+          float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2 y = fma2(make_float2(__uint_as_float(s[16 * i + 2 * c]),
+                                              __uint_as_float(s[16 * i + 2 * c + 1])), f2, a2);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum2 = add2(sum2, e);
+            pk2[c] = pack_half2(e.x, e.y);
+          }
+          if (!far) l += (sum2.x + sum2.y) * ex2(d);
+          ptx::tmem_st8(ts + 8 * i, pk2);
+        }
+        ptx::tmem_wait_st();
+        if (moved) {
+          // O, with PV of tile J - 1 in it, moves to the new references
+          ok = warp_all(wait(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
+          if (ok) {
+            ptx::tc_fence_after();
+            rescale_o_cols(trow + kTmOc + half * 128, alpha);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) {
+          ptx::mbar_arrive_cluster(lead_bar(&sm.p_full[buf]));
+          if (J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
+        }
+      }
+      if (stop) {
+        ptx::named_bar_or(9, 256, true);
+        break;
+      }
+      // ---- the next piece may start while this one ends
+      ok = warp_all(ok && wait_rec(sm, J, tmo));
+      more = ok && sm.rec[J % kTiles].n_tiles > 0;
+      if (more) prepare(pc + 1u);
+      sm.sum[half][row] = l;
+      ok = warp_all(ok && wait(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
+                    wait(&sm.o_full, pc & 1u, tmo, &sm.abort));
+      stop = ptx::named_bar_or(9, 256, !ok);
+      if (stop) break;
+      ptx::tc_fence_after();
+      const float L = l + sm.sum[half ^ 1][row];
+      const float inv = L == 0.f ? 0.f : 1.f / L, ex = ex2(0.5f * (ref - ml));
+      const float lse = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
+      const int set = pc % kHitSets;
+      // every warp is past the last piece, whose hits may go
+      if (half == 0 && row < kHitWords) sm.hit[(pc + kHitSets - 1) % kHitSets][row] = 0u;
+      uint32_t any = 0u;
+#pragma unroll
+      for (int w = 0; w < kHitWords; ++w) any |= *reinterpret_cast<volatile uint32_t*>(&sm.hit[set][w]);
+      const size_t at = size_t(x.t0 + i_new) * p.Hq + x.g * p.gqa + (pk - i_new * p.gqa);
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        const int col = half * 128 + 32 * cc;
+        __syncwarp();
+        uint32_t o[32];
+        ptx::tmem_ld32_wait(trow + kTmOc + col, o);
+        if (!mine) continue;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(L == 0.f ? 0.f : __uint_as_float(o[c]) * inv * ex * ex);
+        if (x.part >= 0) {
+          float4* const d = reinterpret_cast<float4*>(
+              p.o_parts + (size_t(x.part) * kPairRows + int(rank) * 128 + row) * 256 + col);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            d[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+        } else {
+          uint4 gt[4];
+          if (p.gate != nullptr) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              gt[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + col) + c);
+          }
+          uint4* const d = reinterpret_cast<uint4*>(p.out + at * 256 + col);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+            const uint32_t gw[4] = {gt[c].x, gt[c].y, gt[c].z, gt[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float2 y = make_float2(__uint_as_float(o[8 * c + 2 * e]), __uint_as_float(o[8 * c + 2 * e + 1]));
+              if (p.gate != nullptr) {
+                const float2 gf = unpack_elem2<kF16>(gw[e]);
+                y = mul2(y, gate_sigmoid2(gf.x, gf.y));
+              }
+              w[e] = pack_elem2<kF16>(y.x, y.y);
+            }
+            d[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (any != 0u && mine && L != 0.f)
+        put_back(p, sm.hit[set], x.b, x.g, x.base + x.rb * kPairRows / p.gqa + 1, lim, half * 128,
+                 x.part < 0 ? nullptr : p.o_parts + (size_t(x.part) * kPairRows + int(rank) * 128 + row) * 256,
+                 p.out + at * 256, kF16 ? 0x7E00u : 0x7FC0u);
+      if (mine && half == 0) {
+        if (x.part >= 0)
+          p.lse_parts[size_t(x.part) * kPairRows + int(rank) * 128 + row] = lse;
+        else if (p.lse != nullptr)
+          p.lse[at] = lse;
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(lead_bar(&sm.o_free));
+      ++pc;
+    }
+    if (stop && lane == 0) {
+      sm.abort = 1;
+      record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves while the other may still reach its shared or tensor memory
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// Puts the parts of the segments that were cut together, gates and rounds them: a warp a row.
+//   out = (sum_i w_i O_i) / (sum_i w_i) * sigmoid(g),  w_i = exp(lse_i - max lse)
+constexpr int kMaxPairs = 96;
+constexpr int kJoinRows = 32;   // rows of a CTA
+
+template <bool kF16>
+__global__ void __launch_bounds__(256) kv8_join_kernel(const ChunkArgs p) {
+  __shared__ float s_w[8][kMaxPairs];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_next_start();
+  wait_for_last();
+  constexpr int kSplit = kPairRows / kJoinRows;
+  const int pair = int(blockIdx.x) / kSplit;
+  const int* const c = p.cuts + 8 * pair;
+  if (__ldcg(c + 1) == 0) return;
+  const int g = __ldcg(c + 2), rb = __ldcg(c + 3), rows = __ldcg(c + 4), t0 = __ldcg(c + 5);
+  // parts: this pair's last piece and the first ones of the pairs behind it, up to the one that ends
+  int cnt = 1;
+  for (int k0 = pair + 1; k0 < p.pairs; k0 += 32) {
+    const int state = k0 + lane < p.pairs ? __ldcg(p.cuts + 8 * (k0 + lane)) : 0;
+    const uint32_t off = __ballot_sync(0xffffffffu, state != 1);
+    const int w = off != 0u ? __ffs(off) - 1 : 32;
+    cnt += w;
+    if (w < 32) {
+      if (__shfl_sync(0xffffffffu, state, w) == 2) ++cnt;
+      break;
+    }
+  }
+  cnt = min(cnt, kMaxPairs);
+  const int p0 = rb * kPairRows, n_rows = min(kPairRows, rows * p.gqa - p0);
+  const auto slot = [&](int i) { return size_t(i == 0 ? 2 * pair + 1 : 2 * (pair + i)) * kPairRows; };
+  for (int r = (int(blockIdx.x) % kSplit) * kJoinRows + warp, e = r - warp + kJoinRows; r < min(e, n_rows);
+       r += 8) {
+    float M = -INFINITY;
+    for (int i = lane; i < cnt; i += 32) {
+      const float ls = __ldcg(p.lse_parts + slot(i) + r);
+      s_w[warp][i] = ls;
+      M = fmaxf(M, ls);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float msub = M == -INFINITY ? 0.f : M;
+    float sum = 0.f;
+    for (int i = lane; i < cnt; i += 32) {
+      const float ls = s_w[warp][i], w = ls == -INFINITY ? 0.f : __expf(ls - msub);
+      s_w[warp][i] = ls == -INFINITY ? -1.f : w;   // -1: the part saw no key
+      sum += w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < cnt; i0 += 4) {
+      float4 v[4][2];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k < cnt) {
+          const float4* const o = reinterpret_cast<const float4*>(p.o_parts + (slot(i0 + k) + r) * 256) + lane * 2;
+          v[k][0] = __ldcg(o);
+          v[k][1] = __ldcg(o + 1);
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = i0 + k < cnt ? s_w[warp][i0 + k] : -1.f;
+        if (w < 0.f) continue;   // (a weight of 0 counts: its part may hold a NaN that the row sees)
+        acc[0] += w * v[k][0].x;
+        acc[1] += w * v[k][0].y;
+        acc[2] += w * v[k][0].z;
+        acc[3] += w * v[k][0].w;
+        acc[4] += w * v[k][1].x;
+        acc[5] += w * v[k][1].y;
+        acc[6] += w * v[k][1].z;
+        acc[7] += w * v[k][1].w;
+      }
+    }
+    __syncwarp();
+    const int pk = p0 + r, i = pk / p.gqa;
+    const size_t at = size_t(t0 + i) * p.Hq + g * p.gqa + (pk - i * p.gqa);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float gs[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (p.gate != nullptr) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256) + lane);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 a = unpack_elem2<kF16>(w[k]);
+        gs[2 * k] = gate_sigmoid(a.x);
+        gs[2 * k + 1] = gate_sigmoid(a.y);
+      }
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = pack_elem2<kF16>(acc[2 * k] * inv * gs[2 * k], acc[2 * k + 1] * inv * gs[2 * k + 1]);
+    reinterpret_cast<uint4*>(p.out + at * 256)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (p.lse != nullptr && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : msub + __logf(sum);
+  }
+}
+
+int pair_count() {
+  const int n = device_sm_count() / 2;
+  return n < 1 ? 1 : n < kMaxPairs ? n : kMaxPairs;
+}
+
+struct Workspace {
+  size_t lse, cuts, bytes;   // o_parts lie first
+};
+Workspace workspace_of(int pairs) {
+  Workspace w;
+  const size_t rows = size_t(2) * pairs * kPairRows;
+  w.lse = rows * 256 * sizeof(float);
+  w.cuts = w.lse + rows * sizeof(float);
+  w.bytes = w.cuts + size_t(8) * pairs * sizeof(int);
+  return w;
+}
+
+template <bool kF16>
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {
+  const size_t smem = sizeof(ChunkSmem) + 1024;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_chunk_kernel<kF16>), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kv8_chunk_kernel<kF16>, dim3(unsigned(2 * a.pairs)), kThreadsC, smem, stream, 2, a);
+  if (e != cudaSuccess) return e;
+  note_launch(kF16 ? "kv8_chunk_kernel<fp16>" : "kv8_chunk_kernel<bf16>", 2 * a.pairs, kThreadsC, smem);
+  const unsigned grid = unsigned(a.pairs * (kPairRows / kJoinRows));
+  e = launch_dependent(kv8_join_kernel<kF16>, dim3(grid), 256, 0, stream, 1, a);
+  if (e == cudaSuccess)
+    note_launch(kF16 ? "kv8_join_kernel<fp16>" : "kv8_join_kernel<bf16>", grid, 256, 0);
+  return e;
+}
+
+int prefill_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
+                 const float* v_scale, const void* G, const int* block_tables, const int* kv_lens,
+                 const int* cu_rows, void* out, float* lse_out, int B, int T, int Hq, int Hkv,
+                 int num_blocks, int block_size, int max_blocks, int max_rows, int max_kv_len,
+                 void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_rows < 1 || max_kv_len < 1 ||
+      max_rows > max_kv_len)
+    return GQA_ERR_INVALID_ARG;
+  const int st = check_kv8_pool(num_blocks, Hkv, block_size);
+  if (st != GQA_OK) return st;
+  if (max_blocks < 1 || max_kv_len > (long long)max_blocks * block_size) return GQA_ERR_INVALID_ARG;
+  if ((long long)T * Hq >= (1LL << 31) || (long long)max_rows * Hq >= (1LL << 31) - kPairRows ||
+      max_kv_len >= (1 << 30))
+    return GQA_ERR_UNSUPPORTED;
+  if (T == 0) return GQA_OK;
+  if (Q == nullptr || k_pool == nullptr || v_pool == nullptr || k_scale == nullptr ||
+      v_scale == nullptr || block_tables == nullptr || kv_lens == nullptr || cu_rows == nullptr ||
+      out == nullptr)
+    return GQA_ERR_INVALID_ARG;
+  for (const void* q : {Q, k_pool, v_pool, G, (const void*)out})
+    if (!aligned_to(q, 16)) return GQA_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)k_scale, (const void*)v_scale, (const void*)block_tables,
+                        (const void*)kv_lens, (const void*)cu_rows, (const void*)lse_out})
+    if (!aligned_to(q, 4)) return GQA_ERR_INVALID_ARG;
+  // the kernel counts a launch's positions (a segment's tiles and a few more) in 31 bits
+  const int gqa = Hq / Hkv;
+  const long long max_rb = ((long long)max_rows * gqa + kPairRows - 1) / kPairRows;
+  const long long tiles = (max_kv_len + kTile - 1LL) / kTile;
+  const long long per_seq = (long long)Hkv * max_rb * (tiles + kLead);
+  if (Hkv * max_rb >= (1LL << 31) || per_seq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  const int most = pair_count();
+  const Workspace ws = workspace_of(most);
+  if (workspace == nullptr || workspace_bytes < ws.bytes) return GQA_ERR_WORKSPACE;
+  if (!aligned_to(workspace, 16)) return GQA_ERR_INVALID_ARG;
+  ChunkArgs a{};
+  a.q = static_cast<const uint4*>(Q);
+  a.k_pool = static_cast<const uint8_t*>(k_pool);
+  a.v_pool = static_cast<const uint8_t*>(v_pool);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.gate = static_cast<const uint16_t*>(G);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse_out;
+  a.o_parts = static_cast<float*>(workspace);
+  a.lse_parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.lse);
+  a.cuts = reinterpret_cast<int*>(static_cast<char*>(workspace) + ws.cuts);
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.gqa = gqa;
+  a.num_blocks = num_blocks;
+  while ((1 << a.bs_log2) < block_size) ++a.bs_log2;
+  a.max_blocks = max_blocks;
+  a.max_rows = max_rows;
+  a.max_kv_len = max_kv_len;
+  if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
+  const long long fit = ((1LL << 31) - 1) / per_seq;
+  const int step = fit < kKv8Seqs ? int(fit) : kKv8Seqs;
+  for (int b0 = 0; b0 < B; b0 += step) {
+    a.B = B - b0 < step ? B - b0 : step;
+    a.tables = block_tables + (long long)b0 * max_blocks;
+    a.kv_lens = kv_lens + b0;
+    a.cu_rows = cu_rows + b0;
+    const long long units = (long long)a.B * Hkv * max_rb * tiles;
+    a.pairs = units < most ? int(units) : most;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((f16 ? launch_chunk<true>(a, s) : launch_chunk<false>(a, s)) != cudaSuccess)
+      return GQA_ERR_CUDA;
+  }
+  return GQA_OK;
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" {
+
+size_t gqa_kv8_prefill_workspace_size(void) { return workspace_of(pair_count()).bytes; }
+
+int gqa_kv8_prefill(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
+                    const float* v_scale, const void* G, const int* block_tables, const int* kv_lens,
+                    const int* cu_rows, void* out, float* lse_out, int B, int T, int Hq, int Hkv,
+                    int num_blocks, int block_size, int max_blocks, int max_rows, int max_kv_len,
+                    void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+  return prefill_impl(false, Q, k_pool, v_pool, k_scale, v_scale, G, block_tables, kv_lens, cu_rows, out,
+                      lse_out, B, T, Hq, Hkv, num_blocks, block_size, max_blocks, max_rows, max_kv_len,
+                      workspace, workspace_bytes, stream);
+}
+int gqa_kv8_prefill_f16(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
+                        const float* v_scale, const void* G, const int* block_tables,
+                        const int* kv_lens, const int* cu_rows, void* out, float* lse_out, int B, int T,
+                        int Hq, int Hkv, int num_blocks, int block_size, int max_blocks, int max_rows,
+                        int max_kv_len, void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+  return prefill_impl(true, Q, k_pool, v_pool, k_scale, v_scale, G, block_tables, kv_lens, cu_rows, out,
+                      lse_out, B, T, Hq, Hkv, num_blocks, block_size, max_blocks, max_rows, max_kv_len,
+                      workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -538,6 +538,32 @@ int gqa_kv8_decode_f16(const void* Q, const void* k_pool, const void* v_pool,
                        int max_rows, int max_kv_len, void* workspace, size_t workspace_bytes,
                        gqa_stream_t stream);
 
+/*
+ * Prompt chunks over the paged 8-bit cache: as gqa_kv8_decode without tree_mask, for many new rows
+ * a sequence.  New row i of sequence b sees keys j < kv_lens[b] - r_b + i + 1, the chunk's own
+ * rows among them (gqa_kv8_append comes first).  Same arguments, rows left as they were, table entries,
+ * NaN and errors; cu_rows is required.  Products are 16-bit ones: a probability is off by 2^-11 of
+ * itself and by 2^-34 of the row's largest (V's scales beside it), q by 2^-33 of its row's largest.
+ * Runs on CTA pairs over 256 packed rows (new rows x Hq / Hkv) at a time; a batch of single tokens
+ * is gqa_kv8_decode's.
+ * workspace: gqa_kv8_prefill_workspace_size() bytes (for the current device, whatever the sizes; about
+ * 40 MB), 16-byte aligned; calls that may overlap on the GPU need one each.
+ * max_kv_len < 2^30 and Hkv * row blocks * (128-key tiles of a sequence + 3) < 2^31
+ * (GQA_ERR_UNSUPPORTED above).
+ */
+size_t gqa_kv8_prefill_workspace_size(void);
+int gqa_kv8_prefill(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
+                    const float* v_scale, const void* G, const int* block_tables, const int* kv_lens,
+                    const int* cu_rows, void* out, float* lse_out, int B, int T, int Hq, int Hkv,
+                    int num_blocks, int block_size, int max_blocks, int max_rows, int max_kv_len,
+                    void* workspace, size_t workspace_bytes, gqa_stream_t stream);
+int gqa_kv8_prefill_f16(const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
+                        const float* v_scale, const void* G, const int* block_tables,
+                        const int* kv_lens, const int* cu_rows, void* out, float* lse_out, int B,
+                        int T, int Hq, int Hkv, int num_blocks, int block_size, int max_blocks,
+                        int max_rows, int max_kv_len, void* workspace, size_t workspace_bytes,
+                        gqa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
