@@ -10,8 +10,8 @@
 // stored and their scales stay apart: K's goes into the scores (fp32, per run of 16 keys), V's into the
 // exponent of the probability, p = 2^(score + log2 vs - ref).  Q goes as fp16 times a power of two
 // per row: exact for what lies within 2^-23 of the row's largest element, off by 2^-33 of that below.
-// p goes as fp16: off by 2^-11 of itself, and by 2^-25 where the row's largest is 2^9 at least (a
-// reference moves when p would pass 2^15, and then leaves the largest at 2^9).  The row's sum l is taken
+// p goes as fp16: off by 2^-11 of itself, and by 2^-25 where the row's largest is 2^3 at least (a
+// reference moves when p would pass 2^15, and then leaves the largest at 2^3).  The row's sum l is taken
 // from the fp32 probabilities against a reference of its own, without the V scales.
 //
 // What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (8-bit terms, as the kernels
@@ -21,8 +21,8 @@
 // one a pair.  A piece that is a whole segment goes straight to `out`; the pieces of a segment that is
 // cut leave fp32 parts, two a pair at most, that kv8_join_kernel puts together.
 //
-// Roles (448 threads): warp 0 schedules (pieces, block numbers and scales of the tiles), warp 1 of the even
-// CTA issues the products, warps 2..5 convert K and V into shared memory, warps 6..13 are softmax and
+// Roles (512 threads): warp 0 schedules (pieces, block numbers and scales of the tiles), warp 1 of the even
+// CTA issues the products, warps 4..7 convert K and V into shared memory, warps 8..15 are softmax and
 // epilogue (row = tensor-memory lane, 64 keys a thread).
 // TMEM: O 256 columns, two buffers of 128 for S and P.
 #include <cuda.h>
@@ -34,9 +34,11 @@ namespace gqa {
 namespace {
 
 constexpr int kPairRows = 256;                  // packed rows of a segment
-constexpr int kConvWarp = 2, kConvWarps = 4;    // first warp of each role
-constexpr int kSoftWarp = kConvWarp + kConvWarps;
-constexpr int kThreadsC = 32 * (kSoftWarp + 8);
+constexpr int kThreadsC = 512;                  // four warpgroups: schedule and products, conversion, softmax
+constexpr int kConvWarp = 4, kSoftWarp = 8;     // first warps
+// Registers a thread, by warpgroup, out of the launch's 128 (inc waits until they are there).
+constexpr int kRegsRest = 80, kRegsConv = 112, kRegsSoft = 160;
+static_assert(kRegsRest + kRegsConv + 2 * kRegsSoft <= 4 * 128, "the launch's registers");
 constexpr int kSlotC = 32768;                   // half a tile of K or V in fp16
 constexpr int kGroup = 4;                       // tiles that the scheduler looks up together
 constexpr int kGroups = 4;                      // groups held
@@ -46,7 +48,7 @@ constexpr int kHitSets = 4;                     // pieces whose NaN keys are hel
 constexpr int kHitWords = kPairRows / 32;       // keys that only some rows of a segment see: < 256
 constexpr uint32_t kLead = 3;                   // what a segment costs beside its tiles, in tiles
 constexpr int kSnap = 4;                        // a cut this close to a segment's end is made there
-constexpr float kCap = 15.f, kTop = 9.f;        // p <= 2^15; a moved reference leaves 2^9
+constexpr float kCap = 15.f, kTop = 3.f;        // p <= 2^15; a moved reference leaves 2^3
 constexpr uint32_t kTmOc = 0, kTmSc = 256;
 constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);
 constexpr uint32_t kIdescOc = ptx::idesc_f32acc(256, 256, 0, 1, 0);
@@ -107,6 +109,20 @@ struct __align__(1024) ChunkSmem {
   int abort, zero;
 };
 static_assert(sizeof(ChunkSmem) + 1024 <= 227 * 1024, "one CTA per SM");
+
+template <int N>
+__device__ __forceinline__ void take_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void leave_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Arrives on a barrier of the even CTA: each CTA's own, or through the cluster's window.
+__device__ __forceinline__ void arrive_lead(uint64_t* bar, bool lead) {
+  if (lead) ptx::mbar_arrive(bar); else ptx::mbar_arrive_remote(ptx::mapa_shared(ptx::smem_addr(bar), 0));
+}
 
 // Tiles that some row of row block rb sees.
 __device__ __forceinline__ int tiles_of(const int4& s, int rb, int gqa) {
@@ -184,9 +200,14 @@ __device__ __forceinline__ void to_f16x16(const uint4& u, uint4& lo, uint4& hi) 
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// (in line: a kernel that shares its registers out again may not call)
+__device__ __forceinline__ bool hold(uint64_t* bar, uint32_t parity, uint64_t tmo, int* abort) {
+  return ptx::mbar_wait(bar, parity, tmo, abort);
+}
+
 __device__ __forceinline__ bool wait_rec(ChunkSmem& sm, uint32_t J, uint64_t tmo) {
   const uint32_t G = J / kGroup;
-  return wait(&sm.rec_full[G % kGroups], (G / kGroups) & 1u, tmo, &sm.abort);
+  return hold(&sm.rec_full[G % kGroups], (G / kGroups) & 1u, tmo, &sm.abort);
 }
 
 // The dims of 128 from `dim` on in which a hit key that this row sees has a NaN: NaN in the row's output
@@ -285,9 +306,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
   ptx::cluster_sync();   // both CTAs' barriers exist before any arrive reaches them
   ptx::tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  const auto lead_bar = [&](uint64_t* bar) { return ptx::mapa_shared(ptx::smem_addr(bar), 0); };
 
   if (warp < kConvWarp) {
+    leave_regs<kRegsRest>();
     if (warp == 0) {
       // ---------------------------------------------------------- schedule
       const unsigned long long W = sm.at[p.B];
@@ -314,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         int my_b = 0;
         const uint32_t G = J / kGroup;
         if (G >= kGroups) {
-          ok = warp_all(wait(&sm.rec_empty[G % kGroups], (G / kGroups - 1) & 1u, tmo, &sm.abort));
+          ok = warp_all(hold(&sm.rec_empty[G % kGroups], (G / kGroups - 1) & 1u, tmo, &sm.abort));
           if (!ok) break;
         }
         for (int q = 0; q < kGroup && !done; ++q) {
@@ -422,7 +443,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
         const uint32_t ks = n & 1u;
-        if (!wait(&sm.k_full[ks], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!hold(&sm.k_full[ks], (n >> 1) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
 #pragma unroll
@@ -435,8 +456,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       };
       const auto issue_pv = [&](uint32_t n, bool first) -> bool {
         const uint32_t vs = n & 1u;
-        if (!wait(&sm.p_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
-        if (!wait(&sm.v_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!hold(&sm.p_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!hold(&sm.v_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), 16384, 1024);
 #pragma unroll
@@ -452,14 +473,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (!ok) break;
         const int n_tiles = sm.rec[J % kTiles].n_tiles;
         if (n_tiles == 0) break;
-        ok = wait(&sm.q_full, pc & 1u, tmo, &sm.abort);
+        ok = hold(&sm.q_full, pc & 1u, tmo, &sm.abort);
         if (!ok) break;
         ptx::tc_fence_after();
         ok = issue_s(J);
         for (int j = 0; ok && j < n_tiles; ++j) {
           if (j + 1 < n_tiles) ok = issue_s(J + j + 1);
           // O of the last piece has been read by every warp
-          if (ok && j == 0 && pc > 0) ok = wait(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
+          if (ok && j == 0 && pc > 0) ok = hold(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
           if (ok) ok = issue_pv(J + j, j == 0);
         }
         if (ok) ptx::tc_commit_pair(&sm.o_full, 3);
@@ -472,20 +493,25 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       }
       // every product issued has to end before tensor memory is given back
       ptx::tc_commit_pair(&sm.drain, 1);
-      wait(&sm.drain, 0, tmo, &sm.zero);
+      hold(&sm.drain, 0, tmo, &sm.zero);
     }
     __syncwarp();
   } else if (warp < kSoftWarp) {
     // ------------------------------------------------------------ conversion
+    leave_regs<kRegsConv>();
     const int w = warp - kConvWarp;
     const int bs_mask = (1 << p.bs_log2) - 1;
     const uint32_t peer_hit = ptx::mapa_shared(ptx::smem_addr(&sm.hit[0][0]), rank ^ 1u);
     bool ok = true;
-    // Items K0, K1, V0, K2, V1, ..: item i is V of tile i / 2 - 1 for even i > 0, K of the others.
-    // An item's eight loads a thread are on their way while the last one is converted.
+    // Items K0, K1, V0, K2, V1, ..; an item's eight loads a thread are on their way while the last one
+    // is converted.  A warp has the 16 keys of one run of K (two keys' 256 bytes a load) and the 32 of
+    // two of V (four keys' 128), so that a run's address is worked out once.
+    const int k_sub = lane >> 4, v_sub = lane >> 3;          // key of a load
+    const bool odd = (lane & 4) != 0;   // the order of a thread's two chunks: 8 lanes meet no bank twice
+    const int kc = (lane & 3) * 2 + (odd ? 1 : 0);           // the first one's place among 8
+    uint32_t const k_off = ((lane & 15) >> 2) * 8192 + (w * 16 + k_sub) * 128 + ((kc ^ k_sub) << 4);
+    uint32_t const v_off = ((lane & 7) >> 2) * 16384 + (w * 32 + v_sub) * 128 + ((kc ^ v_sub) << 4);
     uint4 u[2][8];
-    const auto k_row = [&](int s) { return s * 8 + w * 2 + (lane >> 4); };    // of this CTA's 64 keys
-    const auto v_row = [&](int s) { return s * 16 + w * 4 + (lane >> 3); };   // of the tile's 128
     const auto load = [&](uint32_t J, bool is_v, uint4 (&d)[8]) -> bool {
       if (!warp_all(ok && wait_rec(sm, J, tmo))) {
         ok = false;
@@ -493,60 +519,68 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       }
       const TileRec& r = sm.rec[J % kTiles];
       if (r.n_tiles == 0) return false;
-      const uint8_t* const pool =
-          is_v ? p.v_pool + 128 * rank + (lane & 7) * 16 : p.k_pool + (lane & 15) * 16;
-      const int g = r.g, key0 = r.key0, k_hi = r.k_hi;
+      const int g = r.g, left = r.k_hi - r.key0;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int row = is_v ? v_row(s) : 64 * int(rank) + k_row(s), key = key0 + row;
-        const int blk = r.blk[row >> 4];
-        d[s] = make_uint4(0u, 0u, 0u, 0u);
-        if (key < k_hi && blk >= 0)
-          d[s] = __ldg(reinterpret_cast<const uint4*>(
-              pool + (((size_t(blk) * p.Hkv + g) << p.bs_log2) + (key & bs_mask)) * 256));
+      for (int h = 0; h < 2; ++h) {   // (K: the same run twice)
+        const int run = is_v ? 2 * w + h : 4 * int(rank) + w, blk = r.blk[run];
+        const int n = blk >= 0 ? left - 16 * run : 0;          // its keys
+        const uint8_t* const a =
+            (is_v ? p.v_pool + 128 * rank + (lane & 7) * 16 + v_sub * 256
+                  : p.k_pool + (lane & 15) * 16 + k_sub * 256) +
+            (((size_t(max(blk, 0)) * p.Hkv + g) << p.bs_log2) + ((r.key0 + 16 * run) & bs_mask)) * 256;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = is_v ? 4 * i : 2 * (4 * h + i);
+          d[4 * h + i] = make_uint4(0u, 0u, 0u, 0u);
+          if (key + (is_v ? v_sub : k_sub) < n)
+            d[4 * h + i] = __ldg(reinterpret_cast<const uint4*>(a + key * 256));
+        }
       }
       return true;
     };
     const auto store = [&](uint32_t J, bool is_v, uint4 (&d)[8]) {
       const uint32_t sl = J & 1u;
       if (J >= 2)
-        ok = warp_all(ok && wait(is_v ? &sm.v_empty[sl] : &sm.k_empty[sl], ((J >> 1) - 1u) & 1u, tmo,
+        ok = warp_all(ok && hold(is_v ? &sm.v_empty[sl] : &sm.k_empty[sl], ((J >> 1) - 1u) & 1u, tmo,
                                  &sm.abort));
       if (!ok) return;
       const TileRec& r = sm.rec[J % kTiles];
       if (is_v && r.key0 + kTile > r.pr_lo) {
         // V rows that some rows do not see: their NaN are taken out, and noted in both CTAs
-        const int key0 = r.key0, pr_lo = r.pr_lo, set = r.piece % kHitSets;
-#pragma unroll
+        const int key0 = r.key0 + 32 * w + v_sub, pr_lo = r.pr_lo, set = r.piece % kHitSets;
+#pragma unroll 1
         for (int s = 0; s < 8; ++s) {
-          const int key = key0 + v_row(s);
-          if (key >= pr_lo && clear_nan8(d[s])) {
+          const int key = key0 + 4 * s;
+          uint4 x = d[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) x = s == i ? d[i] : x;
+          if (key >= pr_lo && clear_nan8(x)) {
             const int h = key - pr_lo;
             atomicOr(&sm.hit[set][h >> 5], 1u << (h & 31));
             asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(
                              peer_hit + uint32_t(set * kHitWords + (h >> 5)) * 4u),
                          "r"(1u << (h & 31))
                          : "memory");
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = s == i ? x : d[i];
           }
         }
       }
-      const bool odd = (lane & 4) != 0;   // the two chunks' order: 8 lanes' stores meet no bank twice
-      uint8_t* const slot = is_v ? sm.v[sl] : sm.k[sl];
+      uint8_t* const slot = is_v ? sm.v[sl] + v_off : sm.k[sl] + k_off;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const int row = is_v ? v_row(s) : k_row(s);
-        const int c16 = is_v ? lane & 7 : lane & 15;
-        uint8_t* const at = slot + (c16 >> 2) * (is_v ? 16384 : 8192) + row * 128;
         uint4 lo, hi;
         to_f16x16(d[s], lo, hi);
-        const int c = (c16 & 3) * 2, x = row & 7;
-        *reinterpret_cast<uint4*>(at + (((odd ? c + 1 : c) ^ x) << 4)) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(at + (((odd ? c : c + 1) ^ x) << 4)) = odd ? lo : hi;
+        // row 2 s + k_sub (4 s + v_sub) of the warp's: its swizzle differs from row k_sub's in two bits
+        const uintptr_t a = (reinterpret_cast<uintptr_t>(slot) ^ uintptr_t(is_v ? (s & 1) * 64 : (s & 3) * 32)) +
+                            s * (is_v ? 512 : 256);
+        *reinterpret_cast<uint4*>(a) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(a ^ 16) = odd ? lo : hi;
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        ptx::mbar_arrive_cluster(lead_bar(is_v ? &sm.v_full[sl] : &sm.k_full[sl]));
+        arrive_lead(is_v ? &sm.v_full[sl] : &sm.k_full[sl], lead);
         if (is_v) {
           if (r.last) {
             uint64_t* const h = &sm.hit_full[r.piece % kHitSets];
@@ -582,6 +616,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax, epilogue
+    take_regs<kRegsSoft>();
     const int sw = warp - kSoftWarp, half = sw >> 2, qd = warp & 3, row = qd * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
     const uint32_t bar_id = 1 + qd;   // the two warps of a quadrant
@@ -629,7 +664,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(lead_bar(&sm.q_full));
+      if (lane == 0) arrive_lead(&sm.q_full, lead);
     };
 
     ok = warp_all(wait_rec(sm, 0, tmo));
@@ -640,19 +675,22 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     bool stop = ptx::named_bar_or(9, 256, !ok);
     while (more && !stop) {
       const int n_tiles = sm.rec[J % kTiles].n_tiles;
-      const ChunkPiece x = sm.piece[pc % kPieces];
-      const int pk = x.rb * kPairRows + int(rank) * 128 + row, i_new = pk / p.gqa;
-      const bool mine = pk < x.rows * p.gqa;
-      const int lim = mine ? x.base + i_new + 1 : 0;
+      int lim = 0;   // keys that this thread's row sees; 0: there is no such row
+      {
+        const ChunkPiece& x = sm.piece[pc % kPieces];
+        const int pk = x.rb * kPairRows + int(rank) * 128 + row;
+        if (pk < x.rows * p.gqa) lim = x.base + pk / p.gqa + 1;
+      }
       const float fac = sm.fac[pc & 1u][row];
       float ref = kNone, ml = kNone, l = 0.f;
       for (int j = 0; j < n_tiles; ++j, ++J) {
         const uint32_t buf = J & 1u;
-        ok = ok && wait_rec(sm, J, tmo) && wait(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
+        ok = ok && wait_rec(sm, J, tmo) && hold(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         __syncwarp();
         const TileRec& r = sm.rec[J % kTiles];
         const uint32_t ts = trow + kTmSc + buf * 128 + half * 64;
+        const int key0 = r.key0 + half * 64;
         uint32_t s[64];
         float f[4], lv[4];
         float mp = -INFINITY, ms = -INFINITY;
@@ -661,21 +699,22 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           ptx::tmem_ld64_wait(ts, s);
           const float4 k4 = *reinterpret_cast<const float4*>(&r.ks[4 * half]);
           const float4 v4 = *reinterpret_cast<const float4*>(&r.lv[4 * half]);
-          const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+          // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
+          f[0] = fminf(fmaxf(fac * k4.x, 1e-37f), 3e38f);
+          f[1] = fminf(fmaxf(fac * k4.y, 1e-37f), 3e38f);
+          f[2] = fminf(fmaxf(fac * k4.z, 1e-37f), 3e38f);
+          f[3] = fminf(fmaxf(fac * k4.w, 1e-37f), 3e38f);
           lv[0] = v4.x;
           lv[1] = v4.y;
           lv[2] = v4.z;
           lv[3] = v4.w;
-          const int key0 = r.key0 + half * 64;
-          if (key0 + 64 > lim) {
+          if (key0 + 64 > lim) {   // keys that the row does not see
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (key0 + c >= lim) s[c] = 0xFF800000u;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
-            f[i] = fminf(fmaxf(fac * kk[i], 1e-37f), 3e38f);
             float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
 #pragma unroll
             for (int c = 2; c < 16; c += 2) {
@@ -686,14 +725,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             ms = fmaxf(ms, m);
             mp = fmaxf(mp, m + lv[i]);
           }
-          sm.red[buf][half][row] = make_float2(mp, ms);
         }
-        if (ptx::named_bar_or(bar_id, 64, !ok)) {
-          stop = true;
-          break;
-        }
+        // (a maximum is never NaN: that says that the warp gives up)
+        sm.red[buf][half][row] = make_float2(ok ? mp : __int_as_float(0x7FC00000), ms);
+        ptx::named_bar_sync(bar_id, 64);
         {
           const float2 o = sm.red[buf][half ^ 1][row];
+          if (!ok || o.x != o.x) {
+            stop = true;
+            break;
+          }
           mp = fmaxf(mp, o.x);
           ms = fmaxf(ms, o.y);
         }
@@ -709,20 +750,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         }
         const bool moved = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
         // ---- P goes where the scores were
+        // l's terms come from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them
+        const float back = ref - ml;
+        const bool far = __any_sync(0xffffffffu, back - fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) > 60.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t pk2[8];
           const float a = lv[i] - ref;
           const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
-          // l's terms from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them
-          const float d = -a - ml;
-          const bool far = __any_sync(0xffffffffu, d > 60.f);
-          if (far) {
-            float sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
-            l += sum;
-          }
+          uint32_t pk2[8];
           float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -732,22 +767,37 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             sum2 = add2(sum2, e);
             pk2[c] = pack_half2(e.x, e.y);
           }
-          if (!far) l += (sum2.x + sum2.y) * ex2(d);
           ptx::tmem_st8(ts + 8 * i, pk2);
+          if (!far) {
+            l += (sum2.x + sum2.y) * ex2(back - lv[i]);
+          } else {
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
+            l += sum;
+          }
         }
         ptx::tmem_wait_st();
         if (moved) {
           // O, with PV of tile J - 1 in it, moves to the new references
-          ok = warp_all(wait(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
+          ok = warp_all(hold(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
           if (ok) {
             ptx::tc_fence_after();
-            rescale_o_cols(trow + kTmOc + half * 128, alpha);
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              const uint32_t to = trow + kTmOc + half * 128 + 32 * cc;
+              uint32_t o[32];
+              ptx::tmem_ld32_wait(to, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              ptx::tmem_st32_wait(to, o);
+            }
           }
         }
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) {
-          ptx::mbar_arrive_cluster(lead_bar(&sm.p_full[buf]));
+          arrive_lead(&sm.p_full[buf], lead);
           if (J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
         }
       }
@@ -760,8 +810,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       more = ok && sm.rec[J % kTiles].n_tiles > 0;
       if (more) prepare(pc + 1u);
       sm.sum[half][row] = l;
-      ok = warp_all(ok && wait(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
-                    wait(&sm.o_full, pc & 1u, tmo, &sm.abort));
+      ok = warp_all(ok && hold(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
+                    hold(&sm.o_full, pc & 1u, tmo, &sm.abort));
       stop = ptx::named_bar_or(9, 256, !ok);
       if (stop) break;
       ptx::tc_fence_after();
@@ -774,6 +824,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       uint32_t any = 0u;
 #pragma unroll
       for (int w = 0; w < kHitWords; ++w) any |= *reinterpret_cast<volatile uint32_t*>(&sm.hit[set][w]);
+      const ChunkPiece& x = sm.piece[pc % kPieces];
+      const bool mine = lim > 0;
+      const int i_new = lim - 1 - x.base, pk = x.rb * kPairRows + int(rank) * 128 + row;
       const size_t at = size_t(x.t0 + i_new) * p.Hq + x.g * p.gqa + (pk - i_new * p.gqa);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
@@ -828,7 +881,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(lead_bar(&sm.o_free));
+      if (lane == 0) arrive_lead(&sm.o_free, lead);
       ++pc;
     }
     if (stop && lane == 0) {
