@@ -6,24 +6,25 @@
 // heads of a KV group x new rows, heads innermost) of one sequence; each CTA of a pair has 128 of
 // them, and the two share each tile of 128 keys: CTA r brings keys 64 r .. of K and dims 128 r .. of V.
 //
-// The products are 16-bit ones.  An e4m3 number is an fp16 number, so K and V enter as they are
-// stored and their scales stay apart: K's goes into the scores (fp32, per run of 16 keys), V's into the
-// exponent of the probability, p = 2^(score + log2 vs - ref).  Q goes as fp16 times a power of two
-// per row: exact for what lies within 2^-23 of the row's largest element, off by 2^-33 of that below.
-// p goes as fp16: off by 2^-11 of itself, and by 2^-25 where the row's largest is 2^3 at least (a
-// reference moves when p would pass 2^15, and then leaves the largest at 2^3).  The row's sum l is taken
-// from the fp32 probabilities against a reference of its own, without the V scales.
+// Scores are 8-bit products of the keys as they lie and of Q as e4m3 terms (two for a bf16's 8 bits, three for
+// an fp16's 11; what a row's elements lose is below 2^-19 of its largest), K's scale goes in after, per
+// run of 16 keys.  P.V is a 16-bit product: an e4m3 number is an fp16 number, so V enters as it is stored and its
+// scale goes into the exponent of the probability, p = 2^(score + log2 vs - ref).  p goes as fp16: off by
+// 2^-11 of itself, and by 2^-25 where the row's largest is 2^3 at least (a reference moves when p would pass
+// 2^15, and then leaves the largest at 2^3).  The row's sum l is taken from the fp32 probabilities against a
+// reference of its own, without the V scales.
 //
-// What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (8-bit terms, as the kernels
-// for few rows have them, would take 2560), beside 1024 clocks of ex2.
+// What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (three 8-bit terms of p, as the kernels for
+// few rows have them, would take 2560 in all; fp16 takes 2560), beside 1024 clocks of ex2.
 //
 // The segments' tiles (only those that some row sees) are laid end to end and cut into equal shares,
 // one a pair.  A piece that is a whole segment goes straight to `out`; the pieces of a segment that is
 // cut leave fp32 parts, two a pair at most, that kv8_join_kernel puts together.
 //
 // Roles (512 threads): warp 0 schedules (pieces, block numbers and scales of the tiles), warp 1 of the even
-// CTA issues the products, warps 4..7 convert K and V into shared memory, warps 8..15 are softmax and
-// epilogue (row = tensor-memory lane, 64 keys a thread).
+// CTA issues the products, warp 2 copies K, warps 4..7 convert V into shared memory, warps 8..15 are softmax and
+// epilogue: two teams of four take the tiles in turn, a thread has a row (its tensor-memory lane), so that one
+// team's softmax runs beside the other's and beside the products, and no maximum is exchanged within a tile.
 // TMEM: O 256 columns, two buffers of 128 for S and P.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -39,7 +40,8 @@ constexpr int kConvWarp = 4, kSoftWarp = 8;     // first warps
 // Registers a thread, by warpgroup, out of the launch's 128 (inc waits until they are there).
 constexpr int kRegsRest = 80, kRegsConv = 112, kRegsSoft = 160;
 static_assert(kRegsRest + kRegsConv + 2 * kRegsSoft <= 4 * 128, "the launch's registers");
-constexpr int kSlotC = 32768;                   // half a tile of K or V in fp16
+constexpr int kSlotK = 16384, kKs = 3;          // half a tile of K as it lies; slots
+constexpr int kSlotV = 32768, kVs = 2;          // half a tile of V in fp16
 constexpr int kGroup = 4;                       // tiles that the scheduler looks up together
 constexpr int kGroups = 4;                      // groups held
 constexpr int kTiles = kGroup * kGroups;
@@ -50,8 +52,8 @@ constexpr uint32_t kLead = 3;                   // what a segment costs beside i
 constexpr int kSnap = 4;                        // a cut this close to a segment's end is made there
 constexpr float kCap = 15.f, kTop = 3.f;        // p <= 2^15; a moved reference leaves 2^3
 constexpr uint32_t kTmOc = 0, kTmSc = 256;
-constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);
-constexpr uint32_t kIdescOc = ptx::idesc_f32acc(256, 256, 0, 1, 0);
+constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);   // e4m3 (format 0)
+constexpr uint32_t kIdescOc = ptx::idesc_f32acc(256, 256, 0, 1, 0);   // fp16 (format 0)
 
 struct ChunkArgs {
   const uint4* q;
@@ -85,30 +87,33 @@ struct ChunkPiece {
 struct TileRec {
   int key0, k_hi, pr_lo;       // first key; keys from k_hi on are not there; from pr_lo on not all rows see
   int g, n_tiles, piece;       // n_tiles of the piece that starts here; 0: the end of the share
-  int first, last;             // of its piece
+  int last;                    // of its piece
+  float lv_min;
   int blk[8];                  // by run of 16 keys: block, scale of K, log2 of V's
   float ks[8], lv[8];
 };
 
+template <bool kF16>
 struct __align__(1024) ChunkSmem {
-  uint8_t q[4 * 128 * 128];
-  uint8_t k[2][kSlotC], v[2][kSlotC];
+  static constexpr int kQTerms = kF16 ? 3 : 2;
+  uint8_t q[kQTerms][2][128 * 128];       // [term][half of D][row][128 bytes, swizzled]
+  uint8_t k[kKs][kSlotK], v[kVs][kSlotV];
   TileRec rec[kTiles];
   ChunkPiece piece[kPieces];
-  float2 red[2][2][128];                  // [tile parity][half][row]: maxima with vs, without
-  float sum[2][128];
+  float2 refs[2][128];                    // [tile parity][row]: the references after the tile
+  float sum[2][128];                      // [team][row]
   float fac[2][128];                      // by piece parity
   uint32_t hit[kHitSets][kHitWords];
   uint64_t rec_full[kGroups], rec_empty[kGroups];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done, q_full, o_full, o_free, drain;
+  uint64_t k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
+  uint64_t s_full[2], p_full[2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
   uint64_t hit_full[kHitSets];
   int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
   uint32_t cost[kKv8Seqs], at[kKv8Seqs + 1];   // of one KV head; of all, before each sequence
   uint32_t tmem_base;
   int abort, zero;
 };
-static_assert(sizeof(ChunkSmem) + 1024 <= 227 * 1024, "one CTA per SM");
+static_assert(sizeof(ChunkSmem<true>) + 1024 <= 227 * 1024, "one CTA per SM");
 
 template <int N>
 __device__ __forceinline__ void take_regs() {
@@ -131,7 +136,8 @@ __device__ __forceinline__ int tiles_of(const int4& s, int rb, int gqa) {
 }
 
 // The cut at position pos of the launch's segments (whole warp): at a segment's end where one is near.
-__device__ Cut cut_at(const ChunkSmem& sm, const ChunkArgs& p, uint32_t pos) {
+template <typename Sm>
+__device__ Cut cut_at(const Sm& sm, const ChunkArgs& p, uint32_t pos) {
   const int lane = threadIdx.x & 31;
   if (pos >= sm.at[p.B]) return Cut{p.B, 0, 0, 0};
   int lo = 0, hi = p.B - 1;
@@ -182,12 +188,12 @@ __device__ __forceinline__ bool before(const Cut& a, const Cut& b) {
   return a.b != b.b ? a.b < b.b : a.g != b.g ? a.g < b.g : a.rb != b.rb ? a.rb < b.rb : a.t < b.t;
 }
 
-// 16 e4m3 values to fp16.
-__device__ __forceinline__ void to_f16x16(const uint4& u, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t o[8];
+// Eight e4m3 values to fp16.
+__device__ __forceinline__ uint4 to_f16x8(uint2 u) {
+  const uint32_t w[2] = {u.x, u.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     asm("{\n"
         "  .reg .b16 l, h;\n"
         "  mov.b32 {l, h}, %2;\n"
@@ -196,8 +202,7 @@ __device__ __forceinline__ void to_f16x16(const uint4& u, uint4& lo, uint4& hi) 
         "}\n"
         : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
         : "r"(w[i]));
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // (in line: a kernel that shares its registers out again may not call)
@@ -205,7 +210,8 @@ __device__ __forceinline__ bool hold(uint64_t* bar, uint32_t parity, uint64_t tm
   return ptx::mbar_wait(bar, parity, tmo, abort);
 }
 
-__device__ __forceinline__ bool wait_rec(ChunkSmem& sm, uint32_t J, uint64_t tmo) {
+template <typename Sm>
+__device__ __forceinline__ bool wait_rec(Sm& sm, uint32_t J, uint64_t tmo) {
   const uint32_t G = J / kGroup;
   return hold(&sm.rec_full[G % kGroups], (G / kGroups) & 1u, tmo, &sm.abort);
 }
@@ -230,10 +236,10 @@ __device__ __noinline__ void put_back(const ChunkArgs& p, const uint32_t* hit, i
 }
 
 template <bool kF16>
-__global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_constant__ ChunkArgs p) {
+__global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ ChunkArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~uintptr_t(1023));
+  using Sm = ChunkSmem<kF16>;
+  Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t tmo = p.ctl.timeout_ns;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -242,15 +248,20 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < kGroups; ++i) {
       ptx::mbar_init(&sm.rec_full[i], 1);
-      ptx::mbar_init(&sm.rec_empty[i], 12);
+      ptx::mbar_init(&sm.rec_empty[i], 13);   // K's copies, 4 converting warps, 8 of softmax
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.k_full[i], 8);
-      ptx::mbar_init(&sm.v_full[i], 8);
-      ptx::mbar_init(&sm.k_empty[i], 1);
-      ptx::mbar_init(&sm.v_empty[i], 1);
       ptx::mbar_init(&sm.s_full[i], 1);
-      ptx::mbar_init(&sm.p_full[i], 16);
+      ptx::mbar_init(&sm.p_full[i], 8);
+      for (int k = 0; k < 4; ++k) ptx::mbar_init(&sm.ref_full[i][k], 1);
+    }
+    for (int i = 0; i < kKs; ++i) {
+      ptx::mbar_init(&sm.k_full[i], 1);
+      ptx::mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVs; ++i) {
+      ptx::mbar_init(&sm.v_full[i], 8);
+      ptx::mbar_init(&sm.v_empty[i], 1);
     }
     ptx::mbar_init(&sm.pv_done, 1);
     ptx::mbar_init(&sm.q_full, 16);
@@ -326,12 +337,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       bool ok = true, done = false;
       int4 s = make_int4(0, 0, 0, 0);
       int t = 0, t_end = 0, pr_lo = 0, k_hi = 0;
-      bool in_piece = false, fresh = false;
+      bool in_piece = false;
       while (!done) {
         // this group's tiles: every lane goes through them, and keeps its own
         TileRec r;
         r.n_tiles = 0;
-        r.key0 = r.k_hi = r.pr_lo = r.g = r.piece = r.first = r.last = 0;
+        r.key0 = r.k_hi = r.pr_lo = r.g = r.piece = r.last = 0;
         int my_b = 0;
         const uint32_t G = J / kGroup;
         if (G >= kGroups) {
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
               open = x;
             }
             if (lane == 0) sm.piece[n_pieces % kPieces] = x;
-            in_piece = fresh = true;
+            in_piece = true;
           }
           if ((lane >> 3) == q) {
             r.key0 = t * kTile;
@@ -371,11 +382,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             r.g = at.g;
             r.n_tiles = t_end - t;
             r.piece = int(n_pieces);
-            r.first = fresh;
             r.last = t + 1 == t_end;
             my_b = at.b;
           }
-          fresh = false;
           if (++t == t_end) {
             in_piece = false;
             ++n_pieces;
@@ -407,6 +416,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         o.blk[u] = blk;
         o.ks[u] = ks;
         o.lv[u] = lv;
+        float least = lv;
+#pragma unroll
+        for (int k = 1; k < 8; k <<= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, k));
         if (u == 0) {
           o.key0 = r.key0;
           o.k_hi = r.k_hi;
@@ -414,8 +426,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           o.g = r.g;
           o.n_tiles = r.n_tiles;
           o.piece = r.piece;
-          o.first = r.first;
           o.last = r.last;
+          o.lv_min = least;
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.rec_full[G % kGroups]);
@@ -442,27 +454,31 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       uint32_t J = 0, pc = 0;
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
-        const uint32_t ks = n & 1u;
-        if (!hold(&sm.k_full[ks], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        const uint32_t ks = n % kKs;
+        if (!hold(&sm.k_full[ks], (n / kKs) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
         const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < 16; ++kk)
-          ptx::mma_ss_pair(tmem + kTmSc + ks * 128, ptx::sdesc_at(qd, (kk >> 2) * 16384 + (kk & 3) * 32),
-                           ptx::sdesc_at(kd, (kk >> 2) * 8192 + (kk & 3) * 32), kIdescSc, kk > 0);
-        ptx::tc_commit_pair(&sm.s_full[ks], 3);
+        for (int t = 0; t < Sm::kQTerms; ++t)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_ss_pair_f8(tmem + kTmSc + (n & 1u) * 128,
+                                ptx::sdesc_at(qd, t * 32768 + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                ptx::sdesc_at(kd, (kk >> 2) * (kSlotK / 2) + (kk & 3) * 32), kIdescSc,
+                                t > 0 || kk > 0);
+        ptx::tc_commit_pair(&sm.s_full[n & 1u], 3);
         ptx::tc_commit_pair(&sm.k_empty[ks], 3);
         return true;
       };
       const auto issue_pv = [&](uint32_t n, bool first) -> bool {
-        const uint32_t vs = n & 1u;
-        if (!hold(&sm.p_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
-        if (!hold(&sm.v_full[vs], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        const uint32_t vs = n % kVs;
+        if (!hold(&sm.p_full[n & 1u], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!hold(&sm.v_full[vs], (n / kVs) & 1u, tmo, &sm.abort)) return false;
         ptx::tc_fence_after();
-        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), 16384, 1024);
+        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kSlotV / 2, 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + vs * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+          ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + (n & 1u) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                            ptx::sdesc_at(vd, kk * 2048), kIdescOc, !first || kk > 0);
         ptx::tc_commit_pair(&sm.pv_done, 3);
         ptx::tc_commit_pair(&sm.v_empty[vs], 3);
@@ -477,11 +493,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (!ok) break;
         ptx::tc_fence_after();
         ok = issue_s(J);
+        if (ok && n_tiles > 1) ok = issue_s(J + 1);
+        // O of the last piece has been read by every warp
+        if (ok && pc > 0) ok = hold(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
         for (int j = 0; ok && j < n_tiles; ++j) {
-          if (j + 1 < n_tiles) ok = issue_s(J + j + 1);
-          // O of the last piece has been read by every warp
-          if (ok && j == 0 && pc > 0) ok = hold(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
-          if (ok) ok = issue_pv(J + j, j == 0);
+          ok = issue_pv(J + j, j == 0);
+          // S of tile j + 2 goes where P of tile j lies: products run in the order of issue
+          if (ok && j + 2 < n_tiles) ok = issue_s(J + j + 2);
         }
         if (ok) ptx::tc_commit_pair(&sm.o_full, 3);
         J += n_tiles;
@@ -494,6 +512,51 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       // every product issued has to end before tensor memory is given back
       ptx::tc_commit_pair(&sm.drain, 1);
       hold(&sm.drain, 0, tmo, &sm.zero);
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- copies of K
+      // This CTA's 64 keys of a tile, a box of up to 64 keys x 128 dims a lane; both CTAs' bytes count on the
+      // even CTA's barrier.  Keys that are not there are not copied (their scores are not used).
+      const int box_log2 = min(p.bs_log2, 6), boxes = 64 >> box_log2;
+      uint32_t J = 0;
+      bool ok = true;
+      if (lane == 0) ptx::prefetch_tmap(&tmK);
+      for (;; ++J) {
+        ok = warp_all(wait_rec(sm, J, tmo));
+        if (!ok) break;
+        const TileRec& r = sm.rec[J % kTiles];
+        if (r.n_tiles == 0) break;
+        const uint32_t ks = J % kKs;
+        if (J >= kKs) ok = warp_all(hold(&sm.k_empty[ks], (J / kKs - 1u) & 1u, tmo, &sm.abort));
+        if (!ok) break;
+        const int left = r.k_hi - r.key0;
+        if (lead && lane == 0) {
+          const int n0 = (min(max(left, 0), 64) + (1 << box_log2) - 1) >> box_log2;
+          const int n1 = (min(max(left - 64, 0), 64) + (1 << box_log2) - 1) >> box_log2;
+          ptx::mbar_arrive_expect_tx(&sm.k_full[ks], uint32_t(n0 + n1) << (box_log2 + 8));
+        }
+        __syncwarp();
+        const int at = 64 * int(rank) + (lane << box_log2);   // first key of this lane's box
+        if (lane < boxes && at < left) {
+          const int blk = r.blk[at >> 4];
+          // a block outside the pool: past the map's last row, which copies zeros
+          const int row = blk >= 0 ? ((blk * p.Hkv + r.g) << p.bs_log2) + ((r.key0 + at) & ((1 << p.bs_log2) - 1))
+                                   : (p.num_blocks * p.Hkv) << p.bs_log2;
+          const uint32_t bar = ptx::mapa_shared(ptx::smem_addr(&sm.k_full[ks]), 0);
+          uint8_t* const d = sm.k[ks] + (lane << (box_log2 + 7));
+          ptx::tma_load_2d_pair(d, &tmK, bar, 0, row);
+          ptx::tma_load_2d_pair(d + kSlotK / 2, &tmK, bar, 128, row);
+        }
+        __syncwarp();
+        if (lane == 0 && J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
+      }
+      if (!ok && lane == 0) {
+        sm.abort = 1;
+        record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+      }
+      // every copy of the pair has landed before it ends
+      if (lead && lane == 0)
+        for (uint32_t c = J - min(J, uint32_t(kKs)); c < J; ++c)
+          hold(&sm.k_full[c % kKs], (c / kKs) & 1u, tmo, &sm.zero);
     }
     __syncwarp();
   } else if (warp < kSoftWarp) {
@@ -503,57 +566,51 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     const int bs_mask = (1 << p.bs_log2) - 1;
     const uint32_t peer_hit = ptx::mapa_shared(ptx::smem_addr(&sm.hit[0][0]), rank ^ 1u);
     bool ok = true;
-    // Items K0, K1, V0, K2, V1, ..; an item's eight loads a thread are on their way while the last one
-    // is converted.  A warp has the 16 keys of one run of K (two keys' 256 bytes a load) and the 32 of
-    // two of V (four keys' 128), so that a run's address is worked out once.
-    const int k_sub = lane >> 4, v_sub = lane >> 3;          // key of a load
-    const bool odd = (lane & 4) != 0;   // the order of a thread's two chunks: 8 lanes meet no bank twice
-    const int kc = (lane & 3) * 2 + (odd ? 1 : 0);           // the first one's place among 8
-    uint32_t const k_off = ((lane & 15) >> 2) * 8192 + (w * 16 + k_sub) * 128 + ((kc ^ k_sub) << 4);
-    uint32_t const v_off = ((lane & 7) >> 2) * 16384 + (w * 32 + v_sub) * 128 + ((kc ^ v_sub) << 4);
-    uint4 u[2][8];
-    const auto load = [&](uint32_t J, bool is_v, uint4 (&d)[8]) -> bool {
+    // The next tile's loads are on their way while the slot is waited for.  A warp has the 32 keys of two runs, four
+    // keys a load; a thread has dims 8 c .. of both 64s (c = lane % 8), so that eight lanes' stores meet no bank
+    // twice.
+    const int sub = lane >> 3;          // key of a load
+    const uint32_t off = (w * 32 + sub) * 128 + (((lane & 7) ^ sub) << 4);
+    uint2 u[8][2];
+    const auto load = [&](uint32_t J) -> bool {
       if (!warp_all(ok && wait_rec(sm, J, tmo))) {
         ok = false;
         return false;
       }
       const TileRec& r = sm.rec[J % kTiles];
       if (r.n_tiles == 0) return false;
-      const int g = r.g, left = r.k_hi - r.key0;
+      const int left = r.k_hi - r.key0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {   // (K: the same run twice)
-        const int run = is_v ? 2 * w + h : 4 * int(rank) + w, blk = r.blk[run];
+      for (int h = 0; h < 2; ++h) {
+        const int run = 2 * w + h, blk = r.blk[run];
         const int n = blk >= 0 ? left - 16 * run : 0;          // its keys
         const uint8_t* const a =
-            (is_v ? p.v_pool + 128 * rank + (lane & 7) * 16 + v_sub * 256
-                  : p.k_pool + (lane & 15) * 16 + k_sub * 256) +
-            (((size_t(max(blk, 0)) * p.Hkv + g) << p.bs_log2) + ((r.key0 + 16 * run) & bs_mask)) * 256;
+            p.v_pool + 128 * rank + (lane & 7) * 8 + sub * 256 +
+            (((size_t(max(blk, 0)) * p.Hkv + r.g) << p.bs_log2) + ((r.key0 + 16 * run) & bs_mask)) * 256;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = is_v ? 4 * i : 2 * (4 * h + i);
-          d[4 * h + i] = make_uint4(0u, 0u, 0u, 0u);
-          if (key + (is_v ? v_sub : k_sub) < n)
-            d[4 * h + i] = __ldg(reinterpret_cast<const uint4*>(a + key * 256));
+          u[4 * h + i][0] = u[4 * h + i][1] = make_uint2(0u, 0u);
+          if (4 * i + sub < n) {
+            u[4 * h + i][0] = __ldg(reinterpret_cast<const uint2*>(a + i * 1024));
+            u[4 * h + i][1] = __ldg(reinterpret_cast<const uint2*>(a + i * 1024 + 64));
+          }
         }
       }
       return true;
     };
-    const auto store = [&](uint32_t J, bool is_v, uint4 (&d)[8]) {
-      const uint32_t sl = J & 1u;
-      if (J >= 2)
-        ok = warp_all(ok && hold(is_v ? &sm.v_empty[sl] : &sm.k_empty[sl], ((J >> 1) - 1u) & 1u, tmo,
-                                 &sm.abort));
-      if (!ok) return;
+    for (uint32_t J = 0; load(J); ++J) {
+      const uint32_t vs = J % kVs;
+      if (J >= kVs)
+        ok = warp_all(ok && hold(&sm.v_empty[vs], (J / kVs - 1u) & 1u, tmo, &sm.abort));
+      if (!ok) break;
       const TileRec& r = sm.rec[J % kTiles];
-      if (is_v && r.key0 + kTile > r.pr_lo) {
-        // V rows that some rows do not see: their NaN are taken out, and noted in both CTAs
-        const int key0 = r.key0 + 32 * w + v_sub, pr_lo = r.pr_lo, set = r.piece % kHitSets;
-#pragma unroll 1
+      if (r.key0 + kTile > r.pr_lo) {
+        // rows that some rows of the segment do not see: their NaN are taken out, and noted in both CTAs
+        const int key0 = r.key0 + 32 * w + sub, pr_lo = r.pr_lo, set = r.piece % kHitSets;
+#pragma unroll
         for (int s = 0; s < 8; ++s) {
           const int key = key0 + 4 * s;
-          uint4 x = d[0];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) x = s == i ? d[i] : x;
+          uint4 x = make_uint4(u[s][0].x, u[s][0].y, u[s][1].x, u[s][1].y);
           if (key >= pr_lo && clear_nan8(x)) {
             const int h = key - pr_lo;
             atomicOr(&sm.hit[set][h >> 5], 1u << (h & 31));
@@ -561,53 +618,31 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
                              peer_hit + uint32_t(set * kHitWords + (h >> 5)) * 4u),
                          "r"(1u << (h & 31))
                          : "memory");
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = s == i ? x : d[i];
+            u[s][0] = make_uint2(x.x, x.y);
+            u[s][1] = make_uint2(x.z, x.w);
           }
         }
       }
-      uint8_t* const slot = is_v ? sm.v[sl] + v_off : sm.k[sl] + k_off;
+      const uintptr_t slot = reinterpret_cast<uintptr_t>(sm.v[vs] + off);
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        uint4 lo, hi;
-        to_f16x16(d[s], lo, hi);
-        // row 2 s + k_sub (4 s + v_sub) of the warp's: its swizzle differs from row k_sub's in two bits
-        const uintptr_t a = (reinterpret_cast<uintptr_t>(slot) ^ uintptr_t(is_v ? (s & 1) * 64 : (s & 3) * 32)) +
-                            s * (is_v ? 512 : 256);
-        *reinterpret_cast<uint4*>(a) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(a ^ 16) = odd ? lo : hi;
+        // row 4 s + sub of the warp's: its swizzle differs from row sub's in one bit
+        const uintptr_t a = (slot ^ uintptr_t((s & 1) * 64)) + s * 512;
+        *reinterpret_cast<uint4*>(a) = to_f16x8(u[s][0]);
+        *reinterpret_cast<uint4*>(a + kSlotV / 2) = to_f16x8(u[s][1]);
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_lead(is_v ? &sm.v_full[sl] : &sm.k_full[sl], lead);
-        if (is_v) {
-          if (r.last) {
-            uint64_t* const h = &sm.hit_full[r.piece % kHitSets];
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 0));
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 1));
-          }
-          // the group's last tile has been read
-          if (J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
+        arrive_lead(&sm.v_full[vs], lead);
+        if (r.last) {
+          uint64_t* const h = &sm.hit_full[r.piece % kHitSets];
+          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 0));
+          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 1));
         }
+        if (J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
       }
       __syncwarp();
-    };
-    // two items a round, so that the buffers are fixed: V of tile J and K of tile J + 2
-    bool more = load(0, false, u[0]);
-    if (more) {
-      bool next = load(1, false, u[1]);
-      store(0, false, u[0]);
-      load(0, true, u[0]);
-      if (next) store(1, false, u[1]);
-      for (uint32_t J = 0; ok; ++J) {
-        const bool after = next && load(J + 2, false, u[1]);
-        store(J, true, u[0]);
-        if (!next) break;
-        load(J + 1, true, u[0]);
-        if (after) store(J + 2, false, u[1]);
-        next = after;
-      }
     }
     if (!ok && lane == 0) {
       sm.abort = 1;
@@ -617,12 +652,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------ softmax, epilogue
     take_regs<kRegsSoft>();
-    const int sw = warp - kSoftWarp, half = sw >> 2, qd = warp & 3, row = qd * 32 + lane;
+    const int sw = warp - kSoftWarp, qd = warp & 3, row = qd * 32 + lane;
+    const uint32_t team = uint32_t(sw) >> 2;   // tiles of this parity; in the epilogue, columns 128 team ..
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
-    const uint32_t bar_id = 1 + qd;   // the two warps of a quadrant
     uint32_t J = 0, pc = 0;
     bool ok = true;
-    // Q's rows of piece n as fp16; then its products may start.  (The last piece's S products are done.)
+    // Q's terms of piece n; then its products may start.  (The last piece's S products are done.)
     const auto prepare = [&](uint32_t n) {
       const ChunkPiece& x = sm.piece[n % kPieces];
       const int p0 = x.rb * kPairRows + int(rank) * 128, n_rows = min(128, x.rows * p.gqa - p0);
@@ -652,13 +687,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           // an infinite element makes its row's scores NaN, as in the formula
 #pragma unroll
           for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
-          uint4 o;
-          o.x = pack_half2(f[0], f[1]);
-          o.y = pack_half2(f[2], f[3]);
-          o.z = pack_half2(f[4], f[5]);
-          o.w = pack_half2(f[6], f[7]);
-          *reinterpret_cast<uint4*>(sm.q + (lane >> 3) * 16384 + rr * 128 +
-                                    (((lane & 7) ^ (rr & 7)) << 4)) = o;
+#pragma unroll
+          for (int t = 0; t < Sm::kQTerms; ++t) {
+            uint2 o;
+            o.x = take_term(f[0], f[1], 1.f);
+            o.x |= take_term(f[2], f[3], 1.f) << 16;
+            o.y = take_term(f[4], f[5], 1.f);
+            o.y |= take_term(f[6], f[7], 1.f) << 16;
+            *reinterpret_cast<uint2*>(sm.q[t][lane >> 4] + rr * 128 +
+                                      ((((lane & 15) >> 1) ^ (rr & 7)) << 4) + (lane & 1) * 8) = o;
+          }
         }
       }
       ptx::fence_proxy_async_smem();
@@ -685,142 +723,156 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       float ref = kNone, ml = kNone, l = 0.f;
       for (int j = 0; j < n_tiles; ++j, ++J) {
         const uint32_t buf = J & 1u;
+        if (buf != team) continue;
         ok = ok && wait_rec(sm, J, tmo) && hold(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         __syncwarp();
+        if (!ok) break;
+        ptx::tc_fence_after();
         const TileRec& r = sm.rec[J % kTiles];
-        const uint32_t ts = trow + kTmSc + buf * 128 + half * 64;
-        const int key0 = r.key0 + half * 64;
-        uint32_t s[64];
-        float f[4], lv[4];
+        const uint32_t ts = trow + kTmSc + buf * 128;
+        const int left = lim - r.key0;   // keys of the tile that the row sees
+        // Loops over 32 keys, not unrolled: the roles' code shares the schedulers' instruction caches.
+        // A run's score factor is finite and not 0, so that a hidden key's -inf stays one and 0 stays 0.
+        const auto factors = [&](int q) -> float2 {
+          const float2 k2 = *reinterpret_cast<const float2*>(&r.ks[2 * q]);
+          return make_float2(fminf(fmaxf(fac * k2.x, 1e-37f), 3e38f), fminf(fmaxf(fac * k2.y, 1e-37f), 3e38f));
+        };
+        const auto scores = [&](int q, uint32_t (&s)[32]) {
+          ptx::tmem_ld32_wait(ts + 32 * q, s);
+          if (left < 32 * q + 32) {   // keys that the row does not see
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (32 * q + c >= left) s[c] = 0xFF800000u;
+          }
+        };
         float mp = -INFINITY, ms = -INFINITY;
-        if (ok) {
-          ptx::tc_fence_after();
-          ptx::tmem_ld64_wait(ts, s);
-          const float4 k4 = *reinterpret_cast<const float4*>(&r.ks[4 * half]);
-          const float4 v4 = *reinterpret_cast<const float4*>(&r.lv[4 * half]);
-          // finite and not 0, so that a hidden key's -inf stays one and 0 stays 0
-          f[0] = fminf(fmaxf(fac * k4.x, 1e-37f), 3e38f);
-          f[1] = fminf(fmaxf(fac * k4.y, 1e-37f), 3e38f);
-          f[2] = fminf(fmaxf(fac * k4.z, 1e-37f), 3e38f);
-          f[3] = fminf(fmaxf(fac * k4.w, 1e-37f), 3e38f);
-          lv[0] = v4.x;
-          lv[1] = v4.y;
-          lv[2] = v4.z;
-          lv[3] = v4.w;
-          if (key0 + 64 > lim) {   // keys that the row does not see
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          scores(q, s);
+          const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[2 * q]);
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (key0 + c >= lim) s[c] = 0xFF800000u;
-          }
+          for (int i = 0; i < 2; ++i) {
+            float m = fmaxf(__uint_as_float(s[16 * i]), __uint_as_float(s[16 * i + 1]));
+            float n = fmaxf(__uint_as_float(s[16 * i + 2]), __uint_as_float(s[16 * i + 3]));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float m0 = __uint_as_float(s[16 * i]), m1 = __uint_as_float(s[16 * i + 1]);
-#pragma unroll
-            for (int c = 2; c < 16; c += 2) {
-              m0 = fmaxf(m0, __uint_as_float(s[16 * i + c]));
-              m1 = fmaxf(m1, __uint_as_float(s[16 * i + c + 1]));
+            for (int c = 4; c < 16; c += 4) {
+              m = fmaxf(fmaxf(m, __uint_as_float(s[16 * i + c])), __uint_as_float(s[16 * i + c + 1]));
+              n = fmaxf(fmaxf(n, __uint_as_float(s[16 * i + c + 2])), __uint_as_float(s[16 * i + c + 3]));
             }
-            const float m = fmaxf(m0, m1) * f[i];
+            m = fmaxf(m, n) * (i ? f2.y : f2.x);
             ms = fmaxf(ms, m);
-            mp = fmaxf(mp, m + lv[i]);
+            mp = fmaxf(mp, m + (i ? lv2.y : lv2.x));
           }
         }
-        // (a maximum is never NaN: that says that the warp gives up)
-        sm.red[buf][half][row] = make_float2(ok ? mp : __int_as_float(0x7FC00000), ms);
-        ptx::named_bar_sync(bar_id, 64);
-        {
-          const float2 o = sm.red[buf][half ^ 1][row];
-          if (!ok || o.x != o.x) {
-            stop = true;
-            break;
-          }
-          mp = fmaxf(mp, o.x);
-          ms = fmaxf(ms, o.y);
+        // ---- references: those after the last tile, moved on
+        float2 at = make_float2(kNone, kNone);
+        if (j > 0) {
+          ok = warp_all(hold(&sm.ref_full[buf ^ 1u][qd], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
+          if (!ok) break;
+          at = sm.refs[buf ^ 1u][row];
         }
-        // ---- references (both threads of a row do the same)
-        float alpha = 1.f;
-        if (mp > ref + kCap) {
-          alpha = ex2(ref - (mp - kTop));
-          ref = mp - kTop;
-        }
-        if (ms > ml + kLSlack) {
-          l *= ex2(ml - ms);
-          ml = ms;
-        }
-        const bool moved = j > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+        // (where one row's has to move, O is scaled anyway, and those of the warp's others go along)
+        const bool moved = __any_sync(0xffffffffu, mp > at.x + kCap);
+        ref = moved ? fmaxf(at.x, mp - kTop) : at.x;
+        if (ms > at.y + kLSlack) at.y = ms;
+        sm.refs[buf][row] = make_float2(ref, at.y);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.ref_full[buf][qd]);
+        l *= ex2(ml - at.y);
+        ml = at.y;
         // ---- P goes where the scores were
         // l's terms come from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them
         const float back = ref - ml;
-        const bool far = __any_sync(0xffffffffu, back - fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) > 60.f);
+        const bool far = __any_sync(0xffffffffu, back - r.lv_min > 60.f);
+        if (far) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32];
+            scores(q, s);
+            const float2 f2 = factors(q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = lv[i] - ref;
-          const float2 f2 = make_float2(f[i], f[i]), a2 = make_float2(a, a);
-          uint32_t pk2[8];
-          float2 sum2 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float2 y = fma2(make_float2(__uint_as_float(s[16 * i + 2 * c]),
-                                              __uint_as_float(s[16 * i + 2 * c + 1])), f2, a2);
-            const float2 e = make_float2(ex2(y.x), ex2(y.y));
-            sum2 = add2(sum2, e);
-            pk2[c] = pack_half2(e.x, e.y);
+            for (int c = 0; c < 32; ++c) l += ex2(fmaf(__uint_as_float(s[c]), c < 16 ? f2.x : f2.y, -ml));
           }
-          ptx::tmem_st8(ts + 8 * i, pk2);
-          if (!far) {
-            l += (sum2.x + sum2.y) * ex2(back - lv[i]);
-          } else {
-            float sum = 0.f;
+        }
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          scores(q, s);
+          const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[2 * q]);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) sum += ex2(fmaf(__uint_as_float(s[16 * i + c]), f[i], -ml));
-            l += sum;
+          for (int i = 0; i < 2; ++i) {
+            const float fi = i ? f2.y : f2.x, lv = i ? lv2.y : lv2.x, a = lv - ref;
+            const float2 ff = make_float2(fi, fi), aa = make_float2(a, a);
+            uint32_t pk[8];
+            float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float2 y = fma2(make_float2(__uint_as_float(s[16 * i + 2 * c]),
+                                                __uint_as_float(s[16 * i + 2 * c + 1])), ff, aa);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              sum2 = add2(sum2, e);
+              pk[c] = pack_half2(e.x, e.y);
+            }
+            ptx::tmem_st8(ts + 64 * (q >> 1) + 16 * (q & 1) + 8 * i, pk);
+            if (!far) l += (sum2.x + sum2.y) * ex2(back - lv);
           }
         }
         ptx::tmem_wait_st();
-        if (moved) {
+        if (moved && j > 0) {
           // O, with PV of tile J - 1 in it, moves to the new references
           ok = warp_all(hold(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
-          if (ok) {
-            ptx::tc_fence_after();
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const float alpha = ex2(at.x - ref);
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-              const uint32_t to = trow + kTmOc + half * 128 + 32 * cc;
-              uint32_t o[32];
-              ptx::tmem_ld32_wait(to, o);
+          for (int cc = 0; cc < 8; ++cc) {
+            const uint32_t to = trow + kTmOc + 32 * cc;
+            uint32_t o[32];
+            ptx::tmem_ld32_wait(to, o);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              ptx::tmem_st32_wait(to, o);
-            }
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            ptx::tmem_st32_wait(to, o);
           }
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) {
+        if (lane == 0) {
           arrive_lead(&sm.p_full[buf], lead);
-          if (J % kGroup == kGroup - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
+          // (its second tile of the group)
+          if ((J % kGroup) >> 1 == kGroup / 2 - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
         }
       }
-      if (stop) {
+      if (!ok) {
+        sm.abort = 1;
         ptx::named_bar_or(9, 256, true);
+        stop = true;
         break;
       }
+      // S of the last tile, be it the other team's, has read Q before the next piece's is written
+      ok = warp_all(hold(&sm.s_full[(J - 1u) & 1u], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
       // ---- the next piece may start while this one ends
       ok = warp_all(ok && wait_rec(sm, J, tmo));
       more = ok && sm.rec[J % kTiles].n_tiles > 0;
       if (more) prepare(pc + 1u);
-      sm.sum[half][row] = l;
+      ok = warp_all(ok && hold(&sm.ref_full[(J - 1u) & 1u][qd], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
+      const float2 fin = sm.refs[(J - 1u) & 1u][row];   // the references after the last tile
+      ref = fin.x;
+      l *= ex2(ml - fin.y);
+      ml = fin.y;
+      sm.sum[team][row] = l;
       ok = warp_all(ok && hold(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
                     hold(&sm.o_full, pc & 1u, tmo, &sm.abort));
       stop = ptx::named_bar_or(9, 256, !ok);
       if (stop) break;
       ptx::tc_fence_after();
-      const float L = l + sm.sum[half ^ 1][row];
+      const float L = l + sm.sum[team ^ 1u][row];
       const float inv = L == 0.f ? 0.f : 1.f / L, ex = ex2(0.5f * (ref - ml));
       const float lse = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
       const int set = pc % kHitSets;
       // every warp is past the last piece, whose hits may go
-      if (half == 0 && row < kHitWords) sm.hit[(pc + kHitSets - 1) % kHitSets][row] = 0u;
+      if (team == 0 && row < kHitWords) sm.hit[(pc + kHitSets - 1) % kHitSets][row] = 0u;
       uint32_t any = 0u;
 #pragma unroll
       for (int w = 0; w < kHitWords; ++w) any |= *reinterpret_cast<volatile uint32_t*>(&sm.hit[set][w]);
@@ -830,7 +882,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       const size_t at = size_t(x.t0 + i_new) * p.Hq + x.g * p.gqa + (pk - i_new * p.gqa);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
-        const int col = half * 128 + 32 * cc;
+        const int col = int(team) * 128 + 32 * cc;
         __syncwarp();
         uint32_t o[32];
         ptx::tmem_ld32_wait(trow + kTmOc + col, o);
@@ -870,10 +922,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         }
       }
       if (any != 0u && mine && L != 0.f)
-        put_back(p, sm.hit[set], x.b, x.g, x.base + x.rb * kPairRows / p.gqa + 1, lim, half * 128,
+        put_back(p, sm.hit[set], x.b, x.g, x.base + x.rb * kPairRows / p.gqa + 1, lim, int(team) * 128,
                  x.part < 0 ? nullptr : p.o_parts + (size_t(x.part) * kPairRows + int(rank) * 128 + row) * 256,
                  p.out + at * 256, kF16 ? 0x7E00u : 0x7FC0u);
-      if (mine && half == 0) {
+      if (mine && team == 0) {
         if (x.part >= 0)
           p.lse_parts[size_t(x.part) * kPairRows + int(rank) * 128 + row] = lse;
         else if (p.lse != nullptr)
@@ -1015,12 +1067,12 @@ Workspace workspace_of(int pairs) {
 }
 
 template <bool kF16>
-cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {
-  const size_t smem = sizeof(ChunkSmem) + 1024;
+cudaError_t launch_chunk(const CUtensorMap& tmK, const ChunkArgs& a, cudaStream_t stream) {
+  const size_t smem = sizeof(ChunkSmem<kF16>) + 1024;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_chunk_kernel<kF16>), smem);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kv8_chunk_kernel<kF16>, dim3(unsigned(2 * a.pairs)), kThreadsC, smem, stream, 2, a);
+  e = launch_dependent(kv8_chunk_kernel<kF16>, dim3(unsigned(2 * a.pairs)), kThreadsC, smem, stream, 2, tmK, a);
   if (e != cudaSuccess) return e;
   note_launch(kF16 ? "kv8_chunk_kernel<fp16>" : "kv8_chunk_kernel<bf16>", 2 * a.pairs, kThreadsC, smem);
   const unsigned grid = unsigned(a.pairs * (kPairRows / kJoinRows));
@@ -1028,6 +1080,19 @@ cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess)
     note_launch(kF16 ? "kv8_join_kernel<fp16>" : "kv8_join_kernel<bf16>", grid, 256, 0);
   return e;
+}
+
+// K's pool by rows: boxes of 128 dims x a block's rows, 64 at most.
+bool encode_k(CUtensorMap* map, const ChunkArgs& a) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {256, cuuint64_t(a.num_blocks) * cuuint64_t(a.Hkv) << a.bs_log2};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {128, cuuint32_t(1) << (a.bs_log2 < 6 ? a.bs_log2 : 6)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.k_pool), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int prefill_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool, const float* k_scale,
@@ -1086,6 +1151,8 @@ int prefill_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool
   a.max_rows = max_rows;
   a.max_kv_len = max_kv_len;
   if (!make_launch_ctl(&a.ctl)) return GQA_ERR_CUDA;
+  CUtensorMap tmK;
+  if (!encode_k(&tmK, a)) return GQA_ERR_UNSUPPORTED;
   const long long fit = ((1LL << 31) - 1) / per_seq;
   const int step = fit < kKv8Seqs ? int(fit) : kKv8Seqs;
   for (int b0 = 0; b0 < B; b0 += step) {
@@ -1096,7 +1163,7 @@ int prefill_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool
     const long long units = (long long)a.B * Hkv * max_rb * tiles;
     a.pairs = units < most ? int(units) : most;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((f16 ? launch_chunk<true>(a, s) : launch_chunk<false>(a, s)) != cudaSuccess)
+    if ((f16 ? launch_chunk<true>(tmK, a, s) : launch_chunk<false>(tmK, a, s)) != cudaSuccess)
       return GQA_ERR_CUDA;
   }
   return GQA_OK;

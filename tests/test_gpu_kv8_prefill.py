@@ -30,8 +30,27 @@ def _check(c, rows, Hq, seed, dtype=torch.bfloat16, gate=True, **kw):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
 @pytest.mark.parametrize("rows,lens", [([1], [1]), ([100], [100]), ([5, 130, 1], [5, 700, 129]),
-                                       ([127, 0, 129], [128, 40, 130]), ([64, 300], [1200, 300])])
-def test_parity(rows, lens, dtype):
-    c = Cache(lens, 2, 64, seed=141)
+                                       ([127, 0, 129], [128, 40, 130]), ([64, 300], [1200, 300]),
+                                       ([2], [2900])])
+def test_parity(rows, lens, bs, dtype):
+    c = Cache(lens, 2, bs, seed=141)
     _check(c, rows, 12, 142, dtype)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (24, 4), (16, 2), (16, 1), (17, 1), (10, 2), (300, 1)])
+def test_head_layouts(Hq, Hkv):
+    c = Cache([300, 77], Hkv, 32, seed=143)
+    _check(c, [70, 77], Hq, 144)
+    _check(c, [3, 1], Hq, 145, torch.float16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_many_sequences_and_a_long_one(dtype):
+    """300 sequences go in two launches; one long context is cut among all pairs."""
+    lens = [17 * (i % 23) + 1 for i in range(300)]
+    c = Cache(lens, 1, 16, seed=146)
+    _check(c, [min(n, 1 + i % 40) for i, n in enumerate(lens)], 4, 147, dtype)
+    c = Cache([20000, 40], 1, 128, seed=148)
+    _check(c, [33, 40], 8, 149, dtype)
