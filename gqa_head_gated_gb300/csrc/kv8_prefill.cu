@@ -10,8 +10,8 @@
 // an fp16's 11; what a row's elements lose is below 2^-19 of its largest), K's scale goes in after, per
 // run of 16 keys.  P.V is a 16-bit product: an e4m3 number is an fp16 number, so V enters as it is stored and its
 // scale goes into the exponent of the probability, p = 2^(score + log2 vs - ref).  p goes as fp16: off by
-// 2^-11 of itself, and by 2^-25 where the row's largest is 2^3 at least (a reference moves when p would pass
-// 2^15, and then leaves the largest at 2^3).  The row's sum l is taken from the fp32 probabilities against a
+// 2^-11 of itself, and by 2^-25 where the row's largest is 1 at least (a reference moves when p would pass
+// 2^15, and then leaves the largest at 1).  The row's sum l is taken from the fp32 probabilities against a
 // reference of its own, without the V scales.
 //
 // What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (three 8-bit terms of p, as the kernels for
@@ -50,7 +50,7 @@ constexpr int kHitSets = 4;                     // pieces whose NaN keys are hel
 constexpr int kHitWords = kPairRows / 32;       // keys that only some rows of a segment see: < 256
 constexpr uint32_t kLead = 3;                   // what a segment costs beside its tiles, in tiles
 constexpr int kSnap = 4;                        // a cut this close to a segment's end is made there
-constexpr float kCap = 15.f, kTop = 3.f;        // p <= 2^15; a moved reference leaves 2^3
+constexpr float kCap = 15.f, kTop = 0.f;        // p <= 2^15; a moved reference leaves 1
 constexpr uint32_t kTmOc = 0, kTmSc = 256;
 constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);   // e4m3 (format 0)
 constexpr uint32_t kIdescOc = ptx::idesc_f32acc(256, 256, 0, 1, 0);   // fp16 (format 0)
@@ -106,7 +106,7 @@ struct __align__(1024) ChunkSmem {
   uint32_t hit[kHitSets][kHitWords];
   uint64_t rec_full[kGroups], rec_empty[kGroups];
   uint64_t k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
-  uint64_t s_full[2], p_full[2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
+  uint64_t s_full[2], p_full[2][2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
   uint64_t hit_full[kHitSets];
   int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
   uint32_t cost[kKv8Seqs], at[kKv8Seqs + 1];   // of one KV head; of all, before each sequence
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.s_full[i], 1);
-      ptx::mbar_init(&sm.p_full[i], 8);
+      for (int h = 0; h < 2; ++h) ptx::mbar_init(&sm.p_full[i][h], 8);
       for (int k = 0; k < 4; ++k) ptx::mbar_init(&sm.ref_full[i][k], 1);
     }
     for (int i = 0; i < kKs; ++i) {
@@ -373,6 +373,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
               open = x;
             }
             if (lane == 0) sm.piece[n_pieces % kPieces] = x;
+            // this CTA's rows of Q and of the gate are on their way to L2
+            const int r0 = at.rb * kPairRows + 128 * int(rank), r1 = min(r0 + 128, s.y * p.gqa);
+            for (int i = r0 + (lane >> 2); i < r1; i += 8) {
+              const size_t row = size_t(s.x + i / p.gqa) * p.Hq + at.g * p.gqa + i % p.gqa;
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + row * 32 + (lane & 3) * 8));
+              if (p.gate != nullptr && x.part < 0)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.gate + row * 256 + (lane & 3) * 64));
+            }
             in_piece = true;
           }
           if ((lane >> 3) == q) {
@@ -472,14 +480,17 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       };
       const auto issue_pv = [&](uint32_t n, bool first) -> bool {
         const uint32_t vs = n % kVs;
-        if (!hold(&sm.p_full[n & 1u], (n >> 1) & 1u, tmo, &sm.abort)) return false;
         if (!hold(&sm.v_full[vs], (n / kVs) & 1u, tmo, &sm.abort)) return false;
-        ptx::tc_fence_after();
         const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kSlotV / 2, 1024);
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) {   // (the first half's product runs beside the second's exponentials)
+          if (!hold(&sm.p_full[n & 1u][h], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+          ptx::tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + (n & 1u) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                           ptx::sdesc_at(vd, kk * 2048), kIdescOc, !first || kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + (n & 1u) * 128 + h * 64 + kk * 8,
+                             ptx::sdesc_at(vd, h * 8192 + kk * 2048), kIdescOc, !first || h > 0 || kk > 0);
+        }
         ptx::tc_commit_pair(&sm.pv_done, 3);
         ptx::tc_commit_pair(&sm.v_empty[vs], 3);
         return true;
@@ -662,19 +673,20 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       const ChunkPiece& x = sm.piece[n % kPieces];
       const int p0 = x.rb * kPairRows + int(rank) * 128, n_rows = min(128, x.rows * p.gqa - p0);
 #pragma unroll 1
-      for (int r0 = sw; r0 < 128; r0 += 32) {
-        uint4 u[4];
+      for (int r0 = sw; r0 < 128; r0 += 64) {
+        uint4 u[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int rr = r0 + 8 * k, i = (p0 + rr) / p.gqa;
           const size_t at = size_t(x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
           u[k] = rr < n_rows ? __ldg(p.q + at * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = r0 + 8 * k;
+#pragma unroll 1
+        for (int rr = r0; rr < r0 + 64; rr += 8) {
           float f[8];
-          const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+          const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+          for (int k = 0; k < 7; ++k) u[k] = u[k + 1];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float2 a = unpack_elem2<kF16>(w[c]);
@@ -738,19 +750,28 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           const float2 k2 = *reinterpret_cast<const float2*>(&r.ks[2 * q]);
           return make_float2(fminf(fmaxf(fac * k2.x, 1e-37f), 3e38f), fminf(fmaxf(fac * k2.y, 1e-37f), 3e38f));
         };
-        const auto scores = [&](int q, uint32_t (&s)[32]) {
-          ptx::tmem_ld32_wait(ts + 32 * q, s);
-          if (left < 32 * q + 32) {   // keys that the row does not see
+        if (__any_sync(0xffffffffu, left < kTile)) {   // keys that some row does not see: -inf
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32];
+            ptx::tmem_ld32_wait(ts + 32 * q, s);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (32 * q + c >= left) s[c] = 0xFF800000u;
+            ptx::tmem_st32_wait(ts + 32 * q, s);
+          }
+        }
+        // f(q, scores) for each 32 keys
+        const auto each = [&](auto&& f) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32];
+            ptx::tmem_ld32_wait(ts + 32 * q, s);
+            f(q, s);
           }
         };
         float mp = -INFINITY, ms = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          scores(q, s);
+        each([&](int q, uint32_t (&s)[32]) {
           const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[2 * q]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -765,7 +786,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             ms = fmaxf(ms, m);
             mp = fmaxf(mp, m + (i ? lv2.y : lv2.x));
           }
-        }
+        });
         // ---- references: those after the last tile, moved on
         float2 at = make_float2(kNone, kNone);
         if (j > 0) {
@@ -787,19 +808,21 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         const float back = ref - ml;
         const bool far = __any_sync(0xffffffffu, back - r.lv_min > 60.f);
         if (far) {
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t s[32];
-            scores(q, s);
+          each([&](int q, uint32_t (&s)[32]) {
             const float2 f2 = factors(q);
 #pragma unroll
             for (int c = 0; c < 32; ++c) l += ex2(fmaf(__uint_as_float(s[c]), c < 16 ? f2.x : f2.y, -ml));
-          }
+          });
         }
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          scores(q, s);
+        // Half a tile's P is there for the product (where O has to be scaled first, both at the end).
+        const bool scale = moved && j > 0;
+        const auto done = [&](int h) {
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_lead(&sm.p_full[buf][h], lead);
+        };
+        each([&](int q, uint32_t (&s)[32]) {
           const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[2 * q]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -818,9 +841,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             ptx::tmem_st8(ts + 64 * (q >> 1) + 16 * (q & 1) + 8 * i, pk);
             if (!far) l += (sum2.x + sum2.y) * ex2(back - lv);
           }
-        }
-        ptx::tmem_wait_st();
-        if (moved && j > 0) {
+          if ((q & 1) && !scale) done(q >> 1);
+        });
+        if (scale) {
           // O, with PV of tile J - 1 in it, moves to the new references
           ok = warp_all(hold(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
           if (!ok) break;
@@ -835,14 +858,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
             ptx::tmem_st32_wait(to, o);
           }
+          done(0);
+          done(1);
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          arrive_lead(&sm.p_full[buf], lead);
-          // (its second tile of the group)
-          if ((J % kGroup) >> 1 == kGroup / 2 - 1) ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
-        }
+        // (its second tile of the group)
+        if (lane == 0 && (J % kGroup) >> 1 == kGroup / 2 - 1)
+          ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
       }
       if (!ok) {
         sm.abort = 1;
@@ -862,6 +883,17 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       l *= ex2(ml - fin.y);
       ml = fin.y;
       sm.sum[team][row] = l;
+      const ChunkPiece& x = sm.piece[pc % kPieces];
+      const bool mine = lim > 0;
+      const int i_new = lim - 1 - x.base, pk = x.rb * kPairRows + int(rank) * 128 + row;
+      const size_t at = size_t(x.t0 + i_new) * p.Hq + x.g * p.gqa + (pk - i_new * p.gqa);
+      uint4 gt[16];   // this thread's 128 columns of the gate
+      const bool gated = p.gate != nullptr && mine && x.part < 0;
+      if (gated) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          gt[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + team * 128) + c);
+      }
       ok = warp_all(ok && hold(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
                     hold(&sm.o_full, pc & 1u, tmo, &sm.abort));
       stop = ptx::named_bar_or(9, 256, !ok);
@@ -876,16 +908,19 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       uint32_t any = 0u;
 #pragma unroll
       for (int w = 0; w < kHitWords; ++w) any |= *reinterpret_cast<volatile uint32_t*>(&sm.hit[set][w]);
-      const ChunkPiece& x = sm.piece[pc % kPieces];
-      const bool mine = lim > 0;
-      const int i_new = lim - 1 - x.base, pk = x.rb * kPairRows + int(rank) * 128 + row;
-      const size_t at = size_t(x.t0 + i_new) * p.Hq + x.g * p.gqa + (pk - i_new * p.gqa);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         const int col = int(team) * 128 + 32 * cc;
         __syncwarp();
         uint32_t o[32];
         ptx::tmem_ld32_wait(trow + kTmOc + col, o);
+        uint4 g4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          g4[c] = gt[c];
+#pragma unroll
+          for (int k = c; k < 12; k += 4) gt[k] = gt[k + 4];
+        }
         if (!mine) continue;
 #pragma unroll
         for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(L == 0.f ? 0.f : __uint_as_float(o[c]) * inv * ex * ex);
@@ -897,17 +932,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             d[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
                                __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
         } else {
-          uint4 gt[4];
-          if (p.gate != nullptr) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              gt[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + col) + c);
-          }
           uint4* const d = reinterpret_cast<uint4*>(p.out + at * 256 + col);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[4];
-            const uint32_t gw[4] = {gt[c].x, gt[c].y, gt[c].z, gt[c].w};
+            const uint32_t gw[4] = {g4[c].x, g4[c].y, g4[c].z, g4[c].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float2 y = make_float2(__uint_as_float(o[8 * c + 2 * e]), __uint_as_float(o[8 * c + 2 * e + 1]));
