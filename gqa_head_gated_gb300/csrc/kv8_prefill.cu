@@ -188,6 +188,14 @@ __device__ __forceinline__ bool before(const Cut& a, const Cut& b) {
   return a.b != b.b ? a.b < b.b : a.g != b.g ? a.g < b.g : a.rb != b.rb ? a.rb < b.rb : a.t < b.t;
 }
 
+// Two values to e4m3, and what they leave: h becomes h - e4m3(h), exactly.
+__device__ __forceinline__ uint32_t take_half_term(__half2& h) {
+  const uint32_t t = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&h), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw d = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(t), __NV_E4M3);
+  h = __hsub2(h, __half2(d));
+  return t;
+}
+
 // Eight e4m3 values to fp16.
 __device__ __forceinline__ uint4 to_f16x8(uint2 u) {
   const uint32_t w[2] = {u.x, u.y};
@@ -682,33 +690,36 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           u[k] = rr < n_rows ? __ldg(p.q + at * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll 1
-        for (int rr = r0; rr < r0 + 64; rr += 8) {
-          float f[8];
-          const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+        for (int rr = r0; rr < r0 + 64; rr += 16) {   // two rows at a time
 #pragma unroll
-          for (int k = 0; k < 7; ++k) u[k] = u[k + 1];
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+            // the row's largest |x|: 16-bit patterns without the sign are in order
+            uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                  __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+            m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+            const int e = scale_exp(__float_as_uint(elem_to_float<kF16>(m)));
+            if (lane == 0) sm.fac[n & 1u][rr + 8 * k] = pow2f(e) * kScaleLog2;
+            // a NaN or an infinity makes the row's scores NaN, as it does in the formula
+            const float inv = m >= (kF16 ? 0x7C00u : 0x7F80u) ? __int_as_float(0x7FC00000) : inv_pow2f(e);
+            __half2 h[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 a = unpack_elem2<kF16>(w[c]);
-            f[2 * c] = a.x;
-            f[2 * c + 1] = a.y;
+            for (int c = 0; c < 4; ++c) {
+              const float2 x = mul2(unpack_elem2<kF16>(w[c]), make_float2(inv, inv));
+              h[c] = __floats2half2_rn(x.x, x.y);
+            }
+            uint8_t* const to = sm.q[0][lane >> 4] + (rr + 8 * k) * 128 +
+                                ((((lane & 15) >> 1) ^ (rr & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll
+            for (int t = 0; t < Sm::kQTerms; ++t) {
+              uint32_t o[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[c] = take_half_term(h[c]);
+              *reinterpret_cast<uint2*>(to + t * 2 * 128 * 128) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+            }
           }
-          const int e = scale_exp(__reduce_max_sync(0xffffffffu, finite_amax_bits(f)));
-          if (lane == 0) sm.fac[n & 1u][rr] = pow2f(e) * kScaleLog2;
-          const float inv = inv_pow2f(e);
-          // an infinite element makes its row's scores NaN, as in the formula
 #pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] = isinf(f[c]) ? __int_as_float(0x7FC00000) : f[c] * inv;
-#pragma unroll
-          for (int t = 0; t < Sm::kQTerms; ++t) {
-            uint2 o;
-            o.x = take_term(f[0], f[1], 1.f);
-            o.x |= take_term(f[2], f[3], 1.f) << 16;
-            o.y = take_term(f[4], f[5], 1.f);
-            o.y |= take_term(f[6], f[7], 1.f) << 16;
-            *reinterpret_cast<uint2*>(sm.q[t][lane >> 4] + rr * 128 +
-                                      ((((lane & 15) >> 1) ^ (rr & 7)) << 4) + (lane & 1) * 8) = o;
-          }
+          for (int k = 0; k < 6; ++k) u[k] = u[k + 2];
         }
       }
       ptx::fence_proxy_async_smem();
@@ -900,7 +911,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       if (stop) break;
       ptx::tc_fence_after();
       const float L = l + sm.sum[team ^ 1u][row];
-      const float inv = L == 0.f ? 0.f : 1.f / L, ex = ex2(0.5f * (ref - ml));
+      const float ex = ex2(0.5f * (ref - ml)), inv = L == 0.f ? 0.f : ex / L;   // (O times both)
       const float lse = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
       const int set = pc % kHitSets;
       // every warp is past the last piece, whose hits may go
@@ -923,7 +934,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         }
         if (!mine) continue;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(L == 0.f ? 0.f : __uint_as_float(o[c]) * inv * ex * ex);
+        for (int c = 0; c < 32; c += 2) {
+          const float2 y = mul2(mul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])),
+                                     make_float2(inv, inv)), make_float2(ex, ex));
+          o[c] = __float_as_uint(L == 0.f ? 0.f : y.x);
+          o[c + 1] = __float_as_uint(L == 0.f ? 0.f : y.y);
+        }
         if (x.part >= 0) {
           float4* const d = reinterpret_cast<float4*>(
               p.o_parts + (size_t(x.part) * kPairRows + int(rank) * 128 + row) * 256 + col);
