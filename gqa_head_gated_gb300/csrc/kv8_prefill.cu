@@ -680,47 +680,54 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     const auto prepare = [&](uint32_t n) {
       const ChunkPiece& x = sm.piece[n % kPieces];
       const int p0 = x.rb * kPairRows + int(rank) * 128, n_rows = min(128, x.rows * p.gqa - p0);
-#pragma unroll 1
-      for (int r0 = sw; r0 < 128; r0 += 64) {
-        uint4 u[8];
+      // rows 16 sw .. of the CTA's 128: a lane finds the place of one, four rows' loads run ahead
+      long long place = -1;
+      {
+        const int rr = sw * 16 + (lane & 15), i = (p0 + rr) / p.gqa;
+        if (rr < n_rows) place = (long long)(x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
+      }
+      const auto load4 = [&](int r, uint4 (&u)[4]) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = r0 + 8 * k, i = (p0 + rr) / p.gqa;
-          const size_t at = size_t(x.t0 + i) * p.Hq + x.g * p.gqa + (p0 + rr - i * p.gqa);
-          u[k] = rr < n_rows ? __ldg(p.q + at * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 4; ++k) {
+          const long long at = __shfl_sync(0xffffffffu, place, r + k);
+          u[k] = at >= 0 ? __ldg(p.q + at * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
         }
+      };
+      uint4 u[4], next[4];
+      load4(0, u);
 #pragma unroll 1
-        for (int rr = r0; rr < r0 + 64; rr += 16) {   // two rows at a time
+      for (int r = 0; r < 16; r += 4) {
+        load4(min(r + 4, 12), next);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-            // the row's largest |x|: 16-bit patterns without the sign are in order
-            uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                                  __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-            m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-            const int e = scale_exp(__float_as_uint(elem_to_float<kF16>(m)));
-            if (lane == 0) sm.fac[n & 1u][rr + 8 * k] = pow2f(e) * kScaleLog2;
-            // a NaN or an infinity makes the row's scores NaN, as it does in the formula
-            const float inv = m >= (kF16 ? 0x7C00u : 0x7F80u) ? __int_as_float(0x7FC00000) : inv_pow2f(e);
-            __half2 h[4];
+        for (int k = 0; k < 4; ++k) {
+          const int rr = sw * 16 + r + k;
+          const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+          // the row's largest |x|: 16-bit patterns without the sign are in order
+          uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+          m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+          const int e = scale_exp(__float_as_uint(elem_to_float<kF16>(m)));
+          if (lane == 0) sm.fac[n & 1u][rr] = pow2f(e) * kScaleLog2;
+          // a NaN or an infinity makes the row's scores NaN, as it does in the formula
+          const float inv = m >= (kF16 ? 0x7C00u : 0x7F80u) ? __int_as_float(0x7FC00000) : inv_pow2f(e);
+          __half2 h[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float2 x = mul2(unpack_elem2<kF16>(w[c]), make_float2(inv, inv));
-              h[c] = __floats2half2_rn(x.x, x.y);
-            }
-            uint8_t* const to = sm.q[0][lane >> 4] + (rr + 8 * k) * 128 +
-                                ((((lane & 15) >> 1) ^ (rr & 7)) << 4) + (lane & 1) * 8;
+          for (int c = 0; c < 4; ++c) {
+            const float2 x = mul2(unpack_elem2<kF16>(w[c]), make_float2(inv, inv));
+            h[c] = __floats2half2_rn(x.x, x.y);
+          }
+          uint8_t* const to = sm.q[0][lane >> 4] + rr * 128 +
+                              ((((lane & 15) >> 1) ^ (rr & 7)) << 4) + (lane & 1) * 8;
 #pragma unroll
-            for (int t = 0; t < Sm::kQTerms; ++t) {
-              uint32_t o[4];
+          for (int t = 0; t < Sm::kQTerms; ++t) {
+            uint32_t o[4];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) o[c] = take_half_term(h[c]);
-              *reinterpret_cast<uint2*>(to + t * 2 * 128 * 128) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-            }
+            for (int c = 0; c < 4; ++c) o[c] = take_half_term(h[c]);
+            *reinterpret_cast<uint2*>(to + t * 2 * 128 * 128) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+          }
           }
 #pragma unroll
-          for (int k = 0; k < 6; ++k) u[k] = u[k + 2];
-        }
+        for (int k = 0; k < 4; ++k) u[k] = next[k];
       }
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
@@ -898,13 +905,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       const bool mine = lim > 0;
       const int i_new = lim - 1 - x.base, pk = x.rb * kPairRows + int(rank) * 128 + row;
       const size_t at = size_t(x.t0 + i_new) * p.Hq + x.g * p.gqa + (pk - i_new * p.gqa);
-      uint4 gt[16];   // this thread's 128 columns of the gate
       const bool gated = p.gate != nullptr && mine && x.part < 0;
-      if (gated) {
+      const auto gate32 = [&](int cc, uint4 (&g4)[4]) {   // 32 of this thread's 128 columns
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          gt[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + team * 128) + c);
-      }
+        for (int c = 0; c < 4; ++c)
+          if (gated) g4[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + team * 128) + 4 * cc + c);
+      };
+      uint4 g4[4], g_next[4];
+      gate32(0, g4);
       ok = warp_all(ok && hold(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
                     hold(&sm.o_full, pc & 1u, tmo, &sm.abort));
       stop = ptx::named_bar_or(9, 256, !ok);
@@ -925,14 +933,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         __syncwarp();
         uint32_t o[32];
         ptx::tmem_ld32_wait(trow + kTmOc + col, o);
-        uint4 g4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          g4[c] = gt[c];
-#pragma unroll
-          for (int k = c; k < 12; k += 4) gt[k] = gt[k + 4];
-        }
         if (!mine) continue;
+        gate32(min(cc + 1, 3), g_next);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           const float2 y = mul2(mul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])),
@@ -963,6 +965,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
               w[e] = pack_elem2<kF16>(y.x, y.y);
             }
             d[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            g4[c] = g_next[c];
           }
         }
       }
