@@ -48,7 +48,9 @@ constexpr int kTiles = kGroup * kGroups;
 constexpr int kPieces = 32;                     // more than tiles held, and every piece has one
 constexpr int kHitSets = 4;                     // pieces whose NaN keys are held
 constexpr int kHitWords = kPairRows / 32;       // keys that only some rows of a segment see: < 256
-constexpr uint32_t kLead = 3;                   // what a segment costs beside its tiles, in tiles
+// What a segment costs beside its tiles, in tiles (Q's terms, the first tiles, whose references still move, the
+// end).  8192 rows with 3, 6, 8, 10, 13 and 16: 826, 757, 696, 703, 718, 749 us.
+constexpr uint32_t kLead = 8;
 constexpr int kSnap = 4;                        // a cut this close to a segment's end is made there
 constexpr float kCap = 15.f, kTop = 0.f;        // p <= 2^15; a moved reference leaves 1
 constexpr uint32_t kTmOc = 0, kTmSc = 256;
