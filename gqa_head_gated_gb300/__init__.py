@@ -12,6 +12,7 @@ fp16 tensors (one type per call) and picks the matching entry point.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -21,7 +22,8 @@ HEAD_DIM = 256
 
 __all__ = ["prefill", "prefill_pair", "masked", "decode", "verify_tree", "kv_append", "kv_keep", "block_plan",
            "kv8_append", "kv8_keep", "kv8_decode", "kv8_workspace_size", "kv8_prefill",
-           "kv8_prefill_workspace_size", "decode_plan", "decode_split", "lse_merge",
+           "kv8_prefill_workspace_size", "block_fork", "block_free", "block_compact", "kv8_copy", "rope",
+           "rope_frequencies", "decode_plan", "decode_split", "lse_merge",
            "decode_workspace_size", "last_device_status", "set_wait_timeout_ns",
            "selftest_wait_timeout", "decode_noalloc", "launch_log", "GqaError",
            "load"]
@@ -491,6 +493,164 @@ def kv8_decode(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, cu
           bs, max_blocks, int(max_rows), int(max_kv_len), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     return (out, lse) if return_lse else out
+
+
+def block_fork(src, dst, lens, kv_lens, block_tables, n_blocks, free_list, free_count, shares,
+               block_size, copies=None):
+    """Forks sequences of a paged cache: child dst[f] gets the first lens[f] keys (None: all) of parent
+    src[f], sharing its full blocks; int32 CUDA tensors, kv_lens, block_tables, n_blocks, free_count and
+    shares (int32 [num_blocks]: tables that hold a block beside the first) updated in place.  A child holds
+    no blocks before, and is neither a parent nor a child twice.  Returns copies int32 [F, 3], what
+    kv8_copy() has to copy (from, to, rows): the rows behind a prefix's last full block go to a block of the
+    child's own.  A refused fork records GQA_ERR_DEVICE_RANGE (6), one without a free block
+    GQA_ERR_NO_BLOCKS (7)."""
+    d = _cuda_index(src, "src")
+    F, B, N = src.numel(), kv_lens.numel(), free_list.numel()
+    if copies is None:
+        copies = torch.empty((F, 3), dtype=_I32, device=src.device)
+    tables, max_blocks = _tables(block_tables, B, d)
+    _call("gqa_block_fork", d, _at(src, _I32, (F,), d, "src"), _at(dst, _I32, (F,), d, "dst"),
+          None if lens is None else _at(lens, _I32, (F,), d, "lens"),
+          _at(kv_lens, _I32, (B,), d, "kv_lens"), tables, _at(n_blocks, _I32, (B,), d, "n_blocks"),
+          _at(free_list, _I32, (N,), d, "free_list"), _at(free_count, _I32, (1,), d, "free_count"),
+          _at(shares, _I32, (N,), d, "shares"), _at(copies, _I32, (F, 3), d, "copies"), F, B, max_blocks,
+          N, int(block_size))
+    return copies
+
+
+def block_free(kv_lens, block_tables, n_blocks, free_list, free_count, shares, block_size):
+    """Gives blocks back that sequences may share: sequence b keeps those of its first kv_lens[b] keys (0: it has
+    ended), and a block that no table holds any more goes on the stack.  int32 CUDA tensors, all but
+    kv_lens updated in place.  (block_plan() does the same for blocks that are never shared.)"""
+    d = _cuda_index(kv_lens, "kv_lens")
+    B, N = kv_lens.numel(), free_list.numel()
+    tables, max_blocks = _tables(block_tables, B, d)
+    _call("gqa_block_free", d, _at(kv_lens, _I32, (B,), d, "kv_lens"), tables,
+          _at(n_blocks, _I32, (B,), d, "n_blocks"), _at(free_list, _I32, (N,), d, "free_list"),
+          _at(free_count, _I32, (1,), d, "free_count"), _at(shares, _I32, (N,), d, "shares"), B,
+          max_blocks, N, int(block_size))
+
+
+def block_compact(block_tables, n_blocks, free_list, free_count, shares, block_size):
+    """Moves the live blocks of a pool to its first places.  Returns new tensors (block_tables, free_list,
+    shares, new_index int32 [num_blocks], copies int32 [num_blocks // 2, 3]); the inputs stay as they
+    are.  The new tables hold once kv8_copy(copies, ...) has run on the pools (every layer's, where layers share
+    tables); free_count and n_blocks do not change.  new_index tells where a block went (-1: it is free)."""
+    d = _cuda_index(block_tables, "block_tables")
+    B, N = n_blocks.numel(), free_list.numel()
+    tables, max_blocks = _tables(block_tables, B, d)
+    out = torch.empty_like(block_tables)
+    new_free, new_shares, index = (torch.empty(N, dtype=_I32, device=out.device) for _ in range(3))
+    copies = torch.empty((N // 2, 3), dtype=_I32, device=out.device)
+    _call("gqa_block_compact", d, tables, _at(n_blocks, _I32, (B,), d, "n_blocks"),
+          _at(free_list, _I32, (N,), d, "free_list"), _at(free_count, _I32, (1,), d, "free_count"),
+          _at(shares, _I32, (N,), d, "shares"), out.data_ptr(), new_free.data_ptr(),
+          new_shares.data_ptr(), index.data_ptr(), copies.data_ptr(), B, max_blocks, N, int(block_size))
+    return out, new_free, new_shares, index, copies
+
+
+def kv8_copy(copies, k_pool, v_pool, k_scale, v_scale):
+    """Copies blocks of the paged 8-bit cache, K, V and scales: copies int32 [n, 3] of (from, to, rows) as
+    block_fork() and block_compact() list them (negative: none)."""
+    d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)
+    _cuda_index(copies, "copies")
+    n = copies.shape[0] if copies.dim() else 0
+    _call("gqa_kv8_copy", d, _at(copies, _I32, (n, 3), d, "copies"), *pools, n, Hkv, N, bs)
+
+
+def rope_frequencies(rot_dims, base=10000.0, method=None, factor=1.0, original_len=None, beta_fast=32.0,
+                     beta_slow=1.0, device="cuda"):
+    """(inv_freq float32 [rot_dims / 2] on `device`, scale) for rope(): base^(-2j / rot_dims), for contexts
+    `factor` times longer than trained with the method
+      "linear"  every frequency / factor (position interpolation);
+      "ntk"     base * factor^(rot_dims / (rot_dims - 2)), which leaves the highest frequency as it is;
+      "yarn"    the frequencies that turn less than beta_slow times over original_len / factor, those that turn
+                more than beta_fast times kept, a ramp between them; scale 0.1 ln(factor) + 1.
+    Worked out in 64 bits."""
+    if rot_dims < 16 or rot_dims > HEAD_DIM or rot_dims % 16:
+        raise ValueError(f"rot_dims must be a multiple of 16 up to {HEAD_DIM}, got {rot_dims}")
+    if method not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"method must be None, 'linear', 'ntk' or 'yarn', got {method!r}")
+    if not (base > 1 and factor >= 1):
+        raise ValueError("base must be above 1 and factor 1 or more")
+    if method == "ntk":
+        base = base * factor ** (rot_dims / (rot_dims - 2))
+    j = torch.arange(rot_dims // 2, dtype=torch.float64)
+    freq, scale = base ** (-2.0 * j / rot_dims), 1.0
+    if method == "linear":
+        freq = freq / factor
+    elif method == "yarn":
+        if not original_len or beta_fast <= beta_slow:
+            raise ValueError("yarn needs original_len, and beta_fast above beta_slow")
+        # the pair that turns `beta` times over original_len
+        pair = lambda beta: (rot_dims * math.log(original_len / (beta * 2 * math.pi))  # noqa: E731
+                             / (2 * math.log(base)))
+        low = max(math.floor(pair(beta_fast)), 0)
+        high = min(math.ceil(pair(beta_slow)), rot_dims - 1)
+        ramp = ((j - low) / max(high - low, 1e-3)).clamp(0, 1)
+        freq = freq / factor * ramp + freq * (1 - ramp)
+        scale = 0.1 * math.log(factor) + 1.0
+    return freq.float().to(device), scale
+
+
+def _rope_strides(t, lead, name):
+    """Strides (batch, token, head) of [T, H, 256] or [B, H, L, 256]."""
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have its last dim in a row")
+    s = t.stride()
+    return (0, s[0], s[1]) if lead == 2 else (s[0], s[2], s[1])
+
+
+def rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=False, q_out=None, k_out=None):
+    """Rotary positions of queries and keys in one launch; returns (q, k) rotated.
+
+    q [T,Hq,256] and k [T,Hkv,256] (or None) with positions int32 [T], or the prefill layout [B,Hq,L,256] /
+    [B,Hkv,L,256] with positions int32 [L] or [B,L]; bf16 or fp16, any strides with the last dim in a row
+    (slices of a fused projection).  inv_freq: float32 [rot_dims / 2], see rope_frequencies(); the first rot_dims
+    dims of a head turn, in pairs (j, j + rot_dims / 2) or, interleaved, (2 j, 2 j + 1), the others are copied.
+    scale multiplies what is turned.  inverse: the rotation back (also the gradient's).  q_out / k_out may be
+    q / k themselves; by default the outputs are new and contiguous."""
+    sfx = _elem(q, "q")
+    d = _cuda_index(q, "q")
+    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
+        raise ValueError(f"q must be [T, Hq, {HEAD_DIM}] or [B, Hq, L, {HEAD_DIM}], got {tuple(q.shape)}")
+    if q.dim() == 3:
+        B, (L, Hq, _) = 1, q.shape
+    else:
+        B, Hq, L, _ = q.shape
+    Hkv = 0
+    pairs, strides = [("q", q, q_out, q.shape)], []
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+            raise ValueError("k must be a tensor of q's layout")
+        Hkv = k.shape[-2] if k.dim() == 3 else k.shape[1]
+        pairs.append(("k", k, k_out, (L, Hkv, HEAD_DIM) if k.dim() == 3 else (B, Hkv, L, HEAD_DIM)))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    at, outs = [], []
+    for name, t, out, shape in pairs:
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        for x, n in ((t, name), (out, name + "_out")):
+            if not isinstance(x, torch.Tensor):
+                raise TypeError(f"{n} must be a torch.Tensor")
+            if x.dtype is not q.dtype:
+                raise TypeError(f"{n} must be {q.dtype}, got {x.dtype}")
+            if x.shape != shape or x.get_device() != d:
+                raise ValueError(f"{n} must be {tuple(shape)} on cuda:{d}, got {tuple(x.shape)} on {x.device}")
+            strides += _rope_strides(x, q.dim() - 1, n)
+            at.append(x.data_ptr())
+        outs.append(out)
+    _cuda_index(positions, "positions")
+    pos_batch = int(positions.dim() == 2)
+    where = _at(positions, _I32, (B, L) if pos_batch else (L,), d, "positions")
+    _cuda_index(inv_freq, "inv_freq")
+    half = inv_freq.numel()
+    freq = _at(inv_freq, _F32, (half,), d, "inv_freq")
+    ks, ko = (at[2], at[3]) if k is not None else (None, None)
+    _call("gqa_rope" + sfx, d, at[0], ks, where, freq, at[1], ko, (ctypes.c_longlong * len(strides))(*strides), B, L,
+          Hq, Hkv, 2 * half, pos_batch, int(bool(interleaved)), int(bool(inverse)), float(scale))
+    return outs[0], outs[1] if k is not None else None
 
 
 def kv8_prefill_workspace_size():

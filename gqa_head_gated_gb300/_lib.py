@@ -66,10 +66,15 @@ SIGNATURES = {
     "gqa_kv8_keep": (_I, [_P] * 10 + [_I] * 6 + [_P]),
     "gqa_kv8_workspace_size": (ctypes.c_size_t, [_I] * 6),
     "gqa_kv8_decode": (_I, [_P] * 12 + [_I] * 9 + [_P, ctypes.c_size_t, _P]),
+    "gqa_block_fork": (_I, [_P] * 10 + [_I] * 5 + [_P]),
+    "gqa_block_free": (_I, [_P] * 6 + [_I] * 4 + [_P]),
+    "gqa_block_compact": (_I, [_P] * 10 + [_I] * 4 + [_P]),
+    "gqa_kv8_copy": (_I, [_P] * 5 + [_I] * 4 + [_P]),
+    "gqa_rope": (_I, [_P] * 7 + [_I] * 8 + [ctypes.c_float, _P]),
     "gqa_kv8_prefill_workspace_size": (ctypes.c_size_t, []),
     "gqa_kv8_prefill": (_I, [_P] * 11 + [_I] * 9 + [_P, ctypes.c_size_t, _P]),
 }
-for _name in ("gqa_kv8_append", "gqa_kv8_decode", "gqa_kv8_prefill", "gqa_attn_masked", "gqa_attn_prefill",
+for _name in ("gqa_kv8_append", "gqa_kv8_decode", "gqa_kv8_prefill", "gqa_rope", "gqa_attn_masked", "gqa_attn_prefill",
               "gqa_attn_decode", "gqa_attn_verify_tree", "gqa_attn_decode_split",
               "attn_lse_merge"):
     SIGNATURES[_name + "_f16"] = SIGNATURES[_name]   # fp16 twins, same arguments

@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include "kv8_common.cuh"
+#include "kv8_scan.cuh"
 #include "ptx_sm100.cuh"
 
 namespace gqa {
@@ -42,49 +43,6 @@ struct PlanParams {
   int B, T, max_blocks, num_blocks, bs_log2;
   LaunchCtl ctl;
 };
-
-// Exclusive prefix sums of two arrays of n counts in place; returns both totals.
-__device__ int2 scan2(int* a, int* b, int n, int2* part) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (n + kThreads - 1) / kThreads;
-  const int lo = min(tid * per, n), hi = min(lo + per, n);
-  int2 s = make_int2(0, 0);
-  for (int i = lo; i < hi; ++i) {
-    s.x += a[i];
-    s.y += b[i];
-  }
-  int2 v = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
-    if (lane >= o) {
-      v.x += x;
-      v.y += y;
-    }
-  }
-  if (lane == 31) part[warp] = v;
-  __syncthreads();
-  int2 before = make_int2(0, 0), total = make_int2(0, 0);
-  for (int w = 0; w < kWarps; ++w) {
-    const int2 p = part[w];
-    if (w < warp) {
-      before.x += p.x;
-      before.y += p.y;
-    }
-    total.x += p.x;
-    total.y += p.y;
-  }
-  int2 run = make_int2(before.x + v.x - s.x, before.y + v.y - s.y);
-  for (int i = lo; i < hi; ++i) {
-    const int x = a[i], y = b[i];
-    a[i] = run.x;
-    b[i] = run.y;
-    run.x += x;
-    run.y += y;
-  }
-  __syncthreads();
-  return total;
-}
 
 // Where row offsets fall, rows of one sequence may be rows of another: of those that keep the
 // bounds, one that starts before the end of any before it is refused.  Warp 0, 32 sequences at a
@@ -151,7 +109,7 @@ block_plan_kernel(const PlanParams p) {
   }
   const bool falls = __syncthreads_or(down);   // the same in every CTA
   if (falls) drop_overlaps(s_cu, s_have, s_rel, s_grow, B, cta == 0 ? p.ctl.status : nullptr);
-  const int2 total = scan2(s_rel, s_grow, B, part);
+  const int2 total = scan2<kThreads>(s_rel, s_grow, B, part);
   const int avail = min(fc + total.x, p.num_blocks);
   if (cta == 0 && tid == 0 && (fc != fc_read || fc + (long long)total.x > p.num_blocks))
     record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);   // more blocks than there are

@@ -539,6 +539,89 @@ int gqa_kv8_decode_f16(const void* Q, const void* k_pool, const void* v_pool,
                        gqa_stream_t stream);
 
 /*
+ * Blocks that sequences share (a system prompt, samples of one prompt).  shares: int32
+ * [num_blocks], how many tables hold a block beside the first: all 0 for a pool that only
+ * gqa_block_plan has handed out, which neither reads nor needs it.  A block with shares > 0 is only
+ * read: gqa_kv8_append and gqa_kv8_keep write behind the keys that a sequence holds, and a fork's
+ * child gets a block of its own for the rows behind the last full block.  So fork the keys that are
+ * settled (before a step's drafts, or after gqa_kv8_keep), and give lengths that fall below a fork to
+ * gqa_block_free, not to gqa_block_plan, which would hand a shared block out again.
+ * Limits as for gqa_block_plan (B and F <= 8192, entries < 2^30).
+ *
+ * gqa_block_fork: child dst[f] becomes a copy of the first lens[f] keys (lens NULL: kv_lens[src[f]]) of
+ * parent src[f]; f < F.  Its table takes the parent's full blocks (shares + 1 each) and, for the rows
+ * behind them, the next block of the stack, in order of f; kv_lens[dst], n_blocks[dst], free_count and
+ * shares are updated.
+ *   copies: int32 [F, 3]: what gqa_kv8_copy has to copy for it (from, to, rows), per layer's
+ *   pools where layers share tables; -1, -1, 0 for none.
+ * A child holds no blocks before the call, and the call forks neither from it nor to it twice; a fork
+ * that breaks this, or whose prefix is longer than what the parent holds, is refused
+ * (GQA_ERR_DEVICE_RANGE recorded), one that the stack has no block for takes none
+ * (GQA_ERR_NO_BLOCKS).
+ */
+int gqa_block_fork(const int* src, const int* dst, const int* lens, int* kv_lens, int* block_tables,
+                   int* n_blocks, int* free_list, int* free_count, int* shares, int* copies, int F,
+                   int B, int max_blocks, int num_blocks, int block_size, gqa_stream_t stream);
+
+/*
+ * gqa_block_free: sequence b keeps the blocks of its first kv_lens[b] keys (0: it has ended); each
+ * entry behind them becomes -1 and its block loses an owner.  A block without one goes back on the
+ * stack, with the last of its entries: the k-th of R such in (sequence, place) order to
+ * free_list[free_count + R - 1 - k].  n_blocks, free_count and shares are updated.  With shares of 0
+ * that is gqa_block_plan's release.  A sequence with a negative length or a count out of range keeps its
+ * blocks, an entry outside the pool frees nothing; GQA_ERR_DEVICE_RANGE is recorded.
+ */
+int gqa_block_free(const int* kv_lens, int* block_tables, int* n_blocks, int* free_list,
+                   int* free_count, int* shares, int B, int max_blocks, int num_blocks,
+                   int block_size, gqa_stream_t stream);
+
+/*
+ * gqa_block_compact: the L = num_blocks - free_count live blocks move to places 0 .. L - 1: the k-th live
+ * block at or behind L to the k-th free place before it.  The inputs stay as they are (calls on their
+ * way may still read them), the outputs describe the pool once gqa_kv8_copy has run on `copies`:
+ *   tables_out [B, max_blocks] (-1 behind n_blocks[b]), shares_out [num_blocks] (0 for free blocks),
+ *   free_list_out [num_blocks]: num_blocks - 1 - i at i, so that the stack, of the same count, hands out low
+ *   places first;
+ *   new_index int32 [num_blocks]: where a block went (itself if it stays, -1 if it is free);
+ *   copies int32 [num_blocks / 2, 3]: (from, to, block_size), then -1, -1, 0.
+ * Outputs may not be inputs.  A stack that holds a block twice or one that is none leaves every block where
+ * it is, and a table entry that is no live block becomes -1; GQA_ERR_DEVICE_RANGE is recorded.
+ */
+int gqa_block_compact(const int* block_tables, const int* n_blocks, const int* free_list,
+                      const int* free_count, const int* shares, int* tables_out, int* free_list_out,
+                      int* shares_out, int* new_index, int* copies, int B, int max_blocks,
+                      int num_blocks, int block_size, gqa_stream_t stream);
+
+/*
+ * gqa_kv8_copy: the first `rows` rows of block `from`, K and V of every head, and its scales, to block `to`,
+ * for n listed copies (int32 [n, 3]; from or to < 0, or no rows: none).  No listed block is both written and
+ * read, or written twice.  A copy out of range is skipped and GQA_ERR_DEVICE_RANGE recorded.  Hkv < 16384
+ * (GQA_ERR_UNSUPPORTED above).
+ */
+int gqa_kv8_copy(const int* copies, void* k_pool, void* v_pool, float* k_scale, float* v_scale, int n,
+                 int Hkv, int num_blocks, int block_size, gqa_stream_t stream);
+
+/*
+ * Rotary positions of queries and keys, one launch for both, before the keys go into a cache:
+ *   (x1, x2) -> (x1 cos a - x2 sin a, x2 cos a + x1 sin a) * scale,  a = position * inv_freq[j]
+ * for pairs j of each head's first rot_dims dims (a multiple of 16, 16 .. 256): dims j and j + rot_dims / 2, or
+ * (interleaved != 0) 2 j and 2 j + 1.  The dims behind them are copied.  inverse != 0: the rotation back
+ * (by -a), which is also the gradient's.  Fp32 arithmetic, rounded once; a is right to 2^-29 for every int32
+ * position and |inv_freq| <= 1.
+ * Q, q_out: bf16 (fp16: _f16) [B, L, Hq, 256] in any strides, K, k_out: [B, L, Hkv, 256] likewise (both NULL with
+ *   Hkv == 0).  strides: host array of 3 (batch, token, head, in elements, multiples of 8, >= 0) each for Q, q_out,
+ *   K and k_out; a head's 256 elements lie in a row.  An output's rows may not overlap; it may be its
+ *   input, with the same strides (the dims that are not rotated are then not touched).
+ * positions: int32 [L], or (pos_batch == 1) [B, L].  inv_freq: fp32 [rot_dims / 2].  Device pointers.
+ */
+int gqa_rope(const void* Q, const void* K, const int* positions, const float* inv_freq, void* q_out,
+             void* k_out, const long long* strides, int B, int L, int Hq, int Hkv, int rot_dims,
+             int pos_batch, int interleaved, int inverse, float scale, gqa_stream_t stream);
+int gqa_rope_f16(const void* Q, const void* K, const int* positions, const float* inv_freq, void* q_out,
+                 void* k_out, const long long* strides, int B, int L, int Hq, int Hkv, int rot_dims,
+                 int pos_batch, int interleaved, int inverse, float scale, gqa_stream_t stream);
+
+/*
  * Prompt chunks over the paged 8-bit cache: as gqa_kv8_decode without tree_mask, for many new rows
  * a sequence.  New row i of sequence b sees keys j < kv_lens[b] - r_b + i + 1, the chunk's own
  * rows among them (gqa_kv8_append comes first).  Same arguments, rows left as they were, table entries,
