@@ -12,6 +12,7 @@ fp16 tensors (one type per call) and picks the matching entry point.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -507,7 +508,7 @@ def block_fork(src, dst, lens, kv_lens, block_tables, n_blocks, free_list, free_
     d = _cuda_index(src, "src")
     F, B, N = src.numel(), kv_lens.numel(), free_list.numel()
     if copies is None:
-        copies = torch.empty((F, 3), dtype=_I32, device=src.device)
+        copies = src.new_empty((F, 3), dtype=_I32)
     tables, max_blocks = _tables(block_tables, B, d)
     _call("gqa_block_fork", d, _at(src, _I32, (F,), d, "src"), _at(dst, _I32, (F,), d, "dst"),
           None if lens is None else _at(lens, _I32, (F,), d, "lens"),
@@ -540,10 +541,11 @@ def block_compact(block_tables, n_blocks, free_list, free_count, shares, block_s
     B, N = n_blocks.numel(), free_list.numel()
     tables, max_blocks = _tables(block_tables, B, d)
     out = torch.empty_like(block_tables)
-    new_free, new_shares, index = (torch.empty(N, dtype=_I32, device=out.device) for _ in range(3))
-    copies = torch.empty((N // 2, 3), dtype=_I32, device=out.device)
+    list_at = _at(free_list, _I32, (N,), d, "free_list")
+    new_free, new_shares, index = (torch.empty_like(free_list) for _ in range(3))
+    copies = free_list.new_empty((N // 2, 3))
     _call("gqa_block_compact", d, tables, _at(n_blocks, _I32, (B,), d, "n_blocks"),
-          _at(free_list, _I32, (N,), d, "free_list"), _at(free_count, _I32, (1,), d, "free_count"),
+          list_at, _at(free_count, _I32, (1,), d, "free_count"),
           _at(shares, _I32, (N,), d, "shares"), out.data_ptr(), new_free.data_ptr(),
           new_shares.data_ptr(), index.data_ptr(), copies.data_ptr(), B, max_blocks, N, int(block_size))
     return out, new_free, new_shares, index, copies
@@ -593,12 +595,26 @@ def rope_frequencies(rot_dims, base=10000.0, method=None, factor=1.0, original_l
     return freq.float().to(device), scale
 
 
-def _rope_strides(t, lead, name):
-    """Strides (batch, token, head) of [T, H, 256] or [B, H, L, 256]."""
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name} must have its last dim in a row")
-    s = t.stride()
-    return (0, s[0], s[1]) if lead == 2 else (s[0], s[2], s[1])
+@functools.lru_cache(maxsize=256)
+def _rope_strides(*strides):
+    return (ctypes.c_longlong * len(strides))(*strides)
+
+
+def _rope_rows(t, dtype, shape, d, name):
+    """Address and (batch, token, head) strides of [T, H, 256] or [B, H, L, 256] with the last dim in a row."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == d:
+            s = t.stride()
+            if s[-1] == 1:
+                return (t.data_ptr(), 0, s[0], s[1]) if len(s) == 3 else (t.data_ptr(), s[0], s[2], s[1])
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be {tuple(shape)} on cuda:{d} with its last dim in a row, got {tuple(t.shape)} "
+                     f"of strides {tuple(t.stride())} on {t.device}")
 
 
 def rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=False, q_out=None, k_out=None):
@@ -612,45 +628,41 @@ def rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, inverse=False,
     q / k themselves; by default the outputs are new and contiguous."""
     sfx = _elem(q, "q")
     d = _cuda_index(q, "q")
-    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
-        raise ValueError(f"q must be [T, Hq, {HEAD_DIM}] or [B, Hq, L, {HEAD_DIM}], got {tuple(q.shape)}")
-    if q.dim() == 3:
-        B, (L, Hq, _) = 1, q.shape
+    shape, dt = q.shape, q.dtype
+    if len(shape) == 3:
+        B, (L, Hq, D) = 1, shape
+    elif len(shape) == 4:
+        B, Hq, L, D = shape
     else:
-        B, Hq, L, _ = q.shape
-    Hkv = 0
-    pairs, strides = [("q", q, q_out, q.shape)], []
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        D = None
+    if D != HEAD_DIM:
+        raise ValueError(f"q must be [T, Hq, {HEAD_DIM}] or [B, Hq, L, {HEAD_DIM}], got {tuple(shape)}")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    qa, *qs = _rope_rows(q, dt, shape, d, "q")
+    oa, *os_ = _rope_rows(q_out, dt, shape, d, "q_out")
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        Hkv, ka, koa, ks, kos = 0, None, None, (), ()
+    else:
+        if not isinstance(k, torch.Tensor) or k.dim() != len(shape):
             raise ValueError("k must be a tensor of q's layout")
-        Hkv = k.shape[-2] if k.dim() == 3 else k.shape[1]
-        pairs.append(("k", k, k_out, (L, Hkv, HEAD_DIM) if k.dim() == 3 else (B, Hkv, L, HEAD_DIM)))
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    at, outs = [], []
-    for name, t, out, shape in pairs:
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        for x, n in ((t, name), (out, name + "_out")):
-            if not isinstance(x, torch.Tensor):
-                raise TypeError(f"{n} must be a torch.Tensor")
-            if x.dtype is not q.dtype:
-                raise TypeError(f"{n} must be {q.dtype}, got {x.dtype}")
-            if x.shape != shape or x.get_device() != d:
-                raise ValueError(f"{n} must be {tuple(shape)} on cuda:{d}, got {tuple(x.shape)} on {x.device}")
-            strides += _rope_strides(x, q.dim() - 1, n)
-            at.append(x.data_ptr())
-        outs.append(out)
+        Hkv = k.shape[1]
+        k_shape = (L, Hkv, D) if len(shape) == 3 else (B, Hkv, L, D)
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        ka, *ks = _rope_rows(k, dt, k_shape, d, "k")
+        koa, *kos = _rope_rows(k_out, dt, k_shape, d, "k_out")
     _cuda_index(positions, "positions")
-    pos_batch = int(positions.dim() == 2)
-    where = _at(positions, _I32, (B, L) if pos_batch else (L,), d, "positions")
+    batch = positions.dim() == 2
+    where = _at(positions, _I32, (B, L) if batch else (L,), d, "positions")
     _cuda_index(inv_freq, "inv_freq")
     half = inv_freq.numel()
-    freq = _at(inv_freq, _F32, (half,), d, "inv_freq")
-    ks, ko = (at[2], at[3]) if k is not None else (None, None)
-    _call("gqa_rope" + sfx, d, at[0], ks, where, freq, at[1], ko, (ctypes.c_longlong * len(strides))(*strides), B, L,
-          Hq, Hkv, 2 * half, pos_batch, int(bool(interleaved)), int(bool(inverse)), float(scale))
-    return outs[0], outs[1] if k is not None else None
+    _call("gqa_rope" + sfx, d, qa, ka, where, _at(inv_freq, _F32, (half,), d, "inv_freq"), oa, koa,
+          _rope_strides(*qs, *os_, *ks, *kos), B, L, Hq, Hkv, 2 * half, batch, bool(interleaved),
+          bool(inverse), scale)
+    return q_out, k_out
 
 
 def kv8_prefill_workspace_size():

@@ -30,6 +30,10 @@ constexpr int kThreads = 512;
 constexpr int kMaxCtas = 8;       // the portable cluster size
 constexpr int kMaxSeqs = 8192;    // sequences, and forks, of a call
 constexpr int kWon = 1 << 30;     // entries are fewer
+// Entries that a thread has on their way together: entry k0 + kThreads u + tid of a tile is its u-th.  One CTA has few
+// (kernels this short are bound by fetching their code: a free of 350 entries 7 us with 4, 16 with 16), a
+// cluster many.
+constexpr int kFew = 4, kMany = 16;
 
 struct PagesParams {
   const int* src;
@@ -46,7 +50,23 @@ struct PagesParams {
   LaunchCtl ctl;
 };
 
-__global__ void __launch_bounds__(kThreads) block_fork_kernel(const PagesParams p) {
+// Owners of this thread's entries of the tile at k0 (by their exclusive sums, n of them), searched side by side.
+template <int kRun>
+__device__ __forceinline__ void owners(const int* sums, int n, int k0, int (&b)[kRun]) {
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) b[u] = 0;
+#pragma unroll 1
+  for (int s = 1 << (31 - __clz(n)); s > 0; s >>= 1)
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      const int c = b[u] + s;
+      if (c < n && sums[c] <= k0 + kThreads * u + int(threadIdx.x)) b[u] = c;
+    }
+}
+
+template <int kRun>
+__global__ void __launch_bounds__(kThreads, 1) block_fork_kernel(const PagesParams p) {
+  constexpr int kTile = kThreads * kRun;
   extern __shared__ int smem[];
   __shared__ int2 part[kThreads / 32];
   int* const s_use = smem;             // B: 1 where it is forked from, + 2 per fork to it
@@ -87,13 +107,28 @@ __global__ void __launch_bounds__(kThreads) block_fork_kernel(const PagesParams 
   const auto served = [&](int f) {
     return s_len[f] >= 0 && ((s_len[f] & (bs - 1)) == 0 || s_tail[f] < fc);
   };
-  for (int k = cta * kThreads + tid; k < total.x; k += per) {
-    const int f = owner_of(s_full, p.F, k);
-    if (!served(f)) continue;
-    const int i = k - s_full[f], blk = p.tables[(long long)p.src[f] * p.max_blocks + i];
-    p.tables[(long long)p.dst[f] * p.max_blocks + i] = blk;
-    if (blk >= 0 && blk < p.num_blocks) atomicAdd(&p.shares[blk], 1);
-    else record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+  for (int k0 = cta * kTile; k0 < total.x; k0 += int(gridDim.x) * kTile) {
+    int blk[kRun];
+    int* to[kRun];
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) to[u] = nullptr;
+    int f[kRun];
+    owners(s_full, p.F, k0, f);
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      const int k = k0 + kThreads * u + tid;
+      if (k >= total.x || !served(f[u])) continue;
+      const int i = k - s_full[f[u]];
+      blk[u] = p.tables[(long long)p.src[f[u]] * p.max_blocks + i];
+      to[u] = p.tables + (long long)p.dst[f[u]] * p.max_blocks + i;
+    }
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      if (to[u] == nullptr) continue;
+      *to[u] = blk[u];
+      if (blk[u] >= 0 && blk[u] < p.num_blocks) atomicAdd(&p.shares[blk[u]], 1);
+      else record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+    }
   }
   for (int f = cta * kThreads + tid; f < p.F; f += per) {
     int from = -1, to = -1, rows = 0;
@@ -120,20 +155,56 @@ __global__ void __launch_bounds__(kThreads) block_fork_kernel(const PagesParams 
   }
 }
 
-// Places of the CTA's flagged items before this thread's, and all of them (whole CTA).
-__device__ __forceinline__ int2 ranks(bool flag, int* s_warp) {
+// Sum of the CTA's counts before this thread's, and of all (whole CTA).
+__device__ __forceinline__ int2 counts_to(int n, int* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t m = __ballot_sync(0xffffffffu, flag);
+  int v = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
   __syncthreads();   // (the last round's counts have been read)
-  if (lane == 0) s_warp[warp] = __popc(m);
+  if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  int before = __popc(m & ((1u << lane) - 1u)), all = 0;
+  int before = v - n, all = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s_warp[w];
     all += s_warp[w];
   }
   return make_int2(before, all);
+}
+
+// Counts a tile's flagged entries (bit u of m: this thread's u-th) in their order: afterwards s_cnt[u * 16 + warp] has
+// those before the warp's u-th row.  Returns all (whole CTA).
+constexpr int kWarps = kThreads / 32;
+static_assert(kMany * kWarps <= kThreads, "a thread scans one count");
+template <int kRun>
+__device__ __forceinline__ int rank_tile(uint32_t m, int* s_cnt, int* s_warp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();   // (the last tile's counts have been read)
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) {
+    const uint32_t b = __ballot_sync(0xffffffffu, (m >> u) & 1u);
+    if (lane == 0) s_cnt[u * kWarps + warp] = __popc(b);
+  }
+  __syncthreads();
+  const int2 r = counts_to(tid < kRun * kWarps ? s_cnt[tid] : 0, s_warp);
+  if (tid < kRun * kWarps) s_cnt[tid] = r.x;
+  __syncthreads();
+  return r.y;
+}
+// f(u, rank) for each of this thread's flagged entries.
+template <int kRun, typename F>
+__device__ __forceinline__ void each_ranked(uint32_t m, const int* s_cnt, F&& f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) {
+    const bool flag = (m >> u) & 1u;
+    const uint32_t b = __ballot_sync(0xffffffffu, flag);
+    if (flag) f(u, s_cnt[u * kWarps + warp] + __popc(b & ((1u << lane) - 1u)));
+  }
 }
 
 // Tells every CTA of the cluster this one's counts; returns the sums before it and of all (whole CTA).
@@ -157,10 +228,12 @@ __device__ __forceinline__ int4 counts_before(int2 mine, int2* s_all) {
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) block_free_kernel(const PagesParams p) {
+template <int kRun>
+__global__ void __launch_bounds__(kThreads, 1) block_free_kernel(const PagesParams p) {
+  constexpr int kTile = kThreads * kRun;
   extern __shared__ int smem[];
   __shared__ int2 part[kThreads / 32];
-  __shared__ int s_warp[kThreads / 32];
+  __shared__ int s_warp[kWarps], s_cnt[kRun * kWarps];
   __shared__ int2 s_all[kMaxCtas];
   int* const s_keep = smem;            // B: blocks that stay
   int* const s_rel = s_keep + p.B;     // B: entries to release, then their exclusive sums
@@ -181,47 +254,74 @@ __global__ void __launch_bounds__(kThreads) block_free_kernel(const PagesParams 
   __syncthreads();
   const int total = scan2<kThreads>(s_rel, s_none, p.B, part).x;
   ptx::cluster_sync();   // every CTA has read the counts
-  const auto entry = [&](int k) {
-    const int b = owner_of(s_rel, p.B, k);
-    return p.tables + (long long)b * p.max_blocks + s_keep[b] + (k - s_rel[b]);
-  };
   const auto inside = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
-  for (int k = cta * kThreads + tid; k < total; k += per) {
-    const int blk = *entry(k);
-    if (inside(blk)) atomicSub(&p.shares[blk], 1);
-    else record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
-  }
-  ptx::cluster_sync();
-  for (int k = cta * kThreads + tid; k < total; k += per) {
-    const int blk = *entry(k);
-    if (inside(blk) && __ldcg(p.shares + blk) < 0) atomicMin(&p.shares[blk], -kWon - k);
-  }
-  ptx::cluster_sync();
   // each CTA has a run of the entries, in order
   const int lo = int((long long)total * cta / int(gridDim.x)), hi = int((long long)total * (cta + 1) / int(gridDim.x));
-  const auto won = [&](int k, int& blk) {
-    blk = k < hi ? *entry(k) : -1;
-    return inside(blk) && __ldcg(p.shares + blk) == -kWon - k;
+  const bool one = hi - lo <= kTile;   // (its blocks stay in registers)
+  int blk[kRun], b[kRun];
+  const auto place = [&](int u, int k) {
+    return p.tables + ((long long)b[u] * p.max_blocks + s_keep[b[u]] + (k - s_rel[b[u]]));
+  };
+  const auto blocks = [&](int k0) {
+    owners(s_rel, p.B, k0, b);
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      const int k = k0 + kThreads * u + tid;
+      blk[u] = k < hi ? *place(u, k) : -1;
+    }
+  };
+  for (int k0 = lo; k0 < hi; k0 += kTile) {
+    blocks(k0);
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      if (inside(blk[u])) atomicSub(&p.shares[blk[u]], 1);
+      else if (k0 + kThreads * u + tid < hi) record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+    }
+  }
+  ptx::cluster_sync();
+  uint32_t m = 0u;   // entries whose block has no owner left; those that won it
+  const auto look = [&](int k0, auto&& is) {
+    int left[kRun];
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) left[u] = inside(blk[u]) ? __ldcg(p.shares + blk[u]) : 0;
+    m = 0u;
+#pragma unroll
+    for (int u = 0; u < kRun; ++u)
+      if (is(left[u], k0 + kThreads * u + tid)) m |= 1u << u;
+  };
+  for (int k0 = lo; k0 < hi; k0 += kTile) {
+    if (!one) blocks(k0);
+    look(k0, [&](int left, int) { return left < 0; });
+#pragma unroll
+    for (int u = 0; u < kRun; ++u)
+      if ((m >> u) & 1u) atomicMin(&p.shares[blk[u]], -kWon - (k0 + kThreads * u + tid));
+  }
+  ptx::cluster_sync();
+  const auto won = [&](int k0) {
+    if (!one) blocks(k0);
+    if (!one || __any_sync(0xffffffffu, m != 0u)) look(k0, [&](int left, int k) { return left == -kWon - k; });
   };
   int mine = 0;
-  for (int k0 = lo; k0 < hi; k0 += kThreads) {
-    int blk;
-    mine += ranks(won(k0 + tid, blk), s_warp).y;
+  for (int k0 = lo; k0 < hi; k0 += kTile) {
+    won(k0);
+    mine += rank_tile<kRun>(m, s_cnt, s_warp);
   }
   const int4 c = counts_before(make_int2(mine, 0), s_all);
   int at = c.x;
-  for (int k0 = lo; k0 < hi; k0 += kThreads) {
-    const int k = k0 + tid;
-    int blk;
-    const bool w = won(k, blk);
-    const int2 r = ranks(w, s_warp);
-    if (w) {
-      const int to = fc + c.z - 1 - (at + r.x);
-      if (to < p.num_blocks) p.free_list[to] = blk;
-      p.shares[blk] = 0;
+  for (int k0 = lo; k0 < hi; k0 += kTile) {
+    if (!one) won(k0);
+    const int n = one ? mine : rank_tile<kRun>(m, s_cnt, s_warp);
+    each_ranked<kRun>(m, s_cnt, [&](int u, int rank) {
+      const int to = fc + c.z - 1 - (at + rank);
+      if (to < p.num_blocks) p.free_list[to] = blk[u];
+      p.shares[blk[u]] = 0;
+    });
+    at += n;
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      const int k = k0 + kThreads * u + tid;
+      if (k < hi) *place(u, k) = -1;
     }
-    at += r.y;
-    if (k < hi) *entry(k) = -1;
   }
   for (int b = cta * kThreads + tid; b < p.B; b += per)
     if (p.n_blocks[b] > s_keep[b]) p.n_blocks[b] = s_keep[b];
@@ -248,8 +348,10 @@ struct CompactParams {
 };
 
 // New places of the blocks, the copies, and the stack.
-__global__ void __launch_bounds__(kThreads) compact_index_kernel(const CompactParams p) {
-  __shared__ int s_warp[kThreads / 32];
+template <int kRun>
+__global__ void __launch_bounds__(kThreads, 1) compact_index_kernel(const CompactParams p) {
+  constexpr int kTile = kThreads * kRun;
+  __shared__ int s_warp[kWarps], s_cnt[2][kRun * kWarps];
   __shared__ int2 s_all[kMaxCtas];
   const int tid = threadIdx.x, cta = blockIdx.x, ctas = gridDim.x, N = p.num_blocks;
   const int per = ctas * kThreads, first = cta * kThreads + tid;
@@ -269,30 +371,47 @@ __global__ void __launch_bounds__(kThreads) compact_index_kernel(const CompactPa
   ptx::cluster_sync();
   // free places below `live` and live blocks from there on: each CTA has a run of the pool
   const int lo = int((long long)N * cta / ctas), hi = int((long long)N * (cta + 1) / ctas);
+  // this thread's places of the tile at n0: free ones below `live`, and live ones from there on
+  uint32_t holes = 0u, movers = 0u;
+  const auto look = [&](int n0) {
+    int to[kRun];
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      const int n = n0 + kThreads * u + tid;
+      to[u] = n < hi ? __ldcg(p.index + n) : 0;
+    }
+    holes = movers = 0u;
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      const int n = n0 + kThreads * u + tid;
+      if (n < hi && to[u] < 0 && n < live) holes |= 1u << u;
+      if (n < hi && to[u] >= 0 && n >= live) movers |= 1u << u;
+    }
+  };
   int2 mine = make_int2(0, 0);
-  for (int n0 = lo; n0 < hi; n0 += kThreads) {
-    const int n = n0 + tid;
-    const bool in = n < hi, is_free = in && __ldcg(p.index + n) < 0;
-    mine.x += __syncthreads_count(is_free && n < live);
-    mine.y += __syncthreads_count(in && !is_free && n >= live);
+  for (int n0 = lo; n0 < hi; n0 += kTile) {
+    look(n0);
+    mine.x += rank_tile<kRun>(holes, s_cnt[0], s_warp);
+    mine.y += rank_tile<kRun>(movers, s_cnt[1], s_warp);
   }
   const int4 c = counts_before(mine, s_all);
   const bool whole = c.z == c.w && fc == fc_read;   // else a block is on the stack twice, or is not one
   int2 at = make_int2(c.x, c.y);
-  for (int n0 = lo; n0 < hi; n0 += kThreads) {
-    const int n = n0 + tid;
-    const bool in = n < hi, is_free = in && __ldcg(p.index + n) < 0;
-    const bool hole = whole && is_free && n < live, mover = whole && in && !is_free && n >= live;
-    const int2 h = ranks(hole, s_warp), m = ranks(mover, s_warp);
-    if (hole) p.copies[3 * (at.x + h.x) + 1] = n;
-    if (mover) {
-      p.copies[3 * (at.y + m.x)] = n;
-      p.copies[3 * (at.y + m.x) + 2] = p.block_size;
+  for (int n0 = lo; whole && n0 < hi; n0 += kTile) {
+    if (hi - lo > kTile) {
+      look(n0);
+      mine.x = rank_tile<kRun>(holes, s_cnt[0], s_warp);
+      mine.y = rank_tile<kRun>(movers, s_cnt[1], s_warp);
     }
-    at.x += h.y;
-    at.y += m.y;
-    if (in) p.free_list_out[n] = whole ? N - 1 - n : p.free_list[n];
+    each_ranked<kRun>(holes, s_cnt[0], [&](int u, int rank) { p.copies[3 * (at.x + rank) + 1] = n0 + kThreads * u + tid; });
+    each_ranked<kRun>(movers, s_cnt[1], [&](int u, int rank) {
+      p.copies[3 * (at.y + rank)] = n0 + kThreads * u + tid;
+      p.copies[3 * (at.y + rank) + 2] = p.block_size;
+    });
+    at.x += mine.x;
+    at.y += mine.y;
   }
+  for (int n = first; n < N; n += per) p.free_list_out[n] = whole ? N - 1 - n : p.free_list[n];
   ptx::cluster_sync();
   if (whole)
     for (int r = first; r < c.z; r += per) p.index[__ldcg(p.copies + 3 * r)] = __ldcg(p.copies + 3 * r + 1);
@@ -437,9 +556,11 @@ int gqa_block_fork(const int* src, const int* dst, const int* lens, int* kv_lens
   while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
   if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
   static std::atomic<unsigned long long> allowed{0};
-  const int ctas = (long long)F * max_blocks > 4 * kThreads ? kMaxCtas : 1;
-  return launch_cluster(block_fork_kernel, "block_fork_kernel", ctas, (size_t(B) + size_t(3) * F) * sizeof(int),
-                        size_t(4) * kMaxSeqs * sizeof(int), stream, allowed, p);
+  const size_t smem = (size_t(B) + size_t(3) * F) * sizeof(int), most = size_t(4) * kMaxSeqs * sizeof(int);
+  static std::atomic<unsigned long long> allowed_few{0};
+  return (long long)F * max_blocks > kFew * kThreads
+             ? launch_cluster(block_fork_kernel<kMany>, "block_fork_kernel", kMaxCtas, smem, most, stream, allowed, p)
+             : launch_cluster(block_fork_kernel<kFew>, "block_fork_kernel", 1, smem, most, stream, allowed_few, p);
 }
 
 int gqa_block_free(const int* kv_lens, int* block_tables, int* n_blocks, int* free_list, int* free_count, int* shares,
@@ -452,9 +573,11 @@ int gqa_block_free(const int* kv_lens, int* block_tables, int* n_blocks, int* fr
   while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
   if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
   static std::atomic<unsigned long long> allowed{0};
-  const int ctas = (long long)B * max_blocks > 4 * kThreads ? kMaxCtas : 1;
-  return launch_cluster(block_free_kernel, "block_free_kernel", ctas, size_t(3) * B * sizeof(int),
-                        size_t(3) * kMaxSeqs * sizeof(int), stream, allowed, p);
+  const size_t smem = size_t(3) * B * sizeof(int), most = size_t(3) * kMaxSeqs * sizeof(int);
+  static std::atomic<unsigned long long> allowed_few{0};
+  return (long long)B * max_blocks > kFew * kThreads
+             ? launch_cluster(block_free_kernel<kMany>, "block_free_kernel", kMaxCtas, smem, most, stream, allowed, p)
+             : launch_cluster(block_free_kernel<kFew>, "block_free_kernel", 1, smem, most, stream, allowed_few, p);
 }
 
 int gqa_block_compact(const int* block_tables, const int* n_blocks, const int* free_list, const int* free_count,
@@ -470,10 +593,12 @@ int gqa_block_compact(const int* block_tables, const int* n_blocks, const int* f
                   new_index, copies, B, max_blocks, num_blocks, block_size, {}};
   if (!make_launch_ctl(&p.ctl)) return GQA_ERR_CUDA;
   static std::atomic<unsigned long long> allowed{0};
-  const int ctas = num_blocks > 4 * kThreads ? kMaxCtas : 1;
-  const int code = launch_cluster(compact_index_kernel, "compact_index_kernel", ctas, 0, 0, stream, allowed, p);
+  const int code =
+      num_blocks > kFew * kThreads
+          ? launch_cluster(compact_index_kernel<kMany>, "compact_index_kernel", kMaxCtas, 0, 0, stream, allowed, p)
+          : launch_cluster(compact_index_kernel<kFew>, "compact_index_kernel", 1, 0, 0, stream, allowed, p);
   if (code != GQA_OK) return code;
-  const long long work = (long long)B * max_blocks + num_blocks, ctas2 = (work + 1023) / 1024;
+  const long long work = (long long)B * max_blocks + num_blocks, ctas2 = (work + 511) / 512;
   const unsigned grid = unsigned(ctas2 < 4 * device_sm_count() ? ctas2 : 4 * device_sm_count());
   if (launch_dependent(compact_tables_kernel, dim3(grid), 256, 0, static_cast<cudaStream_t>(stream), 1, p) !=
       cudaSuccess)

@@ -8,11 +8,11 @@
 // The angle is worked out in turns of 2^-64, modulo a turn, by integer products: inv_freq = m 2^e as 24-bit m times
 // 2^66 / (2 pi) gives the turn's share of one position to 2^-64, times the position, so that a position of 2^31 is
 // off by 2^-32 of a turn (in fp32 a far position's angle is wrong by whole radians; fp64 products, at 2 a clock and
-// SM, would take as long as the copies).  sincospif takes it from there, once per token and pair: a CTA works out its
-// tokens' angles in shared memory while its first rows are on their way.
+// SM, would take as long as the copies).  sincospif takes it from there, once per pair of an item, a
+// lane a pair.
 //
-// Bound by memory: a warp has a token's heads, 512 bytes (16 a lane) each, four of them in flight.  Measured, 24 + 4 heads:
-// see rope's figures below the kernel.
+// Bound by memory: a warp takes items of 8 heads of a token, 512 bytes (16 a lane) each, the next item's loads under way
+// while it turns one.
 #include <cuda_runtime.h>
 
 #include "kv8_common.cuh"
@@ -21,7 +21,7 @@ namespace gqa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBatch = 4;   // rows that a warp has in flight
+constexpr int kRows = 8;    // heads of an item
 constexpr int kMaxPairs = kHeadDim / 2;
 
 struct RopeParams {
@@ -31,107 +31,137 @@ struct RopeParams {
   const int* positions;
   long long pos_batch;        // positions of a batch entry behind those of the last
   const float* inv_freq;
-  int L, heads, q_heads, half, warps_log2;   // half: pairs; warps_log2: of a token
-  long long tokens;
+  int L, heads[2], half, groups, q_groups;   // half: pairs; groups: items of a token, of q
+  uint32_t items;
+  bool one;                   // one batch entry
   float scale;
   bool inverse, in_place[2];
 };
 
-// cos and sin (times scale) of position * freq.
-__device__ float2 turn(int position, float freq, float scale, bool inverse) {
+// freq / (2 pi), the turns that a position adds, in 2^-64 of a turn, modulo a turn.
+__device__ __forceinline__ unsigned long long turns_of(float freq) {
   const uint32_t b = __float_as_uint(freq), exp = (b >> 23) & 255u;
-  if (exp == 255u) return make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
   const unsigned long long m = (b & 0x7FFFFFu) | (exp ? 0x800000u : 0u);
   constexpr unsigned long long kTurns = 0xA2F9836E4E441529ull;   // 2^66 / (2 pi)
   const unsigned long long lo = m * kTurns, hi = __umul64hi(m, kTurns);
-  const int s = 2 - (int(max(exp, 1u)) - 150);                   // m 2^(exp - 150) / (2 pi) = (hi, lo) 2^-s, of 2^64 a turn
+  const int s = 2 - (int(max(exp, 1u)) - 150);   // m 2^(exp - 150) / (2 pi) = (hi, lo) 2^-s, of 2^64 a turn
   unsigned long long f = 0ull;
   if (s >= 64) f = s < 128 ? hi >> (s - 64) : 0ull;
   else if (s > 0) f = (lo >> s) | (hi << (64 - s));
   else if (s > -64) f = lo << -s;
-  unsigned long long a = f * static_cast<unsigned long long>(static_cast<long long>(position));
-  if ((int(b) < 0) != inverse) a = 0ull - a;
+  return int(b) < 0 ? 0ull - f : f;
+}
+
+// cos and sin of a position's turns, whose upper 32 bits do: 2^-32 of a turn.
+__device__ __forceinline__ float2 turn(int position, unsigned long long turns) {
+  const unsigned long long a = turns * static_cast<unsigned long long>(static_cast<long long>(position));
   float sn, cs;
-  sincospif(float(static_cast<long long>(a)) * 1.0842021724855044e-19f, &sn, &cs);   // 2^-63: half turns
-  return make_float2(cs * scale, sn * scale);
+  sincospif(float(int(a >> 32)) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: in half turns
+  return make_float2(cs, sn);
 }
 
 template <bool kF16, bool kInterleaved>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p) {
-  __shared__ float2 cs[kWarps * kMaxPairs];
+__global__ void __launch_bounds__(kWarps * 32, 2) rope_kernel(const RopeParams p) {
+  __shared__ float2 s_cs[kWarps][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_token = 1 << p.warps_log2, tokens = kWarps >> p.warps_log2;   // of a CTA
-  const long long t0 = (long long)blockIdx.x * tokens;
-  const int slot = warp >> p.warps_log2, first = warp & (per_token - 1);
-  const long long t = t0 + slot;
-  const bool live = t < p.tokens;
-  const long long b = live ? t / p.L : 0, i = live ? t - b * p.L : 0;
+  float2* const cs = s_cs[warp];
   const int chunks = p.half >> 2;   // 16-byte chunks of the rotated dims
+  constexpr int kPairs = kInterleaved ? 4 : 8;   // of a lane's dims 8 lane ..
+  const bool turns = lane < chunks, upper = !kInterleaved && lane >= (chunks >> 1);
+  const int pair0 = kPairs * lane - (upper ? p.half : 0);
+  const int partner = turns ? (upper ? lane - (chunks >> 1) : lane + (chunks >> 1)) : lane;
+  const uint32_t step = gridDim.x * kWarps;
+  // An item: up to kRows heads of a token, of q or of k.
+  struct Item {
+    const uint4* x;
+    uint4* y;
+    long long xs, ys;   // from head to head
+    int n;              // heads; 0 for lanes that have nothing to do (of rows that are turned in place, the dims
+                        // that are not turned stay where they are)
+  };
+  const auto place = [&](uint32_t item, int& position) {
+    const uint32_t t = item / uint32_t(p.groups), b = p.one ? 0u : t / uint32_t(p.L), i = t - b * uint32_t(p.L);
+    position = __ldg(p.positions + size_t(b) * p.pos_batch + i);
+    const int g = int(item - t * uint32_t(p.groups));
+    const bool k = g >= p.q_groups;
+    const int h0 = (k ? g - p.q_groups : g) * kRows, heads = k ? p.heads[1] : p.heads[0];
+    Item r;
+    r.xs = k ? p.xs[1][2] : p.xs[0][2];
+    r.ys = k ? p.ys[1][2] : p.ys[0][2];
+    r.x = (k ? p.x[1] : p.x[0]) + (b * (k ? p.xs[1][0] : p.xs[0][0]) + i * (k ? p.xs[1][1] : p.xs[0][1]) + h0 * r.xs + lane);
+    r.y = (k ? p.y[1] : p.y[0]) + (b * (k ? p.ys[1][0] : p.ys[0][0]) + i * (k ? p.ys[1][1] : p.ys[0][1]) + h0 * r.ys + lane);
+    r.n = (k ? p.in_place[1] : p.in_place[0]) && !turns ? 0 : min(kRows, heads - h0);
+    return r;
+  };
+  const auto load = [&](const Item& r, uint4 (&u)[kRows]) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (k < r.n) u[k] = __ldcs(r.x + k * r.xs);
+  };
   let_next_start();
   wait_for_last();
-  uint4 u[kBatch];
-  // rows first + per_token (n0 + k); those of a head in place only as far as they change
-  const auto each = [&](int n0, auto&& f) {
+  unsigned long long freq[kMaxPairs / 32];   // of this lane's pairs
+  float size[kMaxPairs / 32];                // scale; NaN for a frequency that is none
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int h = first + per_token * (n0 + k);
-      if (!live || h >= p.heads) continue;
-      const int w = h >= p.q_heads;
-      if (p.in_place[w] && lane >= chunks) continue;
-      f(k, w, h - (w ? p.q_heads : 0));
-    }
-  };
-  const auto load = [&](int n0) {
-    each(n0, [&](int k, int w, int h) { u[k] = p.x[w][b * p.xs[w][0] + i * p.xs[w][1] + h * p.xs[w][2] + lane]; });
-  };
-#pragma unroll
-  for (int k = 0; k < kBatch; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
-  load(0);
-  for (int k = threadIdx.x; k < tokens * p.half; k += kWarps * 32) {
-    const int n = k / p.half, j = k - n * p.half;
-    const long long tt = t0 + n;
-    if (tt < p.tokens) {
-      const long long bb = tt / p.L;
-      cs[n * p.half + j] = turn(__ldg(p.positions + bb * p.pos_batch + (tt - bb * p.L)), __ldg(p.inv_freq + j), p.scale,
-                                p.inverse);
-    }
+  for (int m = 0; m < kMaxPairs / 32; ++m) {
+    const int j = lane + 32 * m;
+    const float f = j < p.half ? __ldg(p.inv_freq + j) : 0.f;
+    freq[m] = turns_of(p.inverse ? -f : f);
+    size[m] = fabsf(f) < INFINITY ? p.scale : __int_as_float(0x7FC00000);
   }
-  __syncthreads();
-  // this lane's pairs: of dims 8 lane .., the same for all heads
-  constexpr int kPairs = kInterleaved ? 4 : 8;
-  const bool upper = !kInterleaved && lane >= (chunks >> 1);
-  const bool turns = lane < chunks;
-  float2 a[kPairs];
+  uint4 u[kRows], next[kRows];
 #pragma unroll
-  for (int k = 0; k < kPairs; ++k) {
-    const int j = kPairs * lane - (upper ? p.half : 0) + k;
-    a[k] = turns && live ? cs[slot * p.half + j] : make_float2(1.f, 0.f);
-    if (upper) a[k].y = -a[k].y;
-  }
-  const int partner = turns ? (upper ? lane - (chunks >> 1) : lane + (chunks >> 1)) : lane;
-  const int n_rows = live ? (p.heads - first + per_token - 1) >> p.warps_log2 : 0;
-  for (int n0 = 0; n0 < n_rows; n0 += kBatch) {
-    if (n0 > 0) load(n0);
+  for (int k = 0; k < kRows; ++k) u[k] = next[k] = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t item = blockIdx.x * kWarps + warp;
+  if (item >= p.items) return;
+  int at, at_next = 0;
+  Item r = place(item, at), r_next = r;
+  load(r, u);
+  for (;;) {
+    const bool more = p.items - item > step;
+    if (more) {
+      r_next = place(item + step, at_next);
+      load(r_next, next);
+    }
+    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w}, o[4];
-      if constexpr (kInterleaved) {
+    for (int m = 0; m < kMaxPairs / 32; ++m)
+      if (32 * m < p.half) {
+        const float2 c = turn(at, freq[m]);
+        if (lane + 32 * m < p.half) cs[lane + 32 * m] = make_float2(c.x * size[m], c.y * size[m]);
+      }
+    __syncwarp();
+    float2 a[kPairs];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 x = unpack_elem2<kF16>(w[c]);
+    for (int k = 0; k < kPairs; ++k) {
+      a[k] = turns ? cs[pair0 + k] : make_float2(1.f, 0.f);
+      if (upper) a[k].y = -a[k].y;
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 x = unpack_elem2<kF16>(w[c]);
+        if constexpr (kInterleaved) {
           o[c] = pack_elem2<kF16>(x.x * a[c].x - x.y * a[c].y, x.y * a[c].x + x.x * a[c].y);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 x = unpack_elem2<kF16>(w[c]);
+        } else {
           const float2 y = unpack_elem2<kF16>(__shfl_sync(0xffffffffu, w[c], partner));
           o[c] = pack_elem2<kF16>(x.x * a[2 * c].x - y.x * a[2 * c].y, x.y * a[2 * c + 1].x - y.y * a[2 * c + 1].y);
         }
       }
       if (turns) u[k] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    each(n0, [&](int k, int w, int h) { p.y[w][b * p.ys[w][0] + i * p.ys[w][1] + h * p.ys[w][2] + lane] = u[k]; });
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (k < r.n) __stcs(r.y + k * r.ys, u[k]);
+    if (!more) break;
+    item += step;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) u[k] = next[k];
+    r = r_next;
+    at = at_next;
   }
 }
 
@@ -173,15 +203,20 @@ int rope_impl(bool f16, const void* Q, const void* K, const int* positions, cons
   p.pos_batch = pos_batch ? L : 0;
   p.inv_freq = inv_freq;
   p.L = L;
-  p.heads = Hq + Hkv;
-  p.q_heads = Hq;
+  p.heads[0] = Hq;
+  p.heads[1] = Hkv;
   p.half = rot_dims / 2;
-  while ((kBatch << p.warps_log2) < p.heads && (1 << p.warps_log2) < kWarps) ++p.warps_log2;
-  p.tokens = (long long)B * L;
+  p.q_groups = (Hq + kRows - 1) / kRows;
+  p.groups = p.q_groups + (Hkv + kRows - 1) / kRows;
+  const long long items = (long long)B * L * p.groups;
+  if (items >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  p.items = uint32_t(items);
+  p.one = B == 1;
   p.scale = scale;
   p.inverse = inverse != 0;
-  const int per_cta = kWarps >> p.warps_log2;
-  const unsigned grid = unsigned((p.tokens + per_cta - 1) / per_cta);
+  // as many CTAs as the SMs hold, of a warp's worth of items each where there are few
+  const long long ctas = (items + kWarps - 1) / kWarps, most = 2LL * device_sm_count();
+  const unsigned grid = unsigned(ctas < most ? ctas : most);
   const auto kernel = f16 ? (interleaved ? rope_kernel<true, true> : rope_kernel<true, false>)
                           : (interleaved ? rope_kernel<false, true> : rope_kernel<false, false>);
   if (launch_dependent(kernel, dim3(grid), kWarps * 32, 0, static_cast<cudaStream_t>(stream), 1, p) != cudaSuccess)
