@@ -16,3 +16,6 @@ from .kv8 import (  # noqa: F401
     E4M3, E4M3_MAX, e4m3_encode, scale_exponent, block_plan, kv8_append, kv8_keep,
     kv8_contiguous,
 )
+from .pages import (  # noqa: F401
+    angle, block_fork, block_free, block_compact, kv8_copy, rope,
+)
