@@ -23,8 +23,7 @@
 //
 // Roles (512 threads): warp 0 schedules (pieces, block numbers and scales of the tiles), warp 1 of the even
 // CTA issues the products, warp 2 copies K, warps 4..7 convert V into shared memory, warps 8..15 are softmax and
-// epilogue: two teams of four take the tiles in turn, a thread has a row (its tensor-memory lane), so that one
-// team's softmax runs beside the other's and beside the products, and no maximum is exchanged within a tile.
+// epilogue: a thread has a row (its tensor-memory lane) and 64 keys of each tile.
 // TMEM: O 256 columns, two buffers of 128 for S and P.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -102,13 +101,13 @@ struct __align__(1024) ChunkSmem {
   uint8_t k[kKs][kSlotK], v[kVs][kSlotV];
   TileRec rec[kTiles];
   ChunkPiece piece[kPieces];
-  float2 refs[2][128];                    // [tile parity][row]: the references after the tile
-  float sum[2][128];                      // [team][row]
+  float2 red[2][2][128];                  // [tile parity][half][row]: maxima with vs, without
+  float sum[2][128];                      // [half][row]
   float fac[2][128];                      // by piece parity
   uint32_t hit[kHitSets][kHitWords];
   uint64_t rec_full[kGroups], rec_empty[kGroups];
   uint64_t k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
-  uint64_t s_full[2], p_full[2][2], ref_full[2][4], pv_done, q_full, o_full, o_free, drain;
+  uint64_t s_full[2], p_full[2][2], pv_done, q_full, o_full, o_free, drain;
   uint64_t hit_full[kHitSets];
   int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
   uint32_t cost[kKv8Seqs], at[kKv8Seqs + 1];   // of one KV head; of all, before each sequence
@@ -262,8 +261,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.s_full[i], 1);
-      for (int h = 0; h < 2; ++h) ptx::mbar_init(&sm.p_full[i][h], 8);
-      for (int k = 0; k < 4; ++k) ptx::mbar_init(&sm.ref_full[i][k], 1);
+      for (int h = 0; h < 2; ++h) ptx::mbar_init(&sm.p_full[i][h], 16);
     }
     for (int i = 0; i < kKs; ++i) {
       ptx::mbar_init(&sm.k_full[i], 1);
@@ -493,13 +491,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (!hold(&sm.v_full[vs], (n / kVs) & 1u, tmo, &sm.abort)) return false;
         const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kSlotV / 2, 1024);
 #pragma unroll 1
-        for (uint32_t h = 0; h < 2; ++h) {   // (the first half's product runs beside the second's exponentials)
+        for (uint32_t h = 0; h < 2; ++h) {   // (the product of each half's first 32 keys runs beside the others' exponentials)
           if (!hold(&sm.p_full[n & 1u][h], (n >> 1) & 1u, tmo, &sm.abort)) return false;
           ptx::tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + (n & 1u) * 128 + h * 64 + kk * 8,
-                             ptx::sdesc_at(vd, h * 8192 + kk * 2048), kIdescOc, !first || h > 0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk) {   // keys 64 (kk / 2) + 32 h + 16 (kk % 2) ..
+            const uint32_t k16 = (kk >> 1) * 4 + 2 * h + (kk & 1);
+            ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + (n & 1u) * 128 + (kk >> 1) * 64 + 16 * h + (kk & 1) * 8,
+                             ptx::sdesc_at(vd, k16 * 2048), kIdescOc, !first || h > 0 || kk > 0);
+          }
         }
         ptx::tc_commit_pair(&sm.pv_done, 3);
         ptx::tc_commit_pair(&sm.v_empty[vs], 3);
@@ -673,9 +673,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------ softmax, epilogue
     take_regs<kRegsSoft>();
-    const int sw = warp - kSoftWarp, qd = warp & 3, row = qd * 32 + lane;
-    const uint32_t team = uint32_t(sw) >> 2;   // tiles of this parity; in the epilogue, columns 128 team ..
+    const int sw = warp - kSoftWarp, half = sw >> 2, qd = warp & 3, row = qd * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(qd * 32) << 16);
+    const uint32_t bar_id = 1 + qd;   // the two warps of a quadrant
     uint32_t J = 0, pc = 0;
     bool ok = true;
     // Q's terms of piece n; then its products may start.  (The last piece's S products are done.)
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             for (int c = 0; c < 4; ++c) o[c] = take_half_term(h[c]);
             *reinterpret_cast<uint2*>(to + t * 2 * 128 * 128) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
           }
-          }
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) u[k] = next[k];
       }
@@ -755,24 +755,22 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       float ref = kNone, ml = kNone, l = 0.f;
       for (int j = 0; j < n_tiles; ++j, ++J) {
         const uint32_t buf = J & 1u;
-        if (buf != team) continue;
         ok = ok && wait_rec(sm, J, tmo) && hold(&sm.s_full[buf], (J >> 1) & 1u, tmo, &sm.abort);
         ok = warp_all(ok);
         __syncwarp();
-        if (!ok) break;
         ptx::tc_fence_after();
         const TileRec& r = sm.rec[J % kTiles];
-        const uint32_t ts = trow + kTmSc + buf * 128;
-        const int left = lim - r.key0;   // keys of the tile that the row sees
+        const uint32_t ts = trow + kTmSc + buf * 128 + half * 64;
+        const int left = lim - r.key0 - half * 64;   // of this thread's keys, those that the row sees
         // Loops over 32 keys, not unrolled: the roles' code shares the schedulers' instruction caches.
         // A run's score factor is finite and not 0, so that a hidden key's -inf stays one and 0 stays 0.
         const auto factors = [&](int q) -> float2 {
-          const float2 k2 = *reinterpret_cast<const float2*>(&r.ks[2 * q]);
+          const float2 k2 = *reinterpret_cast<const float2*>(&r.ks[4 * half + 2 * q]);
           return make_float2(fminf(fmaxf(fac * k2.x, 1e-37f), 3e38f), fminf(fmaxf(fac * k2.y, 1e-37f), 3e38f));
         };
-        if (__any_sync(0xffffffffu, left < kTile)) {   // keys that some row does not see: -inf
+        if (ok && __any_sync(0xffffffffu, left < 64)) {   // keys that some row does not see: -inf
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t s[32];
             ptx::tmem_ld32_wait(ts + 32 * q, s);
 #pragma unroll
@@ -784,15 +782,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         // f(q, scores) for each 32 keys
         const auto each = [&](auto&& f) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t s[32];
             ptx::tmem_ld32_wait(ts + 32 * q, s);
             f(q, s);
           }
         };
         float mp = -INFINITY, ms = -INFINITY;
-        each([&](int q, uint32_t (&s)[32]) {
-          const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[2 * q]);
+        if (ok) each([&](int q, uint32_t (&s)[32]) {
+          const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[4 * half + 2 * q]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float m = fmaxf(__uint_as_float(s[16 * i]), __uint_as_float(s[16 * i + 1]));
@@ -807,22 +805,28 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             mp = fmaxf(mp, m + (i ? lv2.y : lv2.x));
           }
         });
-        // ---- references: those after the last tile, moved on
-        float2 at = make_float2(kNone, kNone);
-        if (j > 0) {
-          ok = warp_all(hold(&sm.ref_full[buf ^ 1u][qd], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
-          if (!ok) break;
-          at = sm.refs[buf ^ 1u][row];
+        // (a maximum is never NaN: that says that the warp gives up)
+        sm.red[buf][half][row] = make_float2(ok ? mp : __int_as_float(0x7FC00000), ms);
+        ptx::named_bar_sync(bar_id, 64);
+        {
+          const float2 o = sm.red[buf][half ^ 1][row];
+          ok = ok && o.x == o.x;
+          mp = fmaxf(mp, o.x);
+          ms = fmaxf(ms, o.y);
         }
-        // (where one row's has to move, O is scaled anyway, and those of the warp's others go along)
-        const bool moved = __any_sync(0xffffffffu, mp > at.x + kCap);
-        ref = moved ? fmaxf(at.x, mp - kTop) : at.x;
-        if (ms > at.y + kLSlack) at.y = ms;
-        sm.refs[buf][row] = make_float2(ref, at.y);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.ref_full[buf][qd]);
-        l *= ex2(ml - at.y);
-        ml = at.y;
+        if (!warp_all(ok)) {
+          ok = false;
+          break;
+        }
+        // ---- references (both threads of a row do the same).  Where one row's has to move, O is scaled anyway, and those
+        // of the warp's others go along.
+        const float at = ref;
+        const bool moved = __any_sync(0xffffffffu, mp > at + kCap);
+        if (moved) ref = fmaxf(at, mp - kTop);
+        if (ms > ml + kLSlack) {
+          l *= ex2(ml - ms);
+          ml = ms;
+        }
         // ---- P goes where the scores were
         // l's terms come from p's: p * 2^(ref - log2 vs - ml), unless p may have lost them
         const float back = ref - ml;
@@ -834,7 +838,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             for (int c = 0; c < 32; ++c) l += ex2(fmaf(__uint_as_float(s[c]), c < 16 ? f2.x : f2.y, -ml));
           });
         }
-        // Half a tile's P is there for the product (where O has to be scaled first, both at the end).
+        // 32 keys' P are there for the product (where O has to be scaled first, all at the end).
         const bool scale = moved && j > 0;
         const auto done = [&](int h) {
           ptx::tmem_wait_st();
@@ -843,7 +847,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           if (lane == 0) arrive_lead(&sm.p_full[buf][h], lead);
         };
         each([&](int q, uint32_t (&s)[32]) {
-          const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[2 * q]);
+          const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[4 * half + 2 * q]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float fi = i ? f2.y : f2.x, lv = i ? lv2.y : lv2.x, a = lv - ref;
@@ -858,31 +862,32 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
               sum2 = add2(sum2, e);
               pk[c] = pack_half2(e.x, e.y);
             }
-            ptx::tmem_st8(ts + 64 * (q >> 1) + 16 * (q & 1) + 8 * i, pk);
+            ptx::tmem_st8(ts + 16 * q + 8 * i, pk);
             if (!far) l += (sum2.x + sum2.y) * ex2(back - lv);
           }
-          if ((q & 1) && !scale) done(q >> 1);
+          if (!scale) done(q);
         });
         if (scale) {
-          // O, with PV of tile J - 1 in it, moves to the new references
+          // O, with PV of tile J - 1 in it, moves to the new references.  (A warp that gives up here says so at the
+          // next tile's barrier, or at the piece's end.)
           ok = warp_all(hold(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const float alpha = ex2(at.x - ref);
+          if (ok) {
+            ptx::tc_fence_after();
+            const float alpha = ex2(at - ref);
 #pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            const uint32_t to = trow + kTmOc + 32 * cc;
-            uint32_t o[32];
-            ptx::tmem_ld32_wait(to, o);
+            for (int cc = 0; cc < 4; ++cc) {
+              const uint32_t to = trow + kTmOc + half * 128 + 32 * cc;
+              uint32_t o[32];
+              ptx::tmem_ld32_wait(to, o);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            ptx::tmem_st32_wait(to, o);
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              ptx::tmem_st32_wait(to, o);
+            }
+            done(0);
+            done(1);
           }
-          done(0);
-          done(1);
         }
-        // (its second tile of the group)
-        if (lane == 0 && (J % kGroup) >> 1 == kGroup / 2 - 1)
+        if (lane == 0 && J % kGroup == kGroup - 1)
           ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
       }
       if (!ok) {
@@ -891,18 +896,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         stop = true;
         break;
       }
-      // S of the last tile, be it the other team's, has read Q before the next piece's is written
-      ok = warp_all(hold(&sm.s_full[(J - 1u) & 1u], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
       // ---- the next piece may start while this one ends
       ok = warp_all(ok && wait_rec(sm, J, tmo));
       more = ok && sm.rec[J % kTiles].n_tiles > 0;
       if (more) prepare(pc + 1u);
-      ok = warp_all(ok && hold(&sm.ref_full[(J - 1u) & 1u][qd], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
-      const float2 fin = sm.refs[(J - 1u) & 1u][row];   // the references after the last tile
-      ref = fin.x;
-      l *= ex2(ml - fin.y);
-      ml = fin.y;
-      sm.sum[team][row] = l;
+      sm.sum[half][row] = l;
       const ChunkPiece& x = sm.piece[pc % kPieces];
       const bool mine = lim > 0;
       const int i_new = lim - 1 - x.base, pk = x.rb * kPairRows + int(rank) * 128 + row;
@@ -911,7 +909,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       const auto gate32 = [&](int cc, uint4 (&g4)[4]) {   // 32 of this thread's 128 columns
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (gated) g4[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + team * 128) + 4 * cc + c);
+          if (gated) g4[c] = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256 + half * 128) + 4 * cc + c);
       };
       uint4 g4[4], g_next[4];
       gate32(0, g4);
@@ -920,18 +918,18 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       stop = ptx::named_bar_or(9, 256, !ok);
       if (stop) break;
       ptx::tc_fence_after();
-      const float L = l + sm.sum[team ^ 1u][row];
+      const float L = l + sm.sum[half ^ 1][row];
       const float ex = ex2(0.5f * (ref - ml)), inv = L == 0.f ? 0.f : ex / L;   // (O times both)
       const float lse = L == 0.f ? -INFINITY : (ml + __log2f(L)) * kLn2;
       const int set = pc % kHitSets;
       // every warp is past the last piece, whose hits may go
-      if (team == 0 && row < kHitWords) sm.hit[(pc + kHitSets - 1) % kHitSets][row] = 0u;
+      if (half == 0 && row < kHitWords) sm.hit[(pc + kHitSets - 1) % kHitSets][row] = 0u;
       uint32_t any = 0u;
 #pragma unroll
       for (int w = 0; w < kHitWords; ++w) any |= *reinterpret_cast<volatile uint32_t*>(&sm.hit[set][w]);
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
-        const int col = int(team) * 128 + 32 * cc;
+        const int col = half * 128 + 32 * cc;
         __syncwarp();
         uint32_t o[32];
         ptx::tmem_ld32_wait(trow + kTmOc + col, o);
@@ -972,10 +970,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         }
       }
       if (any != 0u && mine && L != 0.f)
-        put_back(p, sm.hit[set], x.b, x.g, x.base + x.rb * kPairRows / p.gqa + 1, lim, int(team) * 128,
+        put_back(p, sm.hit[set], x.b, x.g, x.base + x.rb * kPairRows / p.gqa + 1, lim, half * 128,
                  x.part < 0 ? nullptr : p.o_parts + (size_t(x.part) * kPairRows + int(rank) * 128 + row) * 256,
                  p.out + at * 256, kF16 ? 0x7E00u : 0x7FC0u);
-      if (mine && team == 0) {
+      if (mine && half == 0) {
         if (x.part >= 0)
           p.lse_parts[size_t(x.part) * kPairRows + int(rank) * 128 + row] = lse;
         else if (p.lse != nullptr)
