@@ -27,6 +27,7 @@
 // TMEM: O 256 columns, two buffers of 128 for S and P.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 
 #include "kv8_attn.cuh"
 
@@ -464,75 +465,89 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         sm.abort = 1;
         record_status(p.ctl.status, GQA_ERR_TIMEOUT);
       }
-    } else if (warp == 1 && lead && lane == 0) {
+    } else if (warp == 1 && lead) {
       // ---------------------------------------------------------- products
-      const uint64_t qd = ptx::sdesc_sw128(ptx::smem_addr(sm.q), 16, 1024);
+      // The whole warp goes through the loop, with what the products take in uniform registers (hence the shuffles);
+      // one lane issues.
+      const uint32_t go = lane == 0;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t base = __shfl_sync(0xffffffffu, ptx::smem_addr(&sm), 0);
+      const uint64_t qd = ptx::sdesc_sw128(base + offsetof(Sm, q), 16, 1024);
       uint32_t J = 0, pc = 0;
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
         const uint32_t ks = n % kKs;
-        if (!hold(&sm.k_full[ks], (n / kKs) & 1u, tmo, &sm.abort)) return false;
+        if (!warp_all(hold(&sm.k_full[ks], (n / kKs) & 1u, tmo, &sm.abort))) return false;
         ptx::tc_fence_after();
-        const uint64_t kd = ptx::sdesc_sw128(ptx::smem_addr(sm.k[ks]), 16, 1024);
+        const uint64_t kd = ptx::sdesc_sw128(base + offsetof(Sm, k) + ks * kSlotK, 16, 1024);
+        const uint32_t d = tm + kTmSc + (n & 1u) * 128;
 #pragma unroll
         for (int t = 0; t < Sm::kQTerms; ++t)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            ptx::mma_ss_pair_f8(tmem + kTmSc + (n & 1u) * 128,
-                                ptx::sdesc_at(qd, t * 32768 + (kk >> 2) * 16384 + (kk & 3) * 32),
-                                ptx::sdesc_at(kd, (kk >> 2) * (kSlotK / 2) + (kk & 3) * 32), kIdescSc,
-                                t > 0 || kk > 0);
-        ptx::tc_commit_pair(&sm.s_full[n & 1u], 3);
-        ptx::tc_commit_pair(&sm.k_empty[ks], 3);
+            ptx::mma_ss_pair_f8_if(go, d, ptx::sdesc_at(qd, t * 32768 + (kk >> 2) * 16384 + (kk & 3) * 32),
+                                   ptx::sdesc_at(kd, (kk >> 2) * (kSlotK / 2) + (kk & 3) * 32), kIdescSc,
+                                   t > 0 || kk > 0);
+        if (go) {
+          ptx::tc_commit_pair(&sm.s_full[n & 1u], 3);
+          ptx::tc_commit_pair(&sm.k_empty[ks], 3);
+        }
+        __syncwarp();
         return true;
       };
-      const auto issue_pv = [&](uint32_t n, bool first) -> bool {
+      const auto issue_pv = [&](uint32_t n, uint32_t accumulate) -> bool {
         const uint32_t vs = n % kVs;
-        if (!hold(&sm.v_full[vs], (n / kVs) & 1u, tmo, &sm.abort)) return false;
-        const uint64_t vd = ptx::sdesc_sw128(ptx::smem_addr(sm.v[vs]), kSlotV / 2, 1024);
-#pragma unroll 1
-        for (uint32_t h = 0; h < 2; ++h) {   // (the product of each half's first 32 keys runs beside the others' exponentials)
-          if (!hold(&sm.p_full[n & 1u][h], (n >> 1) & 1u, tmo, &sm.abort)) return false;
+        if (!warp_all(hold(&sm.v_full[vs], (n / kVs) & 1u, tmo, &sm.abort))) return false;
+        const uint64_t vd = ptx::sdesc_sw128(base + offsetof(Sm, v) + vs * kSlotV, kSlotV / 2, 1024);
+        const uint32_t a = tm + kTmSc + (n & 1u) * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // (the product of each half's first 32 keys runs beside the others' exponentials)
+          if (!warp_all(hold(&sm.p_full[n & 1u][h], (n >> 1) & 1u, tmo, &sm.abort))) return false;
           ptx::tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {   // keys 64 (kk / 2) + 32 h + 16 (kk % 2) ..
-            const uint32_t k16 = (kk >> 1) * 4 + 2 * h + (kk & 1);
-            ptx::mma_ts_pair(tmem + kTmOc, tmem + kTmSc + (n & 1u) * 128 + (kk >> 1) * 64 + 16 * h + (kk & 1) * 8,
-                             ptx::sdesc_at(vd, k16 * 2048), kIdescOc, !first || h > 0 || kk > 0);
-          }
+          for (int kk = 0; kk < 4; ++kk)   // keys 64 (kk / 2) + 32 h + 16 (kk % 2) ..
+            ptx::mma_ts_pair_if(go, tm + kTmOc, a + (kk >> 1) * 64 + 16 * h + (kk & 1) * 8,
+                                ptx::sdesc_at(vd, ((kk >> 1) * 4 + 2 * h + (kk & 1)) * 2048), kIdescOc,
+                                h > 0 || kk > 0 ? 1u : accumulate);
         }
-        ptx::tc_commit_pair(&sm.pv_done, 3);
-        ptx::tc_commit_pair(&sm.v_empty[vs], 3);
+        if (go) {
+          ptx::tc_commit_pair(&sm.pv_done, 3);
+          ptx::tc_commit_pair(&sm.v_empty[vs], 3);
+        }
+        __syncwarp();
         return true;
       };
       while (ok) {
-        ok = wait_rec(sm, J, tmo);
+        ok = warp_all(wait_rec(sm, J, tmo));
         if (!ok) break;
-        const int n_tiles = sm.rec[J % kTiles].n_tiles;
+        const int n_tiles = __shfl_sync(0xffffffffu, sm.rec[J % kTiles].n_tiles, 0);
         if (n_tiles == 0) break;
-        ok = hold(&sm.q_full, pc & 1u, tmo, &sm.abort);
+        ok = warp_all(hold(&sm.q_full, pc & 1u, tmo, &sm.abort));
         if (!ok) break;
         ptx::tc_fence_after();
         ok = issue_s(J);
         if (ok && n_tiles > 1) ok = issue_s(J + 1);
         // O of the last piece has been read by every warp
-        if (ok && pc > 0) ok = hold(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort);
+        if (ok && pc > 0) ok = warp_all(hold(&sm.o_free, (pc - 1u) & 1u, tmo, &sm.abort));
         for (int j = 0; ok && j < n_tiles; ++j) {
-          ok = issue_pv(J + j, j == 0);
+          ok = issue_pv(J + j, j > 0);
           // S of tile j + 2 goes where P of tile j lies: products run in the order of issue
           if (ok && j + 2 < n_tiles) ok = issue_s(J + j + 2);
         }
-        if (ok) ptx::tc_commit_pair(&sm.o_full, 3);
+        if (ok && go) ptx::tc_commit_pair(&sm.o_full, 3);
+        __syncwarp();
         J += n_tiles;
         ++pc;
       }
-      if (!ok) {
-        sm.abort = 1;
-        record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+      if (go) {
+        if (!ok) {
+          sm.abort = 1;
+          record_status(p.ctl.status, GQA_ERR_TIMEOUT);
+        }
+        // every product issued has to end before tensor memory is given back
+        ptx::tc_commit_pair(&sm.drain, 1);
+        hold(&sm.drain, 0, tmo, &sm.zero);
       }
-      // every product issued has to end before tensor memory is given back
-      ptx::tc_commit_pair(&sm.drain, 1);
-      hold(&sm.drain, 0, tmo, &sm.zero);
     } else if (warp == 2) {
       // ---------------------------------------------------------- copies of K
       // This CTA's 64 keys of a tile, a box of up to 64 keys x 128 dims a lane; both CTAs' bytes count on the
