@@ -40,7 +40,7 @@ constexpr int kConvWarp = 4, kSoftWarp = 8;     // first warps
 // Registers a thread, by warpgroup, out of the launch's 128 (inc waits until they are there).
 constexpr int kRegsRest = 80, kRegsConv = 112, kRegsSoft = 160;
 static_assert(kRegsRest + kRegsConv + 2 * kRegsSoft <= 4 * 128, "the launch's registers");
-constexpr int kSlotK = 16384, kKs = 3;          // half a tile of K as it lies; slots
+constexpr int kSlotK = 16384, kKs = 2;          // half a tile of K as it lies; slots
 constexpr int kSlotV = 32768, kVs = 2;          // half a tile of V in fp16
 constexpr int kGroup = 4;                       // tiles that the scheduler looks up together
 constexpr int kGroups = 4;                      // groups held
@@ -107,8 +107,10 @@ struct __align__(1024) ChunkSmem {
   float fac[2][128];                      // by piece parity
   uint32_t hit[kHitSets][kHitWords];
   uint64_t rec_full[kGroups], rec_empty[kGroups];
-  uint64_t k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
-  uint64_t s_full[2], p_full[2][2], pv_done, q_full, o_full, o_free, drain;
+  // By tile parity (a slot's barrier cannot come round again before its user has waited): K has landed; S is done, and
+  // its K slot free; V and the first 32 keys' P of each half are there, the others'; PV is done, its V slot free.
+  uint64_t k_full[2], s_full[2], p_full[2][2], pv_done[2];
+  uint64_t q_full, o_free, drain;
   uint64_t hit_full[kHitSets];
   int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
   uint32_t cost[kKv8Seqs], at[kKv8Seqs + 1];   // of one KV head; of all, before each sequence
@@ -261,20 +263,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       ptx::mbar_init(&sm.rec_empty[i], 13);   // K's copies, 4 converting warps, 8 of softmax
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.s_full[i], 1);
-      for (int h = 0; h < 2; ++h) ptx::mbar_init(&sm.p_full[i][h], 16);
-    }
-    for (int i = 0; i < kKs; ++i) {
       ptx::mbar_init(&sm.k_full[i], 1);
-      ptx::mbar_init(&sm.k_empty[i], 1);
+      ptx::mbar_init(&sm.s_full[i], 1);
+      ptx::mbar_init(&sm.p_full[i][0], 16 + 8);   // softmax and converting warps of both CTAs
+      ptx::mbar_init(&sm.p_full[i][1], 16);
+      ptx::mbar_init(&sm.pv_done[i], 1);
     }
-    for (int i = 0; i < kVs; ++i) {
-      ptx::mbar_init(&sm.v_full[i], 8);
-      ptx::mbar_init(&sm.v_empty[i], 1);
-    }
-    ptx::mbar_init(&sm.pv_done, 1);
     ptx::mbar_init(&sm.q_full, 16);
-    ptx::mbar_init(&sm.o_full, 1);
     ptx::mbar_init(&sm.o_free, 16);
     ptx::mbar_init(&sm.drain, 1);
     for (int i = 0; i < kHitSets; ++i) ptx::mbar_init(&sm.hit_full[i], 8);
@@ -476,11 +471,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       uint32_t J = 0, pc = 0;
       bool ok = true;
       const auto issue_s = [&](uint32_t n) -> bool {
-        const uint32_t ks = n % kKs;
-        if (!warp_all(hold(&sm.k_full[ks], (n / kKs) & 1u, tmo, &sm.abort))) return false;
+        const uint32_t ks = n & 1u;
+        if (!warp_all(hold(&sm.k_full[ks], (n >> 1) & 1u, tmo, &sm.abort))) return false;
         ptx::tc_fence_after();
         const uint64_t kd = ptx::sdesc_sw128(base + offsetof(Sm, k) + ks * kSlotK, 16, 1024);
-        const uint32_t d = tm + kTmSc + (n & 1u) * 128;
+        const uint32_t d = tm + kTmSc + ks * 128;
 #pragma unroll
         for (int t = 0; t < Sm::kQTerms; ++t)
 #pragma unroll
@@ -488,21 +483,17 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             ptx::mma_ss_pair_f8_if(go, d, ptx::sdesc_at(qd, t * 32768 + (kk >> 2) * 16384 + (kk & 3) * 32),
                                    ptx::sdesc_at(kd, (kk >> 2) * (kSlotK / 2) + (kk & 3) * 32), kIdescSc,
                                    t > 0 || kk > 0);
-        if (go) {
-          ptx::tc_commit_pair(&sm.s_full[n & 1u], 3);
-          ptx::tc_commit_pair(&sm.k_empty[ks], 3);
-        }
+        if (go) ptx::tc_commit_pair(&sm.s_full[ks], 3);
         __syncwarp();
         return true;
       };
       const auto issue_pv = [&](uint32_t n, uint32_t accumulate) -> bool {
-        const uint32_t vs = n % kVs;
-        if (!warp_all(hold(&sm.v_full[vs], (n / kVs) & 1u, tmo, &sm.abort))) return false;
+        const uint32_t vs = n & 1u;
         const uint64_t vd = ptx::sdesc_sw128(base + offsetof(Sm, v) + vs * kSlotV, kSlotV / 2, 1024);
-        const uint32_t a = tm + kTmSc + (n & 1u) * 128;
+        const uint32_t a = tm + kTmSc + vs * 128;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {   // (the product of each half's first 32 keys runs beside the others' exponentials)
-          if (!warp_all(hold(&sm.p_full[n & 1u][h], (n >> 1) & 1u, tmo, &sm.abort))) return false;
+          if (!warp_all(hold(&sm.p_full[vs][h], (n >> 1) & 1u, tmo, &sm.abort))) return false;
           ptx::tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)   // keys 64 (kk / 2) + 32 h + 16 (kk % 2) ..
@@ -510,10 +501,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
                                 ptx::sdesc_at(vd, ((kk >> 1) * 4 + 2 * h + (kk & 1)) * 2048), kIdescOc,
                                 h > 0 || kk > 0 ? 1u : accumulate);
         }
-        if (go) {
-          ptx::tc_commit_pair(&sm.pv_done, 3);
-          ptx::tc_commit_pair(&sm.v_empty[vs], 3);
-        }
+        if (go) ptx::tc_commit_pair(&sm.pv_done[vs], 3);
         __syncwarp();
         return true;
       };
@@ -534,8 +522,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
           // S of tile j + 2 goes where P of tile j lies: products run in the order of issue
           if (ok && j + 2 < n_tiles) ok = issue_s(J + j + 2);
         }
-        if (ok && go) ptx::tc_commit_pair(&sm.o_full, 3);
-        __syncwarp();
         J += n_tiles;
         ++pc;
       }
@@ -561,8 +547,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (!ok) break;
         const TileRec& r = sm.rec[J % kTiles];
         if (r.n_tiles == 0) break;
-        const uint32_t ks = J % kKs;
-        if (J >= kKs) ok = warp_all(hold(&sm.k_empty[ks], (J / kKs - 1u) & 1u, tmo, &sm.abort));
+        const uint32_t ks = J & 1u;
+        if (J >= kKs) ok = warp_all(hold(&sm.s_full[ks], ((J >> 1) - 1u) & 1u, tmo, &sm.abort));
         if (!ok) break;
         const int left = r.k_hi - r.key0;
         if (lead && lane == 0) {
@@ -635,9 +621,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       return true;
     };
     for (uint32_t J = 0; load(J); ++J) {
-      const uint32_t vs = J % kVs;
+      const uint32_t vs = J & 1u;
       if (J >= kVs)
-        ok = warp_all(ok && hold(&sm.v_empty[vs], (J / kVs - 1u) & 1u, tmo, &sm.abort));
+        ok = warp_all(ok && hold(&sm.pv_done[vs], ((J >> 1) - 1u) & 1u, tmo, &sm.abort));
       if (!ok) break;
       const TileRec& r = sm.rec[J % kTiles];
       if (r.key0 + kTile > r.pr_lo) {
@@ -670,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_lead(&sm.v_full[vs], lead);
+        arrive_lead(&sm.p_full[vs][0], lead);
         if (r.last) {
           uint64_t* const h = &sm.hit_full[r.piece % kHitSets];
           ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 0));
@@ -885,7 +871,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (scale) {
           // O, with PV of tile J - 1 in it, moves to the new references.  (A warp that gives up here says so at the
           // next tile's barrier, or at the piece's end.)
-          ok = warp_all(hold(&sm.pv_done, (J - 1u) & 1u, tmo, &sm.abort));
+          ok = warp_all(hold(&sm.pv_done[buf ^ 1u], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
           if (ok) {
             ptx::tc_fence_after();
             const float alpha = ex2(at - ref);
@@ -929,7 +915,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       uint4 g4[4], g_next[4];
       gate32(0, g4);
       ok = warp_all(ok && hold(&sm.hit_full[pc % kHitSets], (pc / kHitSets) & 1u, tmo, &sm.abort) &&
-                    hold(&sm.o_full, pc & 1u, tmo, &sm.abort));
+                    hold(&sm.pv_done[(J - 1u) & 1u], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
       stop = ptx::named_bar_or(9, 256, !ok);
       if (stop) break;
       ptx::tc_fence_after();
