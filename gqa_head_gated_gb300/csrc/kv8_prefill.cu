@@ -108,8 +108,8 @@ struct __align__(1024) ChunkSmem {
   uint32_t hit[kHitSets][kHitWords];
   uint64_t rec_full[kGroups], rec_empty[kGroups];
   // By tile parity (a slot's barrier cannot come round again before its user has waited): K has landed; S is done, and
-  // its K slot free; V and the first 32 keys' P of each half are there, the others'; PV is done, its V slot free.
-  uint64_t k_full[2], s_full[2], p_full[2][2], pv_done[2];
+  // its K slot free; V and P are there; PV is done, its V slot free.
+  uint64_t k_full[2], s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_free, drain;
   uint64_t hit_full[kHitSets];
   int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
@@ -265,8 +265,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.k_full[i], 1);
       ptx::mbar_init(&sm.s_full[i], 1);
-      ptx::mbar_init(&sm.p_full[i][0], 16 + 8);   // softmax and converting warps of both CTAs
-      ptx::mbar_init(&sm.p_full[i][1], 16);
+      ptx::mbar_init(&sm.p_full[i], 16 + 8);   // softmax and converting warps of both CTAs
       ptx::mbar_init(&sm.pv_done[i], 1);
     }
     ptx::mbar_init(&sm.q_full, 16);
@@ -491,16 +490,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         const uint32_t vs = n & 1u;
         const uint64_t vd = ptx::sdesc_sw128(base + offsetof(Sm, v) + vs * kSlotV, kSlotV / 2, 1024);
         const uint32_t a = tm + kTmSc + vs * 128;
+        if (!warp_all(hold(&sm.p_full[vs], (n >> 1) & 1u, tmo, &sm.abort))) return false;
+        ptx::tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // (the product of each half's first 32 keys runs beside the others' exponentials)
-          if (!warp_all(hold(&sm.p_full[vs][h], (n >> 1) & 1u, tmo, &sm.abort))) return false;
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)   // keys 64 (kk / 2) + 32 h + 16 (kk % 2) ..
-            ptx::mma_ts_pair_if(go, tm + kTmOc, a + (kk >> 1) * 64 + 16 * h + (kk & 1) * 8,
-                                ptx::sdesc_at(vd, ((kk >> 1) * 4 + 2 * h + (kk & 1)) * 2048), kIdescOc,
-                                h > 0 || kk > 0 ? 1u : accumulate);
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_ts_pair_if(go, tm + kTmOc, a + (kk >> 2) * 64 + (kk & 3) * 8, ptx::sdesc_at(vd, kk * 2048), kIdescOc,
+                              kk > 0 ? 1u : accumulate);
         if (go) ptx::tc_commit_pair(&sm.pv_done[vs], 3);
         __syncwarp();
         return true;
@@ -656,7 +651,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        arrive_lead(&sm.p_full[vs][0], lead);
+        arrive_lead(&sm.p_full[vs], lead);
         if (r.last) {
           uint64_t* const h = &sm.hit_full[r.piece % kHitSets];
           ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(h), 0));
@@ -839,14 +834,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             for (int c = 0; c < 32; ++c) l += ex2(fmaf(__uint_as_float(s[c]), c < 16 ? f2.x : f2.y, -ml));
           });
         }
-        // 32 keys' P are there for the product (where O has to be scaled first, all at the end).
-        const bool scale = moved && j > 0;
-        const auto done = [&](int h) {
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_lead(&sm.p_full[buf][h], lead);
-        };
         each([&](int q, uint32_t (&s)[32]) {
           const float2 f2 = factors(q), lv2 = *reinterpret_cast<const float2*>(&r.lv[4 * half + 2 * q]);
 #pragma unroll
@@ -866,9 +853,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
             ptx::tmem_st8(ts + 16 * q + 8 * i, pk);
             if (!far) l += (sum2.x + sum2.y) * ex2(back - lv);
           }
-          if (!scale) done(q);
         });
-        if (scale) {
+        ptx::tmem_wait_st();
+        if (moved && j > 0) {
           // O, with PV of tile J - 1 in it, moves to the new references.  (A warp that gives up here says so at the
           // next tile's barrier, or at the piece's end.)
           ok = warp_all(hold(&sm.pv_done[buf ^ 1u], ((J - 1u) >> 1) & 1u, tmo, &sm.abort));
@@ -884,10 +871,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
               for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
               ptx::tmem_st32_wait(to, o);
             }
-            done(0);
-            done(1);
           }
         }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) arrive_lead(&sm.p_full[buf], lead);
         if (lane == 0 && J % kGroup == kGroup - 1)
           ptx::mbar_arrive(&sm.rec_empty[(J / kGroup) % kGroups]);
       }
