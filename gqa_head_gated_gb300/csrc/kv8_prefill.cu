@@ -1104,7 +1104,7 @@ Workspace workspace_of(int pairs) {
 }
 
 template <bool kF16>
-cudaError_t launch_chunk(const CUtensorMap& tmK, const ChunkArgs& a, cudaStream_t stream) {
+cudaError_t launch_chunk(const CUtensorMap& tmK, const ChunkArgs& a, bool join, cudaStream_t stream) {
   const size_t smem = sizeof(ChunkSmem<kF16>) + 1024;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_smem_once(allowed, reinterpret_cast<const void*>(kv8_chunk_kernel<kF16>), smem);
@@ -1112,6 +1112,7 @@ cudaError_t launch_chunk(const CUtensorMap& tmK, const ChunkArgs& a, cudaStream_
   e = launch_dependent(kv8_chunk_kernel<kF16>, dim3(unsigned(2 * a.pairs)), kThreadsC, smem, stream, 2, tmK, a);
   if (e != cudaSuccess) return e;
   note_launch(kF16 ? "kv8_chunk_kernel<fp16>" : "kv8_chunk_kernel<bf16>", 2 * a.pairs, kThreadsC, smem);
+  if (!join) return cudaSuccess;
   const unsigned grid = unsigned(a.pairs * (kPairRows / kJoinRows));
   e = launch_dependent(kv8_join_kernel<kF16>, dim3(grid), 256, 0, stream, 1, a);
   if (e == cudaSuccess)
@@ -1200,7 +1201,9 @@ int prefill_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool
     const long long units = (long long)a.B * Hkv * max_rb * tiles;
     a.pairs = units < most ? int(units) : most;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((f16 ? launch_chunk<true>(tmK, a, s) : launch_chunk<false>(tmK, a, s)) != cudaSuccess)
+    // a cut lies more than kSnap tiles from either end of a segment: in shorter ones there is none
+    const bool join = tiles > 2 * kSnap + 1;
+    if ((f16 ? launch_chunk<true>(tmK, a, join, s) : launch_chunk<false>(tmK, a, join, s)) != cudaSuccess)
       return GQA_ERR_CUDA;
   }
   return GQA_OK;
