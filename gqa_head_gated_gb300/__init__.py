@@ -395,8 +395,8 @@ def block_plan(kv_lens, cu_rows, block_tables, n_blocks, free_list, free_count, 
     Sequence b holds kv_lens[b] keys and gets cu_rows[b+1] - cu_rows[b] new rows; after the
     call it owns exactly the blocks that they need.  int32 CUDA tensors, updated in place:
     block_tables [B, max_blocks], n_blocks [B], free_list [num_blocks] and free_count [1] (a
-    stack).  No block is in two tables or in a table and the stack: blocks that sequences share
-    have no owner here.  Surplus blocks go back first (length 0 and no rows: a finished request), then
+    stack).  A block that it releases is in no other table: blocks that block_fork() shared are given
+    back by block_free().  Surplus blocks go back first (length 0 and no rows: a finished request), then
     growing sequences take theirs in order.  T: rows in the batch, cu_rows[B] or more.
     Returns (slots int32 [T], kv_lens_out int32 [B]): the place of each new row (block *
     block_size + row; -1 without one) for kv8_append, and the lengths with the new rows for
@@ -675,7 +675,8 @@ def kv8_prefill(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, c
     """Prompt chunks over the paged 8-bit cache: kv8_decode() for many new rows a sequence, without
     a tree.  New row i of sequence b sees the keys before the chunk and the chunk's first i + 1, which
     kv8_append() has put into the cache.  q, g: [T,Hq,256] bf16 or fp16; kv_lens int32 [B] counts the
-    new rows; cu_rows int32 [B+1].  workspace: kv8_prefill_workspace_size() bytes (about 40 MB).
+    new rows; cu_rows int32 [B+1].  workspace: kv8_prefill_workspace_size() bytes (about 40 MB).  For
+    a hundred packed rows (new rows x Hq / Hkv) a sequence and fewer kv8_decode() is faster.
     Returns out [T,Hq,256]; rows behind cu_rows[B] are left as they were in a given out."""
     sfx = _elem(q, "q")
     d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)

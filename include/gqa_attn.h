@@ -417,8 +417,9 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
 
 /*
  * The paged 8-bit KV cache: half the bytes of a 16-bit cache in blocks that are handed
- * out as sequences grow, for decode and draft verification.  A step is
- *   gqa_block_plan -> gqa_kv8_append -> gqa_kv8_decode (-> gqa_kv8_keep after a verify).
+ * out as sequences grow, for decode, draft verification and prompt chunks.  A step is
+ *   gqa_block_plan -> gqa_rope -> gqa_kv8_append -> gqa_kv8_decode (-> gqa_kv8_keep after a verify),
+ * or gqa_kv8_prefill in the place of gqa_kv8_decode where prompts or chunks of them come in.
  *
  * k_pool, v_pool: e4m3 [num_blocks, Hkv, block_size, 256]; block_size 16, 32, 64 or 128.
  * k_scale, v_scale: fp32 [num_blocks, Hkv]: a row's values are e4m3 * scale.  The writing
@@ -426,8 +427,9 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  * block_tables: int32 [B, max_blocks]: entry i of sequence b is the pool block that holds
  *   its keys i*block_size .. (i+1)*block_size - 1.  No block belongs to two sequences that
  *   one call writes: its contents are unspecified after such a call (no access is out of
- *   range).  A block that is only read may be shared by the tables that gqa_kv8_decode reads;
- *   gqa_block_plan does not count owners, so its tables share none.
+ *   range).  A block that is only read may be shared by the tables that gqa_kv8_decode and
+ *   gqa_kv8_prefill read; gqa_block_plan does not count owners: gqa_block_fork shares blocks, and
+ *   gqa_block_free gives them back.
  * The calls are launched as programmatic dependents of what is before them on the stream, and
  * keep stream order.
  * num_blocks * Hkv * block_size < 2^31 and max_blocks * block_size < 2^31
@@ -435,8 +437,9 @@ int gqa_attn_masked_f16(const void* Q, const void* K, const void* V, const void*
  *
  * gqa_block_plan: block tables and slot maps from request lengths, on the device.  After it
  * sequence b owns exactly ceil((kv_lens[b] + r_b) / block_size) blocks, r_b = cu_rows[b+1] -
- * cu_rows[b] new rows, and no other sequence or the free list has them: a block that is in two
- * tables (a shared prompt) would be released twice and handed to two sequences.  A finished
+ * cu_rows[b] new rows, and no other sequence or the free list has those that it takes or releases: a
+ * block that is in two tables (gqa_block_fork) would be released twice and handed to two sequences, so
+ * lengths that fall below a fork go to gqa_block_free first.  A finished
  * request is one with length 0 and no rows, refused drafts are given back by the next call
  * with the shorter length.
  *   n_blocks: int32 [B], blocks that b owns (block_tables[b, 0 .. n_blocks[b])); updated.
@@ -625,10 +628,11 @@ int gqa_rope_f16(const void* Q, const void* K, const int* positions, const float
  * Prompt chunks over the paged 8-bit cache: as gqa_kv8_decode without tree_mask, for many new rows
  * a sequence.  New row i of sequence b sees keys j < kv_lens[b] - r_b + i + 1, the chunk's own
  * rows among them (gqa_kv8_append comes first).  Same arguments, rows left as they were, table entries,
- * NaN and errors; cu_rows is required.  Products are 16-bit ones: a probability is off by 2^-11 of
- * itself and by 2^-34 of the row's largest (V's scales beside it), q by 2^-33 of its row's largest.
- * Runs on CTA pairs over 256 packed rows (new rows x Hq / Hkv) at a time; a batch of single tokens
- * is gqa_kv8_decode's.
+ * NaN and errors; cu_rows is required.  A probability is off by 2^-11 of itself and by 2^-25 of the
+ * row's largest beside it (V's scales in both), an element of q by 2^-19 of its row's largest.
+ * Runs on CTA pairs over 256 packed rows (new rows x Hq / Hkv) at a time and writes `out` itself but
+ * for the segments that are cut between pairs: 1.4 to 2.5 times as fast as gqa_kv8_decode from some 200
+ * packed rows a sequence on, slower below a hundred (of one token: half as fast).
  * workspace: gqa_kv8_prefill_workspace_size() bytes (for the current device, whatever the sizes; about
  * 40 MB), 16-byte aligned; calls that may overlap on the GPU need one each.
  * max_kv_len < 2^30 and Hkv * row blocks * (128-key tiles of a sequence + 3) < 2^31
