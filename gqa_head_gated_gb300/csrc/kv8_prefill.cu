@@ -989,109 +989,128 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
 
 // Puts the parts of the segments that were cut together, gates and rounds them: a warp a row.
 //   out = (sum_i w_i O_i) / (sum_i w_i) * sigmoid(g),  w_i = exp(lse_i - max lse)
-// Two round trips to memory bound it, one for what is cut where, one for weights, values and gate side by side (with
-// four rows a warp, one after the other, and the weights before the values: 25 us for 76 segments, 21 for 16).
+// One wave of CTAs that read what is cut where, and go through the rows of those segments alone (eight rows a CTA, as
+// many CTAs as all pairs may leave rows: 42 rows behind 4000 keys 47 us for 35, 1000 new ones 66 for 52; most of those CTAs
+// found nothing to do, 16 to an SM).
 constexpr int kMaxPairs = 96;
-constexpr int kJoinRows = 8;    // rows of a CTA
+constexpr int kJoinCtas = 3;    // of an SM
 constexpr int kAhead = 4;       // parts whose values are on their way together
 
 template <bool kF16>
-__global__ void __launch_bounds__(256) kv8_join_kernel(const ChunkArgs p) {
+__global__ void __launch_bounds__(256, kJoinCtas) kv8_join_kernel(const ChunkArgs p) {
   __shared__ float s_w[8][kMaxPairs];
+  __shared__ int4 s_cut[2 * kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   let_next_start();
   wait_for_last();
-  constexpr int kSplit = kPairRows / kJoinRows;
-  const int pair = int(blockIdx.x) / kSplit;
-  const int4 c0 = __ldcg(reinterpret_cast<const int4*>(p.cuts + 8 * pair));
-  const int4 c1 = __ldcg(reinterpret_cast<const int4*>(p.cuts + 8 * pair) + 1);
-  // parts: this pair's last piece and the first ones of the pairs behind it, up to the one that ends
-  int state[kMaxPairs / 32];
+  if (threadIdx.x < 2 * kMaxPairs)
+    s_cut[threadIdx.x] = int(threadIdx.x) < 2 * p.pairs
+                             ? __ldcg(reinterpret_cast<const int4*>(p.cuts) + threadIdx.x) : make_int4(0, 0, 0, 0);
+  __syncthreads();
+  // parts: a pair's last piece and the first ones of the pairs behind it, up to the one that ends
+  uint32_t starts[kMaxPairs / 32], off[kMaxPairs / 32], ends[kMaxPairs / 32];
 #pragma unroll
   for (int k = 0; k < kMaxPairs / 32; ++k) {
-    const int at = pair + 1 + 32 * k + lane;
-    state[k] = at < p.pairs ? __ldcg(p.cuts + 8 * at) : 0;
+    const int4 c = s_cut[2 * (32 * k + lane)];
+    starts[k] = __ballot_sync(0xffffffffu, c.y != 0);
+    off[k] = __ballot_sync(0xffffffffu, c.x != 1);
+    ends[k] = __ballot_sync(0xffffffffu, c.x == 2);
   }
-  const int g = c0.z, rb = c0.w, rows = c1.x, t0 = c1.y;
-  const int p0 = rb * kPairRows, n_rows = min(kPairRows, rows * p.gqa - p0);
-  const int r = (int(blockIdx.x) % kSplit) * kJoinRows + warp;
-  if (c0.y == 0 || r >= n_rows) return;
-  int cnt = 1;
-  bool on = true;
+#pragma unroll 1
+  for (int R = int(blockIdx.x) * 8 + warp;; R += int(gridDim.x) * 8) {
+    int left = R / kPairRows, pair = -1;
+    const int r = R % kPairRows;
 #pragma unroll
-  for (int k = 0; k < kMaxPairs / 32; ++k) {
-    const uint32_t off = __ballot_sync(0xffffffffu, state[k] != 1);
-    const int w = off != 0u ? __ffs(off) - 1 : 32;
-    if (on) cnt += w + (w < 32 && __shfl_sync(0xffffffffu, state[k], w & 31) == 2 ? 1 : 0);
-    on = on && w == 32;
-  }
-  cnt = min(cnt, kMaxPairs);
-  const auto slot = [&](int i) { return size_t(i == 0 ? 2 * pair + 1 : 2 * (pair + i)) * kPairRows + r; };
-  float4 v[kAhead][2];
-  const auto load = [&](int i0) {
+    for (int k = 0; k < kMaxPairs / 32; ++k) {
+      const uint32_t hit = __ballot_sync(0xffffffffu, ((starts[k] >> lane) & 1u) != 0u &&
+                                                          __popc(starts[k] & ((1u << lane) - 1u)) == left);
+      if (hit != 0u) pair = 32 * k + __ffs(hit) - 1;
+      left -= __popc(starts[k]);
+    }
+    if (pair < 0) return;
+    const int4 c0 = s_cut[2 * pair], c1 = s_cut[2 * pair + 1];
+    const int g = c0.z, rb = c0.w, rows = c1.x, t0 = c1.y;
+    const int p0 = rb * kPairRows, n_rows = min(kPairRows, rows * p.gqa - p0);
+    if (r >= n_rows) continue;
+    int stop = kMaxPairs, last = 0;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (i0 + k < cnt) {
-        const float4* const o = reinterpret_cast<const float4*>(p.o_parts + slot(i0 + k) * 256) + lane * 2;
-        v[k][0] = __ldcg(o);
-        v[k][1] = __ldcg(o + 1);
+    for (int k = kMaxPairs / 32 - 1; k >= 0; --k) {
+      const int from = pair + 1 - 32 * k;
+      const uint32_t m = from >= 32 ? 0u : off[k] & (0xffffffffu << max(from, 0));
+      if (m != 0u) {
+        stop = 32 * k + __ffs(m) - 1;
+        last = int((ends[k] >> (__ffs(m) - 1)) & 1u);
       }
-  };
-  load(0);
-  const int pk = p0 + r, i = pk / p.gqa;
-  const size_t at = size_t(t0 + i) * p.Hq + g * p.gqa + (pk - i * p.gqa);
-  uint4 gate = make_uint4(0u, 0u, 0u, 0u);
-  if (p.gate != nullptr) gate = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256) + lane);
-  float ls[kMaxPairs / 32], M = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kMaxPairs / 32; ++k) {
-    ls[k] = 32 * k + lane < cnt ? __ldcg(p.lse_parts + slot(32 * k + lane)) : -INFINITY;
-    M = fmaxf(M, ls[k]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float msub = M == -INFINITY ? 0.f : M;
-  float sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < kMaxPairs / 32; ++k) {
-    const float w = ls[k] == -INFINITY ? 0.f : __expf(ls[k] - msub);
-    s_w[warp][32 * k + lane] = ls[k] == -INFINITY ? -1.f : w;   // -1: the part saw no key
-    sum += w;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  __syncwarp();
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < cnt; i0 += kAhead) {
-    if (i0 > 0) load(i0);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const float w = i0 + k < cnt ? s_w[warp][i0 + k] : -1.f;
-      if (w < 0.f) continue;   // (a weight of 0 counts: its part may hold a NaN that the row sees)
-      acc[0] += w * v[k][0].x;
-      acc[1] += w * v[k][0].y;
-      acc[2] += w * v[k][0].z;
-      acc[3] += w * v[k][0].w;
-      acc[4] += w * v[k][1].x;
-      acc[5] += w * v[k][1].y;
-      acc[6] += w * v[k][1].z;
-      acc[7] += w * v[k][1].w;
     }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const uint32_t gw[4] = {gate.x, gate.y, gate.z, gate.w};
-  uint32_t w[4];
+    const int cnt = stop - pair + last;
+    const auto slot = [&](int i) { return size_t(i == 0 ? 2 * pair + 1 : 2 * (pair + i)) * kPairRows + r; };
+    float4 v[kAhead][2];
+    const auto load = [&](int i0) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float2 y = make_float2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    if (p.gate != nullptr) {
-      const float2 a = unpack_elem2<kF16>(gw[k]);
-      y = make_float2(y.x * gate_sigmoid(a.x), y.y * gate_sigmoid(a.y));
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k < cnt) {
+          const float4* const o = reinterpret_cast<const float4*>(p.o_parts + slot(i0 + k) * 256) + lane * 2;
+          v[k][0] = __ldcg(o);
+          v[k][1] = __ldcg(o + 1);
+        }
+    };
+    load(0);
+    const int pk = p0 + r, i = pk / p.gqa;
+    const size_t at = size_t(t0 + i) * p.Hq + g * p.gqa + (pk - i * p.gqa);
+    uint4 gate = make_uint4(0u, 0u, 0u, 0u);
+    if (p.gate != nullptr) gate = __ldg(reinterpret_cast<const uint4*>(p.gate + at * 256) + lane);
+    float ls[kMaxPairs / 32], M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMaxPairs / 32; ++k) {
+      ls[k] = 32 * k + lane < cnt ? __ldcg(p.lse_parts + slot(32 * k + lane)) : -INFINITY;
+      M = fmaxf(M, ls[k]);
     }
-    w[k] = pack_elem2<kF16>(y.x, y.y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float msub = M == -INFINITY ? 0.f : M;
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxPairs / 32; ++k) {
+      const float w = ls[k] == -INFINITY ? 0.f : __expf(ls[k] - msub);
+      s_w[warp][32 * k + lane] = ls[k] == -INFINITY ? -1.f : w;   // -1: the part saw no key
+      sum += w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < cnt; i0 += kAhead) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float w = i0 + k < cnt ? s_w[warp][i0 + k] : -1.f;
+        if (w < 0.f) continue;   // (a weight of 0 counts: its part may hold a NaN that the row sees)
+        acc[0] += w * v[k][0].x;
+        acc[1] += w * v[k][0].y;
+        acc[2] += w * v[k][0].z;
+        acc[3] += w * v[k][0].w;
+        acc[4] += w * v[k][1].x;
+        acc[5] += w * v[k][1].y;
+        acc[6] += w * v[k][1].z;
+        acc[7] += w * v[k][1].w;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const uint32_t gw[4] = {gate.x, gate.y, gate.z, gate.w};
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 y = make_float2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+      if (p.gate != nullptr) {
+        const float2 a = unpack_elem2<kF16>(gw[k]);
+        y = make_float2(y.x * gate_sigmoid(a.x), y.y * gate_sigmoid(a.y));
+      }
+      w[k] = pack_elem2<kF16>(y.x, y.y);
+    }
+    reinterpret_cast<uint4*>(p.out + at * 256)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (p.lse != nullptr && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : msub + __logf(sum);
+    __syncwarp();   // before the next row's weights
   }
-  reinterpret_cast<uint4*>(p.out + at * 256)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-  if (p.lse != nullptr && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : msub + __logf(sum);
 }
 
 int pair_count() {
@@ -1121,7 +1140,7 @@ cudaError_t launch_chunk(const CUtensorMap& tmK, const ChunkArgs& a, bool join, 
   if (e != cudaSuccess) return e;
   note_launch(kF16 ? "kv8_chunk_kernel<fp16>" : "kv8_chunk_kernel<bf16>", 2 * a.pairs, kThreadsC, smem);
   if (!join) return cudaSuccess;
-  const unsigned grid = unsigned(a.pairs * (kPairRows / kJoinRows));
+  const unsigned grid = unsigned(device_sm_count() * kJoinCtas);
   e = launch_dependent(kv8_join_kernel<kF16>, dim3(grid), 256, 0, stream, 1, a);
   if (e == cudaSuccess)
     note_launch(kF16 ? "kv8_join_kernel<fp16>" : "kv8_join_kernel<bf16>", grid, 256, 0);
