@@ -52,6 +52,11 @@ constexpr int kHitWords = kPairRows / 32;       // keys that only some rows of a
 // end).  8192 rows with 3, 6, 8, 10, 13 and 16: 826, 757, 696, 703, 718, 749 us.
 constexpr uint32_t kLead = 8;
 constexpr int kSnap = 2;                        // a cut this close to a segment's end is made there
+// No segment is cut where there is a pair for each and the longest is at most this many tiles above an equal share:
+// parts and their joining cost as much (24/4 heads, cut always, kept whole up to 6, 10 and 20 tiles above: 16 sequences
+// of 40 rows behind 2000 keys 61, 52, 52, 49 us; 4 of 64 behind 1000 40, 36, 34, 34; 512 rows behind 2000 57, 58, 52, 50,
+// behind 4000 72, 74, 74, 76; 64 behind 1000 30, 30, 33, 34).
+constexpr uint32_t kWhole = 10;
 constexpr float kCap = 15.f, kTop = 0.f;        // p <= 2^15; a moved reference leaves 1
 constexpr uint32_t kTmOc = 0, kTmSc = 256;
 constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);   // e4m3 (format 0)
@@ -114,6 +119,7 @@ struct __align__(1024) ChunkSmem {
   uint64_t hit_full[kHitSets];
   int4 seq[kKv8Seqs];                     // first token, rows, keys, row blocks
   uint32_t cost[kKv8Seqs], at[kKv8Seqs + 1];   // of one KV head; of all, before each sequence
+  uint32_t segments, longest, whole;      // of the launch; tiles; none is cut, and each costs 1
   uint32_t tmem_base;
   int abort, zero;
 };
@@ -155,7 +161,9 @@ __device__ Cut cut_at(const Sm& sm, const ChunkArgs& p, uint32_t pos) {
   rest -= uint32_t(c.g) * sm.cost[lo];
   int n = 0;
   for (int rb0 = 0;; rb0 += 32) {   // (the last row block's sum is the cost, which rest is below)
-    const uint32_t own = rb0 + lane < s.w ? uint32_t(tiles_of(s, rb0 + lane, p.gqa)) + kLead : 0u;
+    const uint32_t own = rb0 + lane >= s.w ? 0u
+                         : sm.whole != 0u  ? 1u
+                                           : uint32_t(tiles_of(s, rb0 + lane, p.gqa)) + kLead;
     uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -277,6 +285,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     sm.abort = 0;
     sm.zero = 0;
     sm.at[0] = 0;
+    sm.segments = sm.longest = sm.whole = 0u;
     ptx::fence_mbar_init();
   }
   if (tid < kHitSets * kHitWords) (&sm.hit[0][0])[tid] = 0u;
@@ -301,20 +310,36 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
     uint32_t sum = 0;
     for (int rb = lane; rb < s.w; rb += 32) sum += uint32_t(tiles_of(s, rb, p.gqa)) + kLead;
     sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) sm.cost[b] = sum;
+    if (lane == 0) {
+      sm.cost[b] = sum;
+      if (s.w > 0) {
+        atomicAdd(&sm.segments, uint32_t(s.w) * uint32_t(p.Hkv));
+        atomicMax(&sm.longest, uint32_t(tiles_of(s, s.w - 1, p.gqa)));
+      }
+    }
   }
   __syncthreads();
-  if (warp == 0) {   // inclusive sums over the sequences, 32 at a time
-    uint32_t run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      uint32_t v = b0 + lane < p.B ? sm.cost[b0 + lane] * uint32_t(p.Hkv) : 0u;
+  if (warp == 0) {   // inclusive sums over the sequences, 32 at a time; once more where no segment is cut
+#pragma unroll 1
+    for (;;) {
+      uint32_t run = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        uint32_t v = b0 + lane < p.B ? sm.cost[b0 + lane] * uint32_t(p.Hkv) : 0u;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += u;
+        }
+        if (b0 + lane < p.B) sm.at[b0 + lane + 1] = run + v;
+        run += __shfl_sync(0xffffffffu, v, 31);
       }
-      if (b0 + lane < p.B) sm.at[b0 + lane + 1] = run + v;
-      run += __shfl_sync(0xffffffffu, v, 31);
+      const uint32_t pairs = uint32_t(p.pairs);
+      if (sm.whole != 0u || sm.segments > pairs || sm.longest > (run - sm.segments * kLead) / pairs + kWhole)
+        break;
+      for (int b = lane; b < p.B; b += 32) sm.cost[b] = uint32_t(sm.seq[b].w);
+      __syncwarp();
+      if (lane == 0) sm.whole = 1u;
+      __syncwarp();
     }
   }
   ptx::tc_fence_before();
@@ -1230,8 +1255,9 @@ int prefill_impl(bool f16, const void* Q, const void* k_pool, const void* v_pool
     const long long units = (long long)a.B * Hkv * max_rb * tiles;
     a.pairs = units < most ? int(units) : most;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // a cut lies more than kSnap tiles from either end of a segment: in shorter ones there is none
-    const bool join = tiles > 2 * kSnap + 1;
+    // a cut lies more than kSnap tiles from either end of a segment: in shorter ones there is none; and none in
+    // any where the kernel leaves them whole
+    const bool join = tiles > 2 * kSnap + 1 && (tiles > int(kWhole) || (long long)a.B * Hkv * max_rb > a.pairs);
     if ((f16 ? launch_chunk<true>(tmK, a, join, s) : launch_chunk<false>(tmK, a, join, s)) != cudaSuccess)
       return GQA_ERR_CUDA;
   }

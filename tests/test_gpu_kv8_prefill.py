@@ -405,3 +405,22 @@ def test_a_prompt_in_chunks_is_the_whole_prompt():
     check()
     step([20, 1, 33, 0])
     step([1, 1, 1, 1])
+
+
+@pytest.mark.parametrize("Hkv,rows,lens,max_kv_len", [
+    (2, [20] * 6, [1280] * 6, None),                       # ten tiles
+    (2, [20] * 6, [1281] * 6, None),                       # one more
+    (2, [20] * 6, [1409, 1537, 1665, 20, 100, 1300], None),
+    (2, [45, 0, 30, 1, 200], [1290, 70, 500, 1, 1500], None),
+    (1, [30] * 30, [700] * 30, 5000),                      # a bound far above the lengths
+    (1, [64] + [1] * 9, [1700] + [40] * 9, None),
+    (4, [9] * 19, [900 + 7 * i for i in range(19)], None),   # 76 segments
+    (7, [9] * 11, [800 + 7 * i for i in range(11)], None),   # 77
+    (1, [40, 40], [9000, 2600], None),
+])
+def test_short_segments_whole_and_cut(Hkv, rows, lens, max_kv_len):
+    """Segments on either side of where they are shared between pairs, after a call that cut all."""
+    ws = torch.empty(G.kv8_prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    _check(Cache([20000], 1, 128, seed=181), [30], 8, 182, workspace=ws)
+    c = Cache(lens, Hkv, 64, seed=183, room=max(0, (max_kv_len or 0) - min(lens)))
+    _check(c, rows, 6 * Hkv, 184, max_kv_len=max_kv_len, workspace=ws)
