@@ -675,8 +675,8 @@ def kv8_prefill(q, k_pool, v_pool, k_scale, v_scale, g, block_tables, kv_lens, c
     """Prompt chunks over the paged 8-bit cache: kv8_decode() for many new rows a sequence, without
     a tree.  New row i of sequence b sees the keys before the chunk and the chunk's first i + 1, which
     kv8_append() has put into the cache.  q, g: [T,Hq,256] bf16 or fp16; kv_lens int32 [B] counts the
-    new rows; cu_rows int32 [B+1].  workspace: kv8_prefill_workspace_size() bytes (about 40 MB).  For
-    a hundred packed rows (new rows x Hq / Hkv) a sequence and fewer kv8_decode() is faster.
+    new rows; cu_rows int32 [B+1].  workspace: kv8_prefill_workspace_size() bytes (about 40 MB).  Up
+    to a hundred packed rows (new rows x Hq / Hkv) a sequence kv8_decode() is faster, from some 500 on this.
     Returns out [T,Hq,256]; rows behind cu_rows[B] are left as they were in a given out."""
     sfx = _elem(q, "q")
     d, N, Hkv, bs, *pools = _kv8_pools(k_pool, v_pool, k_scale, v_scale)

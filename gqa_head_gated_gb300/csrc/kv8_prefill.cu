@@ -15,7 +15,18 @@
 // reference of its own, without the V scales.
 //
 // What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (three 8-bit terms of p, as the kernels for
-// few rows have them, would take 2560 in all; fp16 takes 2560), beside 1024 clocks of ex2.
+// few rows have them, would take 2560 in all; fp16 takes 2560), beside 1024 clocks of ex2.  Measured, bf16: 2048 rows behind
+// 30720 keys 632 us (1,680 TFLOP/s of 1,919; 603 repeated on two inputs), a prompt of 8192 rows 592 us (1,390: 768
+// segments' starts and ends show); fp16 costs its third term.
+//
+// Tried without gain: scores kept in registers instead of a second read (732 us for 715), two teams of softmax warps
+// that take turns (727 for 721), a third K slot, L2 prefetch of the tiles ahead, four rows' outputs stored together
+// (721 for 703), fp16 with K converted instead of a third term (740 for 805 behind 30720 keys, but 1740 for 1675 on chunks
+// that are not in L2).
+//
+// The hot loops are small on purpose, but for the issuing warp's: five roles share an SM's instruction caches (the
+// softmax unrolled over all of a row's keys: 1077 us), while operands made in a loop make a product's issue longer than its
+// 64 clocks (856 us for 718).
 //
 // The segments' tiles (only those that some row sees) are laid end to end and cut into equal shares,
 // one a pair.  A piece that is a whole segment goes straight to `out`; the pieces of a segment that is
@@ -49,13 +60,13 @@ constexpr int kPieces = 32;                     // more than tiles held, and eve
 constexpr int kHitSets = 4;                     // pieces whose NaN keys are held
 constexpr int kHitWords = kPairRows / 32;       // keys that only some rows of a segment see: < 256
 // What a segment costs beside its tiles, in tiles (Q's terms, the first tiles, whose references still move, the
-// end).  8192 rows with 3, 6, 8, 10, 13 and 16: 826, 757, 696, 703, 718, 749 us.
+// end).  8192 rows with 4, 6, 7, 8, 10 and 12: 711, 649, 607, 582, 597, 597 us.
 constexpr uint32_t kLead = 8;
 constexpr int kSnap = 2;                        // a cut this close to a segment's end is made there
 // No segment is cut where there is a pair for each and the longest is at most this many tiles above an equal share:
-// parts and their joining cost as much (24/4 heads, cut always, kept whole up to 6, 10 and 20 tiles above: 16 sequences
-// of 40 rows behind 2000 keys 61, 52, 52, 49 us; 4 of 64 behind 1000 40, 36, 34, 34; 512 rows behind 2000 57, 58, 52, 50,
-// behind 4000 72, 74, 74, 76; 64 behind 1000 30, 30, 33, 34).
+// parts and their joining cost as much (24/4 heads, with 0, 6, 10 and 14: 16 sequences of 40 rows behind 2000 keys 60, 50,
+// 50, 50 us; of 42 behind 4000 84, 75, 75, 78; 4 of 64 behind 1000 39, 35, 33, 33; 512 rows behind 2000 55, 55, 50, 49;
+// 64 behind 1000 29, 29, 32, 32).
 constexpr uint32_t kWhole = 10;
 constexpr float kCap = 15.f, kTop = 0.f;        // p <= 2^15; a moved reference leaves 1
 constexpr uint32_t kTmOc = 0, kTmSc = 256;

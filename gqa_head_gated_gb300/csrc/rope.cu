@@ -12,7 +12,8 @@
 // lane a pair.
 //
 // Bound by memory: a warp takes items of 8 heads of a token, 512 bytes (16 a lane) each, the next item's loads under way
-// while it turns one.
+// while it turns one.  8192 tokens of 24 + 4 heads, 64 dims turned: 42 us (83 % of the copy rate); 32749 of 16 + 2, whole
+// heads: 100 us (89 %).  With a CTA a token they took 56 and 172.
 #include <cuda_runtime.h>
 
 #include "kv8_common.cuh"

@@ -631,11 +631,12 @@ int gqa_rope_f16(const void* Q, const void* K, const int* positions, const float
  * NaN and errors; cu_rows is required.  A probability is off by 2^-11 of itself and by 2^-25 of the
  * row's largest beside it (V's scales in both), an element of q by 2^-19 of its row's largest.
  * Runs on CTA pairs over 256 packed rows (new rows x Hq / Hkv) at a time and writes `out` itself but
- * for the segments that are cut between pairs: 1.4 to 2.5 times as fast as gqa_kv8_decode from some 200
- * packed rows a sequence on, slower below a hundred (of one token: half as fast).
+ * for the segments that are cut between pairs.  Against gqa_kv8_decode, measured: from some 500 packed
+ * rows a sequence on 1.1 to 2.7 times as fast (a single sequence of about a thousand keys: 0.8 times);
+ * between 190 and 400 0.8 to 1.5 times; at a hundred and fewer 0.5 to 0.8 times.
  * workspace: gqa_kv8_prefill_workspace_size() bytes (for the current device, whatever the sizes; about
  * 40 MB), 16-byte aligned; calls that may overlap on the GPU need one each.
- * max_kv_len < 2^30 and Hkv * row blocks * (128-key tiles of a sequence + 3) < 2^31
+ * max_kv_len < 2^30 and Hkv * row blocks * (128-key tiles of a sequence + 8) < 2^31
  * (GQA_ERR_UNSUPPORTED above).
  */
 size_t gqa_kv8_prefill_workspace_size(void);
