@@ -424,3 +424,61 @@ def test_short_segments_whole_and_cut(Hkv, rows, lens, max_kv_len):
     _check(Cache([20000], 1, 128, seed=181), [30], 8, 182, workspace=ws)
     c = Cache(lens, Hkv, 64, seed=183, room=max(0, (max_kv_len or 0) - min(lens)))
     _check(c, rows, 6 * Hkv, 184, max_kv_len=max_kv_len, workspace=ws)
+
+
+def test_captured_steps_on_a_growing_cache_and_a_shared_workspace():
+    """A captured step (plan, rope, append, attention of its rows) grows the cache at each replay as eager calls do; a
+    second graph with the same workspace, whose segments are cut where the first's are whole, runs in between."""
+    B, Hq, Hkv, bs, N, width = 2, 8, 2, 64, 40, 20
+    gen = torch.Generator().manual_seed(190)
+    rows = [70, 45]
+    T, cu = sum(rows), i32(cu_of(rows))
+    x = torch.randn(T, Hq + 2 * Hkv, 256, generator=gen).to(DEV, torch.bfloat16)
+    g = torch.randn(T, Hq, 256, generator=gen).to(DEV, torch.bfloat16)
+    v = x[:, Hq + Hkv:].contiguous()
+    freq, scale = G.rope_frequencies(64)
+    ws = torch.empty(G.kv8_prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+
+    def fresh():
+        return dict(lens=i32([0] * B), tables=i32([[-1] * width] * B), n=i32([0] * B), free=i32(list(range(N))),
+                    fc=i32([N]), pos=torch.cat([torch.arange(r) for r in rows]).to(DEV, torch.int32),
+                    pools=[torch.zeros(N, Hkv, bs, 256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+                           for _ in "kv"], scales=[torch.ones(N, Hkv, device=DEV) for _ in "kv"],
+                    slots=i32([0] * T), new=i32([0] * B), out=torch.zeros(T, Hq, 256, dtype=torch.bfloat16, device=DEV))
+
+    by_seq = i32([b for b in range(B) for _ in range(rows[b])])
+    grow = i32(rows)[by_seq.long()]
+
+    def step(s):
+        G.block_plan(s["lens"], cu, s["tables"], s["n"], s["free"], s["fc"], bs, T, slots=s["slots"],
+                     kv_lens_out=s["new"])
+        q, k = G.rope(x[:, :Hq], x[:, Hq:Hq + Hkv], s["pos"], freq, scale=scale)
+        G.kv8_append(k, v, s["slots"], *s["pools"], *s["scales"])
+        G.kv8_prefill(q, *s["pools"], *s["scales"], g, s["tables"], s["new"], cu, max_rows=max(rows),
+                      max_kv_len=width * bs, workspace=ws, out=s["out"])
+        s["lens"].copy_(s["new"])
+        s["pos"].add_(grow)
+
+    c = Cache([9000, 300], 2, 32, seed=191)
+    q2, g2 = (t.to(DEV) for t in rows_qg(360, 8, 192))
+    dev, tab, lens2, cu2 = c.device()[:4], i32(c.tables), i32(c.lens), i32(cu_of([60, 300]))
+    other = lambda out: G.kv8_prefill(q2, *dev, g2, tab, lens2, cu2, max_rows=300, max_kv_len=9000,  # noqa: E731
+                                      workspace=ws, out=out)
+    want2 = other(torch.zeros_like(q2)).clone()
+    a, b, out2 = fresh(), fresh(), torch.zeros_like(q2)
+    step(fresh())                                          # (everything is loaded before the captures)
+    torch.cuda.synchronize()
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        step(a)
+    with torch.cuda.graph(second):
+        other(out2)
+    for _ in range(5):
+        out2.zero_()
+        first.replay()
+        second.replay()
+        step(b)
+        torch.cuda.synchronize()
+        assert torch.equal(a["out"], b["out"]) and torch.equal(out2, want2)
+        assert a["lens"].tolist() == b["lens"].tolist() and torch.equal(a["tables"], b["tables"])
+    assert G.last_device_status() == 0 and a["lens"].tolist() == [350, 225]
