@@ -123,8 +123,9 @@ struct __align__(1024) ChunkSmem {
   float fac[2][128];                      // by piece parity
   uint32_t hit[kHitSets][kHitWords];
   uint64_t rec_full[kGroups], rec_empty[kGroups];
-  // By tile parity (a slot's barrier cannot come round again before its user has waited): K has landed; S is done, and
-  // its K slot free; V and P are there; PV is done, its V slot free.
+  // By tile parity: K has landed; S is done, and its K slot free; V and P are there; PV is done, its V slot free.  None
+  // can come round again before all of its users have waited: each of them arrives on what leads to the next phase, the
+  // odd CTA's copying warp too where it has no key of a tile to bring.
   uint64_t k_full[2], s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_free, drain;
   uint64_t hit_full[kHitSets];
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
       ptx::mbar_init(&sm.rec_empty[i], 13);   // K's copies, 4 converting warps, 8 of softmax
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.k_full[i], 1);
+      ptx::mbar_init(&sm.k_full[i], 2);       // both CTAs' copying warps
       ptx::mbar_init(&sm.s_full[i], 1);
       ptx::mbar_init(&sm.p_full[i], 16 + 8);   // softmax and converting warps of both CTAs
       ptx::mbar_init(&sm.pv_done[i], 1);
@@ -584,6 +585,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (J >= kKs) ok = warp_all(hold(&sm.s_full[ks], ((J >> 1) - 1u) & 1u, tmo, &sm.abort));
         if (!ok) break;
         const int left = r.k_hi - r.key0;
+        if (!lead && lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(ptx::smem_addr(&sm.k_full[ks]), 0));
         if (lead && lane == 0) {
           const int n0 = (min(max(left, 0), 64) + (1 << box_log2) - 1) >> box_log2;
           const int n1 = (min(max(left - 64, 0), 64) + (1 << box_log2) - 1) >> box_log2;
