@@ -10,9 +10,13 @@
 // an fp16's 11; what a row's elements lose is below 2^-19 of its largest), K's scale goes in after, per
 // run of 16 keys.  P.V is a 16-bit product: an e4m3 number is an fp16 number, so V enters as it is stored and its
 // scale goes into the exponent of the probability, p = 2^(score + log2 vs - ref).  p goes as fp16: off by
-// 2^-11 of itself, and by 2^-25 where the row's largest is 1 at least (a reference moves when p would pass
-// 2^15, and then leaves the largest at 1).  The row's sum l is taken from the fp32 probabilities against a
-// reference of its own, without the V scales.
+// 2^-11 of itself, and by 2^-25 at least.  A reference moves when p would pass 2^15, and then leaves the largest at
+// 2^top, which the row's largest does not fall below.  In a piece of 64 tiles or fewer top is 0: its 8192 keys lose
+// 2^-12 of that one's weight at most, together.  In a longer one it is 8, so that very many keys far below one keep
+// theirs: 131071 keys 18 nats below come out within 2^-7 (with 0 they were lost, and 1.76 times themselves at 17.2).
+// It costs moves of O: 2048 rows at 30720 keys 646 us for 637 (with 10 for 8: 650), ragged fp16 chunks 1640 for 1613; in
+// every piece it would cost 8192 rows 606 for 592, and 4 x 37 behind 65000 111 for 108.  The row's sum l is taken from the
+// fp32 probabilities against a reference of its own, without the V scales.
 //
 // What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (three 8-bit terms of p, as the kernels for
 // few rows have them, would take 2560 in all; fp16 takes 2560), beside 1024 clocks of ex2.  Measured, bf16: 2048 rows behind
@@ -68,7 +72,8 @@ constexpr int kSnap = 2;                        // a cut this close to a segment
 // 50, 50 us; of 42 behind 4000 84, 75, 75, 78; 4 of 64 behind 1000 39, 35, 33, 33; 512 rows behind 2000 55, 55, 50, 49;
 // 64 behind 1000 29, 29, 32, 32).
 constexpr uint32_t kWhole = 10;
-constexpr float kCap = 15.f, kTop = 0.f;        // p <= 2^15; a moved reference leaves 1
+constexpr float kCap = 15.f;                    // p <= 2^15
+constexpr float kLongTop = 8.f;                 // what a moved reference leaves in a piece of more than kLongPiece tiles
 constexpr uint32_t kTmOc = 0, kTmSc = 256;
 constexpr uint32_t kIdescSc = ptx::idesc_f32acc(256, 128, 0, 0, 0);   // e4m3 (format 0)
 constexpr uint32_t kIdescOc = ptx::idesc_f32acc(256, 256, 0, 1, 0);   // fp16 (format 0)
@@ -788,6 +793,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         if (pk < x.rows * p.gqa) lim = x.base + pk / p.gqa + 1;
       }
       const float fac = sm.fac[pc & 1u][row];
+      const float top = n_tiles > kLongPiece ? kLongTop : 0.f;
       float ref = kNone, ml = kNone, l = 0.f;
       for (int j = 0; j < n_tiles; ++j, ++J) {
         const uint32_t buf = J & 1u;
@@ -858,7 +864,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
         // of the warp's others go along.
         const float at = ref;
         const bool moved = __any_sync(0xffffffffu, mp > at + kCap);
-        if (moved) ref = fmaxf(at, mp - kTop);
+        if (moved) ref = fmaxf(at, mp - top);
         if (ms > ml + kLSlack) {
           l *= ex2(ml - ms);
           ml = ms;

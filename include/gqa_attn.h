@@ -628,8 +628,10 @@ int gqa_rope_f16(const void* Q, const void* K, const int* positions, const float
  * Prompt chunks over the paged 8-bit cache: as gqa_kv8_decode without tree_mask, for many new rows
  * a sequence.  New row i of sequence b sees keys j < kv_lens[b] - r_b + i + 1, the chunk's own
  * rows among them (gqa_kv8_append comes first).  Same arguments, rows left as they were, table entries,
- * NaN and errors; cu_rows is required.  A probability is off by 2^-11 of itself and by 2^-25 of the
- * row's largest beside it (V's scales in both), an element of q by 2^-19 of its row's largest.
+ * NaN and errors; cu_rows is required.  A probability is off by 2^-11 of itself and by 2^-33 of the
+ * row's largest beside it (V's scales in both), an element of q by 2^-19 of its row's largest.  Where a
+ * CTA pair has 8192 keys of a row or fewer at a time it is 2^-25, which for all of them is 2^-12 of the
+ * largest: very many keys far below one keep their weight together, as in gqa_kv8_decode.
  * Runs on CTA pairs over 256 packed rows (new rows x Hq / Hkv) at a time and writes `out` itself but
  * for the segments that are cut between pairs.  Against gqa_kv8_decode, measured: from some 500 packed
  * rows a sequence on 1.1 to 2.7 times as fast (a single sequence of about a thousand keys: 0.8 times);
