@@ -137,13 +137,19 @@ __global__ void __launch_bounds__(kThreads, 1) block_fork_kernel(const PagesPara
     if (served(f)) {
       const int len = s_len[f], full = len >> p.bs_log2, d = p.dst[f];
       rows = len & (bs - 1);
+      p.n_blocks[d] = full + (rows != 0);
+      p.kv_lens[d] = len;
       if (rows != 0) {
         from = p.tables[(long long)p.src[f] * p.max_blocks + full];
         to = p.free_list[fc - 1 - s_tail[f]];
+        if (to < 0 || to >= p.num_blocks) to = -1;
         p.tables[(long long)d * p.max_blocks + full] = to;
+        if (to < 0 || from < 0 || from >= p.num_blocks) {   // nothing to copy, or nowhere
+          from = to = -1;
+          rows = 0;
+          record_status(p.ctl.status, GQA_ERR_DEVICE_RANGE);
+        }
       }
-      p.n_blocks[d] = full + (rows != 0);
-      p.kv_lens[d] = len;
     } else if (s_len[f] >= 0) {
       record_status(p.ctl.status, GQA_ERR_NO_BLOCKS);
     }

@@ -560,7 +560,9 @@ int gqa_kv8_decode_f16(const void* Q, const void* k_pool, const void* v_pool,
  * A child holds no blocks before the call, and the call forks neither from it nor to it twice; a fork
  * that breaks this, or whose prefix is longer than what the parent holds, is refused
  * (GQA_ERR_DEVICE_RANGE recorded), one that the stack has no block for takes none
- * (GQA_ERR_NO_BLOCKS).
+ * (GQA_ERR_NO_BLOCKS).  An entry of the parent's table that is no block of the pool goes into the child's
+ * as it is, one of the stack as -1; rows that cannot be copied for it are not listed, and
+ * GQA_ERR_DEVICE_RANGE is recorded.
  */
 int gqa_block_fork(const int* src, const int* dst, const int* lens, int* kv_lens, int* block_tables,
                    int* n_blocks, int* free_list, int* free_count, int* shares, int* copies, int F,
