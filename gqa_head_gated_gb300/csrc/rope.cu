@@ -182,13 +182,13 @@ int rope_impl(bool f16, const void* Q, const void* K, const int* positions, cons
   if (!aligned_to(positions, 4) || !aligned_to(inv_freq, 4)) return GQA_ERR_INVALID_ARG;
   RopeParams p{};
   const int n = Hkv > 0 ? 4 : 2;   // rows of strides: Q, q_out, K, k_out
-  for (int k = 0; k < 3 * n; ++k)
-    if (strides[k] % 8 != 0 || strides[k] < 0) return GQA_ERR_INVALID_ARG;
+  const int sizes[2][3] = {{B, L, Hq}, {B, L, Hkv}};
+  for (int k = 0; k < 3 * n; ++k)   // (the stride of a dim of one is nobody's)
+    if (sizes[k / 6][k % 3] > 1 && (strides[k] % 8 != 0 || strides[k] < 0)) return GQA_ERR_INVALID_ARG;
   p.x[0] = static_cast<const uint4*>(Q);
   p.x[1] = static_cast<const uint4*>(K);
   p.y[0] = static_cast<uint4*>(q_out);
   p.y[1] = static_cast<uint4*>(k_out);
-  const int sizes[2][3] = {{B, L, Hq}, {B, L, Hkv}};
   for (int w = 0; w < n / 2; ++w) {
     bool same = true;
     for (int k = 0; k < 3; ++k) {
