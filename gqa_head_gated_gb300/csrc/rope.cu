@@ -166,6 +166,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_kernel(const RopeParams p
   }
 }
 
+// Whether two of the rows (512 bytes each) that na x nb steps of sa and sb reach share bytes; steps of a row or more,
+// in 16 bytes.  Nested dims end at the first test; else the multiples of the longer step are compared with the
+// nearest of the shorter, over one period of what is left.
+bool rows_meet(long long sa, int na, long long sb, int nb) {
+  if (sa > sb) return rows_meet(sb, nb, sa, na);
+  constexpr int kRow = kHeadDim / 8;
+  const __int128 reach = __int128(na - 1) * sa + kRow;   // of the shorter one
+  for (int j = 1; j < nb && j <= sa && __int128(j) * sb < reach; ++j) {
+    const __int128 at = __int128(j) * sb, i = at / sa, rest = at - i * sa;
+    if (rest < kRow || (sa - rest < kRow && i + 1 < na)) return true;
+  }
+  return false;
+}
+
 int rope_impl(bool f16, const void* Q, const void* K, const int* positions, const float* inv_freq, void* q_out,
               void* k_out, const long long* strides, int B, int L, int Hq, int Hkv, int rot_dims, int pos_batch,
               int interleaved, int inverse, float scale, gqa_stream_t stream) {
@@ -211,6 +225,12 @@ int rope_impl(bool f16, const void* Q, const void* K, const int* positions, cons
   p.groups = p.q_groups + (Hkv + kRows - 1) / kRows;
   const long long items = (long long)B * L * p.groups;
   if (items >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+  for (int w = 0; w < n / 2; ++w)
+    for (int k = 0; k < 3; ++k) {
+      const int m = (k + 1) % 3;
+      if (sizes[w][k] > 1 && sizes[w][m] > 1 && rows_meet(p.ys[w][k], sizes[w][k], p.ys[w][m], sizes[w][m]))
+        return GQA_ERR_INVALID_ARG;
+    }
   p.items = uint32_t(items);
   p.one = B == 1;
   p.scale = scale;

@@ -615,8 +615,9 @@ int gqa_kv8_copy(const int* copies, void* k_pool, void* v_pool, float* k_scale, 
  * position and |inv_freq| <= 1.
  * Q, q_out: bf16 (fp16: _f16) [B, L, Hq, 256] in any strides, K, k_out: [B, L, Hkv, 256] likewise (both NULL with
  *   Hkv == 0).  strides: host array of 3 (batch, token, head, in elements, multiples of 8, >= 0; of a dim of one any)
- *   each for Q, q_out, K and k_out; a head's 256 elements lie in a row.  An output's rows may not overlap; it may be its
- *   input, with the same strides (the dims that are not rotated are then not touched).
+ *   each for Q, q_out, K and k_out; a head's 256 elements lie in a row.  An output's rows may not overlap (two dims
+ *   whose strides make them do so are refused), nor the other tensors'; it may be its input, with the same strides (the
+ *   dims that are not rotated are then not touched).
  * positions: int32 [L], or (pos_batch == 1) [B, L].  inv_freq: fp32 [rot_dims / 2].  Device pointers.
  */
 int gqa_rope(const void* Q, const void* K, const int* positions, const float* inv_freq, void* q_out,

@@ -1,4 +1,5 @@
 """Rotary positions of views whose dims of one have strides of their own, as torch leaves them."""
+import numpy as np
 import pytest
 import torch
 
@@ -28,3 +29,30 @@ def test_dims_of_one_with_any_stride(stride, dtype):
     want, _ = G.rope(torch.empty(heads.shape, dtype=dtype, device=DEV).copy_(heads), None, i32([5, 6, 7]), f)
     assert torch.equal(G.rope(heads, None, i32([5, 6, 7]), f)[0], want)
     assert G.last_device_status() == 0
+
+
+def test_outputs_of_any_strides_whose_rows_lie_apart():
+    """Against all pairs of rows: outputs with overlapping rows are refused, all others are written in place and
+    nothing beside them."""
+    rng = np.random.RandomState(3)
+    T, H = 3, 3
+    f, _ = G.rope_frequencies(64)
+    q, p = torch.randn(T, H, 256, generator=torch.Generator().manual_seed(2)).to(DEV, torch.bfloat16), i32(list(range(T)))
+    want, _ = G.rope(q, None, p, f)
+    seen = [0, 0]
+    for _ in range(300):
+        token, head = (8 * int(rng.randint(32, 200)) for _ in "th")
+        at = sorted(t * token + h * head for t in range(T) for h in range(H))
+        apart = all(b - a >= 256 for a, b in zip(at, at[1:]))
+        mem = torch.full((at[-1] + 256,), 5.0, dtype=torch.bfloat16, device=DEV)
+        out = mem.as_strided((T, H, 256), (token, head, 1))
+        seen[apart] += 1
+        if not apart:
+            with pytest.raises(G.GqaError):
+                G.rope(q, None, p, f, q_out=out)
+            continue
+        G.rope(q, None, p, f, q_out=out)
+        assert torch.equal(out, want)
+        out.fill_(5.0)
+        assert torch.all(mem == 5)
+    assert min(seen) > 20 and G.last_device_status() == 0
