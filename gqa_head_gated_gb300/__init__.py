@@ -589,7 +589,7 @@ def rope_frequencies(rot_dims, base=10000.0, method=None, factor=1.0, original_l
                              / (2 * math.log(base)))
         low = max(math.floor(pair(beta_fast)), 0)
         high = min(math.ceil(pair(beta_slow)), rot_dims - 1)
-        ramp = ((j - low) / max(high - low, 1e-3)).clamp(0, 1)
+        ramp = ((j - low) / (high - low)).clamp(0, 1) if high > low else (j >= high).double()
         freq = freq / factor * ramp + freq * (1 - ramp)
         scale = 0.1 * math.log(factor) + 1.0
     return freq.float().to(device), scale
