@@ -19,14 +19,9 @@
 // fp32 probabilities against a reference of its own, without the V scales.
 //
 // What bounds it: 2 x 1024 tensor clocks a tile of 128 rows x 128 keys (three 8-bit terms of p, as the kernels for
-// few rows have them, would take 2560 in all; fp16 takes 2560), beside 1024 clocks of ex2.  Measured, bf16: 2048 rows behind
-// 30720 keys 632 us (1,680 TFLOP/s of 1,919; 603 repeated on two inputs), a prompt of 8192 rows 592 us (1,390: 768
+// few rows have them, would take 2560 in all; fp16 takes 2560), beside 1024 clocks of ex2.  Measured, bf16, new inputs at
+// each call: 2048 rows behind 30720 keys 645 us (1,650 TFLOP/s of 1,919), a prompt of 8192 rows 592 us (1,390: 768
 // segments' starts and ends show); fp16 costs its third term.
-//
-// Tried without gain: scores kept in registers instead of a second read (732 us for 715), two teams of softmax warps
-// that take turns (727 for 721), a third K slot, L2 prefetch of the tiles ahead, four rows' outputs stored together
-// (721 for 703), fp16 with K converted instead of a third term (740 for 805 behind 30720 keys, but 1740 for 1675 on chunks
-// that are not in L2).
 //
 // The hot loops are small on purpose, but for the issuing warp's: five roles share an SM's instruction caches (the
 // softmax unrolled over all of a row's keys: 1077 us), while operands made in a loop make a product's issue longer than its
@@ -242,7 +237,7 @@ __device__ __forceinline__ uint4 to_f16x8(uint2 u) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// (in line: a kernel that shares its registers out again may not call)
+// (in line: the warps that gave registers away hold fewer than a called function of this launch may use)
 __device__ __forceinline__ bool hold(uint64_t* bar, uint32_t parity, uint64_t tmo, int* abort) {
   return ptx::mbar_wait(bar, parity, tmo, abort);
 }
@@ -254,7 +249,8 @@ __device__ __forceinline__ bool wait_rec(Sm& sm, uint32_t J, uint64_t tmo) {
 }
 
 // The dims of 128 from `dim` on in which a hit key that this row sees has a NaN: NaN in the row's output
-// (rare).  part: its fp32 part, else out: its 16-bit output.
+// (rare; called by the softmax warps, which hold more registers than a function of this launch may use).  part: its
+// fp32 part, else out: its 16-bit output.
 __device__ __noinline__ void put_back(const ChunkArgs& p, const uint32_t* hit, int b, int g, int pr_lo,
                                       int lim, int dim, float* part, uint16_t* out, uint16_t nan16) {
   for (int w = 0; w < kHitWords; ++w)
@@ -277,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) kv8_chunk_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   using Sm = ChunkSmem<kF16>;
   // (an offset, not a rounded pointer: the compiler then knows that it is shared memory; with generic accesses 2048
-  // rows at 30720 took 640 us for 603, 8192 rows 608 for 583)
+  // rows at 30720 took 640 us for 603, 8192 rows 608 for 583, each repeated on two inputs)
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((0u - ptx::smem_addr(smem_raw)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t tmo = p.ctl.timeout_ns;

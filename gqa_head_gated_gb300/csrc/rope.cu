@@ -8,12 +8,13 @@
 // The angle is worked out in turns of 2^-64, modulo a turn, by integer products: inv_freq = m 2^e as 24-bit m times
 // 2^66 / (2 pi) gives the turn's share of one position to 2^-64, times the position, so that a position of 2^31 is
 // off by 2^-32 of a turn (in fp32 a far position's angle is wrong by whole radians; fp64 products, at 2 a clock and
-// SM, would take as long as the copies).  sincospif takes it from there, once per pair of an item, a
-// lane a pair.
+// SM, would take as long as the copies).  What is left of it, half a turn at most, is rounded to fp32 (2^-23 of a radian)
+// for sincospif, once per pair of an item, a lane a pair.
 //
 // Bound by memory: a warp takes items of 8 heads of a token, 512 bytes (16 a lane) each, the next item's loads under way
 // while it turns one.  8192 tokens of 24 + 4 heads, 64 dims turned: 42 us (83 % of the copy rate); 32749 of 16 + 2, whole
-// heads: 100 us (89 %).  With a CTA a token they took 56 and 172.
+// heads: 100 us (89 %).  With a CTA a token they took 56 and 172.  [B, H, L, 256] takes 7 % longer than token-major rows
+// (single calls of the first case, L2 full of other data: 62 us for 58; in place 51 for 49).
 #include <cuda_runtime.h>
 
 #include "kv8_common.cuh"
@@ -53,7 +54,7 @@ __device__ __forceinline__ unsigned long long turns_of(float freq) {
   return int(b) < 0 ? 0ull - f : f;
 }
 
-// cos and sin of a position's turns, whose upper 32 bits do: 2^-32 of a turn.
+// cos and sin of a position's turns, whose upper 32 bits do: 2^-32 of a turn, and then fp32's 24 bits of up to half a turn.
 __device__ __forceinline__ float2 turn(int position, unsigned long long turns) {
   const unsigned long long a = turns * static_cast<unsigned long long>(static_cast<long long>(position));
   float sn, cs;

@@ -611,8 +611,8 @@ int gqa_kv8_copy(const int* copies, void* k_pool, void* v_pool, float* k_scale, 
  *   (x1, x2) -> (x1 cos a - x2 sin a, x2 cos a + x1 sin a) * scale,  a = position * inv_freq[j]
  * for pairs j of each head's first rot_dims dims (a multiple of 16, 16 .. 256): dims j and j + rot_dims / 2, or
  * (interleaved != 0) 2 j and 2 j + 1.  The dims behind them are copied.  inverse != 0: the rotation back
- * (by -a), which is also the gradient's.  Fp32 arithmetic, rounded once; a is right to 2^-29 for every int32
- * position and |inv_freq| <= 1.
+ * (by -a), which is also the gradient's.  Fp32 arithmetic, rounded once.  a is reduced to half a turn in integers,
+ * right to 2^-29 for every int32 position and |inv_freq| <= 1, and what is left is rounded to fp32: 2^-23 of a radian.
  * Q, q_out: bf16 (fp16: _f16) [B, L, Hq, 256] in any strides, K, k_out: [B, L, Hkv, 256] likewise (both NULL with
  *   Hkv == 0).  strides: host array of 3 (batch, token, head, in elements, multiples of 8, >= 0; of a dim of one any)
  *   each for Q, q_out, K and k_out; a head's 256 elements lie in a row.  An output's rows may not overlap (two dims
